@@ -8,7 +8,8 @@ the library is missing the import fails loudly, there is no fallback.
 
 Layouts and semantics are those of include/mamba2_ssd.h ("Accelerating
 Mamba-2 with High-Performance Forward Pass Kernels in NVIDIA CUDA Tile",
-§Kernel 1-3).
+§Kernel 1-3) and, for the gated delta rule, the causal convolution and the
+group norm, of include/mamba2_gated_delta.h.
 """
 from __future__ import annotations
 
@@ -21,8 +22,14 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmamba2ssd.so")
 HEADER = os.path.join(os.path.dirname(_PKG), "include", "mamba2_ssd.h")
+HEADER_GATED_DELTA = os.path.join(os.path.dirname(_PKG), "include", "mamba2_gated_delta.h")
 
 MAMBA2_F32, MAMBA2_BF16 = 0, 1
+MAMBA2_GDR_QK_L2NORM = 1
+MAMBA2_CONV_SILU = 1
+MAMBA2_NORM_SUBTRACT_MEAN, MAMBA2_NORM_GATE_BEFORE, MAMBA2_NORM_GATE_AFTER, MAMBA2_NORM_SILU = 1, 2, 4, 8
+NORM_MODES = {"none": 0, "before": MAMBA2_NORM_GATE_BEFORE, "after": MAMBA2_NORM_GATE_AFTER,
+              "silu": MAMBA2_NORM_SILU}
 STATUS = {0: "MAMBA2_OK", 1: "MAMBA2_ERR_INVALID_ARG", 2: "MAMBA2_ERR_UNSUPPORTED",
           3: "MAMBA2_ERR_CUDA", 4: "MAMBA2_ERR_TIMEOUT"}
 
@@ -39,6 +46,25 @@ class mamba2_shape(ctypes.Structure):
                 ("chunk_size", ctypes.c_int64), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class mamba2_gdr_options(ctypes.Structure):
+    _fields_ = [("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("scale", ctypes.c_float), ("l2_eps", ctypes.c_float), ("flags", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class mamba2_conv_shape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("width", ctypes.c_int64), ("x_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("flags", ctypes.c_int32)]
+
+
+class mamba2_norm_shape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("channels", ctypes.c_int64), ("ngroups", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64),
+                ("eps", ctypes.c_float), ("dtype", ctypes.c_int32), ("flags", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -52,6 +78,7 @@ def load_library(path: str = LIB_PATH):
                           "`python -m mamba_chunked_ssd_gb300.build_lib` (needs nvcc)")
     lib = ctypes.CDLL(path)
     P, S = ctypes.c_void_p, ctypes.POINTER(mamba2_shape)
+    O, V, N = (ctypes.POINTER(t) for t in (mamba2_gdr_options, mamba2_conv_shape, mamba2_norm_shape))
     sig = {
         "mamba2_chunk_cumsum": (ctypes.c_int, [S, P, P, P, P]),
         "mamba2_state_pass": (ctypes.c_int, [S, P, P, P, P, P, P, P, P]),
@@ -61,6 +88,11 @@ def load_library(path: str = LIB_PATH):
         "mamba2_ssd_fwd": (ctypes.c_int, [S, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]),
         "mamba2_ssd_fwd_noalloc": (ctypes.c_int, [S, P, P, P, P, P, P, P, P, P, P]),
         "mamba2_ssd_step": (ctypes.c_int, [S, P, P, P, P, P, P, P, P, P, P]),
+        "mamba2_gdr_fwd": (ctypes.c_int, [S, O, P, P, P, P, P, P, P, P, P, P]),
+        "mamba2_gdr_step": (ctypes.c_int, [S, O, P, P, P, P, P, P, P, P, P]),
+        "mamba2_causal_conv_fwd": (ctypes.c_int, [V, P, P, P, P, P, P, P, P]),
+        "mamba2_causal_conv_step": (ctypes.c_int, [V, P, P, P, P, P, P, P]),
+        "mamba2_group_norm": (ctypes.c_int, [N, P, P, P, P, P, P]),
         "mamba2_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_int64, P]),
         "mamba2_check_device_status": (ctypes.c_int, [P]),
         "mamba2_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -228,6 +260,179 @@ def mamba2_ssd_step(x, dt, A, B, C, state_in=None, D=None, state_out=None, y=Non
         ctypes.byref(shape), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
         _ptr(state_in), _ptr(state_out), _ptr(y), _stream(stream)))
     return y, state_out
+
+
+def _rows(t, name, inner):
+    """Stride from row to row of a tensor whose last ``inner`` dimensions are
+    packed and whose leading ones form one run of rows, e.g. a channel slice of
+    a contiguous [b, L, C] tensor."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    shape, st = t.shape, t.stride()
+    if t.is_contiguous():
+        width = 1
+        for d in shape[len(shape) - inner:]:
+            width *= d
+        return width
+    lead, want = len(shape) - inner, 1
+    for d in range(len(shape) - 1, lead - 1, -1):
+        if shape[d] != 1 and st[d] != want:
+            raise ValueError(f"{name}: the last {inner} dimension(s) must be packed")
+        want *= shape[d]
+    row = None
+    for d in range(lead - 1, -1, -1):
+        if shape[d] == 1:
+            continue
+        if row is None:
+            row = run = st[d]
+        elif st[d] != run:
+            raise ValueError(f"{name}: its rows must be one run with one stride")
+        run *= shape[d]
+    if row is None:
+        return want
+    if row < want:
+        raise ValueError(f"{name}: its rows overlap")
+    return row
+
+
+def _want(t, name, dtype, shape):
+    """A contiguous CUDA tensor of this dtype and shape (or None)."""
+    if t is None:
+        return
+    _need(t, name)
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {dtype} {shape}, not {t.dtype} {tuple(t.shape)}")
+
+
+def _gdr_args(q, k, v, g, beta, scale, qk_l2norm, l2_eps):
+    """The shape and options of a gated-delta-rule call; checks q, k, v, g, beta."""
+    *rows, nh, H = v.shape
+    G, S = q.shape[-2:]
+    if q.shape != k.shape or tuple(q.shape[:-2]) != tuple(rows):
+        raise ValueError(f"q and k must be {tuple(rows)} + (groups, state): got {tuple(q.shape)}, {tuple(k.shape)}")
+    if q.dtype != v.dtype or k.dtype != v.dtype:
+        raise TypeError("q, k and v must have one dtype")
+    _want(g, "g", torch.float32, (*rows, nh)), _want(beta, "beta", torch.float32, (*rows, nh))
+    shape = mamba2_shape(rows[0], rows[1] if len(rows) > 1 else 1, nh, H, S, G, 64, _dtype_code(v), 0)
+    opt = mamba2_gdr_options(_rows(q, "q", 2), _rows(k, "k", 2), _rows(v, "v", 2), S ** -0.5 if scale is None else scale,
+                             l2_eps, MAMBA2_GDR_QK_L2NORM if qk_l2norm else 0, 0)
+    return shape, opt
+
+
+def mamba2_gdr_fwd(q, k, v, g, beta, scale=None, qk_l2norm=False, l2_eps=1e-6, initial_state=None, lengths=None,
+                   y=None, final_state=None, want_final_state=True, stream=None):
+    """The gated delta rule over whole sequences: (y [b, L, nh, H], final_state
+    [b, nh, S, H] fp32 or None).  q, k [b, L, G, S] and v [b, L, nh, H] may be
+    slices of a wider tensor; g (log decay), beta [b, L, nh] fp32; scale
+    defaults to S ** -0.5; lengths [b] int32 or None."""
+    shape, opt = _gdr_args(q, k, v, g, beta, scale, qk_l2norm, l2_eps)
+    b, nh, S, H = shape.batch, shape.nheads, shape.dstate, shape.headdim
+    _want(initial_state, "initial_state", torch.float32, (b, nh, S, H)), _want(lengths, "lengths", torch.int32, (b,))
+    if y is None:
+        y = torch.empty(v.shape, device=v.device, dtype=v.dtype)
+    else:
+        _want(y, "y", v.dtype, tuple(v.shape))
+    if final_state is not None:
+        _want(final_state, "final_state", torch.float32, (b, nh, S, H))
+    elif want_final_state:
+        final_state = torch.empty(b, nh, S, H, device=v.device, dtype=torch.float32)
+    _check("mamba2_gdr_fwd", load_library().mamba2_gdr_fwd(
+        ctypes.byref(shape), ctypes.byref(opt), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(lengths),
+        _ptr(initial_state), _ptr(y), _ptr(final_state), _stream(stream)))
+    return y, final_state
+
+
+def mamba2_gdr_step(q, k, v, g, beta, state_in=None, scale=None, qk_l2norm=False, l2_eps=1e-6, state_out=None, y=None,
+                    stream=None):
+    """One token of the gated delta rule: q, k [b, G, S], v [b, nh, H], g, beta
+    [b, nh], state [b, nh, S, H] fp32.  Returns (y [b, nh, H], state_out).  Pass
+    state_out=state_in to update the state in place."""
+    shape, opt = _gdr_args(q, k, v, g, beta, scale, qk_l2norm, l2_eps)
+    b, nh, S, H = shape.batch, shape.nheads, shape.dstate, shape.headdim
+    _want(state_in, "state_in", torch.float32, (b, nh, S, H))
+    if y is None:
+        y = torch.empty(v.shape, device=v.device, dtype=v.dtype)
+    else:
+        _want(y, "y", v.dtype, tuple(v.shape))
+    if state_out is None:
+        state_out = torch.empty(b, nh, S, H, device=v.device, dtype=torch.float32)
+    else:
+        _want(state_out, "state_out", torch.float32, (b, nh, S, H))
+    _check("mamba2_gdr_step", load_library().mamba2_gdr_step(
+        ctypes.byref(shape), ctypes.byref(opt), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state_in),
+        _ptr(state_out), _ptr(y), _stream(stream)))
+    return y, state_out
+
+
+def mamba2_causal_conv_fwd(x, weight, bias=None, silu=True, initial_state=None, lengths=None, y=None,
+                           final_state=None, want_final_state=True, stream=None):
+    """Depthwise causal convolution over time: x [b, L, C] (may be a channel
+    slice), weight [C, W] and bias [C] fp32, states [b, W - 1, C] in x's dtype.
+    Returns (y [b, L, C], final_state or None)."""
+    b, L, C = x.shape
+    W = weight.shape[-1]
+    _want(weight, "weight", torch.float32, (C, W)), _want(bias, "bias", torch.float32, (C,))
+    _want(initial_state, "initial_state", x.dtype, (b, W - 1, C)), _want(lengths, "lengths", torch.int32, (b,))
+    if y is None:
+        y = torch.empty(b, L, C, device=x.device, dtype=x.dtype)
+    elif y.dtype != x.dtype or y.shape != x.shape:
+        raise ValueError("y must have x's dtype and shape")
+    if final_state is not None:
+        _want(final_state, "final_state", x.dtype, (b, W - 1, C))
+    elif want_final_state:
+        final_state = torch.empty(b, W - 1, C, device=x.device, dtype=x.dtype)
+    shape = mamba2_conv_shape(b, L, C, W, _rows(x, "x", 1), _rows(y, "y", 1), _dtype_code(x),
+                              MAMBA2_CONV_SILU if silu else 0)
+    _check("mamba2_causal_conv_fwd", load_library().mamba2_causal_conv_fwd(
+        ctypes.byref(shape), _ptr(x), _ptr(weight), _ptr(bias), _ptr(lengths), _ptr(initial_state), _ptr(y),
+        _ptr(final_state), _stream(stream)))
+    return y, final_state
+
+
+def mamba2_causal_conv_step(x, weight, state_in=None, bias=None, silu=True, state_out=None, y=None, stream=None):
+    """One token of the convolution: x [b, C], state [b, W - 1, C] in x's dtype.
+    Returns (y [b, C], state_out); state_out=state_in updates in place."""
+    b, C = x.shape
+    W = weight.shape[-1]
+    _want(weight, "weight", torch.float32, (C, W)), _want(bias, "bias", torch.float32, (C,))
+    _want(state_in, "state_in", x.dtype, (b, W - 1, C))
+    if y is None:
+        y = torch.empty(b, C, device=x.device, dtype=x.dtype)
+    elif y.dtype != x.dtype or y.shape != x.shape:
+        raise ValueError("y must have x's dtype and shape")
+    if state_out is None:
+        state_out = torch.empty(b, W - 1, C, device=x.device, dtype=x.dtype)
+    else:
+        _want(state_out, "state_out", x.dtype, (b, W - 1, C))
+    shape = mamba2_conv_shape(b, 1, C, W, _rows(x, "x", 1), _rows(y, "y", 1), _dtype_code(x),
+                              MAMBA2_CONV_SILU if silu else 0)
+    _check("mamba2_causal_conv_step", load_library().mamba2_causal_conv_step(
+        ctypes.byref(shape), _ptr(x), _ptr(weight), _ptr(bias), _ptr(state_in), _ptr(state_out), _ptr(y),
+        _stream(stream)))
+    return y, state_out
+
+
+def mamba2_group_norm(x, weight, ngroups, z=None, bias=None, eps=1e-5, subtract_mean=False, mode="none", y=None,
+                      stream=None):
+    """Group norm of each row of x [.., C] over its ngroups groups of channels:
+    mode "none", "silu" (SiLU of the result), "before" or "after" (a gate
+    SiLU(z) before or after the norm).  weight, bias [C] fp32 or None."""
+    C = x.shape[-1]
+    _want(weight, "weight", torch.float32, (C,)), _want(bias, "bias", torch.float32, (C,))
+    if mode not in NORM_MODES:
+        raise ValueError(f"mode must be one of {sorted(NORM_MODES)}, not {mode!r}")
+    for t, n in ((z, "z"), (y, "y")):
+        if t is not None and (t.dtype != x.dtype or t.shape != x.shape):
+            raise ValueError(f"{n} must have x's dtype and shape")
+    if y is None:
+        y = torch.empty(x.shape, device=x.device, dtype=x.dtype)
+    rows = x.numel() // C if C else 0
+    shape = mamba2_norm_shape(rows, C, ngroups, _rows(x, "x", 1), 0 if z is None else _rows(z, "z", 1),
+                              _rows(y, "y", 1), eps, _dtype_code(x),
+                              NORM_MODES[mode] | (MAMBA2_NORM_SUBTRACT_MEAN if subtract_mean else 0), 0)
+    _check("mamba2_group_norm", load_library().mamba2_group_norm(
+        ctypes.byref(shape), _ptr(x), _ptr(z), _ptr(weight), _ptr(bias), _ptr(y), _stream(stream)))
+    return y
 
 
 def mamba2_selftest_wait_timeout(limit_ns: int, stream=None):

@@ -8,6 +8,7 @@
 #include <mutex>
 #include <utility>
 
+#include "abi_checks.cuh"
 #include "common.cuh"
 
 namespace m2 {
@@ -18,9 +19,39 @@ constexpr int kVersion = 1 * 10000 + 2 * 100 + 0;
 // Per-device status word: kernels with bounded waits record a timeout here.
 __device__ unsigned int g_status_word = 0;
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 int64_t elt_size(const mamba2_shape& s) { return s.dtype == MAMBA2_BF16 ? 2 : 4; }
+
+struct Sizes {
+    int64_t x, dt, A, bc, D, G, cs, state;
+};
+Sizes sizes_of(const mamba2_shape& s) {
+    const int64_t e = elt_size(s);
+    const int64_t nc = (s.seqlen + s.chunk_size - 1) / s.chunk_size;
+    Sizes z;
+    z.x = s.batch * s.seqlen * s.nheads * s.headdim * e;
+    z.dt = s.batch * s.seqlen * s.nheads * 4;
+    z.A = s.nheads * 4;
+    z.D = s.nheads * 4;
+    z.bc = s.batch * s.seqlen * s.ngroups * s.dstate * e;
+    z.G = s.batch * s.nheads * s.seqlen * 4;
+    z.cs = s.batch * s.nheads * nc * s.dstate * s.headdim * e;
+    z.state = s.batch * s.nheads * s.dstate * s.headdim * 4;
+    return z;
+}
+
+// final_state <- initial_state (or zeros) for an empty sequence.
+mamba2_status empty_sequence_state(const mamba2_shape& s, const float* init, float* final_state,
+                                   cudaStream_t st) {
+    if (!final_state || s.batch == 0) return MAMBA2_OK;
+    const size_t bytes = (size_t)sizes_of(s).state;
+    cudaError_t e = init ? cudaMemcpyAsync(final_state, init, bytes, cudaMemcpyDeviceToDevice, st)
+                         : cudaMemsetAsync(final_state, 0, bytes, st);
+    return from_cuda(e);
+}
+
+int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
+
+}  // namespace
 
 // Shape checks shared by every entry point.
 mamba2_status check_shape(const mamba2_shape* s) {
@@ -41,77 +72,6 @@ mamba2_status check_shape(const mamba2_shape* s) {
         return MAMBA2_ERR_UNSUPPORTED;
     return MAMBA2_OK;
 }
-
-struct Range {
-    uintptr_t lo, hi;
-};
-Range range_of(const void* p, int64_t bytes) {
-    return {reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + (uintptr_t)bytes};
-}
-bool overlap(Range a, Range b) {
-    return a.lo != a.hi && b.lo != b.hi && a.lo < b.hi && b.lo < a.hi;
-}
-
-// A tensor argument: pointer, byte size, whether it may be null.
-struct Arg {
-    const void* p;
-    int64_t bytes;
-    bool optional;
-};
-
-mamba2_status check_ptrs(const Arg* in, int nin, const Arg* out, int nout) {
-    for (int i = 0; i < nin + nout; ++i) {
-        const Arg& a = i < nin ? in[i] : out[i - nin];
-        if (!a.p) {
-            if (!a.optional && a.bytes > 0) return MAMBA2_ERR_INVALID_ARG;
-            continue;
-        }
-        if (!aligned16(a.p)) return MAMBA2_ERR_INVALID_ARG;
-    }
-    for (int o = 0; o < nout; ++o) {
-        if (!out[o].p) continue;
-        const Range ro = range_of(out[o].p, out[o].bytes);
-        for (int i = 0; i < nin; ++i)
-            if (in[i].p && overlap(ro, range_of(in[i].p, in[i].bytes))) return MAMBA2_ERR_INVALID_ARG;
-        for (int j = o + 1; j < nout; ++j)
-            if (out[j].p && overlap(ro, range_of(out[j].p, out[j].bytes))) return MAMBA2_ERR_INVALID_ARG;
-    }
-    return MAMBA2_OK;
-}
-
-struct Sizes {
-    int64_t x, dt, A, bc, D, G, cs, state;
-};
-Sizes sizes_of(const mamba2_shape& s) {
-    const int64_t e = elt_size(s);
-    const int64_t nc = (s.seqlen + s.chunk_size - 1) / s.chunk_size;
-    Sizes z;
-    z.x = s.batch * s.seqlen * s.nheads * s.headdim * e;
-    z.dt = s.batch * s.seqlen * s.nheads * 4;
-    z.A = s.nheads * 4;
-    z.D = s.nheads * 4;
-    z.bc = s.batch * s.seqlen * s.ngroups * s.dstate * e;
-    z.G = s.batch * s.nheads * s.seqlen * 4;
-    z.cs = s.batch * s.nheads * nc * s.dstate * s.headdim * e;
-    z.state = s.batch * s.nheads * s.dstate * s.headdim * 4;
-    return z;
-}
-
-mamba2_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MAMBA2_OK : MAMBA2_ERR_CUDA; }
-
-// final_state <- initial_state (or zeros) for an empty sequence.
-mamba2_status empty_sequence_state(const mamba2_shape& s, const float* init, float* final_state,
-                                   cudaStream_t st) {
-    if (!final_state || s.batch == 0) return MAMBA2_OK;
-    const size_t bytes = (size_t)sizes_of(s).state;
-    cudaError_t e = init ? cudaMemcpyAsync(final_state, init, bytes, cudaMemcpyDeviceToDevice, st)
-                         : cudaMemsetAsync(final_state, 0, bytes, st);
-    return from_cuda(e);
-}
-
-int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
-
-}  // namespace
 
 cudaError_t ensure_max_dynamic_smem(const void* func, int bytes) {
     static std::mutex mu;

@@ -1,0 +1,168 @@
+// k_causal_conv.cu — depthwise causal convolution over time, channels last,
+// with an optional SiLU: over whole sequences, and one token at a time.
+//
+//   y_t = act(bias + sum_{w < W} weight[c, w] x_{t - (W - 1) + w})
+//
+// Each input is read once and each output written once: the kernels are
+// bound by memory.  A thread owns the channels of one 16-byte vector and a run
+// of consecutive tokens, and slides a window of the last W - 1 inputs through
+// its registers, so a token's input is loaded once per run (plus the W - 1
+// tokens before the run, which the neighbouring run has just brought into L2).
+#include "gated_delta.cuh"
+
+namespace m2 {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kRun = 32;    // tokens per thread
+constexpr int kAhead = 8;   // loads in flight per thread
+
+template <typename T, int VEC, int W>
+__global__ void __launch_bounds__(kThreads) k_causal_conv(const ConvArgs a) {
+    using V = typename VecOf<T, VEC>::type;
+    const int64_t c = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * VEC;
+    if (c >= a.channels) return;
+    const int64_t b = blockIdx.z;
+    const int64_t n = row_length(a.lengths, b, a.seqlen);
+    const T* x = static_cast<const T*>(a.x) + b * a.seqlen * a.x_stride + c;
+    T* y = static_cast<T*>(a.y) + b * a.seqlen * a.y_stride + c;
+    const T* init = a.init ? static_cast<const T*>(a.init) + b * (W - 1) * a.channels + c : nullptr;
+
+    // the input at token t < n, from the initial state where t < 0
+    auto input = [&](int64_t t) -> V {
+        if (t >= 0) return *reinterpret_cast<const V*>(x + t * a.x_stride);
+        if (init) return *reinterpret_cast<const V*>(init + (t + W - 1) * a.channels);
+        return V{};
+    };
+
+    if (blockIdx.y == 0 && a.final_state) {
+        T* fin = static_cast<T*>(a.final_state) + b * (W - 1) * a.channels + c;
+#pragma unroll
+        for (int w = 0; w < W - 1; ++w) *reinterpret_cast<V*>(fin + w * a.channels) = input(n - (W - 1) + w);
+    }
+
+    float wt[W][VEC], bias[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        bias[i] = a.bias ? a.bias[c + i] : 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) wt[w][i] = a.weight[(c + i) * W + w];
+    }
+
+    for (int64_t t0 = (int64_t)blockIdx.y * kRun; t0 < a.seqlen; t0 += (int64_t)gridDim.y * kRun) {
+        const int64_t t1 = imin64(t0 + kRun, a.seqlen);
+        const int64_t tv = imin64(t1, n);  // tokens that are computed
+        float win[W][VEC];                 // win[w]: the input W - 1 - w tokens back
+        if (t0 < tv) {
+#pragma unroll
+            for (int w = 0; w < W - 1; ++w) unpack<VEC>(input(t0 - (W - 1) + w), win[w + 1], (const T*)nullptr);
+        }
+        for (int64_t t = t0; t < tv; t += kAhead) {
+            V in[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (t + u < tv) in[u] = *reinterpret_cast<const V*>(x + (t + u) * a.x_stride);
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (t + u >= tv) break;
+#pragma unroll
+                for (int w = 0; w < W - 1; ++w)
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) win[w][i] = win[w + 1][i];
+                unpack<VEC>(in[u], win[W - 1], (const T*)nullptr);
+                float s[VEC];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    s[i] = bias[i];
+#pragma unroll
+                    for (int w = 0; w < W; ++w) s[i] = fmaf(wt[w][i], win[w][i], s[i]);
+                    if (a.silu) s[i] = silu_f32<T>(s[i]);
+                }
+                *reinterpret_cast<V*>(y + (t + u) * a.y_stride) = pack<T, VEC>(s);
+            }
+        }
+        for (int64_t t = t0 > tv ? t0 : tv; t < t1; ++t) *reinterpret_cast<V*>(y + t * a.y_stride) = V{};
+    }
+}
+
+// One token: a thread reads its channels' state and input, and writes the
+// output and the state moved on by one (in place is safe: it reads all of its
+// own elements first).
+template <typename T, int VEC, int W>
+__global__ void __launch_bounds__(kThreads) k_causal_conv_step(const ConvArgs a) {
+    using V = typename VecOf<T, VEC>::type;
+    const int64_t c = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * VEC;
+    if (c >= a.channels) return;
+    const int64_t b = blockIdx.y;
+    const int64_t at = b * (W - 1) * a.channels + c;
+    V in[W];
+#pragma unroll
+    for (int w = 0; w < W - 1; ++w)
+        in[w] = a.init ? *reinterpret_cast<const V*>(static_cast<const T*>(a.init) + at + w * a.channels) : V{};
+    in[W - 1] = *reinterpret_cast<const V*>(static_cast<const T*>(a.x) + b * a.x_stride + c);
+    float s[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) s[i] = a.bias ? a.bias[c + i] : 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        float f[VEC];
+        unpack<VEC>(in[w], f, (const T*)nullptr);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) s[i] = fmaf(a.weight[(c + i) * W + w], f[i], s[i]);
+    }
+#pragma unroll
+    for (int w = 0; w < W - 1; ++w)
+        *reinterpret_cast<V*>(static_cast<T*>(a.final_state) + at + w * a.channels) = in[w + 1];
+    if (a.silu) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) s[i] = silu_f32<T>(s[i]);
+    }
+    *reinterpret_cast<V*>(static_cast<T*>(a.y) + b * a.y_stride + c) = pack<T, VEC>(s);
+}
+
+template <typename T, int VEC, int W>
+cudaError_t launch_w(const ConvArgs& a, bool step, cudaStream_t st) {
+    const unsigned gx = (unsigned)((a.channels + (int64_t)kThreads * VEC - 1) / (kThreads * VEC));
+    if (step) {
+        k_causal_conv_step<T, VEC, W><<<dim3(gx, (unsigned)a.batch), kThreads, 0, st>>>(a);
+    } else {
+        const int64_t runs = (a.seqlen + kRun - 1) / kRun;
+        k_causal_conv<T, VEC, W>
+            <<<dim3(gx, (unsigned)imin64(runs, 65535), (unsigned)a.batch), kThreads, 0, st>>>(a);
+    }
+    return cudaGetLastError();
+}
+
+template <typename T, int VEC>
+cudaError_t launch_v(const ConvArgs& a, bool step, cudaStream_t st) {
+    switch (a.width) {
+        case 2: return launch_w<T, VEC, 2>(a, step, st);
+        case 3: return launch_w<T, VEC, 3>(a, step, st);
+        case 4: return launch_w<T, VEC, 4>(a, step, st);
+        case 5: return launch_w<T, VEC, 5>(a, step, st);
+        case 6: return launch_w<T, VEC, 6>(a, step, st);
+        case 7: return launch_w<T, VEC, 7>(a, step, st);
+        default: return launch_w<T, VEC, 8>(a, step, st);
+    }
+}
+
+// Vectors of 16 bytes where every row of every tensor starts on 16 bytes,
+// single elements elsewhere.
+template <typename T>
+cudaError_t launch_t(const ConvArgs& a, bool step, cudaStream_t st) {
+    constexpr int VEC = 16 / sizeof(T);
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y);
+    const bool vec = a.channels % VEC == 0 && a.x_stride % VEC == 0 && a.y_stride % VEC == 0 && (p & 15) == 0;
+    return vec ? launch_v<T, VEC>(a, step, st) : launch_v<T, 1>(a, step, st);
+}
+
+}  // namespace
+
+cudaError_t launch_causal_conv(const ConvArgs& a, bool bf16, cudaStream_t st) {
+    return bf16 ? launch_t<__nv_bfloat16>(a, false, st) : launch_t<float>(a, false, st);
+}
+cudaError_t launch_causal_conv_step(const ConvArgs& a, bool bf16, cudaStream_t st) {
+    return bf16 ? launch_t<__nv_bfloat16>(a, true, st) : launch_t<float>(a, true, st);
+}
+
+}  // namespace m2
