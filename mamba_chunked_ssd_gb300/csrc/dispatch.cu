@@ -3,6 +3,7 @@
 #include <string.h>
 
 #include "common.cuh"
+#include "gated_delta.cuh"
 
 namespace m2 {
 
@@ -80,6 +81,11 @@ bool f32_chunk_out_tensor_cores(const Geom& g, bool bf16) {
 
 bool use_f32_tensor_cores(const Geom& g, bool bf16) {
     return f32_chunk_out_tensor_cores(g, bf16) && state_pass_split_fits(g);
+}
+
+cudaError_t launch_gdr_fwd(const GdrArgs& a, bool bf16, cudaStream_t st) {
+    if (bf16 && gdr_chunk_tc_fits(a)) return launch_gdr_chunk_tc(a, st);
+    return launch_gdr_recurrent(a, bf16, st);
 }
 
 }  // namespace m2

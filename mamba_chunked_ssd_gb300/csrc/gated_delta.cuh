@@ -102,6 +102,9 @@ __device__ __forceinline__ typename VecOf<T, N>::type pack(const float (&f)[N]) 
 }
 
 cudaError_t launch_gdr_fwd(const GdrArgs& a, bool bf16, cudaStream_t st);
+// The chunked kernel on the tensor cores (bf16) and the calls it covers.
+bool gdr_chunk_tc_fits(const GdrArgs& a);
+cudaError_t launch_gdr_chunk_tc(const GdrArgs& a, cudaStream_t st);
 cudaError_t launch_gdr_recurrent(const GdrArgs& a, bool bf16, cudaStream_t st);
 cudaError_t launch_gdr_step(const GdrArgs& a, bool bf16, cudaStream_t st);
 cudaError_t launch_causal_conv(const ConvArgs& a, bool bf16, cudaStream_t st);

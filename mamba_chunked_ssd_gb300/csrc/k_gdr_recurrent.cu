@@ -172,6 +172,4 @@ cudaError_t launch_gdr_recurrent(const GdrArgs& a, bool bf16, cudaStream_t st) {
     return bf16 ? launch_t<__nv_bfloat16>(a, st) : launch_t<float>(a, st);
 }
 
-cudaError_t launch_gdr_fwd(const GdrArgs& a, bool bf16, cudaStream_t st) { return launch_gdr_recurrent(a, bf16, st); }
-
 }  // namespace m2
