@@ -25,8 +25,9 @@
 //   warps 0-7    chain: h -> two bf16 parts and e^{G_last} h;  R = K h -> X;  W ->
 //                its parts (two per TMEM lane quadrant, half of the columns each)
 //   warps 8-11   output: y from Q h and P W
-//   then 4 NV    scores: G, norms, A, P and N of the next chunk, while the
-//                chain runs on this one
+//   then 4 NV    G, k's norms, A and N of the next chunk, while the chain runs on
+//                this one (four warps to a head)
+//   then 4       q's norms and P
 //   then 1, 1    TMA producer; tcgen05.mma issuer
 // What bounds it is the chain from state to state: three dependent products and
 // three conversions a chunk.  What enters the fp32 state is as good as fp32: N, X
@@ -47,8 +48,8 @@
 // Forward substitution by blocks is stable for any A; a product of powers of A
 // would not be (equal keys make A all ones below the diagonal).
 //
-// G is summed in 32.32 fixed point and kept as an integer and a fraction, so
-// that G_i - G_j is good to 2^-23 even behind a token that forgets everything.
+// G is summed in fixed point and kept as an integer and a fraction, so that
+// G_i - G_j is good to 2^-22 even behind a token that forgets everything.
 // Log2 decays of a token are clamped to +-160, beyond which fp32 has only 0 and
 // infinity.
 #include "gated_delta.cuh"
@@ -59,24 +60,26 @@ namespace m2 {
 namespace {
 
 constexpr int kT = 64;             // tokens per chunk
-constexpr int kChainWarps = 8, kOutWarp0 = 8, kOutWarps = 4, kScoreWarp0 = 12;
+constexpr int kChainWarps = 8, kOutWarp0 = 8, kOutWarps = 4, kNWarp0 = 12, kPWarps = 4;
+// whole warpgroups, for the register split: the last one is TMA, MMA and two idle warps
+constexpr int threads_of(int nv) { return (kNWarp0 + 4 * nv + kPWarps + 4) * 32; }
 constexpr uint32_t kBox = kT * 128;  // one box: 64 tokens x 64 columns of bf16
 constexpr int kMaxStages = 3;
 constexpr int kSmemLimit = 232448;
 
-struct TokScore {  // what the scores need of a token
+struct Tok {       // what the scores need of a token
     float gi, gf;  // G in log2 units: integer part, fraction
     float rk;      // 1 / norm of k
     float beta;
 };
-struct TokChain {
-    float cb, cr, d, pad;  // X = cb v - cr R;  W's share of the state: d
-};
 struct Scalars {  // one head's, per chunk
-    TokChain chain[kT];
-    float2 out[kT];  // y = x Qh + y PW
-    float g_last;    // e^{G_last}
-    float pad[7];
+    Tok tok[kT];
+    float cb[kT], cr[kT];  // X = cb v + cr R
+    float d[kT];           // W's share of the state
+    float gam[kT];         // e^G
+    float oq[kT];          // y = oq (gam Q h + P W)
+    float g_last;          // e^{G_last}
+    float pad[3];
 };
 
 // A head's results of the scores: N's three and P's two planes of 64 rows of
@@ -84,33 +87,37 @@ struct Scalars {  // one head's, per chunk
 // when the chunk before has used them), the scalars in two.
 constexpr uint32_t kPlane = kT * 128;
 constexpr uint32_t kNPlanes = 3, kPPlanes = 2;
-constexpr uint32_t kScalBytes = 3072;
-static_assert(sizeof(Scalars) <= kScalBytes, "scalars");
+constexpr uint32_t kScalBytes = sizeof(Scalars);
+static_assert(kScalBytes % 16 == 0, "scalars");
 
-struct ScoreScratch {       // one head's
+struct NScratch {           // one head's
     float diag[4][16][20];  // A's diagonal blocks, [column][row]; then N's, [row][column]
     float2 low[6][16][8];   // A's blocks below the diagonal, see low_at
-    TokScore tok[kT];
-    float rq[kT];
 };
 // Place of columns 2 c2, 2 c2 + 1 of row r in a block of `low` (spread over the
 // banks for eight rows by four pairs).
 __device__ __forceinline__ int low_at(int r, int c2) { return c2 ^ (((r >> 1) & 1) << 2); }
 __device__ __forceinline__ int low_block(int i, int m) { return i * (i - 1) / 2 + m; }
 
+// The ten 16 x 16 blocks (i, j) of a lower triangle, in rounds of four warps:
+// block t = 4 round + warp, the diagonal first.
+__device__ __forceinline__ int tri_i(int t) { return (0x3323213210 >> (4 * t)) & 15; }
+__device__ __forceinline__ int tri_j(int t) { return (0x0102103210 >> (4 * t)) & 15; }
+
 enum : int {
     kBarFull = 0,                        // [stages] TMA
     kBarFree = kBarFull + kMaxStages,    // [stages] every reader of the stage is done
-    kBarSFull = kBarFree + kMaxStages,   // [2] scalars (and K's rows past the end cleared)
+    kBarSFull = kBarFree + kMaxStages,   // [2] scalars but out (and K's rows past the end cleared)
     kBarSFree = kBarSFull + 2,           // [2]
     kBarNFull = kBarSFree + 2,           // N; free again with kBarWDone
-    kBarPFull,
+    kBarPFull,                           // P and the scalars' out
     kBarPFree,
     kBarHReady,  // h's parts are written, h is decayed
     kBarRDone,
     kBarXReady,
     kBarWDone,
-    kBarWReady,
+    kBarWReady,   // W's parts for the state
+    kBarWyReady,  // and for y
     kBarHDone,
     kBarO1Done,  // Q h
     kBarO1Read,
@@ -129,7 +136,7 @@ struct SharedCtl {
 struct GdrTcParams {
     Geom g;
     int nst;  // stages
-    uint32_t off_n, off_p, off_scal, off_scratch, off_bar;
+    uint32_t off_n, off_p, off_y, off_scal, off_scratch, off_bar;
     const float* gate;
     const float* beta;
     const int32_t* lengths;
@@ -164,9 +171,36 @@ __device__ __forceinline__ bool bar_sync_and(int id, int threads, bool ok) {
     return r != 0;
 }
 
-// A whole warp's wait: all lanes leave with one answer.
+// A whole warp's wait for a phase: true once it has completed; false if the
+// kernel was aborted, or after about 2 s.  try_wait suspends the warp in
+// hardware, so a waiting warp takes few issue slots from working ones.  All
+// lanes leave with one answer.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort));
+    bool done = tc::mbar_try_wait(bar, parity);
+    if (!__all_sync(0xffffffffu, done)) {
+        const long long c0 = clock64();
+        bool give_up = false;
+        do {
+            done = tc::mbar_try_wait(bar, parity);
+            give_up = *abort != 0 || clock64() - c0 > tc::kWaitLimitCycles;
+            done = __all_sync(0xffffffffu, done);
+            give_up = __any_sync(0xffffffffu, give_up);
+        } while (!done && !give_up);
+    }
+    return done;
+}
+
+// Registers per thread of the calling warpgroup from here on.  A block is
+// launched with threads_of(NV) x 80 (NV = 2: x 72) registers; the groups'
+// shares (chain twice) sum to 480 and 504 a thread of a warpgroup, six times 80
+// and seven times 72.
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Byte offset of 16-byte piece `ch` (of 8) of row `row` in a box of 128-byte
@@ -210,34 +244,61 @@ __device__ __forceinline__ void mma8(float (&d)[4], const uint32_t (&a)[4], cons
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
-__device__ __forceinline__ void mma_tf32x3(float (&d)[4], const float (&a)[4], float2 b) {
-    const float av[4] = {a[0], a[2], a[1], a[3]}, bv[2] = {b.x, b.y};
-    uint32_t ah[4], al[4], bh[2], bl[2];
+// d += a b over 16 columns of fp32 values: a an accumulator block (as above),
+// b(row n, pair of columns) b's float2.
+template <class B>
+__device__ __forceinline__ void mma_block(float (&d)[2][4], const float (&a)[2][4], int gid, int tig, B b) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        ah[i] = tf32_rn(av[i]);
-        al[i] = tf32_rn(av[i] - __uint_as_float(ah[i]));
-    }
+    for (int kk = 0; kk < 2; ++kk) {
+        uint32_t ah[4], al[4], bh[2][2], bl[2][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        bh[i] = tf32_rn(bv[i]);
-        bl[i] = tf32_rn(bv[i] - __uint_as_float(bh[i]));
+        for (int i = 0; i < 4; ++i) {
+            const float v = a[kk][((i & 1) << 1) | (i >> 1)];
+            ah[i] = tf32_rn(v);
+            al[i] = tf32_rn(v - __uint_as_float(ah[i]));
+        }
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+            const float2 v = b(8 * nt + gid, 4 * kk + tig);
+            bh[nt][0] = tf32_rn(v.x);
+            bh[nt][1] = tf32_rn(v.y);
+            bl[nt][0] = tf32_rn(v.x - __uint_as_float(bh[nt][0]));
+            bl[nt][1] = tf32_rn(v.y - __uint_as_float(bh[nt][1]));
+        }
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) mma8(d[nt], ah, bh[nt]);
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) mma8(d[nt], ah, bl[nt]);
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) mma8(d[nt], al, bh[nt]);
     }
-    mma8(d, ah, bh);
-    mma8(d, ah, bl);
-    mma8(d, al, bh);
 }
 
-// A pair of fp32 values as its two bf16 parts.
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-    hi = tc::pack_bf16x2(a, b);
-    lo = tc::pack_bf16x2(a - tc::bf16_lo(hi), b - tc::bf16_hi(hi));
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
+// e^{G_i - G_j}
+__device__ __forceinline__ float decay(const Tok& i, const Tok& j) { return ex2((i.gi - j.gi) + (i.gf - j.gf)); }
 
-// And as three.
-__device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-    hi = tc::pack_bf16x2(a, b);
-    split2(a - tc::bf16_lo(hi), b - tc::bf16_hi(hi), mid, lo);
+// A pair of fp32 values as its high bf16 parts, and what they leave.
+__device__ __forceinline__ uint32_t high(float2& v) {
+    const uint32_t hi = tc::pack_bf16x2(v.x, v.y);
+    v = tc::fma_f32x2(make_float2(tc::bf16_lo(hi), tc::bf16_hi(hi)), make_float2(-1.f, -1.f), v);
+    return hi;
+}
+// As its two bf16 parts, and as three.
+__device__ __forceinline__ void split2(float2 v, uint32_t& hi, uint32_t& lo) {
+    hi = high(v);
+    lo = tc::pack_bf16x2(v.x, v.y);
+}
+__device__ __forceinline__ void split3(float2 v, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+    hi = high(v);
+    split2(v, mid, lo);
+}
+__device__ __forceinline__ float2 as_f2(const uint32_t* r) {
+    return make_float2(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
 // 32 fp32 columns of this warp's lanes.
@@ -248,57 +309,47 @@ __device__ __forceinline__ void ld32(uint32_t addr, uint32_t (&a)[16], uint32_t 
     tc::tmem_tie16(b);
 }
 
-// 16 rows (from row0 of tile x) against the rows of blocks jmin .. jmax of tile
-// k, summed over the S columns: acc[jb] is the 16 x 16 product with block jb.
+// The 16 x 16 products of rows 16 i .. of tile x with rows 16 j .. of tile k,
+// summed over the S columns.
 template <int S>
-__device__ __forceinline__ void score_rows(uint32_t x, uint32_t k, int row0, int jmin, int jmax, int lane,
-                                           float (&acc)[4][2][4]) {
+__device__ __forceinline__ void score_block(uint32_t x, uint32_t k, int i, int j, int lane, float (&acc)[2][4]) {
 #pragma unroll
-    for (int jb = 0; jb < 4; ++jb)
+    for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+        for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
+    const uint32_t ar = 16 * i + (lane & 15), ac = lane >> 4;
+    const uint32_t br = 16 * j + (lane & 7) + ((lane >> 4) << 3), bc = (lane >> 3) & 1;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[jb][nt][e] = 0.f;
-    const uint32_t ar = row0 + (lane & 15), ac = lane >> 4;
-    const uint32_t br = (lane & 7) + ((lane >> 4) << 3), bc = (lane >> 3) & 1;
+    for (int box = 0; box < S / 64; ++box) {
+        uint32_t a[4][4], b[4][4];
 #pragma unroll
-    for (int ks = 0; ks < S / 16; ++ks) {
-        const uint32_t box = (ks >> 2) * kBox, ch = (ks & 3) * 2;
-        uint32_t a[4];
-        ldsm4(x + box + sw(ar, ch + ac), a);
+        for (int ks = 0; ks < 4; ++ks) {
+            ldsm4(x + box * kBox + sw(ar, 2 * ks + ac), a[ks]);
+            ldsm4(k + box * kBox + sw(br, 2 * ks + bc), b[ks]);
+        }
 #pragma unroll
-        for (int jb = 0; jb < 4; ++jb) {
-            if (jb > jmax) break;
-            if (jb < jmin) continue;
-            uint32_t b[4];
-            ldsm4(k + box + sw(16 * jb + br, ch + bc), b);
-            mma16(acc[jb][0], a, b[0], b[1]);
-            mma16(acc[jb][1], a, b[2], b[3]);
+        for (int ks = 0; ks < 4; ++ks) {
+            mma16(acc[0], a[ks], b[ks][0], b[ks][1]);
+            mma16(acc[1], a[ks], b[ks][2], b[ks][3]);
         }
     }
 }
 
-// 1 / sqrt(x + eps) of the diagonal of block jb, handed to put(row, value).
+// 1 / sqrt(x + eps) of a block's diagonal, handed to put(row, value).
 template <class Put>
-__device__ __forceinline__ void diag_norm(const float (&acc)[4][2][4], int jb, int lane, float eps, Put put) {
+__device__ __forceinline__ void diag_norm(const float (&acc)[2][4], int lane, float eps, Put put) {
     const int gid = lane >> 2, tig = lane & 3;
     if (gid >> 1 != tig) return;  // rows gid, gid + 8 meet their columns 2 tig, 2 tig + 1 here
-    float d0 = 0.f, d1 = 0.f;
-#pragma unroll
-    for (int b = 0; b < 4; ++b)
-        if (b == jb) {
-            d0 = gid & 1 ? acc[b][0][1] : acc[b][0][0];
-            d1 = gid & 1 ? acc[b][1][3] : acc[b][1][2];
-        }
-    put(gid, __frsqrt_rn(d0 + eps));
-    put(gid + 8, __frsqrt_rn(d1 + eps));
+    put(gid, __frsqrt_rn((gid & 1 ? acc[0][1] : acc[0][0]) + eps));
+    put(gid + 8, __frsqrt_rn((gid & 1 ? acc[1][3] : acc[1][2]) + eps));
 }
 
 template <int S, int H, int NV>
-__global__ void __launch_bounds__((kScoreWarp0 + 4 * NV + 2) * 32, 1)
+__global__ void __launch_bounds__(threads_of(NV), 1)
 k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-               const __grid_constant__ CUtensorMap tm_v, const GdrTcParams p) {
-    constexpr int kScoreWarps = 4 * NV, kTmaWarp = kScoreWarp0 + kScoreWarps, kMmaWarp = kTmaWarp + 1;
+               const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_y,
+               const GdrTcParams p) {
+    constexpr int kNWarps = 4 * NV, kPWarp0 = kNWarp0 + kNWarps, kTmaWarp = kPWarp0 + kPWarps, kMmaWarp = kTmaWarp + 1;
     constexpr int kBoxes = S / 64, kVBoxes = NV * H / 64;
     constexpr uint32_t kOffQ = kBoxes * kBox, kOffV = 2 * kOffQ, kStage = kOffV + kVBoxes * kBox;
     static_assert((S == 64 || S == 128) && (NV == 1 ? (H == 64 || H == 128) : H == 64), "shapes");
@@ -311,8 +362,9 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     // the other one's rows.
     constexpr uint32_t cU = S == 128 ? cHi : 2 * S + 256;
 
+    // (aligned by an offset, so that the compiler still knows it for shared memory)
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* smem = smem_raw + (-tc::smem_u32(smem_raw) & 1023u);
     const Geom& g = p.g;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int h0 = NV * blockIdx.x;
@@ -336,17 +388,18 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             tc::mbar_init(&bars[kBarFree + i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&bars[kBarSFull + i], kScoreWarps);
-            tc::mbar_init(&bars[kBarSFree + i], 1 + kOutWarps);
+            tc::mbar_init(&bars[kBarSFull + i], kNWarps);
+            tc::mbar_init(&bars[kBarSFree + i], 1 + kOutWarps + kPWarps);
         }
-        tc::mbar_init(&bars[kBarNFull], kScoreWarps);
-        tc::mbar_init(&bars[kBarPFull], kScoreWarps);
+        tc::mbar_init(&bars[kBarNFull], kNWarps);
+        tc::mbar_init(&bars[kBarPFull], kPWarps);
         tc::mbar_init(&bars[kBarPFree], 1);
         tc::mbar_init(&bars[kBarHReady], kChainWarps);
         tc::mbar_init(&bars[kBarRDone], 1);
         tc::mbar_init(&bars[kBarXReady], kChainWarps);
         tc::mbar_init(&bars[kBarWDone], 1);
         tc::mbar_init(&bars[kBarWReady], kChainWarps);
+        tc::mbar_init(&bars[kBarWyReady], kChainWarps);
         tc::mbar_init(&bars[kBarHDone], 1);
         tc::mbar_init(&bars[kBarO1Done], 1);
         tc::mbar_init(&bars[kBarO1Read], kOutWarps);
@@ -370,6 +423,7 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     bool ok = true;
 
     if (warp < kChainWarps) {
+        more_registers<NV == 2 ? 80 : 88>();
         // ============================== chain ==============================
         const int q = warp & 3, hf = warp >> 2;
         const int hv = NV == 2 ? q >> 1 : 0;
@@ -406,39 +460,66 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             const float g_last = sc->g_last;
             if (c > 0 && !warp_wait(&bars[kBarHDone], ph ^ 1, abort_flag)) { ok = false; break; }
             tc::tc_fence_after();
-            // h: its parts, and itself decayed to the chunk's end
+            // h's parts
 #pragma unroll 1
             for (int s = hf * (S / 2); s < (hf + 1) * (S / 2); s += 32) {
                 uint32_t r[2][16], hi[16], lo[16];
                 ld32(tl + cH + s, r[0], r[1]);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    uint32_t* x = &r[j >> 3][(2 * j) & 15];
-                    const float a0 = __uint_as_float(x[0]), a1 = __uint_as_float(x[1]);
-                    split2(a0, a1, hi[j], lo[j]);
-                    x[0] = __float_as_uint(g_last * a0);
-                    x[1] = __float_as_uint(g_last * a1);
+                    split2(as_f2(&r[j >> 3][(2 * j) & 15]), hi[j], lo[j]);
                 }
                 tc::tmem_st16(tl + cHi + s / 2, hi);
                 tc::tmem_st16(tl + cLo + s / 2, lo);
-                tc::tmem_st16(tl + cH + s, r[0]);
-                tc::tmem_st16(tl + cH + s + 16, r[1]);
             }
             tc::tmem_wait_st();
             tc::tc_fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bars[kBarHReady]);
-
-            // R = K h -> X (the stage's V has landed: the scores waited for the same copy)
+            // while R = K h runs: h decayed to the chunk's end, and V from the stage (it has landed: the
+            // scores waited for the same copy)
+#pragma unroll 1
+            for (int s = hf * (S / 2); s < (hf + 1) * (S / 2); s += 32) {
+                uint32_t r[2][16];
+                ld32(tl + cH + s, r[0], r[1]);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    uint32_t* x = &r[j >> 3][(2 * j) & 15];
+                    const float2 v = tc::mul_f32x2(as_f2(x), make_float2(g_last, g_last));
+                    x[0] = __float_as_uint(v.x);
+                    x[1] = __float_as_uint(v.y);
+                }
+                tc::tmem_st16(tl + cH + s, r[0]);
+                tc::tmem_st16(tl + cH + s + 16, r[1]);
+            }
             if (!warp_wait(&bars[kBarFull + st], full_phase, abort_flag)) { ok = false; break; }
-            if (!warp_wait(&bars[kBarRDone], ph, abort_flag)) { ok = false; break; }
-            tc::tc_fence_after();
             const int i0 = 32 * hf;  // this warp's tokens: i0 .. i0 + 31
-            const int64_t left = n - (int64_t)c * kT;
-            const int nv = left < kT ? (int)left : kT;
-            const uint8_t* sv = smem + st * kStage + v_off;
+            uint32_t v2[16];         // their V, two to a register
+            {
+                const int64_t left = n - (int64_t)c * kT;
+                const int nv = left < kT ? (int)left : kT;
+                const uint8_t* sv = smem + st * kStage + v_off;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int k = i0 + 2 * j;
+                    const uint32_t a0 = *reinterpret_cast<const uint16_t*>(sv + k * 128 + ((vch ^ (2 * j & 7)) << 4));
+                    const uint32_t a1 =
+                        *reinterpret_cast<const uint16_t*>(sv + k * 128 + 128 + ((vch ^ ((2 * j + 1) & 7)) << 4));
+                    v2[j] = a0 | (a1 << 16);
+                }
+                if (nv < kT || !live) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const int k = i0 + 2 * j;
+                        v2[j] = !live || k >= nv ? 0u : (k + 1 >= nv ? v2[j] & 0xffffu : v2[j]);
+                    }
+                }
+            }
+            if (!warp_wait(&bars[kBarRDone], ph, abort_flag)) { ok = false; break; }
             // (Q h, which follows R, also reads what X may overwrite)
             if (NV == 2 && S == 128 && !warp_wait(&bars[kBarO1Done], ph, abort_flag)) { ok = false; break; }
+            tc::tc_fence_after();
+            // X
             {
                 const uint32_t mine = hv ? cU : cX;
 #pragma unroll
@@ -447,18 +528,18 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     uint32_t r[16], x0[8], x1[8], x2[8];
                     tc::tmem_ld16(tl + cR + i1, r);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float x[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int k = 2 * j + e;
-                            const float4 t = *reinterpret_cast<const float4*>(&sc->chain[i1 + k]);
-                            float v = __bfloat162float(
-                                *reinterpret_cast<const __nv_bfloat16*>(sv + (i1 + k) * 128 + ((vch ^ (k & 7)) << 4)));
-                            v = (live && i1 + k < nv) ? v : 0.f;
-                            x[e] = fmaf(-t.y, __uint_as_float(r[k]), t.x * v);
-                        }
-                        split3(x[0], x[1], x0[j], x1[j], x2[j]);
+                    for (int j = 0; j < 16; j += 4) {
+                        const float4 cb = *reinterpret_cast<const float4*>(&sc->cb[i1 + j]);
+                        const float4 cr = *reinterpret_cast<const float4*>(&sc->cr[i1 + j]);
+                        const uint32_t va = v2[8 * m + j / 2], vb = v2[8 * m + j / 2 + 1];
+                        const float2 bv0 = tc::mul_f32x2(make_float2(cb.x, cb.y),
+                                                         make_float2(tc::bf16_lo(va), tc::bf16_hi(va)));
+                        const float2 bv1 = tc::mul_f32x2(make_float2(cb.z, cb.w),
+                                                         make_float2(tc::bf16_lo(vb), tc::bf16_hi(vb)));
+                        split3(tc::fma_f32x2(make_float2(cr.x, cr.y), as_f2(&r[j]), bv0), x0[j / 2], x1[j / 2],
+                               x2[j / 2]);
+                        split3(tc::fma_f32x2(make_float2(cr.z, cr.w), as_f2(&r[j + 2]), bv1), x0[j / 2 + 1],
+                               x1[j / 2 + 1], x2[j / 2 + 1]);
                     }
                     tc::tmem_st8(tl + mine + i1 / 2, x0);
                     tc::tmem_st8(tl + mine + 32 + i1 / 2, x1);
@@ -480,28 +561,40 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bars[kBarXReady]);
 
-            // W = N X: its parts for y, and decayed to the chunk's end for the state
+            // W = N X, decayed to the chunk's end for the state, then as it is for y
             if (!warp_wait(&bars[kBarWDone], ph, abort_flag)) { ok = false; break; }
             tc::tc_fence_after();
+            uint32_t r[2][16];
+            ld32(tl + cR + i0, r[0], r[1]);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                uint32_t u0[8], u1[8], u2[8];
+                const int i1 = i0 + 16 * m;
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 d = *reinterpret_cast<const float4*>(&sc->d[i1 + j]);
+                    const uint32_t* x = &r[m][j];
+                    split3(tc::mul_f32x2(make_float2(d.x, d.y), as_f2(x)), u0[j / 2], u1[j / 2], u2[j / 2]);
+                    split3(tc::mul_f32x2(make_float2(d.z, d.w), as_f2(x + 2)), u0[j / 2 + 1], u1[j / 2 + 1],
+                           u2[j / 2 + 1]);
+                }
+                tc::tmem_st8(tl + cU + i1 / 2, u0);
+                tc::tmem_st8(tl + cU + 32 + i1 / 2, u1);
+                tc::tmem_st8(tl + cU + 64 + i1 / 2, u2);
+            }
+            tc::tmem_wait_st();
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bars[kBarWReady]);
             {
                 const uint32_t mine = hv ? cW2 : cX;
+                uint32_t w0[16], w1[16];
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    uint32_t r[16], w0[8], w1[8], u0[8], u1[8], u2[8];
-                    const int i1 = i0 + 16 * m;
-                    tc::tmem_ld16(tl + cR + i1, r);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float a0 = __uint_as_float(r[2 * j]), a1 = __uint_as_float(r[2 * j + 1]);
-                        split2(a0, a1, w0[j], w1[j]);
-                        split3(sc->chain[i1 + 2 * j].d * a0, sc->chain[i1 + 2 * j + 1].d * a1, u0[j], u1[j], u2[j]);
-                    }
-                    tc::tmem_st8(tl + cU + i1 / 2, u0);
-                    tc::tmem_st8(tl + cU + 32 + i1 / 2, u1);
-                    tc::tmem_st8(tl + cU + 64 + i1 / 2, u2);
-                    tc::tmem_st8(tl + mine + i1 / 2, w0);
-                    tc::tmem_st8(tl + mine + 32 + i1 / 2, w1);
+                for (int j = 0; j < 16; ++j) {
+                    split2(as_f2(&r[j >> 3][(2 * j) & 15]), w0[j], w1[j]);
                 }
+                tc::tmem_st16(tl + mine + i0 / 2, w0);
+                tc::tmem_st16(tl + mine + 32 + i0 / 2, w1);
                 if (NV == 2 && hv == 0) {  // the second head's W: the columns that held X
                     uint32_t z[16] = {};
                     tc::tmem_st16(tl + cW2 + i0 / 2, z);
@@ -510,7 +603,7 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             tc::tmem_wait_st();
             tc::tc_fence_before();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&bars[kBarWReady]);
+            if (lane == 0) tc::mbar_arrive(&bars[kBarWyReady]);
             if (++st == p.nst) {
                 st = 0;
                 full_phase ^= 1u;
@@ -531,80 +624,107 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         }
         if (!ok) set_abort(ctl, p.status);
     } else if (warp < kOutWarp0 + kOutWarps) {
+        fewer_registers<NV == 2 ? 64 : 72>();
         // ============================== output ==============================
         const int q = warp & 3;
         const int hv = NV == 2 ? q >> 1 : 0;
         const int colh = 32 * (NV == 2 ? (q & 1) : q) + lane;
         const bool live = colh < H;
         const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16);
-        const int64_t row = (int64_t)g.nheads * H;
-        const int odd = lane & 1;
-        // lanes meet in pairs: the even one stores both columns of token i, the odd one of i + 1
-        __nv_bfloat16* y = p.y + (b * L + odd) * row + (int64_t)(h0 + hv) * H + (colh & ~1);
+        const bool storer = threadIdx.x == kOutWarp0 * 32;
+        // this thread's column of the staged y
+        const uint32_t ych = (32 * (q & 1) + lane) >> 3;
+        uint8_t* sy = smem + p.off_y + (q >> 1) * kBox + (lane & 7) * 2;
         for (int c = 0; c < nc; ++c) {
             const int buf = c & 1;
             const uint32_t ph = c & 1;
             const Scalars* sc = scal_of(buf, hv);
-            if (!warp_wait(&bars[kBarSFull + buf], (c >> 1) & 1, abort_flag)) { ok = false; break; }
-            if (!warp_wait(&bars[kBarO1Done], ph, abort_flag)) { ok = false; break; }
-            tc::tc_fence_after();
-            uint32_t o1[4][16];
+            // Q h -> e^G Q h, onto which P W is summed
+            ok = warp_wait(&bars[kBarO1Done], ph, abort_flag);
+            if (ok) {
+                tc::tc_fence_after();
 #pragma unroll
-            for (int m = 0; m < 4; ++m) tc::tmem_ld16_nowait(tl + cO + 16 * m, o1[m]);
-            tc::tmem_wait_ld16(o1[0]);
-            tc::tmem_tie16(o1[1]);
-            tc::tmem_tie16(o1[2]);
-            tc::tmem_tie16(o1[3]);
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&bars[kBarO1Read]);
-            if (!warp_wait(&bars[kBarO2Done], ph, abort_flag)) { ok = false; break; }
+                for (int m = 0; m < 4; ++m) {
+                    uint32_t r[16];
+                    tc::tmem_ld16(tl + cO + 16 * m, r);
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(&sc->gam[16 * m + j]);
+                        const float2 a0 = tc::mul_f32x2(make_float2(f.x, f.y), as_f2(&r[j]));
+                        const float2 a1 = tc::mul_f32x2(make_float2(f.z, f.w), as_f2(&r[j + 2]));
+                        r[j] = __float_as_uint(a0.x), r[j + 1] = __float_as_uint(a0.y);
+                        r[j + 2] = __float_as_uint(a1.x), r[j + 3] = __float_as_uint(a1.y);
+                    }
+                    tc::tmem_st16(tl + cO + 16 * m, r);
+                }
+                tc::tmem_wait_st();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bars[kBarO1Read]);
+                ok = warp_wait(&bars[kBarPFull], ph, abort_flag) && warp_wait(&bars[kBarO2Done], ph, abort_flag);
+            }
+            if (storer) tc::bulk_wait_read_all();  // the last chunk's y has left its place
+            ok = bar_sync_and(3, 32 * kOutWarps, ok);
+            if (!ok) break;
             tc::tc_fence_after();
-            const int64_t t0 = (int64_t)c * kT;
-            const int64_t nleft = n - t0, lleft = L - t0;
-            const int nv = nleft < kT ? (int)nleft : kT, lv = lleft < kT ? (int)lleft : kT;
-            __nv_bfloat16* yc = y + t0 * row;
+            const int64_t left = n - (int64_t)c * kT;
+            const int nv = left < kT ? (int)left : kT;
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                uint32_t o2[16];
-                tc::tmem_ld16(tl + cO + 16 * m, o2);
+                uint32_t r[16];
+                tc::tmem_ld16(tl + cO + 16 * m, r);
                 if (m == 3) {
                     tc::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&bars[kBarO2Read]);
                 }
 #pragma unroll
-                for (int j = 0; j < 16; j += 2) {
+                for (int j = 0; j < 16; j += 4) {
                     const int i = 16 * m + j;
-                    const float2 f0 = sc->out[i], f1 = sc->out[i + 1];
-                    float a0 = fmaf(f0.x, __uint_as_float(o1[m][j]), f0.y * __uint_as_float(o2[j]));
-                    float a1 = fmaf(f1.x, __uint_as_float(o1[m][j + 1]), f1.y * __uint_as_float(o2[j + 1]));
-                    a0 = i < nv ? a0 : 0.f;
-                    a1 = i + 1 < nv ? a1 : 0.f;
-                    const float got = __shfl_xor_sync(0xffffffffu, odd ? a0 : a1, 1);
-                    const uint32_t pair = odd ? tc::pack_bf16x2(got, a1) : tc::pack_bf16x2(a0, got);
-                    if (live && i + odd < lv) *reinterpret_cast<uint32_t*>(yc + i * row) = pair;
+                    const float4 f = *reinterpret_cast<const float4*>(&sc->oq[i]);
+                    const float2 a0 = tc::mul_f32x2(make_float2(f.x, f.y), as_f2(&r[j]));
+                    const float2 a1 = tc::mul_f32x2(make_float2(f.z, f.w), as_f2(&r[j + 2]));
+                    uint32_t y2[2] = {tc::pack_bf16x2(a0.x, a0.y), tc::pack_bf16x2(a1.x, a1.y)};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t v = e & 1 ? y2[e >> 1] >> 16 : y2[e >> 1] & 0xffffu;
+                        if (live)
+                            *reinterpret_cast<uint16_t*>(sy + (i + e) * 128 + ((ych ^ ((i + e) & 7)) << 4)) =
+                                (uint16_t)(nv == kT || i + e < nv ? v : 0u);
+                    }
                 }
             }
-            __syncwarp();
+            tc::fence_proxy_async_smem();
+            bar_sync(3, 32 * kOutWarps);
+            if (storer) {  // rows past L are clipped
+#pragma unroll
+                for (int x = 0; x < kVBoxes; ++x)
+                    tc::tma_store_4d(&tm_y, smem + p.off_y + x * kBox, NV == 2 ? 0 : 64 * x, NV == 2 ? h0 + x : h0,
+                                     c * kT, (int)b);
+                tc::bulk_commit();
+            }
             if (lane == 0) tc::mbar_arrive(&bars[kBarSFree + buf]);
         }
+        if (storer) tc::bulk_wait_all();
         if (!ok) set_abort(ctl, p.status);
-        if (ok && live)
-            for (int64_t t = (int64_t)nc * kT; t + odd < L; t += 2) *reinterpret_cast<uint32_t*>(y + t * row) = 0u;
-    } else if (warp < kScoreWarp0 + kScoreWarps) {
-        // ============================== scores ==============================
-        const int hv = (warp - kScoreWarp0) >> 2, w = (warp - kScoreWarp0) & 3;  // head, block of 16 rows
+        if (ok && live) {
+            __nv_bfloat16* y = p.y + (b * L * g.nheads + h0 + hv) * (int64_t)H + colh;
+            for (int64_t t = (int64_t)nc * kT; t < L; ++t) y[t * g.nheads * H] = __float2bfloat16_rn(0.f);
+        }
+    } else if (warp < kPWarp0) {
+        more_registers<NV == 2 ? 88 : 120>();
+        // ======================= G, k's norms, A and N =======================
+        const int hv = (warp - kNWarp0) >> 2, w = (warp - kNWarp0) & 3;
         const int tid = w * 32 + lane;
         const int gid = lane >> 2, tig = lane & 3;
-        ScoreScratch* scr = reinterpret_cast<ScoreScratch*>(smem + p.off_scratch) + hv;
+        NScratch* scr = reinterpret_cast<NScratch*>(smem + p.off_scratch) + hv;
         const int64_t gbase = b * L * g.nheads + h0 + hv;
-        // warp 0's lanes hold the next chunk's g and beta of tokens lane, lane + 32
+        // warp 0's lanes hold the next chunk's g and beta of tokens 2 lane, 2 lane + 1
         float gn[2], bn[2];
         auto fetch = [&](int c) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const int64_t t = (int64_t)c * kT + lane + 32 * r;
+                const int64_t t = (int64_t)c * kT + 2 * lane + r;
                 gn[r] = t < n ? p.gate[gbase + t * g.nheads] : 0.f;
                 bn[r] = t < n ? p.beta[gbase + t * g.nheads] : 0.f;
             }
@@ -614,43 +734,45 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         uint32_t full_phase = 0;
         for (int c = 0; c < nc; ++c) {
             const int buf = c & 1;
-            if (w == 0) {
-                long long f[2];
+            Scalars* sc = scal_of(buf, hv);
+            // every warp of the head comes to the barrier below, whatever its waits said
+            if (c >= 2) ok = warp_wait(&bars[kBarSFree + buf], ((c >> 1) - 1) & 1, abort_flag);
+            if (w == 0 && ok) {
+                // log2 decays as an integer and a fraction in units of 2^-24, summed apart
+                int gi[2], gf[2];
                 float be[2];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
+                    constexpr float kL = 1.44269502162933349609375f, kLrest = 1.925963033500011e-8f;  // log2 e
                     const float lim = fminf(fmaxf(gn[r], -112.f), 112.f);  // |log2 decay| < 162
-                    f[r] = __double2ll_rn((double)lim * 1.4426950408889634 * 4294967296.0);
+                    const float x = lim * kL, rest = fmaf(lim, kL, -x) + lim * kLrest, whole = floorf(x);
+                    gi[r] = (int)whole;
+                    gf[r] = __float2int_rn(((x - whole) + rest) * 16777216.f);
                     be[r] = gn[r] != gn[r] ? gn[r] : bn[r];  // a NaN decay shows in the token's correction
                 }
+                int si = gi[0] + gi[1], sf = gf[0] + gf[1];
 #pragma unroll
                 for (int m = 1; m < 32; m <<= 1) {
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const long long o = __shfl_up_sync(0xffffffffu, f[r], m);
-                        if (lane >= m) f[r] += o;
-                    }
+                    const int oi = __shfl_up_sync(0xffffffffu, si, m), of = __shfl_up_sync(0xffffffffu, sf, m);
+                    if (lane >= m) si += oi, sf += of;
                 }
-                f[1] += __shfl_sync(0xffffffffu, f[0], 31);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    TokScore* t = &scr->tok[lane + 32 * r];
-                    t->gi = (float)(int)(f[r] >> 32);
-                    t->gf = (float)(uint32_t)f[r] * 2.3283064365386963e-10f;
-                    t->beta = be[r];
+                    const int ti = r ? si : si - gi[1], tf = r ? sf : sf - gf[1];
+                    sc->tok[2 * lane + r].gi = (float)(ti + (tf >> 24));
+                    sc->tok[2 * lane + r].gf = (float)(tf & 0xffffff) * 5.9604644775390625e-8f;
+                    sc->tok[2 * lane + r].beta = be[r];
                 }
                 if (c + 1 < nc) fetch(c + 1);
             }
-            // every warp of the head comes to the barrier below, whatever its waits said
-            ok = warp_wait(&bars[kBarFull + st], full_phase, abort_flag);
-            if (ok && c >= 2) ok = warp_wait(&bars[kBarSFree + buf], ((c >> 1) - 1) & 1, abort_flag);
+            if (ok) ok = warp_wait(&bars[kBarFull + st], full_phase, abort_flag);
             uint8_t* sK = smem + st * kStage;
-            const uint32_t aK = tc::smem_u32(sK), aQ = aK + kOffQ;
+            const uint32_t aK = tc::smem_u32(sK);
             const int64_t left = n - (int64_t)c * kT;
             const int nv = left < kT ? (int)left : kT;
-            // K K^T; the norms are its diagonal and Q Q^T's (summed by the same instructions, so that
-            // rk_i rk_j (k_i . k_j) is 1 to rounding where keys agree)
-            float acc[4][2][4];
+            // the diagonal block of K K^T, whose diagonal gives the norms: summed by the same
+            // instructions as the rest, so that rk_i rk_j (k_i . k_j) is 1 to rounding where keys agree
+            float acc[2][4];
             if (ok) {
                 if (nv < kT) {
                     // past the row's end: K enters the state's product and has to be 0
@@ -664,60 +786,52 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     }
                     __syncwarp();
                 }
-                if (p.l2norm) {
-                    score_rows<S>(aQ, aQ, 16 * w, w, w, lane, acc);
-                    diag_norm(acc, w, lane, p.l2_eps, [&](int i, float f) { scr->rq[16 * w + i] = f; });
-                }
-                score_rows<S>(aK, aK, 16 * w, 0, w, lane, acc);
-                if (p.l2norm) {
-                    diag_norm(acc, w, lane, p.l2_eps, [&](int i, float f) { scr->tok[16 * w + i].rk = f; });
-                } else if (lane < 16) {
-                    scr->tok[16 * w + lane].rk = 1.f;
-                    scr->rq[16 * w + lane] = 1.f;
-                }
+                score_block<S>(aK, aK, w, w, lane, acc);
+                if (p.l2norm)
+                    diag_norm(acc, lane, p.l2_eps, [&](int i, float f) { sc->tok[16 * w + i].rk = f; });
+                else if (lane < 16)
+                    sc->tok[16 * w + lane].rk = 1.f;
             }
             ok = bar_sync_and(1 + hv, 128, ok);
             if (!ok) break;
             if (tid < kT) {
-                const TokScore t = scr->tok[tid], last = scr->tok[kT - 1];
-                Scalars* sc = scal_of(buf, hv);
-                const float e = exp2f(t.gi) * exp2f(t.gf);
-                const float d = exp2f(last.gi - t.gi) * exp2f(last.gf - t.gf);
-                const float oq = p.scale * scr->rq[tid];
-                *reinterpret_cast<float4*>(&sc->chain[tid]) = make_float4(t.beta, t.beta * e * t.rk, d * t.rk, 0.f);
-                sc->out[tid] = make_float2(oq * e, oq);
+                const Tok t = sc->tok[tid], last = sc->tok[kT - 1];
+                const float e = ex2(t.gi) * ex2(t.gf);
+                sc->cb[tid] = t.beta;
+                sc->cr[tid] = -t.beta * e * t.rk;
+                sc->gam[tid] = e;
+                sc->d[tid] = ex2(last.gi - t.gi) * ex2(last.gf - t.gf) * t.rk;
                 if (tid == kT - 1) sc->g_last = e;
             }
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bars[kBarSFull + buf]);
-            const TokScore ti0 = scr->tok[16 * w + gid], ti1 = scr->tok[16 * w + gid + 8];
-            // A, in fp32: blocks below the diagonal, and the diagonal block by columns
-            {
+            // A's blocks in fp32: this warp's diagonal block (by columns), then one or two below
+#pragma unroll 1
+            for (int t = w; t < 10; t += 4) {
+                const int i = tri_i(t), j = tri_j(t);
+                if (t >= 4) score_block<S>(aK, aK, i, j, lane, acc);
+                const Tok ti0 = sc->tok[16 * i + gid], ti1 = sc->tok[16 * i + gid + 8];
                 const float f0 = ti0.beta * ti0.rk, f1 = ti1.beta * ti1.rk;
-                const bool in0 = 16 * w + gid < nv, in1 = 16 * w + gid + 8 < nv;
+                const bool in0 = 16 * i + gid < nv, in1 = 16 * i + gid + 8 < nv;
 #pragma unroll
-                for (int jb = 0; jb < 4; ++jb) {
-                    if (jb > w) break;
-#pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        const int jj = 8 * nt + 2 * tig, j = 16 * jb + jj;
-                        const TokScore t0 = scr->tok[j], t1 = scr->tok[j + 1];
-                        float (&a)[4] = acc[jb][nt];
-                        a[0] = in0 ? a[0] * (f0 * t0.rk * exp2f((ti0.gi - t0.gi) + (ti0.gf - t0.gf))) : 0.f;
-                        a[1] = in0 ? a[1] * (f0 * t1.rk * exp2f((ti0.gi - t1.gi) + (ti0.gf - t1.gf))) : 0.f;
-                        a[2] = in1 ? a[2] * (f1 * t0.rk * exp2f((ti1.gi - t0.gi) + (ti1.gf - t0.gf))) : 0.f;
-                        a[3] = in1 ? a[3] * (f1 * t1.rk * exp2f((ti1.gi - t1.gi) + (ti1.gf - t1.gf))) : 0.f;
-                        if (jb < w) {
-                            float2 (*low)[8] = scr->low[low_block(w, jb)];
-                            low[gid][low_at(gid, jj / 2)] = make_float2(a[0], a[1]);
-                            low[gid + 8][low_at(gid + 8, jj / 2)] = make_float2(a[2], a[3]);
-                        } else {
-                            scr->diag[w][jj][gid] = jj < gid ? a[0] : 0.f;
-                            scr->diag[w][jj + 1][gid] = jj + 1 < gid ? a[1] : 0.f;
-                            scr->diag[w][jj][gid + 8] = jj < gid + 8 ? a[2] : 0.f;
-                            scr->diag[w][jj + 1][gid + 8] = jj + 1 < gid + 8 ? a[3] : 0.f;
-                        }
+                for (int nt = 0; nt < 2; ++nt) {
+                    const int jj = 8 * nt + 2 * tig;
+                    const Tok t0 = sc->tok[16 * j + jj], t1 = sc->tok[16 * j + jj + 1];
+                    float (&a)[4] = acc[nt];
+                    a[0] = in0 ? a[0] * (f0 * t0.rk * decay(ti0, t0)) : 0.f;
+                    a[1] = in0 ? a[1] * (f0 * t1.rk * decay(ti0, t1)) : 0.f;
+                    a[2] = in1 ? a[2] * (f1 * t0.rk * decay(ti1, t0)) : 0.f;
+                    a[3] = in1 ? a[3] * (f1 * t1.rk * decay(ti1, t1)) : 0.f;
+                    if (t >= 4) {
+                        float2 (*low)[8] = scr->low[low_block(i, j)];
+                        low[gid][low_at(gid, jj / 2)] = make_float2(a[0], a[1]);
+                        low[gid + 8][low_at(gid + 8, jj / 2)] = make_float2(a[2], a[3]);
+                    } else {
+                        scr->diag[w][jj][gid] = jj < gid ? a[0] : 0.f;
+                        scr->diag[w][jj + 1][gid] = jj + 1 < gid ? a[1] : 0.f;
+                        scr->diag[w][jj][gid + 8] = jj < gid + 8 ? a[2] : 0.f;
+                        scr->diag[w][jj + 1][gid + 8] = jj + 1 < gid + 8 ? a[3] : 0.f;
                     }
                 }
             }
@@ -747,7 +861,7 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
             bar_sync(1 + hv, 128);
             // N's block column w, transposed: N_ij^T = -(sum_m N_mj^T A_im^T) N_ii^T, as accumulator
-            // fragments nf[d] (i = w + d), which are also left operands (see mma_tf32x3)
+            // fragments nf[d] (i = w + d), which are also left operands
             {
                 float nf[4][2][4];
 #pragma unroll
@@ -766,22 +880,15 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
                     for (int m = 0; m < d; ++m) {
                         const float2 (*low)[8] = scr->low[low_block(i, w + m)];
-#pragma unroll
-                        for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                            for (int nt = 0; nt < 2; ++nt)
-                                mma_tf32x3(x[nt], nf[m][kk], low[8 * nt + gid][low_at(gid, 4 * kk + tig)]);
+                        mma_block(x, nf[m], gid, tig, [&](int r, int c2) { return low[r][low_at(r, c2)]; });
                     }
 #pragma unroll
                     for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) x[nt][e] = -x[nt][e], nf[d][nt][e] = 0.f;
-#pragma unroll
-                    for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                        for (int nt = 0; nt < 2; ++nt)
-                            mma_tf32x3(nf[d][nt], x[kk],
-                                       *reinterpret_cast<const float2*>(&scr->diag[i][8 * nt + gid][8 * kk + 2 * tig]));
+                    mma_block(nf[d], x, gid, tig, [&](int r, int c2) {
+                        return *reinterpret_cast<const float2*>(&scr->diag[i][r][2 * c2]);
+                    });
                 }
                 // the last chunk's N has been used
                 if (c > 0) ok = warp_wait(&bars[kBarWDone], (c - 1) & 1, abort_flag);
@@ -797,9 +904,10 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
                             float* v = &nf[d][x >> 1][2 * (x & 1)];
-                            r[x] = tc::pack_bf16x2(v[0], v[1]);
-                            v[0] -= tc::bf16_lo(r[x]);
-                            v[1] -= tc::bf16_hi(r[x]);
+                            float2 f = make_float2(v[0], v[1]);
+                            r[x] = high(f);
+                            v[0] = f.x;
+                            v[1] = f.y;
                         }
                         stsm4_trans(at + pl * kPlane, r);
                     }
@@ -808,177 +916,221 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (ok && lane == 0) tc::mbar_arrive(&bars[kBarNFull]);
-            // P, once the last chunk's has been used
-            {
-                score_rows<S>(aQ, aK, 16 * w, 0, w, lane, acc);
-                if (ok && c > 0) ok = warp_wait(&bars[kBarPFree], (c - 1) & 1, abort_flag);
-                uint8_t* sP = p_of(hv);
-#pragma unroll
-                for (int jb = 0; jb < 4; ++jb) {
-                    if (jb > w || !ok) break;
-#pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        const int j = 16 * jb + 8 * nt + 2 * tig, i0 = 16 * w + gid;
-                        const TokScore t0 = scr->tok[j], t1 = scr->tok[j + 1];
-                        const float (&a)[4] = acc[jb][nt];
-                        const float e0 = t0.rk * exp2f((ti0.gi - t0.gi) + (ti0.gf - t0.gf));
-                        const float e1 = t1.rk * exp2f((ti0.gi - t1.gi) + (ti0.gf - t1.gf));
-                        const float e2 = t0.rk * exp2f((ti1.gi - t0.gi) + (ti1.gf - t0.gf));
-                        const float e3 = t1.rk * exp2f((ti1.gi - t1.gi) + (ti1.gf - t1.gf));
-                        const uint32_t o0 = sw(i0, 2 * jb + nt) + 4 * tig;
-                        uint32_t hi, lo;
-                        split2(j <= i0 ? a[0] * e0 : 0.f, j + 1 <= i0 ? a[1] * e1 : 0.f, hi, lo);
-                        *reinterpret_cast<uint32_t*>(sP + o0) = hi;
-                        *reinterpret_cast<uint32_t*>(sP + kPlane + o0) = lo;
-                        split2(j <= i0 + 8 ? a[2] * e2 : 0.f, j + 1 <= i0 + 8 ? a[3] * e3 : 0.f, hi, lo);
-                        *reinterpret_cast<uint32_t*>(sP + o0 + 1024) = hi;
-                        *reinterpret_cast<uint32_t*>(sP + kPlane + o0 + 1024) = lo;
-                    }
-                }
-            }
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (ok && lane == 0) tc::mbar_arrive(&bars[kBarPFull]);
-            ok = bar_sync_and(1 + hv, 128, ok);  // the tokens' scalars have been read
-            if (!ok) break;
             if (++st == p.nst) {
                 st = 0;
                 full_phase ^= 1u;
             }
         }
         if (!ok) set_abort(ctl, p.status);
-    } else if (warp == kTmaWarp) {
-        // ============================ TMA producer ============================
-        if (lane == 0) {
-            tc::tma_prefetch_desc(&tm_q);
-            tc::tma_prefetch_desc(&tm_k);
-            tc::tma_prefetch_desc(&tm_v);
-            int fills[kMaxStages] = {};
-            int st = 0;
-            uint32_t free_phase = 1;
-            for (int c = 0; c < nc; ++c) {
-                if (c >= p.nst && !tc::mbar_wait(&bars[kBarFree + st], free_phase, abort_flag)) { ok = false; break; }
-                uint8_t* s = smem + st * kStage;
-                uint64_t* full = &bars[kBarFull + st];
-                tc::mbar_arrive_expect_tx(full, kStage);
+    } else if (warp < kPWarp0 + kPWarps) {
+        fewer_registers<NV == 2 ? 56 : 64>();
+        // ========================= q's norms and P =========================
+        const int w = warp - kPWarp0;
+        const int gid = lane >> 2, tig = lane & 3;
+        int st = 0;
+        uint32_t full_phase = 0;
+        for (int c = 0; c < nc; ++c) {
+            const int buf = c & 1;
+            ok = warp_wait(&bars[kBarFull + st], full_phase, abort_flag) &&
+                 warp_wait(&bars[kBarSFull + buf], (c >> 1) & 1, abort_flag);
+            const uint32_t aK = tc::smem_u32(smem + st * kStage), aQ = aK + kOffQ;
+            float acc[2][4];
+            if (ok && p.l2norm) {
+                // 1 / norm into oq's place
+                score_block<S>(aQ, aQ, w, w, lane, acc);
+                diag_norm(acc, lane, p.l2_eps, [&](int i, float f) { scal_of(buf, 0)->oq[16 * w + i] = f; });
+                __syncwarp();
+            }
+            if (ok && lane < 16) {  // a row per lane
+                const int i = 16 * w + lane;
+                const float oq = p.l2norm ? p.scale * scal_of(buf, 0)->oq[i] : p.scale;
 #pragma unroll
-                for (int x = 0; x < kBoxes; ++x) {
-                    tc::tma_load_4d(s + x * kBox, &tm_k, full, 64 * x, grp, c * kT, (int)b);
-                    tc::tma_load_4d(s + kOffQ + x * kBox, &tm_q, full, 64 * x, grp, c * kT, (int)b);
-                }
+                for (int hv = 0; hv < NV; ++hv) scal_of(buf, hv)->oq[i] = oq;
+            }
+#pragma unroll 1
+            for (int t = w; t < 10; t += 4) {
+                const int i = tri_i(t), j = tri_j(t), i0 = 16 * i + gid;
+                if (ok) score_block<S>(aQ, aK, i, j, lane, acc);
+                // the last chunk's P has been used
+                if (ok && t < 4 && c > 0) ok = warp_wait(&bars[kBarPFree], (c - 1) & 1, abort_flag);
+                if (!ok) break;
 #pragma unroll
-                for (int x = 0; x < kVBoxes; ++x)
-                    tc::tma_load_4d(s + kOffV + x * kBox, &tm_v, full, NV == 2 ? 0 : 64 * x, NV == 2 ? h0 + x : h0,
-                                    c * kT, (int)b);
-                ++fills[st];
-                if (++st == p.nst) {
-                    st = 0;
-                    free_phase ^= 1u;
+                for (int hv = 0; hv < NV; ++hv) {
+                    const Scalars* sc = scal_of(buf, hv);
+                    uint8_t* sP = p_of(hv);
+                    const Tok ti0 = sc->tok[i0], ti1 = sc->tok[i0 + 8];
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt) {
+                        const int j0 = 16 * j + 8 * nt + 2 * tig;
+                        const Tok t0 = sc->tok[j0], t1 = sc->tok[j0 + 1];
+                        const float (&a)[4] = acc[nt];
+                        const uint32_t o0 = sw(i0, 2 * j + nt) + 4 * tig;
+                        uint32_t hi, lo;
+                        split2(make_float2(j0 <= i0 ? a[0] * (t0.rk * decay(ti0, t0)) : 0.f,
+                                           j0 + 1 <= i0 ? a[1] * (t1.rk * decay(ti0, t1)) : 0.f),
+                               hi, lo);
+                        *reinterpret_cast<uint32_t*>(sP + o0) = hi;
+                        *reinterpret_cast<uint32_t*>(sP + kPlane + o0) = lo;
+                        split2(make_float2(j0 <= i0 + 8 ? a[2] * (t0.rk * decay(ti1, t0)) : 0.f,
+                                           j0 + 1 <= i0 + 8 ? a[3] * (t1.rk * decay(ti1, t1)) : 0.f),
+                               hi, lo);
+                        *reinterpret_cast<uint32_t*>(sP + o0 + 1024) = hi;
+                        *reinterpret_cast<uint32_t*>(sP + kPlane + o0 + 1024) = lo;
+                    }
                 }
             }
-            if (!ok) set_abort(ctl, p.status);
-            // no copy may still be landing when the CTA exits
-#pragma unroll
-            for (int i = 0; i < kMaxStages; ++i)
-                if (fills[i] > 0) (void)tc::mbar_wait(&bars[kBarFull + i], (fills[i] - 1) & 1, never);
+            if (!ok) break;
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tc::mbar_arrive(&bars[kBarPFull]);
+                tc::mbar_arrive(&bars[kBarSFree + buf]);
+            }
+            if (++st == p.nst) {
+                st = 0;
+                full_phase ^= 1u;
+            }
         }
+        if (!ok) set_abort(ctl, p.status);
     } else {
-        // ============================= MMA issuer =============================
-        if (lane == 0 && nc > 0) {
-            constexpr uint32_t id_t = tc::idesc_bf16(128, kT, false, false);  // N = tokens
-            constexpr uint32_t id_s = tc::idesc_bf16(128, S, false, true);    // N = state rows
-            int st = 0;
-            uint32_t full_phase = 0;
-            for (int c = 0; c < nc; ++c) {
-                const int buf = c & 1;
-                const uint32_t ph = c & 1;
-                const uint32_t aK = tc::smem_u32(smem + st * kStage);
-                const uint64_t dK = tc::sdesc_sw128(aK, 16, 1024), dQ = tc::sdesc_sw128(aK + kOffQ, 16, 1024);
-                const uint64_t dKt = tc::sdesc_sw128(aK, kBox, 1024);
-                if (!tc::mbar_wait(&bars[kBarFull + st], full_phase, abort_flag)) { ok = false; break; }
-                if (!tc::mbar_wait(&bars[kBarSFull + buf], (c >> 1) & 1, abort_flag)) { ok = false; break; }
-                if (!tc::mbar_wait(&bars[kBarHReady], ph, abort_flag)) { ok = false; break; }
-                tc::tc_fence_after();
-                // R = K h, from h's two parts
-#pragma unroll
-                for (int ks = 0; ks < S / 16; ++ks)
-                    tc::mma_bf16_ts(tmem + cR, tmem + cHi + 8 * ks, dK + (((ks >> 2) * kBox + (ks & 3) * 32) >> 4), id_t,
-                                    ks > 0);
-#pragma unroll
-                for (int ks = 0; ks < S / 16; ++ks)
-                    tc::mma_bf16_ts(tmem + cR, tmem + cLo + 8 * ks, dK + (((ks >> 2) * kBox + (ks & 3) * 32) >> 4), id_t,
-                                    1);
-                tc::mma_commit(&bars[kBarRDone]);
-                // Q h, once the outputs of the chunk before have been read
-                if (c > 0 && !tc::mbar_wait(&bars[kBarO2Read], ph ^ 1, abort_flag)) { ok = false; break; }
-                tc::tc_fence_after();
-#pragma unroll
-                for (int ks = 0; ks < S / 16; ++ks)
-                    tc::mma_bf16_ts(tmem + cO, tmem + cHi + 8 * ks, dQ + (((ks >> 2) * kBox + (ks & 3) * 32) >> 4), id_t,
-                                    ks > 0);
-                tc::mma_commit(&bars[kBarO1Done]);
-                // W = N X, N's parts times X's down to 2^-16 of hi hi; block column kb of N only has rows from its
-                // own block on
-                if (!tc::mbar_wait(&bars[kBarNFull], ph, abort_flag)) { ok = false; break; }
-                if (!tc::mbar_wait(&bars[kBarXReady], ph, abort_flag)) { ok = false; break; }
-                tc::tc_fence_after();
-#pragma unroll
-                for (int hv = 0; hv < NV; ++hv) {
-                    const uint32_t x = tmem + (hv ? cU : cX);
-                    const uint64_t dN = tc::sdesc_sw128(tc::smem_u32(n_of(hv)), 16, 1024);
-#pragma unroll
-                    for (int kb = 0; kb < 4; ++kb) {
-                        const uint32_t d = tmem + cR + 16 * kb, id = tc::idesc_bf16(128, kT - 16 * kb, false, false);
-                        const uint64_t at = dN + (2048 >> 4) * kb + 2 * kb;
-                        tc::mma_bf16_ts(d, x + 8 * kb, at, id, hv > 0 || kb > 0);
-                        tc::mma_bf16_ts(d, x + 8 * kb, at + (kPlane >> 4), id, 1);
-                        tc::mma_bf16_ts(d, x + 8 * kb, at + 2 * (kPlane >> 4), id, 1);
-                        tc::mma_bf16_ts(d, x + 32 + 8 * kb, at, id, 1);
-                        tc::mma_bf16_ts(d, x + 32 + 8 * kb, at + (kPlane >> 4), id, 1);
-                        tc::mma_bf16_ts(d, x + 64 + 8 * kb, at, id, 1);
+        fewer_registers<48>();
+        if (warp == kTmaWarp) {
+            // ============================ TMA producer ============================
+            if (lane == 0) {
+                tc::tma_prefetch_desc(&tm_q);
+                tc::tma_prefetch_desc(&tm_k);
+                tc::tma_prefetch_desc(&tm_v);
+                tc::tma_prefetch_desc(&tm_y);
+                int fills[kMaxStages] = {};
+                int st = 0;
+                uint32_t free_phase = 1;
+                for (int c = 0; c < nc; ++c) {
+                    if (c >= p.nst && !tc::mbar_wait(&bars[kBarFree + st], free_phase, abort_flag)) { ok = false; break; }
+                    uint8_t* s = smem + st * kStage;
+                    uint64_t* full = &bars[kBarFull + st];
+                    tc::mbar_arrive_expect_tx(full, kStage);
+    #pragma unroll
+                    for (int x = 0; x < kBoxes; ++x) {
+                        tc::tma_load_4d(s + x * kBox, &tm_k, full, 64 * x, grp, c * kT, (int)b);
+                        tc::tma_load_4d(s + kOffQ + x * kBox, &tm_q, full, 64 * x, grp, c * kT, (int)b);
+                    }
+    #pragma unroll
+                    for (int x = 0; x < kVBoxes; ++x)
+                        tc::tma_load_4d(s + kOffV + x * kBox, &tm_v, full, NV == 2 ? 0 : 64 * x, NV == 2 ? h0 + x : h0,
+                                        c * kT, (int)b);
+                    ++fills[st];
+                    if (++st == p.nst) {
+                        st = 0;
+                        free_phase ^= 1u;
                     }
                 }
-                tc::mma_commit(&bars[kBarWDone]);
-                // h += K^T W
-                if (!tc::mbar_wait(&bars[kBarWReady], ph, abort_flag)) { ok = false; break; }
-                tc::tc_fence_after();
-#pragma unroll
-                for (int kt = 0; kt < 4; ++kt) {
-                    tc::mma_bf16_ts(tmem + cH, tmem + cU + 8 * kt, dKt + 128 * kt, id_s, 1);
-                    tc::mma_bf16_ts(tmem + cH, tmem + cU + 32 + 8 * kt, dKt + 128 * kt, id_s, 1);
-                    tc::mma_bf16_ts(tmem + cH, tmem + cU + 64 + 8 * kt, dKt + 128 * kt, id_s, 1);
-                }
-                tc::mma_commit(&bars[kBarHDone]);
-                // P W, once Q h has been read: hi hi + hi lo + lo hi
-                if (!tc::mbar_wait(&bars[kBarPFull], ph, abort_flag)) { ok = false; break; }
-                if (!tc::mbar_wait(&bars[kBarO1Read], ph, abort_flag)) { ok = false; break; }
-                tc::tc_fence_after();
-#pragma unroll
-                for (int hv = 0; hv < NV; ++hv) {
-                    const uint32_t wp = tmem + (hv ? cW2 : cX);
-                    const uint64_t dP = tc::sdesc_sw128(tc::smem_u32(p_of(hv)), 16, 1024);
-#pragma unroll
-                    for (int kb = 0; kb < 4; ++kb) {
-                        const uint32_t d = tmem + cO + 16 * kb, id = tc::idesc_bf16(128, kT - 16 * kb, false, false);
-                        const uint64_t at = dP + (2048 >> 4) * kb + 2 * kb;
-                        tc::mma_bf16_ts(d, wp + 8 * kb, at, id, hv > 0 || kb > 0);
-                        tc::mma_bf16_ts(d, wp + 8 * kb, at + (kPlane >> 4), id, 1);
-                        tc::mma_bf16_ts(d, wp + 32 + 8 * kb, at, id, 1);
-                    }
-                }
-                tc::mma_commit(&bars[kBarO2Done]);
-                tc::mma_commit(&bars[kBarSFree + buf]);
-                tc::mma_commit(&bars[kBarPFree]);
-                tc::mma_commit(&bars[kBarFree + st]);
-                if (++st == p.nst) {
-                    st = 0;
-                    full_phase ^= 1u;
-                }
+                if (!ok) set_abort(ctl, p.status);
+                // no copy may still be landing when the CTA exits
+    #pragma unroll
+                for (int i = 0; i < kMaxStages; ++i)
+                    if (fills[i] > 0) (void)tc::mbar_wait(&bars[kBarFull + i], (fills[i] - 1) & 1, never);
             }
-            if (!ok) set_abort(ctl, p.status);
-            // no product may still run when the tensor memory is freed
-            tc::mma_commit(&bars[kBarDrain]);
-            (void)tc::mbar_wait(&bars[kBarDrain], 0, never);
+        } else if (warp == kMmaWarp) {
+            // ============================= MMA issuer =============================
+            if (nc > 0) {
+                // the whole warp walks the loop, one lane issues
+                const uint32_t me = lane == 0;
+                constexpr uint32_t id_t = tc::idesc_bf16(128, kT, false, false);  // N = tokens
+                constexpr uint32_t id_s = tc::idesc_bf16(128, S, false, true);    // N = state rows
+                int st = 0;
+                uint32_t full_phase = 0;
+                for (int c = 0; c < nc; ++c) {
+                    const int buf = c & 1;
+                    const uint32_t ph = c & 1;
+                    const uint32_t aK = tc::smem_u32(smem + st * kStage);
+                    const uint64_t dK = tc::sdesc_sw128(aK, 16, 1024), dQ = tc::sdesc_sw128(aK + kOffQ, 16, 1024);
+                    const uint64_t dKt = tc::sdesc_sw128(aK, kBox, 1024);
+                    if (!warp_wait(&bars[kBarFull + st], full_phase, abort_flag)) { ok = false; break; }
+                    if (!warp_wait(&bars[kBarSFull + buf], (c >> 1) & 1, abort_flag)) { ok = false; break; }
+                    if (!warp_wait(&bars[kBarHReady], ph, abort_flag)) { ok = false; break; }
+                    tc::tc_fence_after();
+                    // R = K h, from h's two parts
+    #pragma unroll
+                    for (int ks = 0; ks < S / 16; ++ks)
+                        tc::mma_bf16_ts_by(me, tmem + cR, tmem + cHi + 8 * ks, dK + (((ks >> 2) * kBox + (ks & 3) * 32) >> 4), id_t,
+                                        ks > 0);
+    #pragma unroll
+                    for (int ks = 0; ks < S / 16; ++ks)
+                        tc::mma_bf16_ts_by(me, tmem + cR, tmem + cLo + 8 * ks, dK + (((ks >> 2) * kBox + (ks & 3) * 32) >> 4), id_t,
+                                        1);
+                    tc::mma_commit_by(me, &bars[kBarRDone]);
+                    // Q h, once the outputs of the chunk before have been read
+                    if (c > 0 && !warp_wait(&bars[kBarO2Read], ph ^ 1, abort_flag)) { ok = false; break; }
+                    tc::tc_fence_after();
+    #pragma unroll
+                    for (int ks = 0; ks < S / 16; ++ks)
+                        tc::mma_bf16_ts_by(me, tmem + cO, tmem + cHi + 8 * ks, dQ + (((ks >> 2) * kBox + (ks & 3) * 32) >> 4), id_t,
+                                        ks > 0);
+                    tc::mma_commit_by(me, &bars[kBarO1Done]);
+                    // W = N X, N's parts times X's down to 2^-16 of hi hi; block column kb of N only has rows from its
+                    // own block on
+                    if (!warp_wait(&bars[kBarNFull], ph, abort_flag)) { ok = false; break; }
+                    if (!warp_wait(&bars[kBarXReady], ph, abort_flag)) { ok = false; break; }
+                    tc::tc_fence_after();
+    #pragma unroll
+                    for (int hv = 0; hv < NV; ++hv) {
+                        const uint32_t x = tmem + (hv ? cU : cX);
+                        const uint64_t dN = tc::sdesc_sw128(tc::smem_u32(n_of(hv)), 16, 1024);
+    #pragma unroll
+                        for (int kb = 0; kb < 4; ++kb) {
+                            const uint32_t d = tmem + cR + 16 * kb, id = tc::idesc_bf16(128, kT - 16 * kb, false, false);
+                            const uint64_t at = dN + (2048 >> 4) * kb + 2 * kb;
+                            tc::mma_bf16_ts_by(me, d, x + 8 * kb, at, id, hv > 0 || kb > 0);
+                            tc::mma_bf16_ts_by(me, d, x + 8 * kb, at + (kPlane >> 4), id, 1);
+                            tc::mma_bf16_ts_by(me, d, x + 8 * kb, at + 2 * (kPlane >> 4), id, 1);
+                            tc::mma_bf16_ts_by(me, d, x + 32 + 8 * kb, at, id, 1);
+                            tc::mma_bf16_ts_by(me, d, x + 32 + 8 * kb, at + (kPlane >> 4), id, 1);
+                            tc::mma_bf16_ts_by(me, d, x + 64 + 8 * kb, at, id, 1);
+                        }
+                    }
+                    tc::mma_commit_by(me, &bars[kBarWDone]);
+                    // h += K^T W
+                    if (!warp_wait(&bars[kBarWReady], ph, abort_flag)) { ok = false; break; }
+                    tc::tc_fence_after();
+    #pragma unroll
+                    for (int kt = 0; kt < 4; ++kt) {
+                        tc::mma_bf16_ts_by(me, tmem + cH, tmem + cU + 8 * kt, dKt + 128 * kt, id_s, 1);
+                        tc::mma_bf16_ts_by(me, tmem + cH, tmem + cU + 32 + 8 * kt, dKt + 128 * kt, id_s, 1);
+                        tc::mma_bf16_ts_by(me, tmem + cH, tmem + cU + 64 + 8 * kt, dKt + 128 * kt, id_s, 1);
+                    }
+                    tc::mma_commit_by(me, &bars[kBarHDone]);
+                    // P W onto the scaled Q h: hi hi + hi lo + lo hi
+                    if (!warp_wait(&bars[kBarPFull], ph, abort_flag)) { ok = false; break; }
+                    if (!warp_wait(&bars[kBarWyReady], ph, abort_flag)) { ok = false; break; }
+                    if (!warp_wait(&bars[kBarO1Read], ph, abort_flag)) { ok = false; break; }
+                    tc::tc_fence_after();
+    #pragma unroll
+                    for (int hv = 0; hv < NV; ++hv) {
+                        const uint32_t wp = tmem + (hv ? cW2 : cX);
+                        const uint64_t dP = tc::sdesc_sw128(tc::smem_u32(p_of(hv)), 16, 1024);
+    #pragma unroll
+                        for (int kb = 0; kb < 4; ++kb) {
+                            const uint32_t d = tmem + cO + 16 * kb, id = tc::idesc_bf16(128, kT - 16 * kb, false, false);
+                            const uint64_t at = dP + (2048 >> 4) * kb + 2 * kb;
+                            tc::mma_bf16_ts_by(me, d, wp + 8 * kb, at, id, 1);
+                            tc::mma_bf16_ts_by(me, d, wp + 8 * kb, at + (kPlane >> 4), id, 1);
+                            tc::mma_bf16_ts_by(me, d, wp + 32 + 8 * kb, at, id, 1);
+                        }
+                    }
+                    tc::mma_commit_by(me, &bars[kBarO2Done]);
+                    tc::mma_commit_by(me, &bars[kBarSFree + buf]);
+                    tc::mma_commit_by(me, &bars[kBarPFree]);
+                    tc::mma_commit_by(me, &bars[kBarFree + st]);
+                    if (++st == p.nst) {
+                        st = 0;
+                        full_phase ^= 1u;
+                    }
+                }
+                if (!ok) set_abort(ctl, p.status);
+                // no product may still run when the tensor memory is freed
+                tc::mma_commit_by(me, &bars[kBarDrain]);
+                (void)warp_wait(&bars[kBarDrain], 0, never);
+            }
         }
     }
 
@@ -1009,20 +1161,21 @@ cudaError_t launch_k(const GdrArgs& a, cudaStream_t st) {
     p.l2_eps = a.l2_eps;
     p.l2norm = a.l2norm;
     constexpr uint32_t stage = (2 * (S / 64) + NV * H / 64) * kBox;
-    constexpr uint32_t scratch = (NV * (uint32_t)sizeof(ScoreScratch) + 15) / 16 * 16;
+    constexpr uint32_t scratch = NV * (uint32_t)sizeof(NScratch);
     constexpr uint32_t rest =
-        NV * ((kNPlanes + kPPlanes) * kPlane + 2 * kScalBytes) + scratch + kNumBars * 8 + (uint32_t)sizeof(SharedCtl) + 1024;
+        NV * ((kNPlanes + kPPlanes) * kPlane + H / 64 * kBox + 2 * kScalBytes) + scratch + kNumBars * 8 + (uint32_t)sizeof(SharedCtl) + 1024;
     constexpr int fit = (kSmemLimit - (int)rest) / (int)stage;
     static_assert(fit >= 2, "two stages at least");
     p.nst = fit < kMaxStages ? fit : kMaxStages;
     p.off_n = p.nst * stage;
     p.off_p = p.off_n + NV * kNPlanes * kPlane;
-    p.off_scal = p.off_p + NV * kPPlanes * kPlane;
+    p.off_y = p.off_p + NV * kPPlanes * kPlane;
+    p.off_scal = p.off_y + NV * H / 64 * kBox;
     p.off_scratch = p.off_scal + 2 * NV * kScalBytes;
     p.off_bar = p.off_scratch + scratch;
     const int smem = (int)(p.nst * stage + rest);
 
-    CUtensorMap tm_q, tm_k, tm_v;
+    CUtensorMap tm_q, tm_k, tm_v, tm_y;
     const uint64_t L = g.seqlen, B = g.batch;
     const uint32_t box[4] = {64, 1, kT, 1};
     auto map = [&](CUtensorMap* m, const void* base, uint64_t width, uint64_t count, uint64_t stride) {
@@ -1031,12 +1184,11 @@ cudaError_t launch_k(const GdrArgs& a, cudaStream_t st) {
         return make_tmap_bf16(m, base, 4, dims, strides, box);
     };
     if (!map(&tm_q, a.q, S, g.ngroups, a.q_stride) || !map(&tm_k, a.k, S, g.ngroups, a.k_stride) ||
-        !map(&tm_v, a.v, H, g.nheads, a.v_stride))
+        !map(&tm_v, a.v, H, g.nheads, a.v_stride) || !map(&tm_y, a.y, H, g.nheads, (uint64_t)(g.nheads * H)))
         return cudaErrorInvalidValue;
     const cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(k_gdr_chunk_tc<S, H, NV>), smem);
     if (e != cudaSuccess) return e;
-    k_gdr_chunk_tc<S, H, NV><<<dim3((unsigned)(g.nheads / NV), (unsigned)g.batch), (kScoreWarp0 + 4 * NV + 2) * 32,
-                               smem, st>>>(tm_q, tm_k, tm_v, p);
+    k_gdr_chunk_tc<S, H, NV><<<dim3((unsigned)(g.nheads / NV), (unsigned)g.batch), threads_of(NV), smem, st>>>(tm_q, tm_k, tm_v, tm_y, p);
     return cudaGetLastError();
 }
 
