@@ -72,12 +72,17 @@ struct Tok {       // what the scores need of a token
     float rk;      // 1 / norm of k
     float beta;
 };
+// Blocks below the diagonal take their decays from the first token r of their
+// rows' block, e^{G_i - G_j} = e^{G_i - G_r} e^{G_r - G_j}: both factors are at
+// most 1 and one exponential serves a row or a column of the block.
 struct Scalars {  // one head's, per chunk
     Tok tok[kT];
     float cb[kT], cr[kT];  // X = cb v + cr R
     float d[kT];           // W's share of the state
     float gam[kT];         // e^G
     float oq[kT];          // y = oq (gam Q h + P W)
+    float el[kT];          // e^{G_i - G_r}
+    float ea[kT];          // beta_i rk_i e^{G_i - G_r}
     float g_last;          // e^{G_last}
     float pad[3];
 };
@@ -113,13 +118,12 @@ enum : int {
     kBarPFull,                           // P and the scalars' out
     kBarPFree,
     kBarHReady,  // h's parts are written, h is decayed
-    kBarRDone,
+    kBarRDone,   // R and Q h
     kBarXReady,
     kBarWDone,
     kBarWReady,   // W's parts for the state
     kBarWyReady,  // and for y
     kBarHDone,
-    kBarO1Done,  // Q h
     kBarO1Read,
     kBarO2Done,  // P W
     kBarO2Read,
@@ -309,23 +313,24 @@ __device__ __forceinline__ void ld32(uint32_t addr, uint32_t (&a)[16], uint32_t 
     tc::tmem_tie16(b);
 }
 
-// The 16 x 16 products of rows 16 i .. of tile x with rows 16 j .. of tile k,
-// summed over the S columns.
+// The 16 x 16 products of rows 16 i .. of tile x with rows 16 j .. of tile k (K
+// or Q of a stage), summed over the S columns.
 template <int S>
 __device__ __forceinline__ void score_block(uint32_t x, uint32_t k, int i, int j, int lane, float (&acc)[2][4]) {
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
-    const uint32_t ar = 16 * i + (lane & 15), ac = lane >> 4;
-    const uint32_t br = 16 * j + (lane & 7) + ((lane >> 4) << 3), bc = (lane >> 3) & 1;
+    // pieces 2 ks, 2 ks + 1 of a row: the swizzled place of the first, with 2 ks' bits flipped
+    const uint32_t xa = x + sw(16 * i + (lane & 15), lane >> 4);
+    const uint32_t kb = k + sw(16 * j + (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
 #pragma unroll
     for (int box = 0; box < S / 64; ++box) {
         uint32_t a[4][4], b[4][4];
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
-            ldsm4(x + box * kBox + sw(ar, 2 * ks + ac), a[ks]);
-            ldsm4(k + box * kBox + sw(br, 2 * ks + bc), b[ks]);
+            ldsm4((xa ^ (ks << 5)) + box * 2 * kBox, a[ks]);
+            ldsm4((kb ^ (ks << 5)) + box * 2 * kBox, b[ks]);
         }
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
@@ -351,12 +356,13 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                const GdrTcParams p) {
     constexpr int kNWarps = 4 * NV, kPWarp0 = kNWarp0 + kNWarps, kTmaWarp = kPWarp0 + kPWarps, kMmaWarp = kTmaWarp + 1;
     constexpr int kBoxes = S / 64, kVBoxes = NV * H / 64;
-    constexpr uint32_t kOffQ = kBoxes * kBox, kOffV = 2 * kOffQ, kStage = kOffV + kVBoxes * kBox;
+    // A stage: K's and Q's boxes in turn, so that 64 rows of K and 64 of Q are one operand of 128; then V's
+    constexpr uint32_t kOffV = 2 * kBoxes * kBox, kStage = kOffV + kVBoxes * kBox;
     static_assert((S == 64 || S == 128) && (NV == 1 ? (H == 64 || H == 128) : H == 64), "shapes");
     // Tensor memory columns (128 lanes = the head's columns; NV = 2: 64 of each head)
-    constexpr uint32_t cH = 0, cHi = S, cLo = S + S / 2, cR = 2 * S, cX = 2 * S + 64, cW2 = 2 * S + 128,
-                       cO = 2 * S + 192;
-    // R holds R, then W.  cX: X's parts (96 columns), then W's parts for y (64).  cU: the second head's X
+    constexpr uint32_t cH = 0, cHi = S, cLo = S + S / 2, cR = 2 * S, cO = 2 * S + 64, cX = 2 * S + 128,
+                       cW2 = 2 * S + 192;
+    // cR: R, then W.  cO: Q h, then y's sum.  cX: X's parts (96 columns), then W's parts for y (64).  cU: the second head's X
     // parts, then W's parts for the state (96 each), over h's parts, which are done with by then (S = 64:
     // behind the rest).  cW2: the second head's W parts for y.  An operand of one of two heads has zeros in
     // the other one's rows.
@@ -401,7 +407,6 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         tc::mbar_init(&bars[kBarWReady], kChainWarps);
         tc::mbar_init(&bars[kBarWyReady], kChainWarps);
         tc::mbar_init(&bars[kBarHDone], 1);
-        tc::mbar_init(&bars[kBarO1Done], 1);
         tc::mbar_init(&bars[kBarO1Read], kOutWarps);
         tc::mbar_init(&bars[kBarO2Done], 1);
         tc::mbar_init(&bars[kBarO2Read], kOutWarps);
@@ -516,8 +521,6 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 }
             }
             if (!warp_wait(&bars[kBarRDone], ph, abort_flag)) { ok = false; break; }
-            // (Q h, which follows R, also reads what X may overwrite)
-            if (NV == 2 && S == 128 && !warp_wait(&bars[kBarO1Done], ph, abort_flag)) { ok = false; break; }
             tc::tc_fence_after();
             // X
             {
@@ -640,7 +643,7 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             const uint32_t ph = c & 1;
             const Scalars* sc = scal_of(buf, hv);
             // Q h -> e^G Q h, onto which P W is summed
-            ok = warp_wait(&bars[kBarO1Done], ph, abort_flag);
+            ok = warp_wait(&bars[kBarRDone], ph, abort_flag);
             if (ok) {
                 tc::tc_fence_after();
 #pragma unroll
@@ -780,7 +783,7 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     if (r >= nv) {
 #pragma unroll
                         for (int i = 0; i < S / 16; ++i)
-                            *reinterpret_cast<uint4*>(sK + (S == 128 ? (lane & 1) * kBox + sw(r, i)
+                            *reinterpret_cast<uint4*>(sK + (S == 128 ? (lane & 1) * 2 * kBox + sw(r, i)
                                                                      : sw(r, 4 * (lane & 1) + i))) =
                                 make_uint4(0, 0, 0, 0);
                     }
@@ -801,38 +804,48 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 sc->cr[tid] = -t.beta * e * t.rk;
                 sc->gam[tid] = e;
                 sc->d[tid] = ex2(last.gi - t.gi) * ex2(last.gf - t.gf) * t.rk;
+                const float el = decay(t, sc->tok[tid & ~15]);
+                sc->el[tid] = el;
+                sc->ea[tid] = t.beta * t.rk * el;
                 if (tid == kT - 1) sc->g_last = e;
             }
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bars[kBarSFull + buf]);
-            // A's blocks in fp32: this warp's diagonal block (by columns), then one or two below
-#pragma unroll 1
-            for (int t = w; t < 10; t += 4) {
-                const int i = tri_i(t), j = tri_j(t);
-                if (t >= 4) score_block<S>(aK, aK, i, j, lane, acc);
-                const Tok ti0 = sc->tok[16 * i + gid], ti1 = sc->tok[16 * i + gid + 8];
+            // A's diagonal block, by columns
+            {
+                const Tok ti0 = sc->tok[16 * w + gid], ti1 = sc->tok[16 * w + gid + 8];
                 const float f0 = ti0.beta * ti0.rk, f1 = ti1.beta * ti1.rk;
-                const bool in0 = 16 * i + gid < nv, in1 = 16 * i + gid + 8 < nv;
+                const bool in0 = 16 * w + gid < nv, in1 = 16 * w + gid + 8 < nv;
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int jj = 8 * nt + 2 * tig + e;
+                        const Tok tj = sc->tok[16 * w + jj];
+                        scr->diag[w][jj][gid] = in0 && jj < gid ? acc[nt][e] * (f0 * tj.rk * decay(ti0, tj)) : 0.f;
+                        scr->diag[w][jj][gid + 8] =
+                            in1 && jj < gid + 8 ? acc[nt][2 + e] * (f1 * tj.rk * decay(ti1, tj)) : 0.f;
+                    }
+            }
+            // and one or two below
+#pragma unroll 1
+            for (int t = w + 4; t < 10; t += 4) {
+                const int i = tri_i(t), j = tri_j(t);
+                score_block<S>(aK, aK, i, j, lane, acc);
+                // (rows past the end: 0, whatever their products are)
+                const float f0 = 16 * i + gid < nv ? sc->ea[16 * i + gid] : 0.f;
+                const float f1 = 16 * i + gid + 8 < nv ? sc->ea[16 * i + gid + 8] : 0.f;
+                const Tok tr = sc->tok[16 * i];
+                float2 (*low)[8] = scr->low[low_block(i, j)];
 #pragma unroll
                 for (int nt = 0; nt < 2; ++nt) {
                     const int jj = 8 * nt + 2 * tig;
                     const Tok t0 = sc->tok[16 * j + jj], t1 = sc->tok[16 * j + jj + 1];
-                    float (&a)[4] = acc[nt];
-                    a[0] = in0 ? a[0] * (f0 * t0.rk * decay(ti0, t0)) : 0.f;
-                    a[1] = in0 ? a[1] * (f0 * t1.rk * decay(ti0, t1)) : 0.f;
-                    a[2] = in1 ? a[2] * (f1 * t0.rk * decay(ti1, t0)) : 0.f;
-                    a[3] = in1 ? a[3] * (f1 * t1.rk * decay(ti1, t1)) : 0.f;
-                    if (t >= 4) {
-                        float2 (*low)[8] = scr->low[low_block(i, j)];
-                        low[gid][low_at(gid, jj / 2)] = make_float2(a[0], a[1]);
-                        low[gid + 8][low_at(gid + 8, jj / 2)] = make_float2(a[2], a[3]);
-                    } else {
-                        scr->diag[w][jj][gid] = jj < gid ? a[0] : 0.f;
-                        scr->diag[w][jj + 1][gid] = jj + 1 < gid ? a[1] : 0.f;
-                        scr->diag[w][jj][gid + 8] = jj < gid + 8 ? a[2] : 0.f;
-                        scr->diag[w][jj + 1][gid + 8] = jj + 1 < gid + 8 ? a[3] : 0.f;
-                    }
+                    const float2 cj = make_float2(t0.rk * decay(tr, t0), t1.rk * decay(tr, t1));
+                    const float2 c0 = tc::mul_f32x2(cj, make_float2(f0, f0)), c1 = tc::mul_f32x2(cj, make_float2(f1, f1));
+                    low[gid][low_at(gid, jj / 2)] = tc::mul_f32x2(c0, make_float2(acc[nt][0], acc[nt][1]));
+                    low[gid + 8][low_at(gid + 8, jj / 2)] = tc::mul_f32x2(c1, make_float2(acc[nt][2], acc[nt][3]));
                 }
             }
             __syncwarp();
@@ -933,7 +946,7 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             const int buf = c & 1;
             ok = warp_wait(&bars[kBarFull + st], full_phase, abort_flag) &&
                  warp_wait(&bars[kBarSFull + buf], (c >> 1) & 1, abort_flag);
-            const uint32_t aK = tc::smem_u32(smem + st * kStage), aQ = aK + kOffQ;
+            const uint32_t aK = tc::smem_u32(smem + st * kStage), aQ = aK + kBox;
             float acc[2][4];
             if (ok && p.l2norm) {
                 // 1 / norm into oq's place
@@ -958,22 +971,35 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 for (int hv = 0; hv < NV; ++hv) {
                     const Scalars* sc = scal_of(buf, hv);
                     uint8_t* sP = p_of(hv);
-                    const Tok ti0 = sc->tok[i0], ti1 = sc->tok[i0 + 8];
+                    // (the diagonal block takes its decays exactly)
+                    const bool below = i > j;
+                    const Tok tr = sc->tok[16 * i], ti0 = sc->tok[i0], ti1 = sc->tok[i0 + 8];
+                    const float f0 = sc->el[i0], f1 = sc->el[i0 + 8];
 #pragma unroll
                     for (int nt = 0; nt < 2; ++nt) {
                         const int j0 = 16 * j + 8 * nt + 2 * tig;
                         const Tok t0 = sc->tok[j0], t1 = sc->tok[j0 + 1];
-                        const float (&a)[4] = acc[nt];
+                        float2 c0, c1;
+                        if (below) {
+                            const float2 cj = make_float2(t0.rk * decay(tr, t0), t1.rk * decay(tr, t1));
+                            c0 = tc::mul_f32x2(cj, make_float2(f0, f0));
+                            c1 = tc::mul_f32x2(cj, make_float2(f1, f1));
+                        } else {
+                            c0 = make_float2(t0.rk * decay(ti0, t0), t1.rk * decay(ti0, t1));
+                            c1 = make_float2(t0.rk * decay(ti1, t0), t1.rk * decay(ti1, t1));
+                        }
+                        float2 a0 = tc::mul_f32x2(c0, make_float2(acc[nt][0], acc[nt][1]));
+                        float2 a1 = tc::mul_f32x2(c1, make_float2(acc[nt][2], acc[nt][3]));
+                        if (!below) {
+                            a0 = make_float2(j0 <= i0 ? a0.x : 0.f, j0 + 1 <= i0 ? a0.y : 0.f);
+                            a1 = make_float2(j0 <= i0 + 8 ? a1.x : 0.f, j0 + 1 <= i0 + 8 ? a1.y : 0.f);
+                        }
                         const uint32_t o0 = sw(i0, 2 * j + nt) + 4 * tig;
                         uint32_t hi, lo;
-                        split2(make_float2(j0 <= i0 ? a[0] * (t0.rk * decay(ti0, t0)) : 0.f,
-                                           j0 + 1 <= i0 ? a[1] * (t1.rk * decay(ti0, t1)) : 0.f),
-                               hi, lo);
+                        split2(a0, hi, lo);
                         *reinterpret_cast<uint32_t*>(sP + o0) = hi;
                         *reinterpret_cast<uint32_t*>(sP + kPlane + o0) = lo;
-                        split2(make_float2(j0 <= i0 + 8 ? a[2] * (t0.rk * decay(ti1, t0)) : 0.f,
-                                           j0 + 1 <= i0 + 8 ? a[3] * (t1.rk * decay(ti1, t1)) : 0.f),
-                               hi, lo);
+                        split2(a1, hi, lo);
                         *reinterpret_cast<uint32_t*>(sP + o0 + 1024) = hi;
                         *reinterpret_cast<uint32_t*>(sP + kPlane + o0 + 1024) = lo;
                     }
@@ -1011,8 +1037,8 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     tc::mbar_arrive_expect_tx(full, kStage);
     #pragma unroll
                     for (int x = 0; x < kBoxes; ++x) {
-                        tc::tma_load_4d(s + x * kBox, &tm_k, full, 64 * x, grp, c * kT, (int)b);
-                        tc::tma_load_4d(s + kOffQ + x * kBox, &tm_q, full, 64 * x, grp, c * kT, (int)b);
+                        tc::tma_load_4d(s + 2 * x * kBox, &tm_k, full, 64 * x, grp, c * kT, (int)b);
+                        tc::tma_load_4d(s + (2 * x + 1) * kBox, &tm_q, full, 64 * x, grp, c * kT, (int)b);
                     }
     #pragma unroll
                     for (int x = 0; x < kVBoxes; ++x)
@@ -1032,10 +1058,9 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
         } else if (warp == kMmaWarp) {
             // ============================= MMA issuer =============================
-            if (nc > 0) {
-                // the whole warp walks the loop, one lane issues
-                const uint32_t me = lane == 0;
-                constexpr uint32_t id_t = tc::idesc_bf16(128, kT, false, false);  // N = tokens
+            if (lane == 0 && nc > 0) {
+                constexpr uint32_t id_t = tc::idesc_bf16(128, kT, false, false);       // N = tokens
+                constexpr uint32_t id_rq = tc::idesc_bf16(128, 2 * kT, false, false);  // of K and of Q
                 constexpr uint32_t id_s = tc::idesc_bf16(128, S, false, true);    // N = state rows
                 int st = 0;
                 uint32_t full_phase = 0;
@@ -1043,34 +1068,28 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     const int buf = c & 1;
                     const uint32_t ph = c & 1;
                     const uint32_t aK = tc::smem_u32(smem + st * kStage);
-                    const uint64_t dK = tc::sdesc_sw128(aK, 16, 1024), dQ = tc::sdesc_sw128(aK + kOffQ, 16, 1024);
-                    const uint64_t dKt = tc::sdesc_sw128(aK, kBox, 1024);
-                    if (!warp_wait(&bars[kBarFull + st], full_phase, abort_flag)) { ok = false; break; }
-                    if (!warp_wait(&bars[kBarSFull + buf], (c >> 1) & 1, abort_flag)) { ok = false; break; }
-                    if (!warp_wait(&bars[kBarHReady], ph, abort_flag)) { ok = false; break; }
+                    const uint64_t dK = tc::sdesc_sw128(aK, 16, 1024);
+                    const uint64_t dKt = tc::sdesc_sw128(aK, 2 * kBox, 1024);
+                    if (!tc::mbar_wait(&bars[kBarFull + st], full_phase, abort_flag)) { ok = false; break; }
+                    if (!tc::mbar_wait(&bars[kBarSFull + buf], (c >> 1) & 1, abort_flag)) { ok = false; break; }
+                    if (!tc::mbar_wait(&bars[kBarHReady], ph, abort_flag)) { ok = false; break; }
                     tc::tc_fence_after();
-                    // R = K h, from h's two parts
-    #pragma unroll
-                    for (int ks = 0; ks < S / 16; ++ks)
-                        tc::mma_bf16_ts_by(me, tmem + cR, tmem + cHi + 8 * ks, dK + (((ks >> 2) * kBox + (ks & 3) * 32) >> 4), id_t,
-                                        ks > 0);
-    #pragma unroll
-                    for (int ks = 0; ks < S / 16; ++ks)
-                        tc::mma_bf16_ts_by(me, tmem + cR, tmem + cLo + 8 * ks, dK + (((ks >> 2) * kBox + (ks & 3) * 32) >> 4), id_t,
-                                        1);
-                    tc::mma_commit_by(me, &bars[kBarRDone]);
-                    // Q h, once the outputs of the chunk before have been read
-                    if (c > 0 && !warp_wait(&bars[kBarO2Read], ph ^ 1, abort_flag)) { ok = false; break; }
+                    // R | Q h from h's high part, once y's sum of the chunk before has been read; R from its low part
+                    if (c > 0 && !tc::mbar_wait(&bars[kBarO2Read], ph ^ 1, abort_flag)) { ok = false; break; }
                     tc::tc_fence_after();
-    #pragma unroll
+#pragma unroll
                     for (int ks = 0; ks < S / 16; ++ks)
-                        tc::mma_bf16_ts_by(me, tmem + cO, tmem + cHi + 8 * ks, dQ + (((ks >> 2) * kBox + (ks & 3) * 32) >> 4), id_t,
-                                        ks > 0);
-                    tc::mma_commit_by(me, &bars[kBarO1Done]);
+                        tc::mma_bf16_ts(tmem + cR, tmem + cHi + 8 * ks,
+                                        dK + (((ks >> 2) * 2 * kBox + (ks & 3) * 32) >> 4), id_rq, ks > 0);
+#pragma unroll
+                    for (int ks = 0; ks < S / 16; ++ks)
+                        tc::mma_bf16_ts(tmem + cR, tmem + cLo + 8 * ks,
+                                        dK + (((ks >> 2) * 2 * kBox + (ks & 3) * 32) >> 4), id_t, 1);
+                    tc::mma_commit(&bars[kBarRDone]);
                     // W = N X, N's parts times X's down to 2^-16 of hi hi; block column kb of N only has rows from its
                     // own block on
-                    if (!warp_wait(&bars[kBarNFull], ph, abort_flag)) { ok = false; break; }
-                    if (!warp_wait(&bars[kBarXReady], ph, abort_flag)) { ok = false; break; }
+                    if (!tc::mbar_wait(&bars[kBarNFull], ph, abort_flag)) { ok = false; break; }
+                    if (!tc::mbar_wait(&bars[kBarXReady], ph, abort_flag)) { ok = false; break; }
                     tc::tc_fence_after();
     #pragma unroll
                     for (int hv = 0; hv < NV; ++hv) {
@@ -1080,29 +1099,29 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                         for (int kb = 0; kb < 4; ++kb) {
                             const uint32_t d = tmem + cR + 16 * kb, id = tc::idesc_bf16(128, kT - 16 * kb, false, false);
                             const uint64_t at = dN + (2048 >> 4) * kb + 2 * kb;
-                            tc::mma_bf16_ts_by(me, d, x + 8 * kb, at, id, hv > 0 || kb > 0);
-                            tc::mma_bf16_ts_by(me, d, x + 8 * kb, at + (kPlane >> 4), id, 1);
-                            tc::mma_bf16_ts_by(me, d, x + 8 * kb, at + 2 * (kPlane >> 4), id, 1);
-                            tc::mma_bf16_ts_by(me, d, x + 32 + 8 * kb, at, id, 1);
-                            tc::mma_bf16_ts_by(me, d, x + 32 + 8 * kb, at + (kPlane >> 4), id, 1);
-                            tc::mma_bf16_ts_by(me, d, x + 64 + 8 * kb, at, id, 1);
+                            tc::mma_bf16_ts(d, x + 8 * kb, at, id, hv > 0 || kb > 0);
+                            tc::mma_bf16_ts(d, x + 8 * kb, at + (kPlane >> 4), id, 1);
+                            tc::mma_bf16_ts(d, x + 8 * kb, at + 2 * (kPlane >> 4), id, 1);
+                            tc::mma_bf16_ts(d, x + 32 + 8 * kb, at, id, 1);
+                            tc::mma_bf16_ts(d, x + 32 + 8 * kb, at + (kPlane >> 4), id, 1);
+                            tc::mma_bf16_ts(d, x + 64 + 8 * kb, at, id, 1);
                         }
                     }
-                    tc::mma_commit_by(me, &bars[kBarWDone]);
+                    tc::mma_commit(&bars[kBarWDone]);
                     // h += K^T W
-                    if (!warp_wait(&bars[kBarWReady], ph, abort_flag)) { ok = false; break; }
+                    if (!tc::mbar_wait(&bars[kBarWReady], ph, abort_flag)) { ok = false; break; }
                     tc::tc_fence_after();
     #pragma unroll
                     for (int kt = 0; kt < 4; ++kt) {
-                        tc::mma_bf16_ts_by(me, tmem + cH, tmem + cU + 8 * kt, dKt + 128 * kt, id_s, 1);
-                        tc::mma_bf16_ts_by(me, tmem + cH, tmem + cU + 32 + 8 * kt, dKt + 128 * kt, id_s, 1);
-                        tc::mma_bf16_ts_by(me, tmem + cH, tmem + cU + 64 + 8 * kt, dKt + 128 * kt, id_s, 1);
+                        tc::mma_bf16_ts(tmem + cH, tmem + cU + 8 * kt, dKt + 128 * kt, id_s, 1);
+                        tc::mma_bf16_ts(tmem + cH, tmem + cU + 32 + 8 * kt, dKt + 128 * kt, id_s, 1);
+                        tc::mma_bf16_ts(tmem + cH, tmem + cU + 64 + 8 * kt, dKt + 128 * kt, id_s, 1);
                     }
-                    tc::mma_commit_by(me, &bars[kBarHDone]);
+                    tc::mma_commit(&bars[kBarHDone]);
                     // P W onto the scaled Q h: hi hi + hi lo + lo hi
-                    if (!warp_wait(&bars[kBarPFull], ph, abort_flag)) { ok = false; break; }
-                    if (!warp_wait(&bars[kBarWyReady], ph, abort_flag)) { ok = false; break; }
-                    if (!warp_wait(&bars[kBarO1Read], ph, abort_flag)) { ok = false; break; }
+                    if (!tc::mbar_wait(&bars[kBarPFull], ph, abort_flag)) { ok = false; break; }
+                    if (!tc::mbar_wait(&bars[kBarWyReady], ph, abort_flag)) { ok = false; break; }
+                    if (!tc::mbar_wait(&bars[kBarO1Read], ph, abort_flag)) { ok = false; break; }
                     tc::tc_fence_after();
     #pragma unroll
                     for (int hv = 0; hv < NV; ++hv) {
@@ -1112,15 +1131,15 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                         for (int kb = 0; kb < 4; ++kb) {
                             const uint32_t d = tmem + cO + 16 * kb, id = tc::idesc_bf16(128, kT - 16 * kb, false, false);
                             const uint64_t at = dP + (2048 >> 4) * kb + 2 * kb;
-                            tc::mma_bf16_ts_by(me, d, wp + 8 * kb, at, id, 1);
-                            tc::mma_bf16_ts_by(me, d, wp + 8 * kb, at + (kPlane >> 4), id, 1);
-                            tc::mma_bf16_ts_by(me, d, wp + 32 + 8 * kb, at, id, 1);
+                            tc::mma_bf16_ts(d, wp + 8 * kb, at, id, 1);
+                            tc::mma_bf16_ts(d, wp + 8 * kb, at + (kPlane >> 4), id, 1);
+                            tc::mma_bf16_ts(d, wp + 32 + 8 * kb, at, id, 1);
                         }
                     }
-                    tc::mma_commit_by(me, &bars[kBarO2Done]);
-                    tc::mma_commit_by(me, &bars[kBarSFree + buf]);
-                    tc::mma_commit_by(me, &bars[kBarPFree]);
-                    tc::mma_commit_by(me, &bars[kBarFree + st]);
+                    tc::mma_commit(&bars[kBarO2Done]);
+                    tc::mma_commit(&bars[kBarSFree + buf]);
+                    tc::mma_commit(&bars[kBarPFree]);
+                    tc::mma_commit(&bars[kBarFree + st]);
                     if (++st == p.nst) {
                         st = 0;
                         full_phase ^= 1u;
@@ -1128,8 +1147,8 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 }
                 if (!ok) set_abort(ctl, p.status);
                 // no product may still run when the tensor memory is freed
-                tc::mma_commit_by(me, &bars[kBarDrain]);
-                (void)warp_wait(&bars[kBarDrain], 0, never);
+                tc::mma_commit(&bars[kBarDrain]);
+                (void)tc::mbar_wait(&bars[kBarDrain], 0, never);
             }
         }
     }
