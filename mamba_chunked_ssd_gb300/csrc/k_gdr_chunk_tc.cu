@@ -1,5 +1,5 @@
 // k_gdr_chunk_tc.cu — the gated delta rule over whole sequences in chunks of
-// 64 tokens, on the 5th-generation tensor cores (bf16 inputs).
+// 32 tokens, on the 5th-generation tensor cores (bf16 inputs).
 //
 // With h the state entering a chunk (S x H), G the log decay summed from the
 // chunk's start and K, Q, V its rows, the corrections w_i = beta_i (v_i - (state
@@ -22,13 +22,14 @@
 // to tensor memory as the next product's left operand, while K, Q, N and P are
 // right operands in shared memory, straight from the TMA or as the scores' warps
 // wrote them.
-//   warps 0-7    chain: h -> two bf16 parts and e^{G_last} h;  R = K h -> X;  W ->
-//                its parts (two per TMEM lane quadrant, half of the columns each)
-//   warps 8-11   output: y from Q h and P W
-//   then 4 NV    G, k's norms, A and N of the next chunk, while the chain runs on
-//                this one (four warps to a head)
-//   then 4       q's norms and P
-//   then 1, 1    TMA producer; tcgen05.mma issuer
+//   warps 0-15   chain: h -> two bf16 parts and e^{G_last} h;  R = K h -> X;  W ->
+//                its parts (four per TMEM lane quadrant, a quarter of the columns
+//                each)
+//   warps 16-19  output: y from Q h and P W
+//   warps 20-23  G, k's norms, A and N of the next chunk, while the chain runs on
+//                this one
+//   warps 24-27  q's norms and P
+//   warps 28-30  TMA producer of K and Q; tcgen05.mma issuer; TMA producer of V
 // What bounds it is the chain from state to state: three dependent products and
 // three conversions a chunk.  What enters the fp32 state is as good as fp32: N, X
 // and W take part in its products as three bf16 parts each (24 bits), h in the
@@ -39,14 +40,16 @@
 // corrections that cancel, and one part lost 1.8 % of y's largest value.  Q h
 // takes h's high part.
 //
-// The scores K K^T and Q K^T and N's off-diagonal blocks are 16 x 16 pieces that
-// are masked, scaled and fed on in registers; they use the warp-level mma, whose
-// accumulators are registers, and leave the tensor memory (all 512 columns of it)
-// to the chain.  N = (I + A)^-1 goes by blocks of 16: the diagonal blocks by
-// forward substitution in fp32, then N_ij = -N_ii sum_{j <= m < i} A_im N_mj
-// below them, in products of tf32 parts (two of 11 bits each: three products).
-// Forward substitution by blocks is stable for any A; a product of powers of A
-// would not be (equal keys make A all ones below the diagonal).
+// Chunks of 32 and not 64: N and P cost a chunk's square on the CUDA cores, and
+// with 64 tokens N (about 12000 cycles a chunk for four warps) held up a chain of
+// 8000.
+//
+// The scores K K^T and Q K^T are 16 x 16 pieces that are masked, scaled and fed on
+// in registers; they use the warp-level mma, whose accumulators are registers.  N
+// goes by blocks of 16: the diagonal blocks by forward substitution, then
+// N_10 = -N_11 A_10 N_00, all in fp32.  Forward substitution by blocks is stable
+// for any A; a product of powers of A would not be (equal keys make A all ones
+// below the diagonal).
 //
 // G is summed in fixed point and kept as an integer and a fraction, so that
 // G_i - G_j is good to 2^-22 even behind a token that forgets everything.
@@ -59,12 +62,12 @@
 namespace m2 {
 namespace {
 
-constexpr int kT = 64;             // tokens per chunk
-constexpr int kChainWarps = 8, kOutWarp0 = 8, kOutWarps = 4, kNWarp0 = 12, kPWarps = 4;
-// whole warpgroups, for the register split: the last one is TMA, MMA and two idle warps
-constexpr int threads_of(int nv) { return (kNWarp0 + 4 * nv + kPWarps + 4) * 32; }
-constexpr uint32_t kBox = kT * 128;  // one box: 64 tokens x 64 columns of bf16
-constexpr int kMaxStages = 3;
+constexpr int kT = 32;  // tokens per chunk
+constexpr int kChainWarps = 16, kOutWarps = 4, kNWarp0 = 20, kNWarps = 4, kPWarp0 = 24, kPWarps = 4;
+constexpr int kTmaWarp = 28, kMmaWarp = 29, kVWarp = 30;
+constexpr int kThreads = 31 * 32;    // 64 registers each
+constexpr uint32_t kBox = kT * 128;  // one box: the chunk's tokens x 64 columns of bf16
+constexpr int kMaxStages = 6, kMaxVStages = 4;
 constexpr int kSmemLimit = 232448;
 
 struct Tok {       // what the scores need of a token
@@ -72,54 +75,45 @@ struct Tok {       // what the scores need of a token
     float rk;      // 1 / norm of k
     float beta;
 };
-// Blocks below the diagonal take their decays from the first token r of their
-// rows' block, e^{G_i - G_j} = e^{G_i - G_r} e^{G_r - G_j}: both factors are at
-// most 1 and one exponential serves a row or a column of the block.
+// The block below the diagonal takes its decays from its rows' first token r,
+// e^{G_i - G_j} = e^{G_i - G_r} e^{G_r - G_j}: both factors are at most 1 and one
+// exponential serves a row or a column of the block.
 struct Scalars {  // one head's, per chunk
     Tok tok[kT];
     float cb[kT], cr[kT];  // X = cb v + cr R
     float d[kT];           // W's share of the state
     float gam[kT];         // e^G
     float oq[kT];          // y = oq (gam Q h + P W)
-    float el[kT];          // e^{G_i - G_r}
-    float ea[kT];          // beta_i rk_i e^{G_i - G_r}
     float g_last;          // e^{G_last}
     float pad[3];
 };
 
-// A head's results of the scores: N's three and P's two planes of 64 rows of
-// 128 bytes, in one buffer each (they are needed late in a chunk, and written
-// when the chunk before has used them), the scalars in two.
+// A head's results of the scores: N's three and P's two planes of 32 rows of 128
+// bytes (the first 64 of each used), in one buffer each (they are needed late in
+// a chunk, and written when the chunk before has used them), the scalars in two.
 constexpr uint32_t kPlane = kT * 128;
 constexpr uint32_t kNPlanes = 3, kPPlanes = 2;
 constexpr uint32_t kScalBytes = sizeof(Scalars);
 static_assert(kScalBytes % 16 == 0, "scalars");
 
-struct NScratch {           // one head's
-    float diag[4][16][20];  // A's diagonal blocks, [column][row]; then N's, [row][column]
-    float2 low[6][16][8];   // A's blocks below the diagonal, see low_at
+struct NScratch {           // one head's, in fp32
+    float diag[2][16][20];  // A's diagonal blocks, then N's, a column in a row
+    float low[16][20];      // A's block (1, 0), a column in a row
 };
-// Place of columns 2 c2, 2 c2 + 1 of row r in a block of `low` (spread over the
-// banks for eight rows by four pairs).
-__device__ __forceinline__ int low_at(int r, int c2) { return c2 ^ (((r >> 1) & 1) << 2); }
-__device__ __forceinline__ int low_block(int i, int m) { return i * (i - 1) / 2 + m; }
-
-// The ten 16 x 16 blocks (i, j) of a lower triangle, in rounds of four warps:
-// block t = 4 round + warp, the diagonal first.
-__device__ __forceinline__ int tri_i(int t) { return (0x3323213210 >> (4 * t)) & 15; }
-__device__ __forceinline__ int tri_j(int t) { return (0x0102103210 >> (4 * t)) & 15; }
 
 enum : int {
-    kBarFull = 0,                        // [stages] TMA
-    kBarFree = kBarFull + kMaxStages,    // [stages] every reader of the stage is done
-    kBarSFull = kBarFree + kMaxStages,   // [2] scalars but out (and K's rows past the end cleared)
-    kBarSFree = kBarSFull + 2,           // [2]
-    kBarNFull = kBarSFree + 2,           // N; free again with kBarWDone
-    kBarPFull,                           // P and the scalars' out
+    kBarFull = 0,                         // [stages] K and Q
+    kBarFree = kBarFull + kMaxStages,     // [stages] every reader of the stage is done
+    kBarVFull = kBarFree + kMaxStages,    // [V stages]
+    kBarVFree = kBarVFull + kMaxVStages,  // [V stages]
+    kBarSFull = kBarVFree + kMaxVStages,  // [2] scalars but oq (and K's rows past the end cleared)
+    kBarSFree = kBarSFull + 2,            // [2]
+    kBarNFull = kBarSFree + 2,            // N; free again with kBarWDone
+    kBarPFull,                            // P and oq
     kBarPFree,
-    kBarHReady,  // h's parts are written, h is decayed
+    kBarHReady,  // h's parts are written
     kBarRDone,   // R and Q h
-    kBarXReady,
+    kBarXReady,  // and h is decayed
     kBarWDone,
     kBarWReady,   // W's parts for the state
     kBarWyReady,  // and for y
@@ -139,8 +133,8 @@ struct SharedCtl {
 
 struct GdrTcParams {
     Geom g;
-    int nst;  // stages
-    uint32_t off_n, off_p, off_y, off_scal, off_scratch, off_bar;
+    int nst, nvst;  // stages
+    uint32_t off_v, off_n, off_p, off_scal, off_scratch, off_bar;
     const float* gate;
     const float* beta;
     const int32_t* lengths;
@@ -175,36 +169,29 @@ __device__ __forceinline__ bool bar_sync_and(int id, int threads, bool ok) {
     return r != 0;
 }
 
-// A whole warp's wait for a phase: true once it has completed; false if the
-// kernel was aborted, or after about 2 s.  try_wait suspends the warp in
-// hardware, so a waiting warp takes few issue slots from working ones.  All
-// lanes leave with one answer.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    bool done = tc::mbar_try_wait(bar, parity);
-    if (!__all_sync(0xffffffffu, done)) {
-        const long long c0 = clock64();
-        bool give_up = false;
-        do {
-            done = tc::mbar_try_wait(bar, parity);
-            give_up = *abort != 0 || clock64() - c0 > tc::kWaitLimitCycles;
-            done = __all_sync(0xffffffffu, done);
-            give_up = __any_sync(0xffffffffu, give_up);
-        } while (!done && !give_up);
+// Waits for a phase: true once it has completed; false if the kernel was
+// aborted, or after about 2 s.  A waiting thread costs the working warps issue
+// slots with every look (looks with a clock and an abort flag beside them took
+// half of all issued instructions), so a round of looks is a bare loop, and
+// roles off the chain (SLEEP) sleep between looks.
+template <bool SLEEP>
+__device__ __forceinline__ bool thread_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    const long long c0 = clock64();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i) {
+            if (SLEEP) __nanosleep(40);
+            if (tc::mbar_try_wait(bar, parity)) return true;
+        }
+        if (*abort != 0 || clock64() - c0 > tc::kWaitLimitCycles) return false;
     }
-    return done;
 }
-
-// Registers per thread of the calling warpgroup from here on.  A block is
-// launched with threads_of(NV) x 80 (NV = 2: x 72) registers; the groups'
-// shares (chain twice) sum to 480 and 504 a thread of a warpgroup, six times 80
-// and seven times 72.
-template <int N>
-__device__ __forceinline__ void more_registers() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void fewer_registers() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+// A whole warp's wait: all lanes look (each sees the phase complete for itself)
+// and leave with one answer.
+template <bool SLEEP = false>
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    return __all_sync(0xffffffffu, thread_wait<SLEEP>(bar, parity, abort));
 }
 
 // Byte offset of 16-byte piece `ch` (of 8) of row `row` in a box of 128-byte
@@ -217,11 +204,6 @@ __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
                  : "r"(addr)
                  : "memory");
 }
-__device__ __forceinline__ void stsm4_trans(uint32_t addr, const uint32_t (&r)[4]) {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3])
-                 : "memory");
-}
 // d (16 x 8, fp32) += a (16 x 16) b (16 x 8)
 __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -231,50 +213,37 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// d (16 x 8) += a (16 x 8) b (8 x 8) of fp32 values, each as two tf32 parts
-// (hi hi + hi lo + lo hi).  The order of the contracted index is free, and is
-// chosen so that an accumulator is a left operand as it is: a thread's
-// positions t and t + 4 are columns 2 t and 2 t + 1.  b is transposed: b.x, b.y
-// are row g's (n) columns 2 t, 2 t + 1.
-__device__ __forceinline__ uint32_t tf32_rn(float x) {
-    uint32_t r;
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
-    return r;
+// 4 columns of this warp's lanes (packed bf16 pairs).
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
 }
-__device__ __forceinline__ void mma8(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    tc::tmem_ld8_nowait(taddr, r);
+    tc::tmem_wait_ld8(r);
 }
-// d += a b over 16 columns of fp32 values: a an accumulator block (as above),
-// b(row n, pair of columns) b's float2.
-template <class B>
-__device__ __forceinline__ void mma_block(float (&d)[2][4], const float (&a)[2][4], int gid, int tig, B b) {
+
+// Four rows of a 16 x 16 block times a column: o += B[4 rows][16] x, with the
+// block's columns at col(k) as float4 of these rows.
+template <class Col>
+__device__ __forceinline__ void block_times(float2 (&o)[2], const float (&x)[16], Col col) {
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-        uint32_t ah[4], al[4], bh[2][2], bl[2][2];
+    for (int k = 0; k < 16; ++k) {
+        const float4 b = col(k);
+        const float2 xk = make_float2(x[k], x[k]);
+        o[0] = tc::fma_f32x2(make_float2(b.x, b.y), xk, o[0]);
+        o[1] = tc::fma_f32x2(make_float2(b.z, b.w), xk, o[1]);
+    }
+}
+// The 16 values of a column of which each of four neighbouring lanes has four.
+__device__ __forceinline__ void gather(float (&x)[16], const float2 (&o)[2], int lane) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float v = a[kk][((i & 1) << 1) | (i >> 1)];
-            ah[i] = tf32_rn(v);
-            al[i] = tf32_rn(v - __uint_as_float(ah[i]));
-        }
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-            const float2 v = b(8 * nt + gid, 4 * kk + tig);
-            bh[nt][0] = tf32_rn(v.x);
-            bh[nt][1] = tf32_rn(v.y);
-            bl[nt][0] = tf32_rn(v.x - __uint_as_float(bh[nt][0]));
-            bl[nt][1] = tf32_rn(v.y - __uint_as_float(bh[nt][1]));
-        }
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) mma8(d[nt], ah, bh[nt]);
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) mma8(d[nt], ah, bl[nt]);
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) mma8(d[nt], al, bh[nt]);
+    for (int q = 0; q < 4; ++q) {
+        x[4 * q] = __shfl_sync(0xffffffffu, o[0].x, (lane & ~3) | q);
+        x[4 * q + 1] = __shfl_sync(0xffffffffu, o[0].y, (lane & ~3) | q);
+        x[4 * q + 2] = __shfl_sync(0xffffffffu, o[1].x, (lane & ~3) | q);
+        x[4 * q + 3] = __shfl_sync(0xffffffffu, o[1].y, (lane & ~3) | q);
     }
 }
 
@@ -305,22 +274,11 @@ __device__ __forceinline__ float2 as_f2(const uint32_t* r) {
     return make_float2(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
-// 32 fp32 columns of this warp's lanes.
-__device__ __forceinline__ void ld32(uint32_t addr, uint32_t (&a)[16], uint32_t (&b)[16]) {
-    tc::tmem_ld16_nowait(addr, a);
-    tc::tmem_ld16_nowait(addr + 16, b);
-    tc::tmem_wait_ld16(a);
-    tc::tmem_tie16(b);
-}
-
 // The 16 x 16 products of rows 16 i .. of tile x with rows 16 j .. of tile k (K
 // or Q of a stage), summed over the S columns.
 template <int S>
 __device__ __forceinline__ void score_block(uint32_t x, uint32_t k, int i, int j, int lane, float (&acc)[2][4]) {
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
+    float part[S / 64][2][4] = {};  // a chain of four for each box
     // pieces 2 ks, 2 ks + 1 of a row: the swizzled place of the first, with 2 ks' bits flipped
     const uint32_t xa = x + sw(16 * i + (lane & 15), lane >> 4);
     const uint32_t kb = k + sw(16 * j + (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
@@ -334,10 +292,14 @@ __device__ __forceinline__ void score_block(uint32_t x, uint32_t k, int i, int j
         }
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
-            mma16(acc[0], a[ks], b[ks][0], b[ks][1]);
-            mma16(acc[1], a[ks], b[ks][2], b[ks][3]);
+            mma16(part[box][0], a[ks], b[ks][0], b[ks][1]);
+            mma16(part[box][1], a[ks], b[ks][2], b[ks][3]);
         }
     }
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[nt][e] = S == 128 ? part[0][nt][e] + part[S / 64 - 1][nt][e] : part[0][nt][e];
 }
 
 // 1 / sqrt(x + eps) of a block's diagonal, handed to put(row, value).
@@ -350,23 +312,20 @@ __device__ __forceinline__ void diag_norm(const float (&acc)[2][4], int lane, fl
 }
 
 template <int S, int H, int NV>
-__global__ void __launch_bounds__(threads_of(NV), 1)
+__global__ void __launch_bounds__(kThreads, 1)
 k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-               const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_y,
-               const GdrTcParams p) {
-    constexpr int kNWarps = 4 * NV, kPWarp0 = kNWarp0 + kNWarps, kTmaWarp = kPWarp0 + kPWarps, kMmaWarp = kTmaWarp + 1;
+               const __grid_constant__ CUtensorMap tm_v, const GdrTcParams p) {
     constexpr int kBoxes = S / 64, kVBoxes = NV * H / 64;
-    // A stage: K's and Q's boxes in turn, so that 64 rows of K and 64 of Q are one operand of 128; then V's
-    constexpr uint32_t kOffV = 2 * kBoxes * kBox, kStage = kOffV + kVBoxes * kBox;
+    // A stage: K's and Q's boxes in turn, so that 32 rows of K and 32 of Q are one operand of 64.  V has
+    // stages of its own (it is needed late and not for long).
+    constexpr uint32_t kStage = 2 * kBoxes * kBox, kVStage = kVBoxes * kBox;
     static_assert((S == 64 || S == 128) && (NV == 1 ? (H == 64 || H == 128) : H == 64), "shapes");
-    // Tensor memory columns (128 lanes = the head's columns; NV = 2: 64 of each head)
-    constexpr uint32_t cH = 0, cHi = S, cLo = S + S / 2, cR = 2 * S, cO = 2 * S + 64, cX = 2 * S + 128,
-                       cW2 = 2 * S + 192;
-    // cR: R, then W.  cO: Q h, then y's sum.  cX: X's parts (96 columns), then W's parts for y (64).  cU: the second head's X
-    // parts, then W's parts for the state (96 each), over h's parts, which are done with by then (S = 64:
-    // behind the rest).  cW2: the second head's W parts for y.  An operand of one of two heads has zeros in
-    // the other one's rows.
-    constexpr uint32_t cU = S == 128 ? cHi : 2 * S + 256;
+    // Tensor memory columns (128 lanes = the head's columns; NV = 2: 64 of each head): h and its two parts,
+    // R | Q h (then W | y's sum), the second head's W and y's sum (products with N and P cover all lanes,
+    // and each head has its own), X's parts, W's parts for the state and for y.
+    constexpr uint32_t cH = 0, cHi = S, cLo = S + S / 2, cR = 2 * S, cO = 2 * S + 32, cR2 = 2 * S + 64,
+                       cO2 = 2 * S + 96, cX = 2 * S + 128, cU = 2 * S + 176, cW = 2 * S + 224;
+    static_assert(cW + 32 <= 512, "tensor memory");
 
     // (aligned by an offset, so that the compiler still knows it for shared memory)
     extern __shared__ uint8_t smem_raw[];
@@ -392,6 +351,10 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         for (int i = 0; i < kMaxStages; ++i) {
             tc::mbar_init(&bars[kBarFull + i], 1);
             tc::mbar_init(&bars[kBarFree + i], 1);
+        }
+        for (int i = 0; i < kMaxVStages; ++i) {
+            tc::mbar_init(&bars[kBarVFull + i], 1);
+            tc::mbar_init(&bars[kBarVFree + i], kChainWarps);
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&bars[kBarSFull + i], kNWarps);
@@ -428,136 +391,96 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     bool ok = true;
 
     if (warp < kChainWarps) {
-        more_registers<NV == 2 ? 80 : 88>();
         // ============================== chain ==============================
-        const int q = warp & 3, hf = warp >> 2;
+        const int q = warp & 3, part = warp >> 2;
         const int hv = NV == 2 ? q >> 1 : 0;
         const int colh = 32 * (NV == 2 ? (q & 1) : q) + lane;  // column of its head
         const bool live = colh < H;
         const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16);
         const int64_t sbase = (b * g.nheads + h0 + hv) * (int64_t)S * H + colh;
+        const int s0 = part * (S / 4), i0 = part * (kT / 4);  // this warp's state rows and tokens
+        const uint32_t w_at = tl + (hv ? cR2 : cR) + i0;       // W of its head
         // this thread's column of V in a stage: 16-byte piece and place in it
         const uint32_t vch = (32 * (q & 1) + lane) >> 3, vin = (lane & 7) * 2;
-        const uint32_t v_off = kOffV + (q >> 1) * kBox + vin;
-        {
+        uint8_t* v_at = smem + p.off_v + (q >> 1) * kBox + vin;
 #pragma unroll 1
-            for (int s = hf * (S / 2); s < (hf + 1) * (S / 2); s += 16) {
-                uint32_t r[16];
+        for (int s = s0; s < s0 + S / 4; s += 16) {
+            uint32_t r[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    r[j] = (live && p.init) ? __float_as_uint(p.init[sbase + (int64_t)(s + j) * H]) : 0u;
-                tc::tmem_st16(tl + cH + s, r);
-            }
-            if (NV == 2) {  // the rows of the other head's operands: zeros, never written again
-                uint32_t z[16] = {};
-                tc::tmem_st16(tl + (hv ? cX : cW2) + 32 * hf, z);
-                tc::tmem_st16(tl + (hv ? cX : cW2) + 32 * hf + 16, z);
-            }
-            tc::tmem_wait_st();
+            for (int j = 0; j < 16; ++j)
+                r[j] = (live && p.init) ? __float_as_uint(p.init[sbase + (int64_t)(s + j) * H]) : 0u;
+            tc::tmem_st16(tl + cH + s, r);
         }
-        int st = 0;
-        uint32_t full_phase = 0;
+        tc::tmem_wait_st();
+        int vs = 0;
+        uint32_t v_phase = 0;
         for (int c = 0; c < nc; ++c) {
             const int buf = c & 1;
             const uint32_t ph = c & 1;
-            if (!warp_wait(&bars[kBarSFull + buf], (c >> 1) & 1, abort_flag)) { ok = false; break; }
             const Scalars* sc = scal_of(buf, hv);
-            const float g_last = sc->g_last;
             if (c > 0 && !warp_wait(&bars[kBarHDone], ph ^ 1, abort_flag)) { ok = false; break; }
             tc::tc_fence_after();
             // h's parts
 #pragma unroll 1
-            for (int s = hf * (S / 2); s < (hf + 1) * (S / 2); s += 32) {
-                uint32_t r[2][16], hi[16], lo[16];
-                ld32(tl + cH + s, r[0], r[1]);
+            for (int s = s0; s < s0 + S / 4; s += 16) {
+                uint32_t r[16], hi[8], lo[8];
+                tc::tmem_ld16(tl + cH + s, r);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    split2(as_f2(&r[j >> 3][(2 * j) & 15]), hi[j], lo[j]);
-                }
-                tc::tmem_st16(tl + cHi + s / 2, hi);
-                tc::tmem_st16(tl + cLo + s / 2, lo);
+                for (int j = 0; j < 8; ++j) split2(as_f2(&r[2 * j]), hi[j], lo[j]);
+                tc::tmem_st8(tl + cHi + s / 2, hi);
+                tc::tmem_st8(tl + cLo + s / 2, lo);
             }
             tc::tmem_wait_st();
             tc::tc_fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bars[kBarHReady]);
-            // while R = K h runs: h decayed to the chunk's end, and V from the stage (it has landed: the
-            // scores waited for the same copy)
+            // while R = K h runs: h decayed to the chunk's end, and V
+            if (!warp_wait(&bars[kBarSFull + buf], (c >> 1) & 1, abort_flag)) { ok = false; break; }
+            const float g_last = sc->g_last;
 #pragma unroll 1
-            for (int s = hf * (S / 2); s < (hf + 1) * (S / 2); s += 32) {
-                uint32_t r[2][16];
-                ld32(tl + cH + s, r[0], r[1]);
+            for (int s = s0; s < s0 + S / 4; s += 16) {
+                uint32_t r[16];
+                tc::tmem_ld16(tl + cH + s, r);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    uint32_t* x = &r[j >> 3][(2 * j) & 15];
-                    const float2 v = tc::mul_f32x2(as_f2(x), make_float2(g_last, g_last));
-                    x[0] = __float_as_uint(v.x);
-                    x[1] = __float_as_uint(v.y);
+                for (int j = 0; j < 16; j += 2) {
+                    const float2 v = tc::mul_f32x2(as_f2(&r[j]), make_float2(g_last, g_last));
+                    r[j] = __float_as_uint(v.x);
+                    r[j + 1] = __float_as_uint(v.y);
                 }
-                tc::tmem_st16(tl + cH + s, r[0]);
-                tc::tmem_st16(tl + cH + s + 16, r[1]);
+                tc::tmem_st16(tl + cH + s, r);
             }
-            if (!warp_wait(&bars[kBarFull + st], full_phase, abort_flag)) { ok = false; break; }
-            const int i0 = 32 * hf;  // this warp's tokens: i0 .. i0 + 31
-            uint32_t v2[16];         // their V, two to a register
+            if (!warp_wait(&bars[kBarVFull + vs], v_phase, abort_flag)) { ok = false; break; }
+            float2 bv[4];
             {
-                const int64_t left = n - (int64_t)c * kT;
-                const int nv = left < kT ? (int)left : kT;
-                const uint8_t* sv = smem + st * kStage + v_off;
+                const uint8_t* sv = v_at + vs * kVStage + i0 * 128;
+                const int64_t left = n - (int64_t)c * kT - i0;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int k = i0 + 2 * j;
-                    const uint32_t a0 = *reinterpret_cast<const uint16_t*>(sv + k * 128 + ((vch ^ (2 * j & 7)) << 4));
-                    const uint32_t a1 =
-                        *reinterpret_cast<const uint16_t*>(sv + k * 128 + 128 + ((vch ^ ((2 * j + 1) & 7)) << 4));
-                    v2[j] = a0 | (a1 << 16);
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t v = *reinterpret_cast<const uint16_t*>(sv + j * 128 + ((vch ^ j) << 4));
+                    const float x = left > j ? tc::bf16_lo(v) * sc->cb[i0 + j] : 0.f;  // past the end, whatever is there
+                    if (j & 1) bv[j / 2].y = x;
+                    else bv[j / 2].x = x;
                 }
-                if (nv < kT || !live) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int k = i0 + 2 * j;
-                        v2[j] = !live || k >= nv ? 0u : (k + 1 >= nv ? v2[j] & 0xffffu : v2[j]);
-                    }
-                }
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bars[kBarVFree + vs]);
+            if (++vs == p.nvst) {
+                vs = 0;
+                v_phase ^= 1u;
             }
             if (!warp_wait(&bars[kBarRDone], ph, abort_flag)) { ok = false; break; }
             tc::tc_fence_after();
-            // X
+            // X (in lanes that have no column, whatever comes: nothing reads them)
             {
-                const uint32_t mine = hv ? cU : cX;
+                uint32_t r[8], x0[4], x1[4], x2[4];
+                tmem_ld8(tl + cR + i0, r);
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const int i1 = i0 + 16 * m;
-                    uint32_t r[16], x0[8], x1[8], x2[8];
-                    tc::tmem_ld16(tl + cR + i1, r);
-#pragma unroll
-                    for (int j = 0; j < 16; j += 4) {
-                        const float4 cb = *reinterpret_cast<const float4*>(&sc->cb[i1 + j]);
-                        const float4 cr = *reinterpret_cast<const float4*>(&sc->cr[i1 + j]);
-                        const uint32_t va = v2[8 * m + j / 2], vb = v2[8 * m + j / 2 + 1];
-                        const float2 bv0 = tc::mul_f32x2(make_float2(cb.x, cb.y),
-                                                         make_float2(tc::bf16_lo(va), tc::bf16_hi(va)));
-                        const float2 bv1 = tc::mul_f32x2(make_float2(cb.z, cb.w),
-                                                         make_float2(tc::bf16_lo(vb), tc::bf16_hi(vb)));
-                        split3(tc::fma_f32x2(make_float2(cr.x, cr.y), as_f2(&r[j]), bv0), x0[j / 2], x1[j / 2],
-                               x2[j / 2]);
-                        split3(tc::fma_f32x2(make_float2(cr.z, cr.w), as_f2(&r[j + 2]), bv1), x0[j / 2 + 1],
-                               x1[j / 2 + 1], x2[j / 2 + 1]);
-                    }
-                    tc::tmem_st8(tl + mine + i1 / 2, x0);
-                    tc::tmem_st8(tl + mine + 32 + i1 / 2, x1);
-                    tc::tmem_st8(tl + mine + 64 + i1 / 2, x2);
-                }
-                if (NV == 2) {  // zeros in the other head's X: all of it, or the columns that held W
-                    uint32_t z[16] = {};
-                    if (hv == 0) {
-                        tc::tmem_st16(tl + cU + i0 / 2, z);
-                        tc::tmem_st16(tl + cU + 32 + i0 / 2, z);
-                        tc::tmem_st16(tl + cU + 64 + i0 / 2, z);
-                    } else {
-                        tc::tmem_st16(tl + cX + 64 + i0 / 2, z);
-                    }
-                }
+                for (int j = 0; j < 4; ++j)
+                    split3(tc::fma_f32x2(*reinterpret_cast<const float2*>(&sc->cr[i0 + 2 * j]), as_f2(&r[2 * j]), bv[j]),
+                           x0[j], x1[j], x2[j]);
+                tmem_st4(tl + cX + i0 / 2, x0);
+                tmem_st4(tl + cX + 16 + i0 / 2, x1);
+                tmem_st4(tl + cX + 32 + i0 / 2, x2);
             }
             tc::tmem_wait_st();
             tc::tc_fence_before();
@@ -567,56 +490,35 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             // W = N X, decayed to the chunk's end for the state, then as it is for y
             if (!warp_wait(&bars[kBarWDone], ph, abort_flag)) { ok = false; break; }
             tc::tc_fence_after();
-            uint32_t r[2][16];
-            ld32(tl + cR + i0, r[0], r[1]);
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                uint32_t u0[8], u1[8], u2[8];
-                const int i1 = i0 + 16 * m;
-#pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                    const float4 d = *reinterpret_cast<const float4*>(&sc->d[i1 + j]);
-                    const uint32_t* x = &r[m][j];
-                    split3(tc::mul_f32x2(make_float2(d.x, d.y), as_f2(x)), u0[j / 2], u1[j / 2], u2[j / 2]);
-                    split3(tc::mul_f32x2(make_float2(d.z, d.w), as_f2(x + 2)), u0[j / 2 + 1], u1[j / 2 + 1],
-                           u2[j / 2 + 1]);
-                }
-                tc::tmem_st8(tl + cU + i1 / 2, u0);
-                tc::tmem_st8(tl + cU + 32 + i1 / 2, u1);
-                tc::tmem_st8(tl + cU + 64 + i1 / 2, u2);
-            }
-            tc::tmem_wait_st();
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&bars[kBarWReady]);
             {
-                const uint32_t mine = hv ? cW2 : cX;
-                uint32_t w0[16], w1[16];
+                uint32_t r[8], x0[4], x1[4], x2[4];
+                tmem_ld8(w_at, r);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    split2(as_f2(&r[j >> 3][(2 * j) & 15]), w0[j], w1[j]);
-                }
-                tc::tmem_st16(tl + mine + i0 / 2, w0);
-                tc::tmem_st16(tl + mine + 32 + i0 / 2, w1);
-                if (NV == 2 && hv == 0) {  // the second head's W: the columns that held X
-                    uint32_t z[16] = {};
-                    tc::tmem_st16(tl + cW2 + i0 / 2, z);
-                }
-            }
-            tc::tmem_wait_st();
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&bars[kBarWyReady]);
-            if (++st == p.nst) {
-                st = 0;
-                full_phase ^= 1u;
+                for (int j = 0; j < 4; ++j)
+                    split3(tc::mul_f32x2(*reinterpret_cast<const float2*>(&sc->d[i0 + 2 * j]), as_f2(&r[2 * j])), x0[j],
+                           x1[j], x2[j]);
+                tmem_st4(tl + cU + i0 / 2, x0);
+                tmem_st4(tl + cU + 16 + i0 / 2, x1);
+                tmem_st4(tl + cU + 32 + i0 / 2, x2);
+                tc::tmem_wait_st();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bars[kBarWReady]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) split2(as_f2(&r[2 * j]), x0[j], x1[j]);
+                tmem_st4(tl + cW + i0 / 2, x0);
+                tmem_st4(tl + cW + 16 + i0 / 2, x1);
+                tc::tmem_wait_st();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bars[kBarWyReady]);
             }
         }
         if (ok && nc > 0) ok = warp_wait(&bars[kBarHDone], (nc - 1) & 1, abort_flag);
         if (ok && p.final_state) {
             tc::tc_fence_after();
 #pragma unroll 1
-            for (int s = hf * (S / 2); s < (hf + 1) * (S / 2); s += 16) {
+            for (int s = s0; s < s0 + S / 4; s += 16) {
                 uint32_t r[16];
                 tc::tmem_ld16(tl + cH + s, r);
                 if (live) {
@@ -626,232 +528,199 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
         }
         if (!ok) set_abort(ctl, p.status);
-    } else if (warp < kOutWarp0 + kOutWarps) {
-        fewer_registers<NV == 2 ? 64 : 72>();
+    } else if (warp < kNWarp0) {
         // ============================== output ==============================
         const int q = warp & 3;
         const int hv = NV == 2 ? q >> 1 : 0;
         const int colh = 32 * (NV == 2 ? (q & 1) : q) + lane;
         const bool live = colh < H;
         const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16);
-        const bool storer = threadIdx.x == kOutWarp0 * 32;
-        // this thread's column of the staged y
-        const uint32_t ych = (32 * (q & 1) + lane) >> 3;
-        uint8_t* sy = smem + p.off_y + (q >> 1) * kBox + (lane & 7) * 2;
+        const uint32_t o_at = tl + (hv ? cO2 : cO);
+        const int64_t row = (int64_t)g.nheads * H;
+        const int odd = lane & 1;
+        // lanes meet in pairs: the even one stores both columns of token i, the odd one of i + 1
+        __nv_bfloat16* y = p.y + (b * L + odd) * row + (int64_t)(h0 + hv) * H + (colh & ~1);
         for (int c = 0; c < nc; ++c) {
             const int buf = c & 1;
             const uint32_t ph = c & 1;
             const Scalars* sc = scal_of(buf, hv);
-            // Q h -> e^G Q h, onto which P W is summed
-            ok = warp_wait(&bars[kBarRDone], ph, abort_flag);
-            if (ok) {
-                tc::tc_fence_after();
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    uint32_t r[16];
-                    tc::tmem_ld16(tl + cO + 16 * m, r);
-#pragma unroll
-                    for (int j = 0; j < 16; j += 4) {
-                        const float4 f = *reinterpret_cast<const float4*>(&sc->gam[16 * m + j]);
-                        const float2 a0 = tc::mul_f32x2(make_float2(f.x, f.y), as_f2(&r[j]));
-                        const float2 a1 = tc::mul_f32x2(make_float2(f.z, f.w), as_f2(&r[j + 2]));
-                        r[j] = __float_as_uint(a0.x), r[j + 1] = __float_as_uint(a0.y);
-                        r[j + 2] = __float_as_uint(a1.x), r[j + 3] = __float_as_uint(a1.y);
-                    }
-                    tc::tmem_st16(tl + cO + 16 * m, r);
-                }
-                tc::tmem_wait_st();
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bars[kBarO1Read]);
-                ok = warp_wait(&bars[kBarPFull], ph, abort_flag) && warp_wait(&bars[kBarO2Done], ph, abort_flag);
-            }
-            if (storer) tc::bulk_wait_read_all();  // the last chunk's y has left its place
-            ok = bar_sync_and(3, 32 * kOutWarps, ok);
-            if (!ok) break;
+            // Q h -> e^G Q h, onto which P W is summed (the second head's in a place of its own)
+            if (!warp_wait<true>(&bars[kBarSFull + buf], (c >> 1) & 1, abort_flag)) { ok = false; break; }
+            if (!warp_wait<true>(&bars[kBarRDone], ph, abort_flag)) { ok = false; break; }
             tc::tc_fence_after();
-            const int64_t left = n - (int64_t)c * kT;
-            const int nv = left < kT ? (int)left : kT;
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
+#pragma unroll 1
+            for (int m = 0; m < kT; m += 16) {
                 uint32_t r[16];
-                tc::tmem_ld16(tl + cO + 16 * m, r);
-                if (m == 3) {
+                tc::tmem_ld16(tl + cO + m, r);
+#pragma unroll
+                for (int j = 0; j < 16; j += 2) {
+                    const float2 a = tc::mul_f32x2(*reinterpret_cast<const float2*>(&sc->gam[m + j]), as_f2(&r[j]));
+                    r[j] = __float_as_uint(a.x);
+                    r[j + 1] = __float_as_uint(a.y);
+                }
+                tc::tmem_st16(o_at + m, r);
+            }
+            tc::tmem_wait_st();
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bars[kBarO1Read]);
+            if (!warp_wait<true>(&bars[kBarPFull], ph, abort_flag)) { ok = false; break; }
+            if (!warp_wait<true>(&bars[kBarO2Done], ph, abort_flag)) { ok = false; break; }
+            tc::tc_fence_after();
+            const int64_t nleft = n - (int64_t)c * kT, lleft = L - (int64_t)c * kT;
+            const int nv = nleft < kT ? (int)nleft : kT, lv = live ? (lleft < kT ? (int)lleft : kT) : 0;
+            __nv_bfloat16* yc = y + c * kT * row;
+#pragma unroll 1
+            for (int m = 0; m < kT; m += 16) {
+                uint32_t r[16];
+                tc::tmem_ld16(o_at + m, r);
+                if (m == kT - 16) {
                     tc::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&bars[kBarO2Read]);
                 }
 #pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                    const int i = 16 * m + j;
-                    const float4 f = *reinterpret_cast<const float4*>(&sc->oq[i]);
-                    const float2 a0 = tc::mul_f32x2(make_float2(f.x, f.y), as_f2(&r[j]));
-                    const float2 a1 = tc::mul_f32x2(make_float2(f.z, f.w), as_f2(&r[j + 2]));
-                    uint32_t y2[2] = {tc::pack_bf16x2(a0.x, a0.y), tc::pack_bf16x2(a1.x, a1.y)};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t v = e & 1 ? y2[e >> 1] >> 16 : y2[e >> 1] & 0xffffu;
-                        if (live)
-                            *reinterpret_cast<uint16_t*>(sy + (i + e) * 128 + ((ych ^ ((i + e) & 7)) << 4)) =
-                                (uint16_t)(nv == kT || i + e < nv ? v : 0u);
-                    }
+                for (int j = 0; j < 16; j += 2) {
+                    const int i = m + j;
+                    float2 a = tc::mul_f32x2(*reinterpret_cast<const float2*>(&sc->oq[i]), as_f2(&r[j]));
+                    if (nv < kT) a = make_float2(i < nv ? a.x : 0.f, i + 1 < nv ? a.y : 0.f);
+                    const uint32_t both = tc::pack_bf16x2(a.x, a.y);  // this column of tokens i, i + 1
+                    const uint32_t other = __shfl_xor_sync(0xffffffffu, both, 1);
+                    const uint32_t pair = odd ? __byte_perm(other, both, 0x7632) : __byte_perm(both, other, 0x5410);
+                    if (i + odd < lv) *reinterpret_cast<uint32_t*>(yc) = pair;
+                    yc += 2 * row;
                 }
             }
-            tc::fence_proxy_async_smem();
-            bar_sync(3, 32 * kOutWarps);
-            if (storer) {  // rows past L are clipped
-#pragma unroll
-                for (int x = 0; x < kVBoxes; ++x)
-                    tc::tma_store_4d(&tm_y, smem + p.off_y + x * kBox, NV == 2 ? 0 : 64 * x, NV == 2 ? h0 + x : h0,
-                                     c * kT, (int)b);
-                tc::bulk_commit();
-            }
+            __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bars[kBarSFree + buf]);
         }
-        if (storer) tc::bulk_wait_all();
         if (!ok) set_abort(ctl, p.status);
-        if (ok && live) {
-            __nv_bfloat16* y = p.y + (b * L * g.nheads + h0 + hv) * (int64_t)H + colh;
-            for (int64_t t = (int64_t)nc * kT; t < L; ++t) y[t * g.nheads * H] = __float2bfloat16_rn(0.f);
-        }
+        if (ok && live)
+            for (int64_t t = (int64_t)nc * kT; t + odd < L; t += 2) *reinterpret_cast<uint32_t*>(y + t * row) = 0u;
     } else if (warp < kPWarp0) {
-        more_registers<NV == 2 ? 88 : 120>();
         // ======================= G, k's norms, A and N =======================
-        const int hv = (warp - kNWarp0) >> 2, w = (warp - kNWarp0) & 3;
-        const int tid = w * 32 + lane;
+        // K K^T's blocks (0, 0), (1, 1), (1, 0) on warps 0 to 2, for all heads; warp 3: G and the scalars
+        const int w = warp - kNWarp0;
         const int gid = lane >> 2, tig = lane & 3;
-        NScratch* scr = reinterpret_cast<NScratch*>(smem + p.off_scratch) + hv;
-        const int64_t gbase = b * L * g.nheads + h0 + hv;
-        // warp 0's lanes hold the next chunk's g and beta of tokens 2 lane, 2 lane + 1
-        float gn[2], bn[2];
+        NScratch* scr = reinterpret_cast<NScratch*>(smem + p.off_scratch);
+        const int64_t gbase = b * L * g.nheads + h0;
+        // warp 3's lanes hold the next chunk's g and beta, a token each
+        float gn[NV], bn[NV];
         auto fetch = [&](int c) {
+            const int64_t t = (int64_t)c * kT + lane;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int64_t t = (int64_t)c * kT + 2 * lane + r;
-                gn[r] = t < n ? p.gate[gbase + t * g.nheads] : 0.f;
-                bn[r] = t < n ? p.beta[gbase + t * g.nheads] : 0.f;
+            for (int hv = 0; hv < NV; ++hv) {
+                gn[hv] = t < n ? p.gate[gbase + t * g.nheads + hv] : 0.f;
+                bn[hv] = t < n ? p.beta[gbase + t * g.nheads + hv] : 0.f;
             }
         };
-        if (w == 0 && nc > 0) fetch(0);
+        if (w == 3 && nc > 0) fetch(0);
         int st = 0;
         uint32_t full_phase = 0;
         for (int c = 0; c < nc; ++c) {
             const int buf = c & 1;
-            Scalars* sc = scal_of(buf, hv);
-            // every warp of the head comes to the barrier below, whatever its waits said
-            if (c >= 2) ok = warp_wait(&bars[kBarSFree + buf], ((c >> 1) - 1) & 1, abort_flag);
-            if (w == 0 && ok) {
-                // log2 decays as an integer and a fraction in units of 2^-24, summed apart
-                int gi[2], gf[2];
-                float be[2];
+            // every warp comes to the barrier below, whatever its waits said
+            if (ok && c >= 2) ok = warp_wait<true>(&bars[kBarSFree + buf], ((c >> 1) - 1) & 1, abort_flag);
+            if (w == 3 && ok) {
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
+                for (int hv = 0; hv < NV; ++hv) {
+                    // log2 decays as an integer and a fraction in units of 2^-24, summed apart
                     constexpr float kL = 1.44269502162933349609375f, kLrest = 1.925963033500011e-8f;  // log2 e
-                    const float lim = fminf(fmaxf(gn[r], -112.f), 112.f);  // |log2 decay| < 162
+                    const float lim = fminf(fmaxf(gn[hv], -112.f), 112.f);  // |log2 decay| < 162
                     const float x = lim * kL, rest = fmaf(lim, kL, -x) + lim * kLrest, whole = floorf(x);
-                    gi[r] = (int)whole;
-                    gf[r] = __float2int_rn(((x - whole) + rest) * 16777216.f);
-                    be[r] = gn[r] != gn[r] ? gn[r] : bn[r];  // a NaN decay shows in the token's correction
-                }
-                int si = gi[0] + gi[1], sf = gf[0] + gf[1];
+                    int si = (int)whole, sf = __float2int_rn(((x - whole) + rest) * 16777216.f);
 #pragma unroll
-                for (int m = 1; m < 32; m <<= 1) {
-                    const int oi = __shfl_up_sync(0xffffffffu, si, m), of = __shfl_up_sync(0xffffffffu, sf, m);
-                    if (lane >= m) si += oi, sf += of;
-                }
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int ti = r ? si : si - gi[1], tf = r ? sf : sf - gf[1];
-                    sc->tok[2 * lane + r].gi = (float)(ti + (tf >> 24));
-                    sc->tok[2 * lane + r].gf = (float)(tf & 0xffffff) * 5.9604644775390625e-8f;
-                    sc->tok[2 * lane + r].beta = be[r];
+                    for (int m = 1; m < 32; m <<= 1) {
+                        const int oi = __shfl_up_sync(0xffffffffu, si, m), of = __shfl_up_sync(0xffffffffu, sf, m);
+                        if (lane >= m) si += oi, sf += of;
+                    }
+                    Tok* t = &scal_of(buf, hv)->tok[lane];
+                    t->gi = (float)(si + (sf >> 24));
+                    t->gf = (float)(sf & 0xffffff) * 5.9604644775390625e-8f;
+                    t->beta = gn[hv] != gn[hv] ? gn[hv] : bn[hv];  // a NaN decay shows in the token's correction
                 }
                 if (c + 1 < nc) fetch(c + 1);
             }
-            if (ok) ok = warp_wait(&bars[kBarFull + st], full_phase, abort_flag);
+            if (ok) ok = warp_wait<true>(&bars[kBarFull + st], full_phase, abort_flag);
             uint8_t* sK = smem + st * kStage;
             const uint32_t aK = tc::smem_u32(sK);
             const int64_t left = n - (int64_t)c * kT;
             const int nv = left < kT ? (int)left : kT;
-            // the diagonal block of K K^T, whose diagonal gives the norms: summed by the same
-            // instructions as the rest, so that rk_i rk_j (k_i . k_j) is 1 to rounding where keys agree
-            float acc[2][4];
-            if (ok) {
-                if (nv < kT) {
-                    // past the row's end: K enters the state's product and has to be 0
-                    const int r = 16 * w + (lane >> 1);
-                    if (r >= nv) {
-#pragma unroll
-                        for (int i = 0; i < S / 16; ++i)
-                            *reinterpret_cast<uint4*>(sK + (S == 128 ? (lane & 1) * 2 * kBox + sw(r, i)
-                                                                     : sw(r, 4 * (lane & 1) + i))) =
-                                make_uint4(0, 0, 0, 0);
-                    }
-                    __syncwarp();
-                }
-                score_block<S>(aK, aK, w, w, lane, acc);
-                if (p.l2norm)
-                    diag_norm(acc, lane, p.l2_eps, [&](int i, float f) { sc->tok[16 * w + i].rk = f; });
-                else if (lane < 16)
-                    sc->tok[16 * w + lane].rk = 1.f;
+            if (ok && nv < kT && w < 2) {
+                // past the row's end: K enters the state's product and has to be 0
+                const int r = 16 * w + (lane >> 1);
+                if (r >= nv)
+                    for (int i = 0; i < S / 16; ++i)
+                        *reinterpret_cast<uint4*>(sK + (S == 128 ? (lane & 1) * 2 * kBox + sw(r, i)
+                                                                 : sw(r, 4 * (lane & 1) + i))) = make_uint4(0, 0, 0, 0);
+                __syncwarp();
             }
-            ok = bar_sync_and(1 + hv, 128, ok);
+            // The norms are K K^T's diagonal: summed by the same instructions as the rest, so that
+            // rk_i rk_j (k_i . k_j) is 1 to rounding where keys agree.
+            const int bi = w == 0 ? 0 : 1, bj = w == 1 ? 1 : 0;
+            float acc[2][4];
+            if (ok && w < 3) score_block<S>(aK, aK, bi, bj, lane, acc);
+            if (ok && w < 2) {
+#pragma unroll
+                for (int hv = 0; hv < NV; ++hv) {
+                    Tok* tok = scal_of(buf, hv)->tok + 16 * w;
+                    if (p.l2norm) diag_norm(acc, lane, p.l2_eps, [&](int r, float f) { tok[r].rk = f; });
+                    else if (lane < 16) tok[lane].rk = 1.f;
+                }
+            }
+            ok = bar_sync_and(1, 32 * kNWarps, ok);
             if (!ok) break;
-            if (tid < kT) {
-                const Tok t = sc->tok[tid], last = sc->tok[kT - 1];
-                const float e = ex2(t.gi) * ex2(t.gf);
-                sc->cb[tid] = t.beta;
-                sc->cr[tid] = -t.beta * e * t.rk;
-                sc->gam[tid] = e;
-                sc->d[tid] = ex2(last.gi - t.gi) * ex2(last.gf - t.gf) * t.rk;
-                const float el = decay(t, sc->tok[tid & ~15]);
-                sc->el[tid] = el;
-                sc->ea[tid] = t.beta * t.rk * el;
-                if (tid == kT - 1) sc->g_last = e;
+            if (w == 3) {
+#pragma unroll
+                for (int hv = 0; hv < NV; ++hv) {
+                    Scalars* sc = scal_of(buf, hv);
+                    const Tok t = sc->tok[lane], last = sc->tok[kT - 1];
+                    const float e = ex2(t.gi) * ex2(t.gf);
+                    sc->cb[lane] = t.beta;
+                    sc->cr[lane] = -t.beta * e * t.rk;
+                    sc->gam[lane] = e;
+                    sc->d[lane] = ex2(last.gi - t.gi) * ex2(last.gf - t.gf) * t.rk;
+                    if (lane == kT - 1) sc->g_last = e;
+                }
             }
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bars[kBarSFull + buf]);
-            // A's diagonal block, by columns
-            {
-                const Tok ti0 = sc->tok[16 * w + gid], ti1 = sc->tok[16 * w + gid + 8];
-                const float f0 = ti0.beta * ti0.rk, f1 = ti1.beta * ti1.rk;
-                const bool in0 = 16 * w + gid < nv, in1 = 16 * w + gid + 8 < nv;
-#pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int jj = 8 * nt + 2 * tig + e;
-                        const Tok tj = sc->tok[16 * w + jj];
-                        scr->diag[w][jj][gid] = in0 && jj < gid ? acc[nt][e] * (f0 * tj.rk * decay(ti0, tj)) : 0.f;
-                        scr->diag[w][jj][gid + 8] =
-                            in1 && jj < gid + 8 ? acc[nt][2 + e] * (f1 * tj.rk * decay(ti1, tj)) : 0.f;
-                    }
-            }
-            // and one or two below
+            // A = beta rk rk decay (K K^T); rows past the end: 0, whatever their products are
+            if (w < 3) {
+                const bool in0 = 16 * bi + gid < nv, in1 = 16 * bi + gid + 8 < nv;
 #pragma unroll 1
-            for (int t = w + 4; t < 10; t += 4) {
-                const int i = tri_i(t), j = tri_j(t);
-                score_block<S>(aK, aK, i, j, lane, acc);
-                // (rows past the end: 0, whatever their products are)
-                const float f0 = 16 * i + gid < nv ? sc->ea[16 * i + gid] : 0.f;
-                const float f1 = 16 * i + gid + 8 < nv ? sc->ea[16 * i + gid + 8] : 0.f;
-                const Tok tr = sc->tok[16 * i];
-                float2 (*low)[8] = scr->low[low_block(i, j)];
+                for (int hv = 0; hv < NV; ++hv) {
+                    const Tok* tok = scal_of(buf, hv)->tok;
+                    const Tok ti0 = tok[16 * bi + gid], ti1 = tok[16 * bi + gid + 8], tr = tok[16 * bi];
+                    const float f0 = ti0.beta * ti0.rk, f1 = ti1.beta * ti1.rk;
+                    const float e0 = f0 * decay(ti0, tr), e1 = f1 * decay(ti1, tr);
+                    float(*a)[20] = w < 2 ? scr[hv].diag[w] : scr[hv].low;
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    const int jj = 8 * nt + 2 * tig;
-                    const Tok t0 = sc->tok[16 * j + jj], t1 = sc->tok[16 * j + jj + 1];
-                    const float2 cj = make_float2(t0.rk * decay(tr, t0), t1.rk * decay(tr, t1));
-                    const float2 c0 = tc::mul_f32x2(cj, make_float2(f0, f0)), c1 = tc::mul_f32x2(cj, make_float2(f1, f1));
-                    low[gid][low_at(gid, jj / 2)] = tc::mul_f32x2(c0, make_float2(acc[nt][0], acc[nt][1]));
-                    low[gid + 8][low_at(gid + 8, jj / 2)] = tc::mul_f32x2(c1, make_float2(acc[nt][2], acc[nt][3]));
+                    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const int jj = 8 * nt + 2 * tig + x;
+                            const Tok tj = tok[16 * bj + jj];
+                            float a0, a1;
+                            if (w < 2) {
+                                a0 = in0 && jj < gid ? acc[nt][x] * (f0 * tj.rk * decay(ti0, tj)) : 0.f;
+                                a1 = in1 && jj < gid + 8 ? acc[nt][2 + x] * (f1 * tj.rk * decay(ti1, tj)) : 0.f;
+                            } else {
+                                const float cj = tj.rk * decay(tr, tj);
+                                a0 = in0 ? acc[nt][x] * (e0 * cj) : 0.f;
+                                a1 = in1 ? acc[nt][2 + x] * (e1 * cj) : 0.f;
+                            }
+                            a[jj][gid] = a0;
+                            a[jj][gid + 8] = a1;
+                        }
                 }
             }
             __syncwarp();
-            // the diagonal block of N, a column per lane (both halves of the warp the same)
-            {
+            // N's diagonal blocks, a column per lane; the warp's halves take the two heads (or the same one)
+            if (w < 2) {
                 const int l = lane & 15;
+                float(*a)[20] = scr[NV == 2 ? lane >> 4 : 0].diag[w];
                 float x[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) x[i] = i == l ? 1.f : 0.f;
@@ -859,71 +728,60 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 for (int m = 0; m < 15; ++m) {
 #pragma unroll
                     for (int i4 = (m + 1) / 4; i4 < 4; ++i4) {
-                        const float4 a = *reinterpret_cast<const float4*>(&scr->diag[w][m][4 * i4]);
-                        if (4 * i4 > m) x[4 * i4] = fmaf(-a.x, x[m], x[4 * i4]);
-                        if (4 * i4 + 1 > m) x[4 * i4 + 1] = fmaf(-a.y, x[m], x[4 * i4 + 1]);
-                        if (4 * i4 + 2 > m) x[4 * i4 + 2] = fmaf(-a.z, x[m], x[4 * i4 + 2]);
-                        if (4 * i4 + 3 > m) x[4 * i4 + 3] = fmaf(-a.w, x[m], x[4 * i4 + 3]);
+                        const float4 v = *reinterpret_cast<const float4*>(&a[m][4 * i4]);
+                        if (4 * i4 > m) x[4 * i4] = fmaf(-v.x, x[m], x[4 * i4]);
+                        if (4 * i4 + 1 > m) x[4 * i4 + 1] = fmaf(-v.y, x[m], x[4 * i4 + 1]);
+                        if (4 * i4 + 2 > m) x[4 * i4 + 2] = fmaf(-v.z, x[m], x[4 * i4 + 2]);
+                        if (4 * i4 + 3 > m) x[4 * i4 + 3] = fmaf(-v.w, x[m], x[4 * i4 + 3]);
                     }
                 }
                 __syncwarp();
-                if (lane < 16) {
+                if (NV == 2 || lane < 16)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) scr->diag[w][i][l] = x[i];
-                }
+                    for (int i = 0; i < 16; i += 4)
+                        *reinterpret_cast<float4*>(&a[l][i]) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
             }
-            bar_sync(1 + hv, 128);
-            // N's block column w, transposed: N_ij^T = -(sum_m N_mj^T A_im^T) N_ii^T, as accumulator
-            // fragments nf[d] (i = w + d), which are also left operands
-            {
-                float nf[4][2][4];
+            bar_sync(1, 32 * kNWarps);
+            // the last chunk's N has been used (no barrier follows before the next chunk's: the warps may part)
+            if (c > 0) ok = warp_wait<true>(&bars[kBarWDone], (c - 1) & 1, abort_flag);
+            // N_10 = -N_11 A_10 N_00 and all of N into its planes, eight columns (of a head's half) to a
+            // warp, four lanes to a column, four rows each
+            if (ok && w < 2 * NV) {
+                const int hv = w >> 1, col = 8 * (w & 1) + (lane >> 2), r4 = lane & 3;
+                const NScratch& m = scr[hv];
+                float x[16];
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    const int r = 8 * nt + 2 * tig;
-                    nf[0][nt][0] = scr->diag[w][r][gid];
-                    nf[0][nt][1] = scr->diag[w][r + 1][gid];
-                    nf[0][nt][2] = scr->diag[w][r][gid + 8];
-                    nf[0][nt][3] = scr->diag[w][r + 1][gid + 8];
+                for (int i = 0; i < 16; i += 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(&m.diag[0][col][i]);
+                    x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
                 }
+                float2 o[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                block_times(o, x, [&](int k) { return *reinterpret_cast<const float4*>(&m.low[k][4 * r4]); });
+                gather(x, o, lane);
+                o[0] = o[1] = make_float2(0.f, 0.f);
+                block_times(o, x, [&](int k) { return *reinterpret_cast<const float4*>(&m.diag[1][k][4 * r4]); });
+                const uint32_t at = p.off_n + hv * kNPlanes * kPlane + 2 * (col & 7);
 #pragma unroll
-                for (int d = 1; d < 4; ++d) {
-                    if (w + d > 3) break;
-                    const int i = w + d;
-                    float x[2][4] = {};
-#pragma unroll
-                    for (int m = 0; m < d; ++m) {
-                        const float2 (*low)[8] = scr->low[low_block(i, w + m)];
-                        mma_block(x, nf[m], gid, tig, [&](int r, int c2) { return low[r][low_at(r, c2)]; });
+                for (int blk = 0; blk < 3; ++blk) {  // (0, 0), (1, 1), (1, 0)
+                    const int row = (blk ? 16 : 0) + 4 * r4, ch = (blk == 1 ? 2 : 0) + (col >> 3);
+                    float2 v[2];
+                    if (blk < 2) {
+                        const float4 f = *reinterpret_cast<const float4*>(&m.diag[blk][col][4 * r4]);
+                        v[0] = make_float2(f.x, f.y);
+                        v[1] = make_float2(f.z, f.w);
+                    } else {
+                        v[0] = make_float2(-o[0].x, -o[0].y);
+                        v[1] = make_float2(-o[1].x, -o[1].y);
                     }
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt)
+                    for (int pl = 0; pl < (int)kNPlanes; ++pl)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) x[nt][e] = -x[nt][e], nf[d][nt][e] = 0.f;
-                    mma_block(nf[d], x, gid, tig, [&](int r, int c2) {
-                        return *reinterpret_cast<const float2*>(&scr->diag[i][r][2 * c2]);
-                    });
-                }
-                // the last chunk's N has been used
-                if (c > 0) ok = warp_wait(&bars[kBarWDone], (c - 1) & 1, abort_flag);
-                const uint32_t tr = (lane & 7) + ((lane >> 4) << 3), tch = (lane >> 3) & 1;
-                const uint32_t aN = tc::smem_u32(n_of(hv));
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    if (w + d > 3 || !ok) break;
-                    const uint32_t at = aN + sw(16 * (w + d) + tr, 2 * w + tch);
-#pragma unroll
-                    for (int pl = 0; pl < (int)kNPlanes; ++pl) {
-                        uint32_t r[4];
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            float* v = &nf[d][x >> 1][2 * (x & 1)];
-                            float2 f = make_float2(v[0], v[1]);
-                            r[x] = high(f);
-                            v[0] = f.x;
-                            v[1] = f.y;
+                        for (int r = 0; r < 2; ++r) {
+                            const uint32_t two = high(v[r]);
+                            uint8_t* to = smem + at + pl * kPlane;
+                            *reinterpret_cast<uint16_t*>(to + sw(row + 2 * r, ch)) = (uint16_t)two;
+                            *reinterpret_cast<uint16_t*>(to + sw(row + 2 * r + 1, ch)) = (uint16_t)(two >> 16);
                         }
-                        stsm4_trans(at + pl * kPlane, r);
-                    }
                 }
             }
             tc::fence_proxy_async_smem();
@@ -935,52 +793,54 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
         }
         if (!ok) set_abort(ctl, p.status);
-    } else if (warp < kPWarp0 + kPWarps) {
-        fewer_registers<NV == 2 ? 56 : 64>();
+    } else if (warp < kTmaWarp) {
         // ========================= q's norms and P =========================
+        // Q K^T's blocks (0, 0), (1, 1), (1, 0) on warps 0 to 2, for all heads; warp 3: Q Q^T's diagonal
         const int w = warp - kPWarp0;
         const int gid = lane >> 2, tig = lane & 3;
         int st = 0;
         uint32_t full_phase = 0;
         for (int c = 0; c < nc; ++c) {
             const int buf = c & 1;
-            ok = warp_wait(&bars[kBarFull + st], full_phase, abort_flag) &&
-                 warp_wait(&bars[kBarSFull + buf], (c >> 1) & 1, abort_flag);
+            ok = warp_wait<true>(&bars[kBarFull + st], full_phase, abort_flag) &&
+                 warp_wait<true>(&bars[kBarSFull + buf], (c >> 1) & 1, abort_flag);
+            if (!ok) break;
             const uint32_t aK = tc::smem_u32(smem + st * kStage), aQ = aK + kBox;
-            float acc[2][4];
-            if (ok && p.l2norm) {
-                // 1 / norm into oq's place
-                score_block<S>(aQ, aQ, w, w, lane, acc);
-                diag_norm(acc, lane, p.l2_eps, [&](int i, float f) { scal_of(buf, 0)->oq[16 * w + i] = f; });
-                __syncwarp();
-            }
-            if (ok && lane < 16) {  // a row per lane
-                const int i = 16 * w + lane;
-                const float oq = p.l2norm ? p.scale * scal_of(buf, 0)->oq[i] : p.scale;
-#pragma unroll
-                for (int hv = 0; hv < NV; ++hv) scal_of(buf, hv)->oq[i] = oq;
-            }
+            if (w == 3) {
 #pragma unroll 1
-            for (int t = w; t < 10; t += 4) {
-                const int i = tri_i(t), j = tri_j(t), i0 = 16 * i + gid;
-                if (ok) score_block<S>(aQ, aK, i, j, lane, acc);
-                // the last chunk's P has been used
-                if (ok && t < 4 && c > 0) ok = warp_wait(&bars[kBarPFree], (c - 1) & 1, abort_flag);
-                if (!ok) break;
+                for (int i = 0; i < 2; ++i) {
+                    if (p.l2norm) {
+                        float acc[2][4];
+                        score_block<S>(aQ, aQ, i, i, lane, acc);
+                        diag_norm(acc, lane, p.l2_eps, [&](int r, float f) {
 #pragma unroll
+                            for (int hv = 0; hv < NV; ++hv) scal_of(buf, hv)->oq[16 * i + r] = p.scale * f;
+                        });
+                    } else if (lane < 16) {
+#pragma unroll
+                        for (int hv = 0; hv < NV; ++hv) scal_of(buf, hv)->oq[16 * i + lane] = p.scale;
+                    }
+                }
+            } else {
+                const int bi = w == 0 ? 0 : 1, bj = w == 1 ? 1 : 0, i0 = 16 * bi + gid;
+                float acc[2][4];
+                score_block<S>(aQ, aK, bi, bj, lane, acc);
+                // the last chunk's P has been used
+                if (c > 0) ok = warp_wait<true>(&bars[kBarPFree], (c - 1) & 1, abort_flag);
+                if (!ok) break;
+#pragma unroll 1
                 for (int hv = 0; hv < NV; ++hv) {
-                    const Scalars* sc = scal_of(buf, hv);
+                    const Tok* tok = scal_of(buf, hv)->tok;
                     uint8_t* sP = p_of(hv);
-                    // (the diagonal block takes its decays exactly)
-                    const bool below = i > j;
-                    const Tok tr = sc->tok[16 * i], ti0 = sc->tok[i0], ti1 = sc->tok[i0 + 8];
-                    const float f0 = sc->el[i0], f1 = sc->el[i0 + 8];
+                    // (the diagonal blocks take their decays exactly)
+                    const Tok tr = tok[16 * bi], ti0 = tok[i0], ti1 = tok[i0 + 8];
+                    const float f0 = decay(ti0, tr), f1 = decay(ti1, tr);
 #pragma unroll
                     for (int nt = 0; nt < 2; ++nt) {
-                        const int j0 = 16 * j + 8 * nt + 2 * tig;
-                        const Tok t0 = sc->tok[j0], t1 = sc->tok[j0 + 1];
+                        const int j0 = 16 * bj + 8 * nt + 2 * tig;
+                        const Tok t0 = tok[j0], t1 = tok[j0 + 1];
                         float2 c0, c1;
-                        if (below) {
+                        if (w == 2) {
                             const float2 cj = make_float2(t0.rk * decay(tr, t0), t1.rk * decay(tr, t1));
                             c0 = tc::mul_f32x2(cj, make_float2(f0, f0));
                             c1 = tc::mul_f32x2(cj, make_float2(f1, f1));
@@ -990,11 +850,11 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                         }
                         float2 a0 = tc::mul_f32x2(c0, make_float2(acc[nt][0], acc[nt][1]));
                         float2 a1 = tc::mul_f32x2(c1, make_float2(acc[nt][2], acc[nt][3]));
-                        if (!below) {
+                        if (w != 2) {
                             a0 = make_float2(j0 <= i0 ? a0.x : 0.f, j0 + 1 <= i0 ? a0.y : 0.f);
                             a1 = make_float2(j0 <= i0 + 8 ? a1.x : 0.f, j0 + 1 <= i0 + 8 ? a1.y : 0.f);
                         }
-                        const uint32_t o0 = sw(i0, 2 * j + nt) + 4 * tig;
+                        const uint32_t o0 = sw(i0, 2 * bj + nt) + 4 * tig;
                         uint32_t hi, lo;
                         split2(a0, hi, lo);
                         *reinterpret_cast<uint32_t*>(sP + o0) = hi;
@@ -1005,7 +865,6 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     }
                 }
             }
-            if (!ok) break;
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -1019,31 +878,24 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         }
         if (!ok) set_abort(ctl, p.status);
     } else {
-        fewer_registers<48>();
         if (warp == kTmaWarp) {
             // ============================ TMA producer ============================
             if (lane == 0) {
                 tc::tma_prefetch_desc(&tm_q);
                 tc::tma_prefetch_desc(&tm_k);
-                tc::tma_prefetch_desc(&tm_v);
-                tc::tma_prefetch_desc(&tm_y);
                 int fills[kMaxStages] = {};
                 int st = 0;
                 uint32_t free_phase = 1;
                 for (int c = 0; c < nc; ++c) {
-                    if (c >= p.nst && !tc::mbar_wait(&bars[kBarFree + st], free_phase, abort_flag)) { ok = false; break; }
+                    if (c >= p.nst && !thread_wait<true>(&bars[kBarFree + st], free_phase, abort_flag)) { ok = false; break; }
                     uint8_t* s = smem + st * kStage;
                     uint64_t* full = &bars[kBarFull + st];
                     tc::mbar_arrive_expect_tx(full, kStage);
-    #pragma unroll
+#pragma unroll
                     for (int x = 0; x < kBoxes; ++x) {
                         tc::tma_load_4d(s + 2 * x * kBox, &tm_k, full, 64 * x, grp, c * kT, (int)b);
                         tc::tma_load_4d(s + (2 * x + 1) * kBox, &tm_q, full, 64 * x, grp, c * kT, (int)b);
                     }
-    #pragma unroll
-                    for (int x = 0; x < kVBoxes; ++x)
-                        tc::tma_load_4d(s + kOffV + x * kBox, &tm_v, full, NV == 2 ? 0 : 64 * x, NV == 2 ? h0 + x : h0,
-                                        c * kT, (int)b);
                     ++fills[st];
                     if (++st == p.nst) {
                         st = 0;
@@ -1056,12 +908,43 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 for (int i = 0; i < kMaxStages; ++i)
                     if (fills[i] > 0) (void)tc::mbar_wait(&bars[kBarFull + i], (fills[i] - 1) & 1, never);
             }
+        } else if (warp == kVWarp) {
+            // ========================= TMA producer of V =========================
+            if (lane == 0) {
+                tc::tma_prefetch_desc(&tm_v);
+                int fills[kMaxVStages] = {};
+                int vs = 0;
+                uint32_t free_phase = 1;
+                for (int c = 0; c < nc; ++c) {
+                    if (c >= p.nvst && !thread_wait<true>(&bars[kBarVFree + vs], free_phase, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    uint64_t* full = &bars[kBarVFull + vs];
+                    tc::mbar_arrive_expect_tx(full, kVStage);
+#pragma unroll
+                    for (int x = 0; x < kVBoxes; ++x)
+                        tc::tma_load_4d(smem + p.off_v + vs * kVStage + x * kBox, &tm_v, full, NV == 2 ? 0 : 64 * x,
+                                        NV == 2 ? h0 + x : h0, c * kT, (int)b);
+                    ++fills[vs];
+                    if (++vs == p.nvst) {
+                        vs = 0;
+                        free_phase ^= 1u;
+                    }
+                }
+                if (!ok) set_abort(ctl, p.status);
+#pragma unroll
+                for (int i = 0; i < kMaxVStages; ++i)
+                    if (fills[i] > 0) (void)tc::mbar_wait(&bars[kBarVFull + i], (fills[i] - 1) & 1, never);
+            }
         } else if (warp == kMmaWarp) {
             // ============================= MMA issuer =============================
             if (lane == 0 && nc > 0) {
                 constexpr uint32_t id_t = tc::idesc_bf16(128, kT, false, false);       // N = tokens
                 constexpr uint32_t id_rq = tc::idesc_bf16(128, 2 * kT, false, false);  // of K and of Q
-                constexpr uint32_t id_s = tc::idesc_bf16(128, S, false, true);    // N = state rows
+                constexpr uint32_t id_s = tc::idesc_bf16(128, S, false, true);         // N = state rows
+                const uint64_t dN = tc::sdesc_sw128(tc::smem_u32(smem + p.off_n), 16, 1024);
+                const uint64_t dP = tc::sdesc_sw128(tc::smem_u32(smem + p.off_p), 16, 1024);
                 int st = 0;
                 uint32_t full_phase = 0;
                 for (int c = 0; c < nc; ++c) {
@@ -1070,71 +953,65 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     const uint32_t aK = tc::smem_u32(smem + st * kStage);
                     const uint64_t dK = tc::sdesc_sw128(aK, 16, 1024);
                     const uint64_t dKt = tc::sdesc_sw128(aK, 2 * kBox, 1024);
-                    if (!tc::mbar_wait(&bars[kBarFull + st], full_phase, abort_flag)) { ok = false; break; }
-                    if (!tc::mbar_wait(&bars[kBarSFull + buf], (c >> 1) & 1, abort_flag)) { ok = false; break; }
-                    if (!tc::mbar_wait(&bars[kBarHReady], ph, abort_flag)) { ok = false; break; }
-                    tc::tc_fence_after();
+                    if (!thread_wait<false>(&bars[kBarFull + st], full_phase, abort_flag)) { ok = false; break; }
+                    // (with the scalars K's rows past the end are cleared)
+                    if (!thread_wait<false>(&bars[kBarSFull + buf], (c >> 1) & 1, abort_flag)) { ok = false; break; }
+                    if (!thread_wait<false>(&bars[kBarHReady], ph, abort_flag)) { ok = false; break; }
                     // R | Q h from h's high part, once y's sum of the chunk before has been read; R from its low part
-                    if (c > 0 && !tc::mbar_wait(&bars[kBarO2Read], ph ^ 1, abort_flag)) { ok = false; break; }
+                    if (c > 0 && !thread_wait<false>(&bars[kBarO2Read], ph ^ 1, abort_flag)) { ok = false; break; }
                     tc::tc_fence_after();
+#pragma unroll 1
+                    for (int x = 0; x < 2 * kBoxes; ++x) {
+                        const uint32_t id = x < kBoxes ? id_rq : id_t, box = x < kBoxes ? x : x - kBoxes;
+                        const uint64_t d = dK + box * (2 * kBox >> 4);
 #pragma unroll
-                    for (int ks = 0; ks < S / 16; ++ks)
-                        tc::mma_bf16_ts(tmem + cR, tmem + cHi + 8 * ks,
-                                        dK + (((ks >> 2) * 2 * kBox + (ks & 3) * 32) >> 4), id_rq, ks > 0);
-#pragma unroll
-                    for (int ks = 0; ks < S / 16; ++ks)
-                        tc::mma_bf16_ts(tmem + cR, tmem + cLo + 8 * ks,
-                                        dK + (((ks >> 2) * 2 * kBox + (ks & 3) * 32) >> 4), id_t, 1);
+                        for (int ks = 0; ks < 4; ++ks)
+                            tc::mma_bf16_ts(tmem + cR, tmem + cHi + 32 * x + 8 * ks, d + 2 * ks, id, x > 0 || ks > 0);
+                    }
                     tc::mma_commit(&bars[kBarRDone]);
-                    // W = N X, N's parts times X's down to 2^-16 of hi hi; block column kb of N only has rows from its
-                    // own block on
-                    if (!tc::mbar_wait(&bars[kBarNFull], ph, abort_flag)) { ok = false; break; }
-                    if (!tc::mbar_wait(&bars[kBarXReady], ph, abort_flag)) { ok = false; break; }
+                    // W = N X, N's parts times X's down to 2^-16 of hi hi; N's second block column only has
+                    // rows from 16 on
+                    if (!thread_wait<false>(&bars[kBarNFull], ph, abort_flag)) { ok = false; break; }
+                    if (!thread_wait<false>(&bars[kBarXReady], ph, abort_flag)) { ok = false; break; }
                     tc::tc_fence_after();
-    #pragma unroll
-                    for (int hv = 0; hv < NV; ++hv) {
-                        const uint32_t x = tmem + (hv ? cU : cX);
-                        const uint64_t dN = tc::sdesc_sw128(tc::smem_u32(n_of(hv)), 16, 1024);
-    #pragma unroll
-                        for (int kb = 0; kb < 4; ++kb) {
-                            const uint32_t d = tmem + cR + 16 * kb, id = tc::idesc_bf16(128, kT - 16 * kb, false, false);
-                            const uint64_t at = dN + (2048 >> 4) * kb + 2 * kb;
-                            tc::mma_bf16_ts(d, x + 8 * kb, at, id, hv > 0 || kb > 0);
-                            tc::mma_bf16_ts(d, x + 8 * kb, at + (kPlane >> 4), id, 1);
-                            tc::mma_bf16_ts(d, x + 8 * kb, at + 2 * (kPlane >> 4), id, 1);
-                            tc::mma_bf16_ts(d, x + 32 + 8 * kb, at, id, 1);
-                            tc::mma_bf16_ts(d, x + 32 + 8 * kb, at + (kPlane >> 4), id, 1);
-                            tc::mma_bf16_ts(d, x + 64 + 8 * kb, at, id, 1);
-                        }
+#pragma unroll 1
+                    for (int x = 0; x < 2 * NV; ++x) {
+                        const int kb = x & 1, hv = x >> 1;
+                        const uint32_t a = tmem + cX + 8 * kb, d = tmem + (hv ? cR2 : cR) + 16 * kb;
+                        const uint32_t id = id_t - (static_cast<uint32_t>(2 * kb) << 17);  // N = 32 - 16 kb
+                        const uint64_t at = dN + hv * (kNPlanes * kPlane >> 4) + ((2048 >> 4) + 2) * kb;
+                        tc::mma_bf16_ts(d, a, at, id, kb);
+                        tc::mma_bf16_ts(d, a, at + (kPlane >> 4), id, 1);
+                        tc::mma_bf16_ts(d, a, at + 2 * (kPlane >> 4), id, 1);
+                        tc::mma_bf16_ts(d, a + 16, at, id, 1);
+                        tc::mma_bf16_ts(d, a + 16, at + (kPlane >> 4), id, 1);
+                        tc::mma_bf16_ts(d, a + 32, at, id, 1);
                     }
                     tc::mma_commit(&bars[kBarWDone]);
                     // h += K^T W
-                    if (!tc::mbar_wait(&bars[kBarWReady], ph, abort_flag)) { ok = false; break; }
+                    if (!thread_wait<false>(&bars[kBarWReady], ph, abort_flag)) { ok = false; break; }
                     tc::tc_fence_after();
-    #pragma unroll
-                    for (int kt = 0; kt < 4; ++kt) {
-                        tc::mma_bf16_ts(tmem + cH, tmem + cU + 8 * kt, dKt + 128 * kt, id_s, 1);
-                        tc::mma_bf16_ts(tmem + cH, tmem + cU + 32 + 8 * kt, dKt + 128 * kt, id_s, 1);
-                        tc::mma_bf16_ts(tmem + cH, tmem + cU + 64 + 8 * kt, dKt + 128 * kt, id_s, 1);
+#pragma unroll 1
+                    for (int kt = 0; kt < 2; ++kt) {
+#pragma unroll
+                        for (int part = 0; part < 3; ++part)
+                            tc::mma_bf16_ts(tmem + cH, tmem + cU + 16 * part + 8 * kt, dKt + 128 * kt, id_s, 1);
                     }
                     tc::mma_commit(&bars[kBarHDone]);
                     // P W onto the scaled Q h: hi hi + hi lo + lo hi
-                    if (!tc::mbar_wait(&bars[kBarPFull], ph, abort_flag)) { ok = false; break; }
-                    if (!tc::mbar_wait(&bars[kBarWyReady], ph, abort_flag)) { ok = false; break; }
-                    if (!tc::mbar_wait(&bars[kBarO1Read], ph, abort_flag)) { ok = false; break; }
+                    if (!thread_wait<false>(&bars[kBarPFull], ph, abort_flag)) { ok = false; break; }
+                    if (!thread_wait<false>(&bars[kBarWyReady], ph, abort_flag)) { ok = false; break; }
+                    if (!thread_wait<false>(&bars[kBarO1Read], ph, abort_flag)) { ok = false; break; }
                     tc::tc_fence_after();
-    #pragma unroll
-                    for (int hv = 0; hv < NV; ++hv) {
-                        const uint32_t wp = tmem + (hv ? cW2 : cX);
-                        const uint64_t dP = tc::sdesc_sw128(tc::smem_u32(p_of(hv)), 16, 1024);
-    #pragma unroll
-                        for (int kb = 0; kb < 4; ++kb) {
-                            const uint32_t d = tmem + cO + 16 * kb, id = tc::idesc_bf16(128, kT - 16 * kb, false, false);
-                            const uint64_t at = dP + (2048 >> 4) * kb + 2 * kb;
-                            tc::mma_bf16_ts(d, wp + 8 * kb, at, id, 1);
-                            tc::mma_bf16_ts(d, wp + 8 * kb, at + (kPlane >> 4), id, 1);
-                            tc::mma_bf16_ts(d, wp + 32 + 8 * kb, at, id, 1);
-                        }
+#pragma unroll 1
+                    for (int x = 0; x < 2 * NV; ++x) {
+                        const int kb = x & 1, hv = x >> 1;
+                        const uint32_t a = tmem + cW + 8 * kb, d = tmem + (hv ? cO2 : cO) + 16 * kb;
+                        const uint32_t id = id_t - (static_cast<uint32_t>(2 * kb) << 17);
+                        const uint64_t at = dP + hv * (kPPlanes * kPlane >> 4) + ((2048 >> 4) + 2) * kb;
+                        tc::mma_bf16_ts(d, a, at, id, 1);
+                        tc::mma_bf16_ts(d, a, at + (kPlane >> 4), id, 1);
+                        tc::mma_bf16_ts(d, a + 16, at, id, 1);
                     }
                     tc::mma_commit(&bars[kBarO2Done]);
                     tc::mma_commit(&bars[kBarSFree + buf]);
@@ -1179,22 +1056,21 @@ cudaError_t launch_k(const GdrArgs& a, cudaStream_t st) {
     p.scale = a.scale;
     p.l2_eps = a.l2_eps;
     p.l2norm = a.l2norm;
-    constexpr uint32_t stage = (2 * (S / 64) + NV * H / 64) * kBox;
-    constexpr uint32_t scratch = NV * (uint32_t)sizeof(NScratch);
-    constexpr uint32_t rest =
-        NV * ((kNPlanes + kPPlanes) * kPlane + H / 64 * kBox + 2 * kScalBytes) + scratch + kNumBars * 8 + (uint32_t)sizeof(SharedCtl) + 1024;
-    constexpr int fit = (kSmemLimit - (int)rest) / (int)stage;
-    static_assert(fit >= 2, "two stages at least");
-    p.nst = fit < kMaxStages ? fit : kMaxStages;
-    p.off_n = p.nst * stage;
+    constexpr uint32_t stage = 2 * (S / 64) * kBox, vstage = NV * H / 64 * kBox;
+    constexpr uint32_t rest = kMaxVStages * vstage + NV * ((kNPlanes + kPPlanes) * kPlane + 2 * kScalBytes) +
+                              NV * (uint32_t)sizeof(NScratch) + kNumBars * 8 + (uint32_t)sizeof(SharedCtl) + 1024;
+    static_assert(kMaxStages * stage + rest <= (uint32_t)kSmemLimit, "shared memory");
+    p.nst = kMaxStages;
+    p.nvst = kMaxVStages;
+    p.off_v = kMaxStages * stage;
+    p.off_n = p.off_v + kMaxVStages * vstage;
     p.off_p = p.off_n + NV * kNPlanes * kPlane;
-    p.off_y = p.off_p + NV * kPPlanes * kPlane;
-    p.off_scal = p.off_y + NV * H / 64 * kBox;
+    p.off_scal = p.off_p + NV * kPPlanes * kPlane;
     p.off_scratch = p.off_scal + 2 * NV * kScalBytes;
-    p.off_bar = p.off_scratch + scratch;
-    const int smem = (int)(p.nst * stage + rest);
+    p.off_bar = p.off_scratch + NV * (uint32_t)sizeof(NScratch);
+    const int smem = (int)(kMaxStages * stage + rest);
 
-    CUtensorMap tm_q, tm_k, tm_v, tm_y;
+    CUtensorMap tm_q, tm_k, tm_v;
     const uint64_t L = g.seqlen, B = g.batch;
     const uint32_t box[4] = {64, 1, kT, 1};
     auto map = [&](CUtensorMap* m, const void* base, uint64_t width, uint64_t count, uint64_t stride) {
@@ -1203,11 +1079,11 @@ cudaError_t launch_k(const GdrArgs& a, cudaStream_t st) {
         return make_tmap_bf16(m, base, 4, dims, strides, box);
     };
     if (!map(&tm_q, a.q, S, g.ngroups, a.q_stride) || !map(&tm_k, a.k, S, g.ngroups, a.k_stride) ||
-        !map(&tm_v, a.v, H, g.nheads, a.v_stride) || !map(&tm_y, a.y, H, g.nheads, (uint64_t)(g.nheads * H)))
+        !map(&tm_v, a.v, H, g.nheads, a.v_stride))
         return cudaErrorInvalidValue;
     const cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(k_gdr_chunk_tc<S, H, NV>), smem);
     if (e != cudaSuccess) return e;
-    k_gdr_chunk_tc<S, H, NV><<<dim3((unsigned)(g.nheads / NV), (unsigned)g.batch), threads_of(NV), smem, st>>>(tm_q, tm_k, tm_v, tm_y, p);
+    k_gdr_chunk_tc<S, H, NV><<<dim3((unsigned)(g.nheads / NV), (unsigned)g.batch), kThreads, smem, st>>>(tm_q, tm_k, tm_v, p);
     return cudaGetLastError();
 }
 
