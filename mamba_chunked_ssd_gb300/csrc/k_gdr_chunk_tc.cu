@@ -26,10 +26,12 @@
 //                its parts (four per TMEM lane quadrant, a quarter of the columns
 //                each)
 //   warps 16-19  output: y from Q h and P W
-//   warps 20-23  G, k's norms, A and N of the next chunk, while the chain runs on
-//                this one
-//   warps 24-27  q's norms and P
-//   warps 28-30  TMA producer of K and Q; tcgen05.mma issuer; TMA producer of V
+//   warps 20-23  G, k's norms, A and N's diagonal blocks of the next chunks, while the
+//                chain runs on this one
+//   warps 24-27  the rest of N, q's norms and P
+//   warps 28-31  TMA producer of K and Q; TMA producer of V; issuers of the chain's
+//                products and of P W (a product takes its issuer 46 cycles or more
+//                however small it is, so P W would hold up the chain's)
 // What bounds it is the chain from state to state: three dependent products and
 // three conversions a chunk.  What enters the fp32 state is as good as fp32: N, X
 // and W take part in its products as three bf16 parts each (24 bits), h in the
@@ -64,8 +66,8 @@ namespace {
 
 constexpr int kT = 32;  // tokens per chunk
 constexpr int kChainWarps = 16, kOutWarps = 4, kNWarp0 = 20, kNWarps = 4, kPWarp0 = 24, kPWarps = 4;
-constexpr int kTmaWarp = 28, kMmaWarp = 29, kVWarp = 30;
-constexpr int kThreads = 31 * 32;    // 64 registers each
+constexpr int kTmaWarp = 28, kVWarp = 29, kMmaWarp = 30, kPwWarp = 31;
+constexpr int kThreads = 32 * 32;    // 64 registers each
 constexpr uint32_t kBox = kT * 128;  // one box: the chunk's tokens x 64 columns of bf16
 constexpr int kMaxStages = 6, kMaxVStages = 4;
 constexpr int kSmemLimit = 232448;
@@ -96,9 +98,10 @@ constexpr uint32_t kNPlanes = 3, kPPlanes = 2;
 constexpr uint32_t kScalBytes = sizeof(Scalars);
 static_assert(kScalBytes % 16 == 0, "scalars");
 
-struct NScratch {           // one head's, in fp32
+struct NScratch {           // one head's, per chunk, in fp32
     float diag[2][16][20];  // A's diagonal blocks, then N's, a column in a row
     float low[16][20];      // A's block (1, 0), a column in a row
+    float4 fac[3][2][32];   // rk_j e^{G_i - G_j} of the blocks, as the mma's threads hold them: A's and P's factors
 };
 
 enum : int {
@@ -107,22 +110,18 @@ enum : int {
     kBarVFull = kBarFree + kMaxStages,    // [V stages]
     kBarVFree = kBarVFull + kMaxVStages,  // [V stages]
     kBarSFull = kBarVFree + kMaxVStages,  // [2] scalars but oq (and K's rows past the end cleared)
-    kBarSFree = kBarSFull + 2,            // [2]
-    kBarNFull = kBarSFree + 2,            // N; free again with kBarWDone
-    kBarPFull,                            // P and oq
-    kBarPFree,
-    kBarHReady,  // h's parts are written
-    kBarRDone,   // R and Q h
-    kBarXReady,  // and h is decayed
+    kBarSFree = kBarSFull + 2,            // [2] scalars and scratch
+    kBarDFull = kBarSFree + 2,            // [2] scratch: A's block and N's diagonal blocks, factors
+    kBarHReady = kBarDFull + 2,           // h's parts are written; y's sum of the chunk before has been read
+    kBarRDone,                            // R and Q h
+    kBarXReady,                           // X's parts and N are written, h is decayed
     kBarWDone,
-    kBarWReady,   // W's parts for the state
-    kBarWyReady,  // and for y
+    kBarWReady,  // W's parts for the state
     kBarHDone,
-    kBarO1Read,
-    kBarO2Done,  // P W
-    kBarO2Read,
-    kBarDrain,
-    kNumBars
+    kBarPReady,  // P, oq and W's parts for y are written, Q h is scaled
+    kBarPDone,   // P W
+    kBarDrain,  // [2] issuers
+    kNumBars = kBarDrain + 2
 };
 
 struct SharedCtl {
@@ -151,11 +150,8 @@ __device__ __forceinline__ void set_abort(SharedCtl* ctl, unsigned int* status) 
     if (status) atomicExch(status, kStatusTimeout);
 }
 
-__device__ __forceinline__ void bar_sync(int id, int threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
-// bar_sync that also tells every thread whether all of them came with `ok`.
+// A barrier of `threads` threads that also tells each whether all of them came
+// with `ok`.
 __device__ __forceinline__ bool bar_sync_and(int id, int threads, bool ok) {
     uint32_t r;
     asm volatile(
@@ -346,11 +342,14 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     auto scal_of = [&](int buf, int hv) -> Scalars* {
         return reinterpret_cast<Scalars*>(smem + p.off_scal + (buf * NV + hv) * kScalBytes);
     };
+    auto scratch_of = [&](int buf, int hv) -> NScratch* {
+        return reinterpret_cast<NScratch*>(smem + p.off_scratch) + buf * NV + hv;
+    };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
             tc::mbar_init(&bars[kBarFull + i], 1);
-            tc::mbar_init(&bars[kBarFree + i], 1);
+            tc::mbar_init(&bars[kBarFree + i], 1 + kPWarps);
         }
         for (int i = 0; i < kMaxVStages; ++i) {
             tc::mbar_init(&bars[kBarVFull + i], 1);
@@ -359,21 +358,17 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&bars[kBarSFull + i], kNWarps);
             tc::mbar_init(&bars[kBarSFree + i], 1 + kOutWarps + kPWarps);
+            tc::mbar_init(&bars[kBarDFull + i], kNWarps);
+            tc::mbar_init(&bars[kBarDrain + i], 1);
         }
-        tc::mbar_init(&bars[kBarNFull], kNWarps);
-        tc::mbar_init(&bars[kBarPFull], kPWarps);
-        tc::mbar_init(&bars[kBarPFree], 1);
-        tc::mbar_init(&bars[kBarHReady], kChainWarps);
+        tc::mbar_init(&bars[kBarHReady], kChainWarps + kOutWarps);
         tc::mbar_init(&bars[kBarRDone], 1);
-        tc::mbar_init(&bars[kBarXReady], kChainWarps);
+        tc::mbar_init(&bars[kBarXReady], kChainWarps + kPWarps);
         tc::mbar_init(&bars[kBarWDone], 1);
         tc::mbar_init(&bars[kBarWReady], kChainWarps);
-        tc::mbar_init(&bars[kBarWyReady], kChainWarps);
         tc::mbar_init(&bars[kBarHDone], 1);
-        tc::mbar_init(&bars[kBarO1Read], kOutWarps);
-        tc::mbar_init(&bars[kBarO2Done], 1);
-        tc::mbar_init(&bars[kBarO2Read], kOutWarps);
-        tc::mbar_init(&bars[kBarDrain], 1);
+        tc::mbar_init(&bars[kBarPReady], kChainWarps + kOutWarps + kPWarps);
+        tc::mbar_init(&bars[kBarPDone], 1);
         ctl->abort = 0;
         ctl->never = 0;
         tc::fence_barrier_init();
@@ -418,6 +413,8 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             const int buf = c & 1;
             const uint32_t ph = c & 1;
             const Scalars* sc = scal_of(buf, hv);
+            if (!warp_wait(&bars[kBarSFull + buf], (c >> 1) & 1, abort_flag)) { ok = false; break; }
+            const float g_last = sc->g_last;
             if (c > 0 && !warp_wait(&bars[kBarHDone], ph ^ 1, abort_flag)) { ok = false; break; }
             tc::tc_fence_after();
             // h's parts
@@ -435,8 +432,6 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bars[kBarHReady]);
             // while R = K h runs: h decayed to the chunk's end, and V
-            if (!warp_wait(&bars[kBarSFull + buf], (c >> 1) & 1, abort_flag)) { ok = false; break; }
-            const float g_last = sc->g_last;
 #pragma unroll 1
             for (int s = s0; s < s0 + S / 4; s += 16) {
                 uint32_t r[16];
@@ -511,7 +506,7 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 tc::tmem_wait_st();
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bars[kBarWyReady]);
+                if (lane == 0) tc::mbar_arrive(&bars[kBarPReady]);
             }
         }
         if (ok && nc > 0) ok = warp_wait(&bars[kBarHDone], (nc - 1) & 1, abort_flag);
@@ -540,6 +535,7 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const int odd = lane & 1;
         // lanes meet in pairs: the even one stores both columns of token i, the odd one of i + 1
         __nv_bfloat16* y = p.y + (b * L + odd) * row + (int64_t)(h0 + hv) * H + (colh & ~1);
+        if (lane == 0 && nc > 0) tc::mbar_arrive(&bars[kBarHReady]);  // no sum to be read yet
         for (int c = 0; c < nc; ++c) {
             const int buf = c & 1;
             const uint32_t ph = c & 1;
@@ -563,9 +559,8 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             tc::tmem_wait_st();
             tc::tc_fence_before();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&bars[kBarO1Read]);
-            if (!warp_wait<true>(&bars[kBarPFull], ph, abort_flag)) { ok = false; break; }
-            if (!warp_wait<true>(&bars[kBarO2Done], ph, abort_flag)) { ok = false; break; }
+            if (lane == 0) tc::mbar_arrive(&bars[kBarPReady]);
+            if (!warp_wait<true>(&bars[kBarPDone], ph, abort_flag)) { ok = false; break; }
             tc::tc_fence_after();
             const int64_t nleft = n - (int64_t)c * kT, lleft = L - (int64_t)c * kT;
             const int nv = nleft < kT ? (int)nleft : kT, lv = live ? (lleft < kT ? (int)lleft : kT) : 0;
@@ -577,7 +572,7 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 if (m == kT - 16) {
                     tc::tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&bars[kBarO2Read]);
+                    if (lane == 0 && c + 1 < nc) tc::mbar_arrive(&bars[kBarHReady]);
                 }
 #pragma unroll
                 for (int j = 0; j < 16; j += 2) {
@@ -598,11 +593,10 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         if (ok && live)
             for (int64_t t = (int64_t)nc * kT; t + odd < L; t += 2) *reinterpret_cast<uint32_t*>(y + t * row) = 0u;
     } else if (warp < kPWarp0) {
-        // ======================= G, k's norms, A and N =======================
+        // ============== G, k's norms, A and N's diagonal blocks ==============
         // K K^T's blocks (0, 0), (1, 1), (1, 0) on warps 0 to 2, for all heads; warp 3: G and the scalars
         const int w = warp - kNWarp0;
         const int gid = lane >> 2, tig = lane & 3;
-        NScratch* scr = reinterpret_cast<NScratch*>(smem + p.off_scratch);
         const int64_t gbase = b * L * g.nheads + h0;
         // warp 3's lanes hold the next chunk's g and beta, a token each
         float gn[NV], bn[NV];
@@ -692,35 +686,38 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll 1
                 for (int hv = 0; hv < NV; ++hv) {
                     const Tok* tok = scal_of(buf, hv)->tok;
+                    NScratch* scr = scratch_of(buf, hv);
                     const Tok ti0 = tok[16 * bi + gid], ti1 = tok[16 * bi + gid + 8], tr = tok[16 * bi];
-                    const float f0 = ti0.beta * ti0.rk, f1 = ti1.beta * ti1.rk;
-                    const float e0 = f0 * decay(ti0, tr), e1 = f1 * decay(ti1, tr);
-                    float(*a)[20] = w < 2 ? scr[hv].diag[w] : scr[hv].low;
+                    const float f0 = in0 ? ti0.beta * ti0.rk : 0.f, f1 = in1 ? ti1.beta * ti1.rk : 0.f;
+                    const float e0 = decay(ti0, tr), e1 = decay(ti1, tr);
+                    float(*a)[20] = w < 2 ? scr->diag[w] : scr->low;
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt)
+                    for (int nt = 0; nt < 2; ++nt) {
+                        float c[2][2];
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             const int jj = 8 * nt + 2 * tig + x;
                             const Tok tj = tok[16 * bj + jj];
-                            float a0, a1;
                             if (w < 2) {
-                                a0 = in0 && jj < gid ? acc[nt][x] * (f0 * tj.rk * decay(ti0, tj)) : 0.f;
-                                a1 = in1 && jj < gid + 8 ? acc[nt][2 + x] * (f1 * tj.rk * decay(ti1, tj)) : 0.f;
+                                c[0][x] = tj.rk * decay(ti0, tj);
+                                c[1][x] = tj.rk * decay(ti1, tj);
                             } else {
                                 const float cj = tj.rk * decay(tr, tj);
-                                a0 = in0 ? acc[nt][x] * (e0 * cj) : 0.f;
-                                a1 = in1 ? acc[nt][2 + x] * (e1 * cj) : 0.f;
+                                c[0][x] = e0 * cj;
+                                c[1][x] = e1 * cj;
                             }
-                            a[jj][gid] = a0;
-                            a[jj][gid + 8] = a1;
+                            a[jj][gid] = in0 && (w == 2 || jj < gid) ? acc[nt][x] * (f0 * c[0][x]) : 0.f;
+                            a[jj][gid + 8] = in1 && (w == 2 || jj < gid + 8) ? acc[nt][2 + x] * (f1 * c[1][x]) : 0.f;
                         }
+                        scr->fac[w][nt][lane] = make_float4(c[0][0], c[0][1], c[1][0], c[1][1]);
+                    }
                 }
             }
             __syncwarp();
             // N's diagonal blocks, a column per lane; the warp's halves take the two heads (or the same one)
             if (w < 2) {
                 const int l = lane & 15;
-                float(*a)[20] = scr[NV == 2 ? lane >> 4 : 0].diag[w];
+                float(*a)[20] = scratch_of(buf, NV == 2 ? lane >> 4 : 0)->diag[w];
                 float x[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) x[i] = i == l ? 1.f : 0.f;
@@ -741,14 +738,33 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     for (int i = 0; i < 16; i += 4)
                         *reinterpret_cast<float4*>(&a[l][i]) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
             }
-            bar_sync(1, 32 * kNWarps);
-            // the last chunk's N has been used (no barrier follows before the next chunk's: the warps may part)
-            if (c > 0) ok = warp_wait<true>(&bars[kBarWDone], (c - 1) & 1, abort_flag);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bars[kBarDFull + buf]);
+            if (++st == p.nst) {
+                st = 0;
+                full_phase ^= 1u;
+            }
+        }
+        if (!ok) set_abort(ctl, p.status);
+    } else if (warp < kTmaWarp) {
+        // ==================== the rest of N, q's norms and P ====================
+        // Q K^T's blocks (0, 0), (1, 1), (1, 0) on warps 0 to 2, for all heads; warp 3: Q Q^T's diagonal
+        const int w = warp - kPWarp0;
+        const int gid = lane >> 2, tig = lane & 3;
+        int st = 0;
+        uint32_t full_phase = 0;
+        for (int c = 0; c < nc; ++c) {
+            const int buf = c & 1;
+            // N's place is free once the last chunk's W is done
+            ok = warp_wait<true>(&bars[kBarFull + st], full_phase, abort_flag) &&
+                 warp_wait<true>(&bars[kBarDFull + buf], (c >> 1) & 1, abort_flag) &&
+                 (c == 0 || warp_wait<true>(&bars[kBarWDone], (c - 1) & 1, abort_flag));
+            if (!ok) break;
             // N_10 = -N_11 A_10 N_00 and all of N into its planes, eight columns (of a head's half) to a
             // warp, four lanes to a column, four rows each
-            if (ok && w < 2 * NV) {
+            if (w < 2 * NV) {
                 const int hv = w >> 1, col = 8 * (w & 1) + (lane >> 2), r4 = lane & 3;
-                const NScratch& m = scr[hv];
+                const NScratch& m = *scratch_of(buf, hv);
                 float x[16];
 #pragma unroll
                 for (int i = 0; i < 16; i += 4) {
@@ -786,26 +802,9 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
             tc::fence_proxy_async_smem();
             __syncwarp();
-            if (ok && lane == 0) tc::mbar_arrive(&bars[kBarNFull]);
-            if (++st == p.nst) {
-                st = 0;
-                full_phase ^= 1u;
-            }
-        }
-        if (!ok) set_abort(ctl, p.status);
-    } else if (warp < kTmaWarp) {
-        // ========================= q's norms and P =========================
-        // Q K^T's blocks (0, 0), (1, 1), (1, 0) on warps 0 to 2, for all heads; warp 3: Q Q^T's diagonal
-        const int w = warp - kPWarp0;
-        const int gid = lane >> 2, tig = lane & 3;
-        int st = 0;
-        uint32_t full_phase = 0;
-        for (int c = 0; c < nc; ++c) {
-            const int buf = c & 1;
-            ok = warp_wait<true>(&bars[kBarFull + st], full_phase, abort_flag) &&
-                 warp_wait<true>(&bars[kBarSFull + buf], (c >> 1) & 1, abort_flag);
-            if (!ok) break;
+            if (lane == 0) tc::mbar_arrive(&bars[kBarXReady]);
             const uint32_t aK = tc::smem_u32(smem + st * kStage), aQ = aK + kBox;
+            // (P's place is free once the last chunk's P W is done)
             if (w == 3) {
 #pragma unroll 1
                 for (int i = 0; i < 2; ++i) {
@@ -821,35 +820,23 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                         for (int hv = 0; hv < NV; ++hv) scal_of(buf, hv)->oq[16 * i + lane] = p.scale;
                     }
                 }
+                if (c > 0) ok = warp_wait<true>(&bars[kBarPDone], (c - 1) & 1, abort_flag);
+                if (!ok) break;
             } else {
                 const int bi = w == 0 ? 0 : 1, bj = w == 1 ? 1 : 0, i0 = 16 * bi + gid;
                 float acc[2][4];
                 score_block<S>(aQ, aK, bi, bj, lane, acc);
-                // the last chunk's P has been used
-                if (c > 0) ok = warp_wait<true>(&bars[kBarPFree], (c - 1) & 1, abort_flag);
+                if (c > 0) ok = warp_wait<true>(&bars[kBarPDone], (c - 1) & 1, abort_flag);
                 if (!ok) break;
 #pragma unroll 1
                 for (int hv = 0; hv < NV; ++hv) {
-                    const Tok* tok = scal_of(buf, hv)->tok;
                     uint8_t* sP = p_of(hv);
-                    // (the diagonal blocks take their decays exactly)
-                    const Tok tr = tok[16 * bi], ti0 = tok[i0], ti1 = tok[i0 + 8];
-                    const float f0 = decay(ti0, tr), f1 = decay(ti1, tr);
 #pragma unroll
                     for (int nt = 0; nt < 2; ++nt) {
                         const int j0 = 16 * bj + 8 * nt + 2 * tig;
-                        const Tok t0 = tok[j0], t1 = tok[j0 + 1];
-                        float2 c0, c1;
-                        if (w == 2) {
-                            const float2 cj = make_float2(t0.rk * decay(tr, t0), t1.rk * decay(tr, t1));
-                            c0 = tc::mul_f32x2(cj, make_float2(f0, f0));
-                            c1 = tc::mul_f32x2(cj, make_float2(f1, f1));
-                        } else {
-                            c0 = make_float2(t0.rk * decay(ti0, t0), t1.rk * decay(ti0, t1));
-                            c1 = make_float2(t0.rk * decay(ti1, t0), t1.rk * decay(ti1, t1));
-                        }
-                        float2 a0 = tc::mul_f32x2(c0, make_float2(acc[nt][0], acc[nt][1]));
-                        float2 a1 = tc::mul_f32x2(c1, make_float2(acc[nt][2], acc[nt][3]));
+                        const float4 f = scratch_of(buf, hv)->fac[w][nt][lane];
+                        float2 a0 = tc::mul_f32x2(make_float2(f.x, f.y), make_float2(acc[nt][0], acc[nt][1]));
+                        float2 a1 = tc::mul_f32x2(make_float2(f.z, f.w), make_float2(acc[nt][2], acc[nt][3]));
                         if (w != 2) {
                             a0 = make_float2(j0 <= i0 ? a0.x : 0.f, j0 + 1 <= i0 ? a0.y : 0.f);
                             a1 = make_float2(j0 <= i0 + 8 ? a1.x : 0.f, j0 + 1 <= i0 + 8 ? a1.y : 0.f);
@@ -868,8 +855,9 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                tc::mbar_arrive(&bars[kBarPFull]);
+                tc::mbar_arrive(&bars[kBarPReady]);
                 tc::mbar_arrive(&bars[kBarSFree + buf]);
+                tc::mbar_arrive(&bars[kBarFree + st]);
             }
             if (++st == p.nst) {
                 st = 0;
@@ -938,27 +926,22 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     if (fills[i] > 0) (void)tc::mbar_wait(&bars[kBarVFull + i], (fills[i] - 1) & 1, never);
             }
         } else if (warp == kMmaWarp) {
-            // ============================= MMA issuer =============================
+            // ==================== issuer of the chain's products ====================
             if (lane == 0 && nc > 0) {
                 constexpr uint32_t id_t = tc::idesc_bf16(128, kT, false, false);       // N = tokens
                 constexpr uint32_t id_rq = tc::idesc_bf16(128, 2 * kT, false, false);  // of K and of Q
                 constexpr uint32_t id_s = tc::idesc_bf16(128, S, false, true);         // N = state rows
                 const uint64_t dN = tc::sdesc_sw128(tc::smem_u32(smem + p.off_n), 16, 1024);
-                const uint64_t dP = tc::sdesc_sw128(tc::smem_u32(smem + p.off_p), 16, 1024);
                 int st = 0;
-                uint32_t full_phase = 0;
                 for (int c = 0; c < nc; ++c) {
                     const int buf = c & 1;
                     const uint32_t ph = c & 1;
                     const uint32_t aK = tc::smem_u32(smem + st * kStage);
                     const uint64_t dK = tc::sdesc_sw128(aK, 16, 1024);
                     const uint64_t dKt = tc::sdesc_sw128(aK, 2 * kBox, 1024);
-                    if (!thread_wait<false>(&bars[kBarFull + st], full_phase, abort_flag)) { ok = false; break; }
-                    // (with the scalars K's rows past the end are cleared)
-                    if (!thread_wait<false>(&bars[kBarSFull + buf], (c >> 1) & 1, abort_flag)) { ok = false; break; }
+                    // R | Q h from h's high part, R from its low part.  (The chain has waited for the scalars, and
+                    // their makers for K and Q, whose rows past the end they cleared.)
                     if (!thread_wait<false>(&bars[kBarHReady], ph, abort_flag)) { ok = false; break; }
-                    // R | Q h from h's high part, once y's sum of the chunk before has been read; R from its low part
-                    if (c > 0 && !thread_wait<false>(&bars[kBarO2Read], ph ^ 1, abort_flag)) { ok = false; break; }
                     tc::tc_fence_after();
 #pragma unroll 1
                     for (int x = 0; x < 2 * kBoxes; ++x) {
@@ -971,7 +954,6 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     tc::mma_commit(&bars[kBarRDone]);
                     // W = N X, N's parts times X's down to 2^-16 of hi hi; N's second block column only has
                     // rows from 16 on
-                    if (!thread_wait<false>(&bars[kBarNFull], ph, abort_flag)) { ok = false; break; }
                     if (!thread_wait<false>(&bars[kBarXReady], ph, abort_flag)) { ok = false; break; }
                     tc::tc_fence_after();
 #pragma unroll 1
@@ -998,10 +980,23 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                             tc::mma_bf16_ts(tmem + cH, tmem + cU + 16 * part + 8 * kt, dKt + 128 * kt, id_s, 1);
                     }
                     tc::mma_commit(&bars[kBarHDone]);
-                    // P W onto the scaled Q h: hi hi + hi lo + lo hi
-                    if (!thread_wait<false>(&bars[kBarPFull], ph, abort_flag)) { ok = false; break; }
-                    if (!thread_wait<false>(&bars[kBarWyReady], ph, abort_flag)) { ok = false; break; }
-                    if (!thread_wait<false>(&bars[kBarO1Read], ph, abort_flag)) { ok = false; break; }
+                    tc::mma_commit(&bars[kBarSFree + buf]);
+                    tc::mma_commit(&bars[kBarFree + st]);
+                    if (++st == p.nst) st = 0;
+                }
+                if (!ok) set_abort(ctl, p.status);
+                // no product may still run when the tensor memory is freed
+                tc::mma_commit(&bars[kBarDrain]);
+                (void)tc::mbar_wait(&bars[kBarDrain], 0, never);
+            }
+        } else if (warp == kPwWarp) {
+            // ========================= issuer of P W =========================
+            if (lane == 0 && nc > 0) {
+                constexpr uint32_t id_t = tc::idesc_bf16(128, kT, false, false);
+                const uint64_t dP = tc::sdesc_sw128(tc::smem_u32(smem + p.off_p), 16, 1024);
+                for (int c = 0; c < nc; ++c) {
+                    // onto the scaled Q h: hi hi + hi lo + lo hi
+                    if (!thread_wait<true>(&bars[kBarPReady], c & 1, abort_flag)) { ok = false; break; }
                     tc::tc_fence_after();
 #pragma unroll 1
                     for (int x = 0; x < 2 * NV; ++x) {
@@ -1013,19 +1008,11 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                         tc::mma_bf16_ts(d, a, at + (kPlane >> 4), id, 1);
                         tc::mma_bf16_ts(d, a + 16, at, id, 1);
                     }
-                    tc::mma_commit(&bars[kBarO2Done]);
-                    tc::mma_commit(&bars[kBarSFree + buf]);
-                    tc::mma_commit(&bars[kBarPFree]);
-                    tc::mma_commit(&bars[kBarFree + st]);
-                    if (++st == p.nst) {
-                        st = 0;
-                        full_phase ^= 1u;
-                    }
+                    tc::mma_commit(&bars[kBarPDone]);
                 }
                 if (!ok) set_abort(ctl, p.status);
-                // no product may still run when the tensor memory is freed
-                tc::mma_commit(&bars[kBarDrain]);
-                (void)tc::mbar_wait(&bars[kBarDrain], 0, never);
+                tc::mma_commit(&bars[kBarDrain + 1]);
+                (void)tc::mbar_wait(&bars[kBarDrain + 1], 0, never);
             }
         }
     }
@@ -1058,7 +1045,7 @@ cudaError_t launch_k(const GdrArgs& a, cudaStream_t st) {
     p.l2norm = a.l2norm;
     constexpr uint32_t stage = 2 * (S / 64) * kBox, vstage = NV * H / 64 * kBox;
     constexpr uint32_t rest = kMaxVStages * vstage + NV * ((kNPlanes + kPPlanes) * kPlane + 2 * kScalBytes) +
-                              NV * (uint32_t)sizeof(NScratch) + kNumBars * 8 + (uint32_t)sizeof(SharedCtl) + 1024;
+                              2 * NV * (uint32_t)sizeof(NScratch) + kNumBars * 8 + (uint32_t)sizeof(SharedCtl) + 1024;
     static_assert(kMaxStages * stage + rest <= (uint32_t)kSmemLimit, "shared memory");
     p.nst = kMaxStages;
     p.nvst = kMaxVStages;
@@ -1067,7 +1054,7 @@ cudaError_t launch_k(const GdrArgs& a, cudaStream_t st) {
     p.off_p = p.off_n + NV * kNPlanes * kPlane;
     p.off_scal = p.off_p + NV * kPPlanes * kPlane;
     p.off_scratch = p.off_scal + 2 * NV * kScalBytes;
-    p.off_bar = p.off_scratch + NV * (uint32_t)sizeof(NScratch);
+    p.off_bar = p.off_scratch + 2 * NV * (uint32_t)sizeof(NScratch);
     const int smem = (int)(kMaxStages * stage + rest);
 
     CUtensorMap tm_q, tm_k, tm_v;
