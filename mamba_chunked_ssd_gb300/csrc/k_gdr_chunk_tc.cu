@@ -418,14 +418,20 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             if (c > 0 && !warp_wait(&bars[kBarHDone], ph ^ 1, abort_flag)) { ok = false; break; }
             tc::tc_fence_after();
             // h's parts
-#pragma unroll 1
-            for (int s = s0; s < s0 + S / 4; s += 16) {
-                uint32_t r[16], hi[8], lo[8];
-                tc::tmem_ld16(tl + cH + s, r);
+            {
+                uint32_t r[S / 64][16];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) split2(as_f2(&r[2 * j]), hi[j], lo[j]);
-                tc::tmem_st8(tl + cHi + s / 2, hi);
-                tc::tmem_st8(tl + cLo + s / 2, lo);
+                for (int m = 0; m < S / 64; ++m) tc::tmem_ld16_nowait(tl + cH + s0 + 16 * m, r[m]);
+                tc::tmem_wait_ld16(r[0]);
+                if (S == 128) tc::tmem_tie16(r[S / 64 - 1]);
+#pragma unroll
+                for (int m = 0; m < S / 64; ++m) {
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) split2(as_f2(&r[m][2 * j]), hi[j], lo[j]);
+                    tc::tmem_st8(tl + cHi + s0 / 2 + 8 * m, hi);
+                    tc::tmem_st8(tl + cLo + s0 / 2 + 8 * m, lo);
+                }
             }
             tc::tmem_wait_st();
             tc::tc_fence_before();
@@ -943,7 +949,7 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     // their makers for K and Q, whose rows past the end they cleared.)
                     if (!thread_wait<false>(&bars[kBarHReady], ph, abort_flag)) { ok = false; break; }
                     tc::tc_fence_after();
-#pragma unroll 1
+#pragma unroll
                     for (int x = 0; x < 2 * kBoxes; ++x) {
                         const uint32_t id = x < kBoxes ? id_rq : id_t, box = x < kBoxes ? x : x - kBoxes;
                         const uint64_t d = dK + box * (2 * kBox >> 4);
@@ -956,7 +962,7 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     // rows from 16 on
                     if (!thread_wait<false>(&bars[kBarXReady], ph, abort_flag)) { ok = false; break; }
                     tc::tc_fence_after();
-#pragma unroll 1
+#pragma unroll
                     for (int x = 0; x < 2 * NV; ++x) {
                         const int kb = x & 1, hv = x >> 1;
                         const uint32_t a = tmem + cX + 8 * kb, d = tmem + (hv ? cR2 : cR) + 16 * kb;
@@ -973,7 +979,7 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     // h += K^T W
                     if (!thread_wait<false>(&bars[kBarWReady], ph, abort_flag)) { ok = false; break; }
                     tc::tc_fence_after();
-#pragma unroll 1
+#pragma unroll
                     for (int kt = 0; kt < 2; ++kt) {
 #pragma unroll
                         for (int part = 0; part < 3; ++part)
