@@ -262,18 +262,29 @@ def mamba2_ssd_step(x, dt, A, B, C, state_in=None, D=None, state_out=None, y=Non
     return y, state_out
 
 
+# The gated-delta-rule entry points are also called once a token, where the host
+# call is the time: they pass plain integers (ctypes makes the pointers), ask for
+# the raw stream, and check a tensor's layout in as few attribute reads as will do.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _on(stream, t):
+    return _raw_stream(t.device.index) if stream is None else stream.cuda_stream
+
+
 def _rows(t, name, inner):
     """Stride from row to row of a tensor whose last ``inner`` dimensions are
     packed and whose leading ones form one run of rows, e.g. a channel slice of
-    a contiguous [b, L, C] tensor."""
+    a contiguous [b, L, C] tensor (0: packed, as in the C interface)."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    shape, st = t.shape, t.stride()
     if t.is_contiguous():
-        width = 1
-        for d in shape[len(shape) - inner:]:
-            width *= d
-        return width
+        return 0
+    shape, st = t.shape, t.stride()
     lead, want = len(shape) - inner, 1
     for d in range(len(shape) - 1, lead - 1, -1):
         if shape[d] != 1 and st[d] != want:
@@ -297,26 +308,35 @@ def _rows(t, name, inner):
 
 def _want(t, name, dtype, shape):
     """A contiguous CUDA tensor of this dtype and shape (or None)."""
-    if t is None:
+    if t is None or (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()):
         return
-    _need(t, name)
-    if t.dtype != dtype or tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {dtype} {shape}, not {t.dtype} {tuple(t.shape)}")
+    raise ValueError(f"{name} must be a contiguous CUDA tensor, {dtype} {tuple(shape)}, "
+                     f"not {t.dtype} {tuple(t.shape)} on {t.device} with strides {t.stride()}")
+
+
+def _like(t, given, name):
+    """The output for an input's dtype and shape: the given one, checked, or a new one."""
+    if given is None:
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+    if given.dtype is not t.dtype or given.shape != t.shape:
+        raise ValueError(f"{name} must be {t.dtype} {tuple(t.shape)}, not {given.dtype} {tuple(given.shape)}")
+    return given
 
 
 def _gdr_args(q, k, v, g, beta, scale, qk_l2norm, l2_eps):
     """The shape and options of a gated-delta-rule call; checks q, k, v, g, beta."""
-    *rows, nh, H = v.shape
-    G, S = q.shape[-2:]
-    if q.shape != k.shape or tuple(q.shape[:-2]) != tuple(rows):
-        raise ValueError(f"q and k must be {tuple(rows)} + (groups, state): got {tuple(q.shape)}, {tuple(k.shape)}")
-    if q.dtype != v.dtype or k.dtype != v.dtype:
+    vs, qs, dt = v.shape, q.shape, v.dtype
+    rows, nh = vs[:-1], vs[-2]
+    if qs != k.shape or len(qs) != len(vs) or qs[:-2] != vs[:-2]:
+        raise ValueError(f"q and k must be {tuple(vs[:-2])} + (groups, state): got {tuple(qs)}, {tuple(k.shape)}")
+    if q.dtype is not dt or k.dtype is not dt:
         raise TypeError("q, k and v must have one dtype")
-    _want(g, "g", torch.float32, (*rows, nh)), _want(beta, "beta", torch.float32, (*rows, nh))
-    shape = mamba2_shape(rows[0], rows[1] if len(rows) > 1 else 1, nh, H, S, G, 64, _dtype_code(v), 0)
+    _want(g, "g", torch.float32, rows), _want(beta, "beta", torch.float32, rows)
+    S = qs[-1]
+    shape = mamba2_shape(vs[0], vs[1] if len(vs) == 4 else 1, nh, vs[-1], S, qs[-2], 64, _dtype_code(v), 0)
     opt = mamba2_gdr_options(_rows(q, "q", 2), _rows(k, "k", 2), _rows(v, "v", 2), S ** -0.5 if scale is None else scale,
                              l2_eps, MAMBA2_GDR_QK_L2NORM if qk_l2norm else 0, 0)
-    return shape, opt
+    return shape, opt, (vs[0], nh, S, vs[-1])
 
 
 def mamba2_gdr_fwd(q, k, v, g, beta, scale=None, qk_l2norm=False, l2_eps=1e-6, initial_state=None, lengths=None,
@@ -325,20 +345,19 @@ def mamba2_gdr_fwd(q, k, v, g, beta, scale=None, qk_l2norm=False, l2_eps=1e-6, i
     [b, nh, S, H] fp32 or None).  q, k [b, L, G, S] and v [b, L, nh, H] may be
     slices of a wider tensor; g (log decay), beta [b, L, nh] fp32; scale
     defaults to S ** -0.5; lengths [b] int32 or None."""
-    shape, opt = _gdr_args(q, k, v, g, beta, scale, qk_l2norm, l2_eps)
-    b, nh, S, H = shape.batch, shape.nheads, shape.dstate, shape.headdim
-    _want(initial_state, "initial_state", torch.float32, (b, nh, S, H)), _want(lengths, "lengths", torch.int32, (b,))
-    if y is None:
-        y = torch.empty(v.shape, device=v.device, dtype=v.dtype)
-    else:
-        _want(y, "y", v.dtype, tuple(v.shape))
+    shape, opt, state = _gdr_args(q, k, v, g, beta, scale, qk_l2norm, l2_eps)
+    _want(initial_state, "initial_state", torch.float32, state), _want(lengths, "lengths", torch.int32, state[:1])
+    if y is not None:
+        _want(y, "y", v.dtype, v.shape)
+    y = _like(v, y, "y")
     if final_state is not None:
-        _want(final_state, "final_state", torch.float32, (b, nh, S, H))
+        _want(final_state, "final_state", torch.float32, state)
     elif want_final_state:
-        final_state = torch.empty(b, nh, S, H, device=v.device, dtype=torch.float32)
-    _check("mamba2_gdr_fwd", load_library().mamba2_gdr_fwd(
-        ctypes.byref(shape), ctypes.byref(opt), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(lengths),
-        _ptr(initial_state), _ptr(y), _ptr(final_state), _stream(stream)))
+        final_state = torch.empty(state, device=v.device, dtype=torch.float32)
+    rc = load_library().mamba2_gdr_fwd(shape, opt, _at(q), _at(k), _at(v), _at(g), _at(beta), _at(lengths),
+                                       _at(initial_state), _at(y), _at(final_state), _on(stream, v))
+    if rc:
+        _check("mamba2_gdr_fwd", rc)
     return y, final_state
 
 
@@ -347,20 +366,19 @@ def mamba2_gdr_step(q, k, v, g, beta, state_in=None, scale=None, qk_l2norm=False
     """One token of the gated delta rule: q, k [b, G, S], v [b, nh, H], g, beta
     [b, nh], state [b, nh, S, H] fp32.  Returns (y [b, nh, H], state_out).  Pass
     state_out=state_in to update the state in place."""
-    shape, opt = _gdr_args(q, k, v, g, beta, scale, qk_l2norm, l2_eps)
-    b, nh, S, H = shape.batch, shape.nheads, shape.dstate, shape.headdim
-    _want(state_in, "state_in", torch.float32, (b, nh, S, H))
-    if y is None:
-        y = torch.empty(v.shape, device=v.device, dtype=v.dtype)
-    else:
-        _want(y, "y", v.dtype, tuple(v.shape))
+    shape, opt, state = _gdr_args(q, k, v, g, beta, scale, qk_l2norm, l2_eps)
+    _want(state_in, "state_in", torch.float32, state)
+    if y is not None:
+        _want(y, "y", v.dtype, v.shape)
+    y = _like(v, y, "y")
     if state_out is None:
-        state_out = torch.empty(b, nh, S, H, device=v.device, dtype=torch.float32)
-    else:
-        _want(state_out, "state_out", torch.float32, (b, nh, S, H))
-    _check("mamba2_gdr_step", load_library().mamba2_gdr_step(
-        ctypes.byref(shape), ctypes.byref(opt), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state_in),
-        _ptr(state_out), _ptr(y), _stream(stream)))
+        state_out = torch.empty(state, device=v.device, dtype=torch.float32)
+    elif state_out is not state_in:
+        _want(state_out, "state_out", torch.float32, state)
+    rc = load_library().mamba2_gdr_step(shape, opt, _at(q), _at(k), _at(v), _at(g), _at(beta), _at(state_in),
+                                        _at(state_out), _at(y), _on(stream, v))
+    if rc:
+        _check("mamba2_gdr_step", rc)
     return y, state_out
 
 
@@ -373,19 +391,17 @@ def mamba2_causal_conv_fwd(x, weight, bias=None, silu=True, initial_state=None, 
     W = weight.shape[-1]
     _want(weight, "weight", torch.float32, (C, W)), _want(bias, "bias", torch.float32, (C,))
     _want(initial_state, "initial_state", x.dtype, (b, W - 1, C)), _want(lengths, "lengths", torch.int32, (b,))
-    if y is None:
-        y = torch.empty(b, L, C, device=x.device, dtype=x.dtype)
-    elif y.dtype != x.dtype or y.shape != x.shape:
-        raise ValueError("y must have x's dtype and shape")
+    y = _like(x, y, "y")
     if final_state is not None:
         _want(final_state, "final_state", x.dtype, (b, W - 1, C))
     elif want_final_state:
-        final_state = torch.empty(b, W - 1, C, device=x.device, dtype=x.dtype)
+        final_state = torch.empty((b, W - 1, C), device=x.device, dtype=x.dtype)
     shape = mamba2_conv_shape(b, L, C, W, _rows(x, "x", 1), _rows(y, "y", 1), _dtype_code(x),
                               MAMBA2_CONV_SILU if silu else 0)
-    _check("mamba2_causal_conv_fwd", load_library().mamba2_causal_conv_fwd(
-        ctypes.byref(shape), _ptr(x), _ptr(weight), _ptr(bias), _ptr(lengths), _ptr(initial_state), _ptr(y),
-        _ptr(final_state), _stream(stream)))
+    rc = load_library().mamba2_causal_conv_fwd(shape, _at(x), _at(weight), _at(bias), _at(lengths), _at(initial_state),
+                                               _at(y), _at(final_state), _on(stream, x))
+    if rc:
+        _check("mamba2_causal_conv_fwd", rc)
     return y, final_state
 
 
@@ -394,21 +410,20 @@ def mamba2_causal_conv_step(x, weight, state_in=None, bias=None, silu=True, stat
     Returns (y [b, C], state_out); state_out=state_in updates in place."""
     b, C = x.shape
     W = weight.shape[-1]
+    state = (b, W - 1, C)
     _want(weight, "weight", torch.float32, (C, W)), _want(bias, "bias", torch.float32, (C,))
-    _want(state_in, "state_in", x.dtype, (b, W - 1, C))
-    if y is None:
-        y = torch.empty(b, C, device=x.device, dtype=x.dtype)
-    elif y.dtype != x.dtype or y.shape != x.shape:
-        raise ValueError("y must have x's dtype and shape")
+    _want(state_in, "state_in", x.dtype, state)
+    y = _like(x, y, "y")
     if state_out is None:
-        state_out = torch.empty(b, W - 1, C, device=x.device, dtype=x.dtype)
-    else:
-        _want(state_out, "state_out", x.dtype, (b, W - 1, C))
+        state_out = torch.empty(state, device=x.device, dtype=x.dtype)
+    elif state_out is not state_in:
+        _want(state_out, "state_out", x.dtype, state)
     shape = mamba2_conv_shape(b, 1, C, W, _rows(x, "x", 1), _rows(y, "y", 1), _dtype_code(x),
                               MAMBA2_CONV_SILU if silu else 0)
-    _check("mamba2_causal_conv_step", load_library().mamba2_causal_conv_step(
-        ctypes.byref(shape), _ptr(x), _ptr(weight), _ptr(bias), _ptr(state_in), _ptr(state_out), _ptr(y),
-        _stream(stream)))
+    rc = load_library().mamba2_causal_conv_step(shape, _at(x), _at(weight), _at(bias), _at(state_in), _at(state_out),
+                                                _at(y), _on(stream, x))
+    if rc:
+        _check("mamba2_causal_conv_step", rc)
     return y, state_out
 
 
@@ -419,19 +434,18 @@ def mamba2_group_norm(x, weight, ngroups, z=None, bias=None, eps=1e-5, subtract_
     SiLU(z) before or after the norm).  weight, bias [C] fp32 or None."""
     C = x.shape[-1]
     _want(weight, "weight", torch.float32, (C,)), _want(bias, "bias", torch.float32, (C,))
-    if mode not in NORM_MODES:
+    flags = NORM_MODES.get(mode)
+    if flags is None:
         raise ValueError(f"mode must be one of {sorted(NORM_MODES)}, not {mode!r}")
-    for t, n in ((z, "z"), (y, "y")):
-        if t is not None and (t.dtype != x.dtype or t.shape != x.shape):
-            raise ValueError(f"{n} must have x's dtype and shape")
-    if y is None:
-        y = torch.empty(x.shape, device=x.device, dtype=x.dtype)
-    rows = x.numel() // C if C else 0
-    shape = mamba2_norm_shape(rows, C, ngroups, _rows(x, "x", 1), 0 if z is None else _rows(z, "z", 1),
-                              _rows(y, "y", 1), eps, _dtype_code(x),
-                              NORM_MODES[mode] | (MAMBA2_NORM_SUBTRACT_MEAN if subtract_mean else 0), 0)
-    _check("mamba2_group_norm", load_library().mamba2_group_norm(
-        ctypes.byref(shape), _ptr(x), _ptr(z), _ptr(weight), _ptr(bias), _ptr(y), _stream(stream)))
+    if z is not None:
+        _like(x, z, "z")
+    y = _like(x, y, "y")
+    shape = mamba2_norm_shape(x.numel() // C if C else 0, C, ngroups, _rows(x, "x", 1),
+                              0 if z is None else _rows(z, "z", 1), _rows(y, "y", 1), eps, _dtype_code(x),
+                              flags | MAMBA2_NORM_SUBTRACT_MEAN if subtract_mean else flags, 0)
+    rc = load_library().mamba2_group_norm(shape, _at(x), _at(z), _at(weight), _at(bias), _at(y), _on(stream, x))
+    if rc:
+        _check("mamba2_group_norm", rc)
     return y
 
 

@@ -3,19 +3,20 @@
 //
 //   y_t = act(bias + sum_{w < W} weight[c, w] x_{t - (W - 1) + w})
 //
-// Each input is read once and each output written once: the kernels are
-// bound by memory.  A thread owns the channels of one 16-byte vector and a run
-// of consecutive tokens, and slides a window of the last W - 1 inputs through
-// its registers, so a token's input is loaded once per run (plus the W - 1
-// tokens before the run, which the neighbouring run has just brought into L2).
+// Each input is read once and each output written once: the kernels are bound
+// by memory.  A thread owns the channels of one vector and a run of consecutive
+// tokens, and slides a window of the last W - 1 inputs through its registers, so a
+// token's input is loaded once per run (plus the W - 1 tokens before the run,
+// which the neighbouring run has just brought into L2).  The loads of the next
+// eight tokens are under way while eight are computed.
 #include "gated_delta.cuh"
 
 namespace m2 {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kRun = 32;    // tokens per thread
-constexpr int kAhead = 8;   // loads in flight per thread
+constexpr int kRun = 64;   // tokens per thread
+constexpr int kAhead = 8;  // loads in flight per thread
 
 template <typename T, int VEC, int W>
 __global__ void __launch_bounds__(kThreads) k_causal_conv(const ConvArgs a) {
@@ -51,25 +52,19 @@ __global__ void __launch_bounds__(kThreads) k_causal_conv(const ConvArgs a) {
 
     for (int64_t t0 = (int64_t)blockIdx.y * kRun; t0 < a.seqlen; t0 += (int64_t)gridDim.y * kRun) {
         const int64_t t1 = imin64(t0 + kRun, a.seqlen);
-        const int64_t tv = imin64(t1, n);  // tokens that are computed
-        float win[W][VEC];                 // win[w]: the input W - 1 - w tokens back
-        if (t0 < tv) {
+        const int m = (int)(imin64(t1, n) - t0);  // tokens that are computed (none: m <= 0)
+        if (m > 0) {
+            float win[W][VEC];  // win[w]: the input W - 1 - w tokens back
 #pragma unroll
             for (int w = 0; w < W - 1; ++w) unpack<VEC>(input(t0 - (W - 1) + w), win[w + 1], (const T*)nullptr);
-        }
-        for (int64_t t = t0; t < tv; t += kAhead) {
-            V in[kAhead];
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u)
-                if (t + u < tv) in[u] = *reinterpret_cast<const V*>(x + (t + u) * a.x_stride);
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                if (t + u >= tv) break;
+            const T* xt = x + t0 * a.x_stride;
+            T* yt = y + t0 * a.y_stride;
+            auto token = [&](const V& in) {
 #pragma unroll
                 for (int w = 0; w < W - 1; ++w)
 #pragma unroll
                     for (int i = 0; i < VEC; ++i) win[w][i] = win[w + 1][i];
-                unpack<VEC>(in[u], win[W - 1], (const T*)nullptr);
+                unpack<VEC>(in, win[W - 1], (const T*)nullptr);
                 float s[VEC];
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
@@ -78,10 +73,31 @@ __global__ void __launch_bounds__(kThreads) k_causal_conv(const ConvArgs a) {
                     for (int w = 0; w < W; ++w) s[i] = fmaf(wt[w][i], win[w][i], s[i]);
                     if (a.silu) s[i] = silu_f32<T>(s[i]);
                 }
-                *reinterpret_cast<V*>(y + (t + u) * a.y_stride) = pack<T, VEC>(s);
+                *reinterpret_cast<V*>(yt) = pack<T, VEC>(s);
+                yt += a.y_stride;
+            };
+            V next[kAhead];
+            const int whole = m / kAhead;
+            if (whole > 0) {
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) next[u] = *reinterpret_cast<const V*>(xt + u * a.x_stride);
             }
+            for (int k = 0; k < whole; ++k) {
+                V in[kAhead];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) in[u] = next[u];
+                xt += kAhead * a.x_stride;
+                if (k + 1 < whole) {
+#pragma unroll
+                    for (int u = 0; u < kAhead; ++u) next[u] = *reinterpret_cast<const V*>(xt + u * a.x_stride);
+                }
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) token(in[u]);
+            }
+#pragma unroll 1
+            for (int u = whole * kAhead; u < m; ++u, xt += a.x_stride) token(*reinterpret_cast<const V*>(xt));
         }
-        for (int64_t t = t0 > tv ? t0 : tv; t < t1; ++t) *reinterpret_cast<V*>(y + t * a.y_stride) = V{};
+        for (int64_t t = t0 + (m > 0 ? m : 0); t < t1; ++t) *reinterpret_cast<V*>(y + t * a.y_stride) = V{};
     }
 }
 
@@ -123,12 +139,16 @@ __global__ void __launch_bounds__(kThreads) k_causal_conv_step(const ConvArgs a)
 template <typename T, int VEC, int W>
 cudaError_t launch_w(const ConvArgs& a, bool step, cudaStream_t st) {
     const unsigned gx = (unsigned)((a.channels + (int64_t)kThreads * VEC - 1) / (kThreads * VEC));
-    if (step) {
-        k_causal_conv_step<T, VEC, W><<<dim3(gx, (unsigned)a.batch), kThreads, 0, st>>>(a);
-    } else {
+    constexpr bool whole = VEC * sizeof(T) < 16;  // the vectors of whole sequences, of one token, or single elements
+    constexpr bool token = VEC * sizeof(T) == 16 || VEC == 1;
+    if constexpr (token) {
+        if (step) k_causal_conv_step<T, VEC, W><<<dim3(gx, (unsigned)a.batch), kThreads, 0, st>>>(a);
+    }
+    if constexpr (whole) {
         const int64_t runs = (a.seqlen + kRun - 1) / kRun;
-        k_causal_conv<T, VEC, W>
-            <<<dim3(gx, (unsigned)imin64(runs, 65535), (unsigned)a.batch), kThreads, 0, st>>>(a);
+        if (!step)
+            k_causal_conv<T, VEC, W>
+                <<<dim3(gx, (unsigned)imin64(runs, 65535), (unsigned)a.batch), kThreads, 0, st>>>(a);
     }
     return cudaGetLastError();
 }
@@ -146,14 +166,17 @@ cudaError_t launch_v(const ConvArgs& a, bool step, cudaStream_t st) {
     }
 }
 
-// Vectors of 16 bytes where every row of every tensor starts on 16 bytes,
-// single elements elsewhere.
+// Vectors where every row of every tensor starts on 16 bytes, single elements
+// elsewhere.  8-byte vectors over whole sequences (registers for eight channels of
+// weights, window and loads under way would leave too few warps), 16-byte ones
+// for one token.
 template <typename T>
 cudaError_t launch_t(const ConvArgs& a, bool step, cudaStream_t st) {
     constexpr int VEC = 16 / sizeof(T);
     const uintptr_t p = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y);
     const bool vec = a.channels % VEC == 0 && a.x_stride % VEC == 0 && a.y_stride % VEC == 0 && (p & 15) == 0;
-    return vec ? launch_v<T, VEC>(a, step, st) : launch_v<T, 1>(a, step, st);
+    if (!vec) return launch_v<T, 1>(a, step, st);
+    return step ? launch_v<T, VEC>(a, true, st) : launch_v<T, VEC / 2>(a, false, st);
 }
 
 }  // namespace

@@ -8,7 +8,9 @@
 // memory.  A group lives in the registers of TPG threads (a part of a warp, a
 // warp, or a block), so the mean and then the squares of the differences from
 // it are summed from registers, in fp32 and a fixed order, without a second
-// read.
+// read.  Threads keep their channels and walk down the rows: up to 16 channels to
+// a thread, the weights stay in registers and a row's loads are under way while
+// the row before is summed.
 #include "gated_delta.cuh"
 #include "mamba2_gated_delta.h"
 
@@ -33,102 +35,130 @@ __device__ __forceinline__ float group_sum(float v, float* smem) {
     return v;
 }
 
-// VEC elements per load, NV loads per thread, TPG threads per group.
+// VEC elements per load, NV loads per thread, TPG threads per group.  Groups
+// inside warps: a block spans 2^across groups of a row and as many rows as are
+// left of its threads.
 template <typename T, int VEC, int NV, int TPG>
-__global__ void __launch_bounds__(TPG > 32 ? TPG : kWarpBlock) k_group_norm(const NormArgs a) {
+__global__ void __launch_bounds__(TPG > 32 ? TPG : kWarpBlock) k_group_norm(const NormArgs a, int across) {
     using V = typename VecOf<T, VEC>::type;
     __shared__ float smem[32];
-    const int lane = threadIdx.x % TPG;
-    const int64_t per = TPG > 32 ? 1 : kWarpBlock / TPG;
-    int64_t seg = (int64_t)blockIdx.x * per + threadIdx.x / TPG;
-    const bool live = seg < a.rows * a.ngroups;
-    if (!live) seg = 0;  // stays for the warp's shuffles
-    const int64_t row = seg / a.ngroups, grp = seg - row * a.ngroups;
+    constexpr bool kKeep = NV * VEC <= 16;
+    const int lane = threadIdx.x % TPG, slot = threadIdx.x / TPG;
+    const int rows_per = TPG > 32 ? 1 : (kWarpBlock / TPG) >> across;
+    const int64_t grp = ((int64_t)blockIdx.x << across) + (slot & ((1 << across) - 1));
+    const bool mine = grp < a.ngroups;  // the others stay for the warp's shuffles
     const int size = (int)(a.channels / a.ngroups), nvec = size / VEC;
-    const int64_t c0 = grp * size;
-    const T* x = static_cast<const T*>(a.x) + row * a.x_stride + c0;
+    const int64_t c0 = (mine ? grp : 0) * size;
     const bool before = (a.flags & MAMBA2_NORM_GATE_BEFORE) != 0, after = (a.flags & MAMBA2_NORM_GATE_AFTER) != 0;
     const bool gated = before || after;
+    const T* x = static_cast<const T*>(a.x) + c0;
+    const T* z = static_cast<const T*>(a.z) + c0;
+    T* y = static_cast<T*>(a.y) + c0;
 
-    V xr[NV], zr[NV];
+    float w[kKeep ? NV : 1][VEC];
+    auto weights = [&](int j, float (&f)[VEC]) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int j = lane + i * TPG;
-        xr[i] = V{};
-        if (j < nvec) xr[i] = *reinterpret_cast<const V*>(x + (int64_t)j * VEC);
+        for (int e = 0; e < VEC; ++e) f[e] = a.weight && j < nvec ? a.weight[c0 + (int64_t)j * VEC + e] : 1.f;
+    };
+    if (kKeep) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) weights(lane + i * TPG, w[kKeep ? i : 0]);
     }
-    if (gated) {
-        const T* z = static_cast<const T*>(a.z) + row * a.z_stride + c0;
+
+    int64_t row = (int64_t)blockIdx.y * rows_per + (slot >> across);
+    const int64_t step = (int64_t)gridDim.y * rows_per;
+    V xr[NV], zr[NV];
+    auto load = [&](int64_t r) {
+        const bool live = mine && r < a.rows;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int j = lane + i * TPG;
-            zr[i] = V{};
-            if (j < nvec) zr[i] = *reinterpret_cast<const V*>(z + (int64_t)j * VEC);
+            xr[i] = V{};
+            if (live && j < nvec) xr[i] = *reinterpret_cast<const V*>(x + r * a.x_stride + (int64_t)j * VEC);
         }
-    }
-    float u[NV][VEC];
-    float s = 0.f;
+        if (gated) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        unpack<VEC>(xr[i], u[i], (const T*)nullptr);
-        if (before) {
-            float z[VEC];
-            unpack<VEC>(zr[i], z, (const T*)nullptr);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) u[i][e] *= silu_f32<T>(z[e]);
-        }
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) s += u[i][e];
-    }
-    float mean = 0.f;
-    if (a.flags & MAMBA2_NORM_SUBTRACT_MEAN) mean = group_sum<TPG>(s, smem) / (float)size;
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        if (lane + i * TPG < nvec) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                u[i][e] -= mean;
-                ss = fmaf(u[i][e], u[i][e], ss);
+            for (int i = 0; i < NV; ++i) {
+                const int j = lane + i * TPG;
+                zr[i] = V{};
+                if (live && j < nvec) zr[i] = *reinterpret_cast<const V*>(z + r * a.z_stride + (int64_t)j * VEC);
             }
         }
-    }
-    const float r = rsqrtf(group_sum<TPG>(ss, smem) / (float)size + a.eps);
-    if (!live) return;
-    T* y = static_cast<T*>(a.y) + row * a.y_stride + c0;
+    };
+    load(row);
+    // every thread of the block walks as far (blocks larger than a warp meet at barriers)
+    for (int64_t r0 = (int64_t)blockIdx.y * rows_per; r0 < a.rows; r0 += step, row += step) {
+        float u[NV][VEC];
+        V zc[NV];
+        float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int j = lane + i * TPG;
-        if (j >= nvec) break;
-        const int64_t c = c0 + (int64_t)j * VEC;
-        float w[VEC], o[VEC];
+        for (int i = 0; i < NV; ++i) {
+            unpack<VEC>(xr[i], u[i], (const T*)nullptr);
+            zc[i] = zr[i];
+            if (before) {
+                float gate[VEC];
+                unpack<VEC>(zc[i], gate, (const T*)nullptr);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            w[e] = a.weight ? a.weight[c + e] : 1.f;
-            o[e] = u[i][e] * r * w[e];
+                for (int e = 0; e < VEC; ++e) u[i][e] *= silu_f32<T>(gate[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) s += u[i][e];
         }
-        if (a.bias) {
+        if (kKeep) load(row + step);
+        float mean = 0.f;
+        if (a.flags & MAMBA2_NORM_SUBTRACT_MEAN) mean = group_sum<TPG>(s, smem) / (float)size;
+        float ss = 0.f;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) o[e] += a.bias[c + e];
+        for (int i = 0; i < NV; ++i) {
+            if (lane + i * TPG < nvec) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    u[i][e] -= mean;
+                    ss = fmaf(u[i][e], u[i][e], ss);
+                }
+            }
         }
-        if (after) {
-            float z[VEC];
-            unpack<VEC>(zr[i], z, (const T*)nullptr);
+        const float r = rsqrtf(group_sum<TPG>(ss, smem) / (float)size + a.eps);
+        if (mine && row < a.rows) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) o[e] *= silu_f32<T>(z[e]);
-        } else if (a.flags & MAMBA2_NORM_SILU) {
+            for (int i = 0; i < NV; ++i) {
+                const int j = lane + i * TPG;
+                if (j >= nvec) break;
+                float o[VEC];
+                if (!kKeep) weights(j, w[0]);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) o[e] = silu_f32<T>(o[e]);
+                for (int e = 0; e < VEC; ++e) o[e] = u[i][e] * r * w[kKeep ? i : 0][e];
+                if (a.bias) {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) o[e] += a.bias[c0 + (int64_t)j * VEC + e];
+                }
+                if (after) {
+                    float gate[VEC];
+                    unpack<VEC>(zc[i], gate, (const T*)nullptr);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) o[e] *= silu_f32<T>(gate[e]);
+                } else if (a.flags & MAMBA2_NORM_SILU) {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) o[e] = silu_f32<T>(o[e]);
+                }
+                *reinterpret_cast<V*>(y + row * a.y_stride + (int64_t)j * VEC) = pack<T, VEC>(o);
+            }
         }
-        *reinterpret_cast<V*>(y + (int64_t)j * VEC) = pack<T, VEC>(o);
+        if (!kKeep) load(row + step);
     }
 }
 
 template <typename T, int VEC, int NV, int TPG>
 cudaError_t launch_n(const NormArgs& a, cudaStream_t st) {
-    const int64_t per = TPG > 32 ? 1 : kWarpBlock / TPG;
-    const int64_t blocks = (a.rows * a.ngroups + per - 1) / per;
-    k_group_norm<T, VEC, NV, TPG><<<(unsigned)blocks, TPG > 32 ? TPG : kWarpBlock, 0, st>>>(a);
+    constexpr int block = TPG > 32 ? TPG : kWarpBlock, per = block / TPG;
+    int across = 0;  // as many groups side by side as there are, up to the block
+    while ((2 << across) <= per && (1 << across) < a.ngroups) ++across;
+    const int64_t gx = (a.ngroups + (1 << across) - 1) >> across, rows_per = per >> across;
+    // two rounds of blocks on the whole GPU at most: each then keeps its weights for many rows
+    const int sms = sm_count();
+    const int64_t want = (2 * (2048 / block) * (int64_t)(sms > 0 ? sms : 152) + gx - 1) / gx;
+    const int64_t gy = imin64(imin64((a.rows + rows_per - 1) / rows_per, want < 1 ? 1 : want), 65535);
+    k_group_norm<T, VEC, NV, TPG><<<dim3((unsigned)gx, (unsigned)gy), block, 0, st>>>(a, across);
     return cudaGetLastError();
 }
 

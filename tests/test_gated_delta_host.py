@@ -198,8 +198,8 @@ class _Cuda:
 def test_row_strides_of_slices():
     x = torch.zeros(2, 5, 24)
     row = lambda t, inner=1: bd._rows(_Cuda(t), "x", inner)  # noqa: E731
-    assert row(x) == 24 and row(x[..., 8:16]) == 24 and row(x[..., 8:16].unflatten(-1, (2, 4)), 2) == 24
-    assert row(x[:, :1]) == 120 and row(x[:1, :3]) == 24
+    assert row(x) == 0 and row(x[..., 8:16]) == 24 and row(x[..., 8:16].unflatten(-1, (2, 4)), 2) == 24
+    assert row(x[:, :1]) == 120 and row(x[:1, :3, :8]) == 24 and row(x[:1, :3]) == 0
     for bad in (x[:, :3], x[:, ::2], x[..., ::2], x.transpose(0, 1), torch.zeros(1, 1, 24).expand(2, 5, 24)):
         with pytest.raises(ValueError):
             row(bad)
