@@ -15,11 +15,35 @@ namespace m2 {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kRun = 64;   // tokens per thread
+constexpr int kRun = 128;  // tokens per thread, less where that leaves too few blocks
 constexpr int kAhead = 8;  // loads in flight per thread
 
+// The weights of VEC neighbouring channels: one run of VEC W floats, in 16-byte
+// loads where that is whole ones.
+template <int VEC, int W>
+__device__ __forceinline__ void load_weights(const float* weight, int64_t c, float (&wt)[W][VEC]) {
+    float f[VEC * W];
+    if (VEC * W % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < VEC * W; i += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(weight + c * W + i);
+            f[i] = v.x;
+            if (i + 1 < VEC * W) f[i + 1] = v.y;
+            if (i + 2 < VEC * W) f[i + 2] = v.z;
+            if (i + 3 < VEC * W) f[i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC * W; ++i) f[i] = weight[c * W + i];
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+#pragma unroll
+        for (int w = 0; w < W; ++w) wt[w][i] = f[i * W + w];
+}
+
 template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(kThreads) k_causal_conv(const ConvArgs a) {
+__global__ void __launch_bounds__(kThreads, VEC * W <= 16 ? 5 : 1) k_causal_conv(const ConvArgs a, int run) {
     using V = typename VecOf<T, VEC>::type;
     const int64_t c = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * VEC;
     if (c >= a.channels) return;
@@ -44,14 +68,11 @@ __global__ void __launch_bounds__(kThreads) k_causal_conv(const ConvArgs a) {
 
     float wt[W][VEC], bias[VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        bias[i] = a.bias ? a.bias[c + i] : 0.f;
-#pragma unroll
-        for (int w = 0; w < W; ++w) wt[w][i] = a.weight[(c + i) * W + w];
-    }
+    for (int i = 0; i < VEC; ++i) bias[i] = a.bias ? a.bias[c + i] : 0.f;
+    load_weights<VEC, W>(a.weight, c, wt);
 
-    for (int64_t t0 = (int64_t)blockIdx.y * kRun; t0 < a.seqlen; t0 += (int64_t)gridDim.y * kRun) {
-        const int64_t t1 = imin64(t0 + kRun, a.seqlen);
+    for (int64_t t0 = (int64_t)blockIdx.y * run; t0 < a.seqlen; t0 += (int64_t)gridDim.y * run) {
+        const int64_t t1 = imin64(t0 + run, a.seqlen);
         const int m = (int)(imin64(t1, n) - t0);  // tokens that are computed (none: m <= 0)
         if (m > 0) {
             float win[W][VEC];  // win[w]: the input W - 1 - w tokens back
@@ -103,37 +124,45 @@ __global__ void __launch_bounds__(kThreads) k_causal_conv(const ConvArgs a) {
 
 // One token: a thread reads its channels' state and input, and writes the
 // output and the state moved on by one (in place is safe: it reads all of its
-// own elements first).
+// own elements first).  It takes `rows` batch rows, for which it loads its weights
+// once: they are as many bytes as a row's data.
 template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(kThreads) k_causal_conv_step(const ConvArgs a) {
+__global__ void __launch_bounds__(kThreads) k_causal_conv_step(const ConvArgs a, int rows) {
     using V = typename VecOf<T, VEC>::type;
     const int64_t c = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * VEC;
     if (c >= a.channels) return;
-    const int64_t b = blockIdx.y;
-    const int64_t at = b * (W - 1) * a.channels + c;
-    V in[W];
+    float wt[W][VEC], bias[VEC];
+    load_weights<VEC, W>(a.weight, c, wt);
 #pragma unroll
-    for (int w = 0; w < W - 1; ++w)
-        in[w] = a.init ? *reinterpret_cast<const V*>(static_cast<const T*>(a.init) + at + w * a.channels) : V{};
-    in[W - 1] = *reinterpret_cast<const V*>(static_cast<const T*>(a.x) + b * a.x_stride + c);
-    float s[VEC];
+    for (int i = 0; i < VEC; ++i) bias[i] = a.bias ? a.bias[c + i] : 0.f;
+    const int64_t b0 = (int64_t)blockIdx.y * rows, b1 = imin64(b0 + rows, a.batch);
+#pragma unroll 2
+    for (int64_t b = b0; b < b1; ++b) {
+        const int64_t at = b * (W - 1) * a.channels + c;
+        V in[W];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) s[i] = a.bias ? a.bias[c + i] : 0.f;
+        for (int w = 0; w < W - 1; ++w)
+            in[w] = a.init ? *reinterpret_cast<const V*>(static_cast<const T*>(a.init) + at + w * a.channels) : V{};
+        in[W - 1] = *reinterpret_cast<const V*>(static_cast<const T*>(a.x) + b * a.x_stride + c);
+        float s[VEC];
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-        float f[VEC];
-        unpack<VEC>(in[w], f, (const T*)nullptr);
+        for (int i = 0; i < VEC; ++i) s[i] = bias[i];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) s[i] = fmaf(a.weight[(c + i) * W + w], f[i], s[i]);
+        for (int w = 0; w < W; ++w) {
+            float f[VEC];
+            unpack<VEC>(in[w], f, (const T*)nullptr);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) s[i] = fmaf(wt[w][i], f[i], s[i]);
+        }
+#pragma unroll
+        for (int w = 0; w < W - 1; ++w)
+            *reinterpret_cast<V*>(static_cast<T*>(a.final_state) + at + w * a.channels) = in[w + 1];
+        if (a.silu) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) s[i] = silu_f32<T>(s[i]);
+        }
+        *reinterpret_cast<V*>(static_cast<T*>(a.y) + b * a.y_stride + c) = pack<T, VEC>(s);
     }
-#pragma unroll
-    for (int w = 0; w < W - 1; ++w)
-        *reinterpret_cast<V*>(static_cast<T*>(a.final_state) + at + w * a.channels) = in[w + 1];
-    if (a.silu) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) s[i] = silu_f32<T>(s[i]);
-    }
-    *reinterpret_cast<V*>(static_cast<T*>(a.y) + b * a.y_stride + c) = pack<T, VEC>(s);
 }
 
 template <typename T, int VEC, int W>
@@ -142,13 +171,26 @@ cudaError_t launch_w(const ConvArgs& a, bool step, cudaStream_t st) {
     constexpr bool whole = VEC * sizeof(T) < 16;  // the vectors of whole sequences, of one token, or single elements
     constexpr bool token = VEC * sizeof(T) == 16 || VEC == 1;
     if constexpr (token) {
-        if (step) k_causal_conv_step<T, VEC, W><<<dim3(gx, (unsigned)a.batch), kThreads, 0, st>>>(a);
+        if (step) {
+            // rows per thread: as many as leave eight blocks to an SM, at most 16
+            const int sms = sm_count();
+            const int64_t fill = a.batch * gx / (8 * (int64_t)(sms > 0 ? sms : 152));
+            const int rows = (int)(fill < 1 ? 1 : imin64(fill, 16));
+            k_causal_conv_step<T, VEC, W>
+                <<<dim3(gx, (unsigned)((a.batch + rows - 1) / rows)), kThreads, 0, st>>>(a, rows);
+        }
     }
     if constexpr (whole) {
-        const int64_t runs = (a.seqlen + kRun - 1) / kRun;
-        if (!step)
+        if (!step) {
+            // Runs of 128 tokens (4 x 8192 x 8192: 180 us, 64: 186, 32: 197), halved down to 16 while there are
+            // fewer than four blocks to an SM.
+            const int sms = sm_count();
+            int run = kRun;
+            while (run > 16 && gx * a.batch * ((a.seqlen + run - 1) / run) < 4 * (int64_t)(sms > 0 ? sms : 152)) run /= 2;
+            const int64_t runs = (a.seqlen + run - 1) / run;
             k_causal_conv<T, VEC, W>
-                <<<dim3(gx, (unsigned)imin64(runs, 65535), (unsigned)a.batch), kThreads, 0, st>>>(a);
+                <<<dim3(gx, (unsigned)imin64(runs, 65535), (unsigned)a.batch), kThreads, 0, st>>>(a, run);
+        }
     }
     return cudaGetLastError();
 }

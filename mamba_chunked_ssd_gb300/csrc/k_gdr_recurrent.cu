@@ -11,7 +11,8 @@
 // summed beside r = h^T k over the state before the update, and
 //   w = beta (v - a r),   y = scale (a p + (q . k) w),   h <- a h + k w^T.
 // Sixteen tokens at a time are staged in shared memory as fp32, normalised
-// there where asked, while the next sixteen are on their way in registers.
+// there where asked, while the next sixteen are on their way in registers; a
+// token's row is read from there while the token before is computed.
 #include "gated_delta.cuh"
 
 namespace m2 {
@@ -100,23 +101,32 @@ __global__ void __launch_bounds__(kThreads) k_gdr_recurrent(const GdrArgs a) {
         __syncthreads();
         if (t0 + kTok < n) fetch(t0 + kTok);
         const int nt = (int)imin64(kTok, n - t0);
-        for (int t = 0; t < nt; ++t) {
-            const float4 co = s_c[t];
-            const float vt = s_v[t][c];
-            float kv[RP], r[4] = {0.f, 0.f, 0.f, 0.f}, p[4] = {0.f, 0.f, 0.f, 0.f};
+        float4 k4[2][RP / 4], q4[2][RP / 4], co[2];
+        float vt[2];
+        auto read = [&](int t, int x) {
+            co[x] = s_c[t];
+            vt[x] = s_v[t][c];
 #pragma unroll
-            for (int i = 0; i < RP; i += 4) {
-                const float4 k4 = *reinterpret_cast<const float4*>(&s_k[t][(i / 4) * 32 + rl * 4]);
-                const float4 q4 = *reinterpret_cast<const float4*>(&s_q[t][(i / 4) * 32 + rl * 4]);
-                kv[i] = k4.x, kv[i + 1] = k4.y, kv[i + 2] = k4.z, kv[i + 3] = k4.w;
-                r[0] = fmaf(k4.x, hs[i], r[0]);
-                r[1] = fmaf(k4.y, hs[i + 1], r[1]);
-                r[2] = fmaf(k4.z, hs[i + 2], r[2]);
-                r[3] = fmaf(k4.w, hs[i + 3], r[3]);
-                p[0] = fmaf(q4.x, hs[i], p[0]);
-                p[1] = fmaf(q4.y, hs[i + 1], p[1]);
-                p[2] = fmaf(q4.z, hs[i + 2], p[2]);
-                p[3] = fmaf(q4.w, hs[i + 3], p[3]);
+            for (int i = 0; i < RP / 4; ++i) {
+                k4[x][i] = *reinterpret_cast<const float4*>(&s_k[t][i * 32 + rl * 4]);
+                q4[x][i] = *reinterpret_cast<const float4*>(&s_q[t][i * 32 + rl * 4]);
+            }
+        };
+        auto token = [&](int t, int x) {
+            float r[4] = {0.f, 0.f, 0.f, 0.f}, p[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < RP / 4; ++i) {
+                r[0] = fmaf(k4[x][i].x, hs[4 * i], r[0]);
+                r[1] = fmaf(k4[x][i].y, hs[4 * i + 1], r[1]);
+                r[2] = fmaf(k4[x][i].z, hs[4 * i + 2], r[2]);
+                r[3] = fmaf(k4[x][i].w, hs[4 * i + 3], r[3]);
+            }
+#pragma unroll
+            for (int i = 0; i < RP / 4; ++i) {
+                p[0] = fmaf(q4[x][i].x, hs[4 * i], p[0]);
+                p[1] = fmaf(q4[x][i].y, hs[4 * i + 1], p[1]);
+                p[2] = fmaf(q4[x][i].z, hs[4 * i + 2], p[2]);
+                p[3] = fmaf(q4[x][i].w, hs[4 * i + 3], p[3]);
             }
             float rs = (r[0] + r[1]) + (r[2] + r[3]), ps = (p[0] + p[1]) + (p[2] + p[3]);
 #pragma unroll
@@ -124,10 +134,23 @@ __global__ void __launch_bounds__(kThreads) k_gdr_recurrent(const GdrArgs a) {
                 rs += __shfl_xor_sync(0xffffffffu, rs, m);
                 ps += __shfl_xor_sync(0xffffffffu, ps, m);
             }
-            const float w = co.y * fmaf(-co.x, rs, vt);
+            const float w = co[x].y * fmaf(-co[x].x, rs, vt[x]);
 #pragma unroll
-            for (int i = 0; i < RP; ++i) hs[i] = fmaf(kv[i], w, co.x * hs[i]);
-            if (rl == 0) s_y[t][c] = co.z * fmaf(co.x, ps, co.w * w);
+            for (int i = 0; i < RP / 4; ++i) {
+                hs[4 * i] = fmaf(k4[x][i].x, w, co[x].x * hs[4 * i]);
+                hs[4 * i + 1] = fmaf(k4[x][i].y, w, co[x].x * hs[4 * i + 1]);
+                hs[4 * i + 2] = fmaf(k4[x][i].z, w, co[x].x * hs[4 * i + 2]);
+                hs[4 * i + 3] = fmaf(k4[x][i].w, w, co[x].x * hs[4 * i + 3]);
+            }
+            if (rl == 0) s_y[t][c] = co[x].z * fmaf(co[x].x, ps, co[x].w * w);
+        };
+        read(0, 0);
+        for (int t = 0; t < nt; t += 2) {  // (rows past nt are zeros, and stay unused)
+            read(t + 1, 1);
+            token(t, 0);
+            if (t + 1 >= nt) break;
+            read(t + 2 < kTok ? t + 2 : 0, 0);
+            token(t + 1, 1);
         }
         __syncthreads();
         if (row < nt) {

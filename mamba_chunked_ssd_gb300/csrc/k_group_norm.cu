@@ -35,11 +35,19 @@ __device__ __forceinline__ float group_sum(float v, float* smem) {
     return v;
 }
 
+// Blocks of an SM that the registers have to allow: 1024 threads for up to eight
+// channels to a thread (32768 x 4096 in groups of 64, gated: 132 us, 768 threads
+// 154), 768 for 16 (8192 x 4096 in one group, gated: 46 us, 1024 threads 53, 512 50).
+constexpr int min_blocks(int channels, int tpg) {
+    return tpg > 256 || channels > 16 ? 1 : (channels <= 8 ? 1024 : 768) / (tpg > 32 ? tpg : kWarpBlock);
+}
+
 // VEC elements per load, NV loads per thread, TPG threads per group.  Groups
 // inside warps: a block spans 2^across groups of a row and as many rows as are
 // left of its threads.
 template <typename T, int VEC, int NV, int TPG>
-__global__ void __launch_bounds__(TPG > 32 ? TPG : kWarpBlock) k_group_norm(const NormArgs a, int across) {
+__global__ void __launch_bounds__(TPG > 32 ? TPG : kWarpBlock, min_blocks(NV * VEC, TPG))
+k_group_norm(const NormArgs a, int across) {
     using V = typename VecOf<T, VEC>::type;
     __shared__ float smem[32];
     constexpr bool kKeep = NV * VEC <= 16;
@@ -154,9 +162,15 @@ cudaError_t launch_n(const NormArgs& a, cudaStream_t st) {
     int across = 0;  // as many groups side by side as there are, up to the block
     while ((2 << across) <= per && (1 << across) < a.ngroups) ++across;
     const int64_t gx = (a.ngroups + (1 << across) - 1) >> across, rows_per = per >> across;
-    // two rounds of blocks on the whole GPU at most: each then keeps its weights for many rows
+    // as many blocks as fit on the GPU at once: each keeps its weights for its share of the rows
+    static const int resident = [] {
+        int n = 0;
+        const cudaError_t e =
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_group_norm<T, VEC, NV, TPG>, block, 0);
+        return e == cudaSuccess && n > 0 ? n : 1;
+    }();
     const int sms = sm_count();
-    const int64_t want = (2 * (2048 / block) * (int64_t)(sms > 0 ? sms : 152) + gx - 1) / gx;
+    const int64_t want = (resident * (int64_t)(sms > 0 ? sms : 152) + gx - 1) / gx;
     const int64_t gy = imin64(imin64((a.rows + rows_per - 1) / rows_per, want < 1 ? 1 : want), 65535);
     k_group_norm<T, VEC, NV, TPG><<<dim3((unsigned)gx, (unsigned)gy), block, 0, st>>>(a, across);
     return cudaGetLastError();
