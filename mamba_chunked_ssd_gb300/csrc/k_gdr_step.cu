@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) k_gdr_step(const GdrArgs a) {
     if (!live) return;
 
     const int64_t bh = b * g.nheads + h;
-    const float dec = exp2f(kLog2e * a.gate[bh]), beta = a.beta[bh];
+    const float dec = expf(a.gate[bh]), beta = a.beta[bh];
     qq = s_red[0][0] + s_red[1][0] + s_red[2][0] + s_red[3][0];
     kk = s_red[0][1] + s_red[1][1] + s_red[2][1] + s_red[3][1];
     qk = s_red[0][2] + s_red[1][2] + s_red[2][2] + s_red[3][2];
