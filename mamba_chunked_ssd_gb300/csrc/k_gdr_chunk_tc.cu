@@ -69,7 +69,8 @@ constexpr int kChainWarps = 16, kOutWarps = 4, kNWarp0 = 20, kNWarps = 4, kPWarp
 constexpr int kTmaWarp = 28, kVWarp = 29, kMmaWarp = 30, kPwWarp = 31;
 constexpr int kThreads = 32 * 32;    // 64 registers each
 constexpr uint32_t kBox = kT * 128;  // one box: the chunk's tokens x 64 columns of bf16
-constexpr int kMaxStages = 6, kMaxVStages = 4;
+constexpr int kMaxStages = 5, kMaxVStages = 4;
+constexpr int kBufs = 4;  // of scalars and scratch: how far N's makers may be ahead of the outputs
 constexpr int kSmemLimit = 232448;
 
 struct Tok {       // what the scores need of a token
@@ -92,7 +93,7 @@ struct Scalars {  // one head's, per chunk
 
 // A head's results of the scores: N's three and P's two planes of 32 rows of 128
 // bytes (the first 64 of each used), in one buffer each (they are needed late in
-// a chunk, and written when the chunk before has used them), the scalars in two.
+// a chunk, and written when the chunk before has used them), the scalars in kBufs.
 constexpr uint32_t kPlane = kT * 128;
 constexpr uint32_t kNPlanes = 3, kPPlanes = 2;
 constexpr uint32_t kScalBytes = sizeof(Scalars);
@@ -109,10 +110,10 @@ enum : int {
     kBarFree = kBarFull + kMaxStages,     // [stages] every reader of the stage is done
     kBarVFull = kBarFree + kMaxStages,    // [V stages]
     kBarVFree = kBarVFull + kMaxVStages,  // [V stages]
-    kBarSFull = kBarVFree + kMaxVStages,  // [2] scalars but oq (and K's rows past the end cleared)
-    kBarSFree = kBarSFull + 2,            // [2] scalars and scratch
-    kBarDFull = kBarSFree + 2,            // [2] scratch: A's block and N's diagonal blocks, factors
-    kBarHReady = kBarDFull + 2,           // h's parts are written; y's sum of the chunk before has been read
+    kBarSFull = kBarVFree + kMaxVStages,  // [bufs] scalars but oq (and K's rows past the end cleared)
+    kBarSFree = kBarSFull + kBufs,        // [bufs] scalars and scratch
+    kBarDFull = kBarSFree + kBufs,        // [bufs] scratch: A's block and N's diagonal blocks, factors
+    kBarHReady = kBarDFull + kBufs,        // h's parts are written; y's sum of the chunk before has been read
     kBarRDone,                            // R and Q h
     kBarXReady,                           // X's parts and N are written, h is decayed
     kBarWDone,
@@ -329,7 +330,24 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     const Geom& g = p.g;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int h0 = NV * blockIdx.x;
-    const int64_t b = blockIdx.y;
+    // Ragged batches: blocks are started in order, so the longest rows come first (16 rows of 0 to 1024
+    // tokens, 16 heads of 128: 157 -> 130 us).  A row's place is the number of rows before it.
+    __shared__ int s_row;
+    int64_t b = blockIdx.y;
+    if (p.lengths && g.batch <= kThreads) {
+        const int t = threadIdx.x, count = (int)g.batch;
+        if (t < count) {
+            const int64_t mine = row_length(p.lengths, t, g.seqlen);
+            int before = 0;
+            for (int i = 0; i < count; ++i) {
+                const int64_t other = row_length(p.lengths, i, g.seqlen);
+                before += other > mine || (other == mine && i < t);
+            }
+            if (before == (int)blockIdx.y) s_row = t;
+        }
+        __syncthreads();
+        b = s_row;
+    }
     const int grp = (int)(h0 / g.heads_per_group);
     const int64_t L = g.seqlen, n = row_length(p.lengths, b, L);
     const int nc = (int)((n + kT - 1) / kT);
@@ -355,12 +373,12 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             tc::mbar_init(&bars[kBarVFull + i], 1);
             tc::mbar_init(&bars[kBarVFree + i], kChainWarps);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kBufs; ++i) {
             tc::mbar_init(&bars[kBarSFull + i], kNWarps);
             tc::mbar_init(&bars[kBarSFree + i], 1 + kOutWarps + kPWarps);
             tc::mbar_init(&bars[kBarDFull + i], kNWarps);
-            tc::mbar_init(&bars[kBarDrain + i], 1);
         }
+        for (int i = 0; i < 2; ++i) tc::mbar_init(&bars[kBarDrain + i], 1);
         tc::mbar_init(&bars[kBarHReady], kChainWarps + kOutWarps);
         tc::mbar_init(&bars[kBarRDone], 1);
         tc::mbar_init(&bars[kBarXReady], kChainWarps + kPWarps);
@@ -410,10 +428,10 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         int vs = 0;
         uint32_t v_phase = 0;
         for (int c = 0; c < nc; ++c) {
-            const int buf = c & 1;
+            const int buf = c % kBufs;
             const uint32_t ph = c & 1;
             const Scalars* sc = scal_of(buf, hv);
-            if (!warp_wait(&bars[kBarSFull + buf], (c >> 1) & 1, abort_flag)) { ok = false; break; }
+            if (!warp_wait(&bars[kBarSFull + buf], (c / kBufs) & 1, abort_flag)) { ok = false; break; }
             const float g_last = sc->g_last;
             if (c > 0 && !warp_wait(&bars[kBarHDone], ph ^ 1, abort_flag)) { ok = false; break; }
             tc::tc_fence_after();
@@ -543,11 +561,11 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         __nv_bfloat16* y = p.y + (b * L + odd) * row + (int64_t)(h0 + hv) * H + (colh & ~1);
         if (lane == 0 && nc > 0) tc::mbar_arrive(&bars[kBarHReady]);  // no sum to be read yet
         for (int c = 0; c < nc; ++c) {
-            const int buf = c & 1;
+            const int buf = c % kBufs;
             const uint32_t ph = c & 1;
             const Scalars* sc = scal_of(buf, hv);
             // Q h -> e^G Q h, onto which P W is summed (the second head's in a place of its own)
-            if (!warp_wait<true>(&bars[kBarSFull + buf], (c >> 1) & 1, abort_flag)) { ok = false; break; }
+            if (!warp_wait<true>(&bars[kBarSFull + buf], (c / kBufs) & 1, abort_flag)) { ok = false; break; }
             if (!warp_wait<true>(&bars[kBarRDone], ph, abort_flag)) { ok = false; break; }
             tc::tc_fence_after();
 #pragma unroll 1
@@ -571,26 +589,24 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             const int64_t nleft = n - (int64_t)c * kT, lleft = L - (int64_t)c * kT;
             const int nv = nleft < kT ? (int)nleft : kT, lv = live ? (lleft < kT ? (int)lleft : kT) : 0;
             __nv_bfloat16* yc = y + c * kT * row;
-#pragma unroll 1
-            for (int m = 0; m < kT; m += 16) {
-                uint32_t r[16];
-                tc::tmem_ld16(o_at + m, r);
-                if (m == kT - 16) {
-                    tc::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0 && c + 1 < nc) tc::mbar_arrive(&bars[kBarHReady]);
-                }
+            // (all of it into registers: the next chunk's R | Q h waits for the place)
+            uint32_t r[2][16];
+            tc::tmem_ld16_nowait(o_at, r[0]);
+            tc::tmem_ld16_nowait(o_at + 16, r[1]);
+            tc::tmem_wait_ld16(r[0]);
+            tc::tmem_tie16(r[1]);
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0 && c + 1 < nc) tc::mbar_arrive(&bars[kBarHReady]);
 #pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                    const int i = m + j;
-                    float2 a = tc::mul_f32x2(*reinterpret_cast<const float2*>(&sc->oq[i]), as_f2(&r[j]));
-                    if (nv < kT) a = make_float2(i < nv ? a.x : 0.f, i + 1 < nv ? a.y : 0.f);
-                    const uint32_t both = tc::pack_bf16x2(a.x, a.y);  // this column of tokens i, i + 1
-                    const uint32_t other = __shfl_xor_sync(0xffffffffu, both, 1);
-                    const uint32_t pair = odd ? __byte_perm(other, both, 0x7632) : __byte_perm(both, other, 0x5410);
-                    if (i + odd < lv) *reinterpret_cast<uint32_t*>(yc) = pair;
-                    yc += 2 * row;
-                }
+            for (int i = 0; i < kT; i += 2) {
+                float2 a = tc::mul_f32x2(*reinterpret_cast<const float2*>(&sc->oq[i]), as_f2(&r[i >> 4][i & 15]));
+                if (nv < kT) a = make_float2(i < nv ? a.x : 0.f, i + 1 < nv ? a.y : 0.f);
+                const uint32_t both = tc::pack_bf16x2(a.x, a.y);  // this column of tokens i, i + 1
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, both, 1);
+                const uint32_t pair = odd ? __byte_perm(other, both, 0x7632) : __byte_perm(both, other, 0x5410);
+                if (i + odd < lv) *reinterpret_cast<uint32_t*>(yc) = pair;
+                yc += 2 * row;
             }
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bars[kBarSFree + buf]);
@@ -618,9 +634,9 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         int st = 0;
         uint32_t full_phase = 0;
         for (int c = 0; c < nc; ++c) {
-            const int buf = c & 1;
+            const int buf = c % kBufs;
             // every warp comes to the barrier below, whatever its waits said
-            if (ok && c >= 2) ok = warp_wait<true>(&bars[kBarSFree + buf], ((c >> 1) - 1) & 1, abort_flag);
+            if (ok && c >= kBufs) ok = warp_wait<true>(&bars[kBarSFree + buf], (c / kBufs - 1) & 1, abort_flag);
             if (w == 3 && ok) {
 #pragma unroll
                 for (int hv = 0; hv < NV; ++hv) {
@@ -760,10 +776,10 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         int st = 0;
         uint32_t full_phase = 0;
         for (int c = 0; c < nc; ++c) {
-            const int buf = c & 1;
+            const int buf = c % kBufs;
             // N's place is free once the last chunk's W is done
             ok = warp_wait<true>(&bars[kBarFull + st], full_phase, abort_flag) &&
-                 warp_wait<true>(&bars[kBarDFull + buf], (c >> 1) & 1, abort_flag) &&
+                 warp_wait<true>(&bars[kBarDFull + buf], (c / kBufs) & 1, abort_flag) &&
                  (c == 0 || warp_wait<true>(&bars[kBarWDone], (c - 1) & 1, abort_flag));
             if (!ok) break;
             // N_10 = -N_11 A_10 N_00 and all of N into its planes, eight columns (of a head's half) to a
@@ -940,7 +956,7 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 const uint64_t dN = tc::sdesc_sw128(tc::smem_u32(smem + p.off_n), 16, 1024);
                 int st = 0;
                 for (int c = 0; c < nc; ++c) {
-                    const int buf = c & 1;
+                    const int buf = c % kBufs;
                     const uint32_t ph = c & 1;
                     const uint32_t aK = tc::smem_u32(smem + st * kStage);
                     const uint64_t dK = tc::sdesc_sw128(aK, 16, 1024);
@@ -1050,8 +1066,8 @@ cudaError_t launch_k(const GdrArgs& a, cudaStream_t st) {
     p.l2_eps = a.l2_eps;
     p.l2norm = a.l2norm;
     constexpr uint32_t stage = 2 * (S / 64) * kBox, vstage = NV * H / 64 * kBox;
-    constexpr uint32_t rest = kMaxVStages * vstage + NV * ((kNPlanes + kPPlanes) * kPlane + 2 * kScalBytes) +
-                              2 * NV * (uint32_t)sizeof(NScratch) + kNumBars * 8 + (uint32_t)sizeof(SharedCtl) + 1024;
+    constexpr uint32_t rest = kMaxVStages * vstage + NV * ((kNPlanes + kPPlanes) * kPlane + kBufs * kScalBytes) +
+                              kBufs * NV * (uint32_t)sizeof(NScratch) + kNumBars * 8 + (uint32_t)sizeof(SharedCtl) + 1024;
     static_assert(kMaxStages * stage + rest <= (uint32_t)kSmemLimit, "shared memory");
     p.nst = kMaxStages;
     p.nvst = kMaxVStages;
@@ -1059,8 +1075,8 @@ cudaError_t launch_k(const GdrArgs& a, cudaStream_t st) {
     p.off_n = p.off_v + kMaxVStages * vstage;
     p.off_p = p.off_n + NV * kNPlanes * kPlane;
     p.off_scal = p.off_p + NV * kPPlanes * kPlane;
-    p.off_scratch = p.off_scal + 2 * NV * kScalBytes;
-    p.off_bar = p.off_scratch + 2 * NV * (uint32_t)sizeof(NScratch);
+    p.off_scratch = p.off_scal + kBufs * NV * kScalBytes;
+    p.off_bar = p.off_scratch + kBufs * NV * (uint32_t)sizeof(NScratch);
     const int smem = (int)(kMaxStages * stage + rest);
 
     CUtensorMap tm_q, tm_k, tm_v;
