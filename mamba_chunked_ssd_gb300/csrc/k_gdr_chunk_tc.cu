@@ -69,7 +69,7 @@ constexpr int kChainWarps = 16, kOutWarps = 4, kNWarp0 = 20, kNWarps = 4, kPWarp
 constexpr int kTmaWarp = 28, kVWarp = 29, kMmaWarp = 30, kPwWarp = 31;
 constexpr int kThreads = 32 * 32;    // 64 registers each
 constexpr uint32_t kBox = kT * 128;  // one box: the chunk's tokens x 64 columns of bf16
-constexpr int kMaxStages = 5, kMaxVStages = 4;
+constexpr int kMaxStages = 4, kMaxVStages = 4;
 constexpr int kBufs = 4;  // of scalars and scratch: how far N's makers may be ahead of the outputs
 constexpr int kSmemLimit = 232448;
 
@@ -101,7 +101,8 @@ static_assert(kScalBytes % 16 == 0, "scalars");
 
 struct NScratch {           // one head's, per chunk, in fp32
     float diag[2][16][20];  // A's diagonal blocks, then N's, a column in a row
-    float low[16][20];      // A's block (1, 0), a column in a row
+    float n10[16][20];      // N's block (1, 0) (behind the others: see its use)
+    float low[16][20];      // A's block (1, 0)
     float4 fac[3][2][32];   // rk_j e^{G_i - G_j} of the blocks, as the mma's threads hold them: A's and P's factors
 };
 
@@ -436,20 +437,14 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             if (c > 0 && !warp_wait(&bars[kBarHDone], ph ^ 1, abort_flag)) { ok = false; break; }
             tc::tc_fence_after();
             // h's parts
-            {
-                uint32_t r[S / 64][16];
+#pragma unroll 1
+            for (int s = s0; s < s0 + S / 4; s += 16) {
+                uint32_t r[16], hi[8], lo[8];
+                tc::tmem_ld16(tl + cH + s, r);
 #pragma unroll
-                for (int m = 0; m < S / 64; ++m) tc::tmem_ld16_nowait(tl + cH + s0 + 16 * m, r[m]);
-                tc::tmem_wait_ld16(r[0]);
-                if (S == 128) tc::tmem_tie16(r[S / 64 - 1]);
-#pragma unroll
-                for (int m = 0; m < S / 64; ++m) {
-                    uint32_t hi[8], lo[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) split2(as_f2(&r[m][2 * j]), hi[j], lo[j]);
-                    tc::tmem_st8(tl + cHi + s0 / 2 + 8 * m, hi);
-                    tc::tmem_st8(tl + cLo + s0 / 2 + 8 * m, lo);
-                }
+                for (int j = 0; j < 8; ++j) split2(as_f2(&r[2 * j]), hi[j], lo[j]);
+                tc::tmem_st8(tl + cHi + s / 2, hi);
+                tc::tmem_st8(tl + cLo + s / 2, lo);
             }
             tc::tmem_wait_st();
             tc::tc_fence_before();
@@ -713,9 +708,11 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     const float f0 = in0 ? ti0.beta * ti0.rk : 0.f, f1 = in1 ? ti1.beta * ti1.rk : 0.f;
                     const float e0 = decay(ti0, tr), e1 = decay(ti1, tr);
                     float(*a)[20] = w < 2 ? scr->diag[w] : scr->low;
-#pragma unroll
+#pragma unroll 1
                     for (int nt = 0; nt < 2; ++nt) {
-                        float c[2][2];
+                        float c[2][2], s[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) s[x] = nt ? acc[1][x] : acc[0][x];
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             const int jj = 8 * nt + 2 * tig + x;
@@ -728,8 +725,8 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                                 c[0][x] = e0 * cj;
                                 c[1][x] = e1 * cj;
                             }
-                            a[jj][gid] = in0 && (w == 2 || jj < gid) ? acc[nt][x] * (f0 * c[0][x]) : 0.f;
-                            a[jj][gid + 8] = in1 && (w == 2 || jj < gid + 8) ? acc[nt][2 + x] * (f1 * c[1][x]) : 0.f;
+                            a[jj][gid] = in0 && (w == 2 || jj < gid) ? s[x] * (f0 * c[0][x]) : 0.f;
+                            a[jj][gid + 8] = in1 && (w == 2 || jj < gid + 8) ? s[2 + x] * (f1 * c[1][x]) : 0.f;
                         }
                         scr->fac[w][nt][lane] = make_float4(c[0][0], c[0][1], c[1][0], c[1][1]);
                     }
@@ -793,87 +790,80 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     const float4 v = *reinterpret_cast<const float4*>(&m.diag[0][col][i]);
                     x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
                 }
-                float2 o[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                block_times(o, x, [&](int k) { return *reinterpret_cast<const float4*>(&m.low[k][4 * r4]); });
-                gather(x, o, lane);
-                o[0] = o[1] = make_float2(0.f, 0.f);
-                block_times(o, x, [&](int k) { return *reinterpret_cast<const float4*>(&m.diag[1][k][4 * r4]); });
+                float2 o[2];
+#pragma unroll 1
+                for (int f = 0; f < 2; ++f) {  // A_10's product, then N_11's
+                    const float(*blk)[20] = f ? m.diag[1] : m.low;
+                    o[0] = o[1] = make_float2(0.f, 0.f);
+                    block_times(o, x, [&](int k) { return *reinterpret_cast<const float4*>(&blk[k][4 * r4]); });
+                    gather(x, o, lane);
+                }
+                NScratch& to = *scratch_of(buf, hv);
+                *reinterpret_cast<float4*>(&to.n10[col][4 * r4]) = make_float4(-o[0].x, -o[0].y, -o[1].x, -o[1].y);
                 const uint32_t at = p.off_n + hv * kNPlanes * kPlane + 2 * (col & 7);
-#pragma unroll
-                for (int blk = 0; blk < 3; ++blk) {  // (0, 0), (1, 1), (1, 0)
+#pragma unroll 1
+                for (int blk = 0; blk < 3; ++blk) {  // (0, 0), (1, 1), (1, 0), one behind the other in the scratch
+                    const float4 f = *reinterpret_cast<const float4*>(&to.diag[0][0][0] + blk * 320 + col * 20 + 4 * r4);
                     const int row = (blk ? 16 : 0) + 4 * r4, ch = (blk == 1 ? 2 : 0) + (col >> 3);
-                    float2 v[2];
-                    if (blk < 2) {
-                        const float4 f = *reinterpret_cast<const float4*>(&m.diag[blk][col][4 * r4]);
-                        v[0] = make_float2(f.x, f.y);
-                        v[1] = make_float2(f.z, f.w);
-                    } else {
-                        v[0] = make_float2(-o[0].x, -o[0].y);
-                        v[1] = make_float2(-o[1].x, -o[1].y);
+                    float2 v0 = make_float2(f.x, f.y), v1 = make_float2(f.z, f.w);
+#pragma unroll 1
+                    for (uint32_t pl = 0; pl < kNPlanes; ++pl) {
+                        const uint32_t t0 = high(v0), t1 = high(v1);
+                        uint8_t* dst = smem + at + pl * kPlane;
+                        *reinterpret_cast<uint16_t*>(dst + sw(row, ch)) = (uint16_t)t0;
+                        *reinterpret_cast<uint16_t*>(dst + sw(row + 1, ch)) = (uint16_t)(t0 >> 16);
+                        *reinterpret_cast<uint16_t*>(dst + sw(row + 2, ch)) = (uint16_t)t1;
+                        *reinterpret_cast<uint16_t*>(dst + sw(row + 3, ch)) = (uint16_t)(t1 >> 16);
                     }
-#pragma unroll
-                    for (int pl = 0; pl < (int)kNPlanes; ++pl)
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const uint32_t two = high(v[r]);
-                            uint8_t* to = smem + at + pl * kPlane;
-                            *reinterpret_cast<uint16_t*>(to + sw(row + 2 * r, ch)) = (uint16_t)two;
-                            *reinterpret_cast<uint16_t*>(to + sw(row + 2 * r + 1, ch)) = (uint16_t)(two >> 16);
-                        }
                 }
             }
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bars[kBarXReady]);
             const uint32_t aK = tc::smem_u32(smem + st * kStage), aQ = aK + kBox;
-            // (P's place is free once the last chunk's P W is done)
-            if (w == 3) {
 #pragma unroll 1
-                for (int i = 0; i < 2; ++i) {
+            for (int r = 0; r < (w == 3 ? 2 : 1); ++r) {
+                const int bi = w == 3 ? r : (w == 0 ? 0 : 1), bj = w == 3 ? r : (w == 1 ? 1 : 0), i0 = 16 * bi + gid;
+                float acc[2][4];
+                if (w < 3 || p.l2norm) score_block<S>(aQ, w == 3 ? aQ : aK, bi, bj, lane, acc);
+                // P's place is free once the last chunk's P W is done
+                if (c > 0) ok = warp_wait<true>(&bars[kBarPDone], (c - 1) & 1, abort_flag);
+                if (!ok) break;
+                if (w == 3) {
                     if (p.l2norm) {
-                        float acc[2][4];
-                        score_block<S>(aQ, aQ, i, i, lane, acc);
-                        diag_norm(acc, lane, p.l2_eps, [&](int r, float f) {
+                        diag_norm(acc, lane, p.l2_eps, [&](int r16, float f) {
 #pragma unroll
-                            for (int hv = 0; hv < NV; ++hv) scal_of(buf, hv)->oq[16 * i + r] = p.scale * f;
+                            for (int hv = 0; hv < NV; ++hv) scal_of(buf, hv)->oq[16 * bi + r16] = p.scale * f;
                         });
                     } else if (lane < 16) {
 #pragma unroll
-                        for (int hv = 0; hv < NV; ++hv) scal_of(buf, hv)->oq[16 * i + lane] = p.scale;
+                        for (int hv = 0; hv < NV; ++hv) scal_of(buf, hv)->oq[16 * bi + lane] = p.scale;
                     }
+                    continue;
                 }
-                if (c > 0) ok = warp_wait<true>(&bars[kBarPDone], (c - 1) & 1, abort_flag);
-                if (!ok) break;
-            } else {
-                const int bi = w == 0 ? 0 : 1, bj = w == 1 ? 1 : 0, i0 = 16 * bi + gid;
-                float acc[2][4];
-                score_block<S>(aQ, aK, bi, bj, lane, acc);
-                if (c > 0) ok = warp_wait<true>(&bars[kBarPDone], (c - 1) & 1, abort_flag);
-                if (!ok) break;
 #pragma unroll 1
-                for (int hv = 0; hv < NV; ++hv) {
+                for (int t = 0; t < 2 * NV; ++t) {
+                    const int hv = t >> 1, nt = t & 1, j0 = 16 * bj + 8 * nt + 2 * tig;
                     uint8_t* sP = p_of(hv);
-#pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        const int j0 = 16 * bj + 8 * nt + 2 * tig;
-                        const float4 f = scratch_of(buf, hv)->fac[w][nt][lane];
-                        float2 a0 = tc::mul_f32x2(make_float2(f.x, f.y), make_float2(acc[nt][0], acc[nt][1]));
-                        float2 a1 = tc::mul_f32x2(make_float2(f.z, f.w), make_float2(acc[nt][2], acc[nt][3]));
-                        if (w != 2) {
-                            a0 = make_float2(j0 <= i0 ? a0.x : 0.f, j0 + 1 <= i0 ? a0.y : 0.f);
-                            a1 = make_float2(j0 <= i0 + 8 ? a1.x : 0.f, j0 + 1 <= i0 + 8 ? a1.y : 0.f);
-                        }
-                        const uint32_t o0 = sw(i0, 2 * bj + nt) + 4 * tig;
-                        uint32_t hi, lo;
-                        split2(a0, hi, lo);
-                        *reinterpret_cast<uint32_t*>(sP + o0) = hi;
-                        *reinterpret_cast<uint32_t*>(sP + kPlane + o0) = lo;
-                        split2(a1, hi, lo);
-                        *reinterpret_cast<uint32_t*>(sP + o0 + 1024) = hi;
-                        *reinterpret_cast<uint32_t*>(sP + kPlane + o0 + 1024) = lo;
-                    }
+                    const float4 f = scratch_of(buf, hv)->fac[w][nt][lane];
+                    float2 a0 = nt ? make_float2(acc[1][0], acc[1][1]) : make_float2(acc[0][0], acc[0][1]);
+                    float2 a1 = nt ? make_float2(acc[1][2], acc[1][3]) : make_float2(acc[0][2], acc[0][3]);
+                    a0 = tc::mul_f32x2(make_float2(f.x, f.y), a0);
+                    a1 = tc::mul_f32x2(make_float2(f.z, f.w), a1);
+                    // (in block (1, 0) every j is below every i)
+                    a0 = make_float2(j0 <= i0 ? a0.x : 0.f, j0 + 1 <= i0 ? a0.y : 0.f);
+                    a1 = make_float2(j0 <= i0 + 8 ? a1.x : 0.f, j0 + 1 <= i0 + 8 ? a1.y : 0.f);
+                    const uint32_t o0 = sw(i0, 2 * bj + nt) + 4 * tig;
+                    uint32_t hi, lo;
+                    split2(a0, hi, lo);
+                    *reinterpret_cast<uint32_t*>(sP + o0) = hi;
+                    *reinterpret_cast<uint32_t*>(sP + kPlane + o0) = lo;
+                    split2(a1, hi, lo);
+                    *reinterpret_cast<uint32_t*>(sP + o0 + 1024) = hi;
+                    *reinterpret_cast<uint32_t*>(sP + kPlane + o0 + 1024) = lo;
                 }
             }
+            if (!ok) break;
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -965,7 +955,7 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     // their makers for K and Q, whose rows past the end they cleared.)
                     if (!thread_wait<false>(&bars[kBarHReady], ph, abort_flag)) { ok = false; break; }
                     tc::tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                     for (int x = 0; x < 2 * kBoxes; ++x) {
                         const uint32_t id = x < kBoxes ? id_rq : id_t, box = x < kBoxes ? x : x - kBoxes;
                         const uint64_t d = dK + box * (2 * kBox >> 4);
@@ -978,7 +968,7 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     // rows from 16 on
                     if (!thread_wait<false>(&bars[kBarXReady], ph, abort_flag)) { ok = false; break; }
                     tc::tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                     for (int x = 0; x < 2 * NV; ++x) {
                         const int kb = x & 1, hv = x >> 1;
                         const uint32_t a = tmem + cX + 8 * kb, d = tmem + (hv ? cR2 : cR) + 16 * kb;
@@ -995,7 +985,7 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     // h += K^T W
                     if (!thread_wait<false>(&bars[kBarWReady], ph, abort_flag)) { ok = false; break; }
                     tc::tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                     for (int kt = 0; kt < 2; ++kt) {
 #pragma unroll
                         for (int part = 0; part < 3; ++part)
