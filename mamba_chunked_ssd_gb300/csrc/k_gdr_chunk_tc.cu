@@ -791,7 +791,7 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
                 }
                 float2 o[2];
-#pragma unroll 1
+#pragma unroll (NV)
                 for (int f = 0; f < 2; ++f) {  // A_10's product, then N_11's
                     const float(*blk)[20] = f ? m.diag[1] : m.low;
                     o[0] = o[1] = make_float2(0.f, 0.f);
@@ -806,7 +806,7 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     const float4 f = *reinterpret_cast<const float4*>(&to.diag[0][0][0] + blk * 320 + col * 20 + 4 * r4);
                     const int row = (blk ? 16 : 0) + 4 * r4, ch = (blk == 1 ? 2 : 0) + (col >> 3);
                     float2 v0 = make_float2(f.x, f.y), v1 = make_float2(f.z, f.w);
-#pragma unroll 1
+#pragma unroll
                     for (uint32_t pl = 0; pl < kNPlanes; ++pl) {
                         const uint32_t t0 = high(v0), t1 = high(v1);
                         uint8_t* dst = smem + at + pl * kPlane;
@@ -985,7 +985,7 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     // h += K^T W
                     if (!thread_wait<false>(&bars[kBarWReady], ph, abort_flag)) { ok = false; break; }
                     tc::tc_fence_after();
-#pragma unroll 1
+#pragma unroll
                     for (int kt = 0; kt < 2; ++kt) {
 #pragma unroll
                         for (int part = 0; part < 3; ++part)
