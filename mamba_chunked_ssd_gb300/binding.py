@@ -14,6 +14,7 @@ group norm, of include/mamba2_gated_delta.h.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -264,7 +265,8 @@ def mamba2_ssd_step(x, dt, A, B, C, state_in=None, D=None, state_out=None, y=Non
 
 # The gated-delta-rule entry points are also called once a token, where the host
 # call is the time: they pass plain integers (ctypes makes the pointers), ask for
-# the raw stream, and check a tensor's layout in as few attribute reads as will do.
+# the raw stream, check a tensor's layout in as few attribute reads as will do, and
+# keep the structures that describe a call's sizes (never its tensors).
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
@@ -323,6 +325,12 @@ def _like(t, given, name):
     return given
 
 
+_gdr_shape = functools.lru_cache(maxsize=1024)(lambda *a: mamba2_shape(*a))
+_gdr_options = functools.lru_cache(maxsize=1024)(lambda *a: mamba2_gdr_options(*a))
+_conv_shape = functools.lru_cache(maxsize=1024)(lambda *a: mamba2_conv_shape(*a))
+_norm_shape = functools.lru_cache(maxsize=1024)(lambda *a: mamba2_norm_shape(*a))
+
+
 def _gdr_args(q, k, v, g, beta, scale, qk_l2norm, l2_eps):
     """The shape and options of a gated-delta-rule call; checks q, k, v, g, beta."""
     vs, qs, dt = v.shape, q.shape, v.dtype
@@ -333,9 +341,9 @@ def _gdr_args(q, k, v, g, beta, scale, qk_l2norm, l2_eps):
         raise TypeError("q, k and v must have one dtype")
     _want(g, "g", torch.float32, rows), _want(beta, "beta", torch.float32, rows)
     S = qs[-1]
-    shape = mamba2_shape(vs[0], vs[1] if len(vs) == 4 else 1, nh, vs[-1], S, qs[-2], 64, _dtype_code(v), 0)
-    opt = mamba2_gdr_options(_rows(q, "q", 2), _rows(k, "k", 2), _rows(v, "v", 2), S ** -0.5 if scale is None else scale,
-                             l2_eps, MAMBA2_GDR_QK_L2NORM if qk_l2norm else 0, 0)
+    shape = _gdr_shape(vs[0], vs[1] if len(vs) == 4 else 1, nh, vs[-1], S, qs[-2], 64, _dtype_code(v), 0)
+    opt = _gdr_options(_rows(q, "q", 2), _rows(k, "k", 2), _rows(v, "v", 2), S ** -0.5 if scale is None else scale,
+                       l2_eps, MAMBA2_GDR_QK_L2NORM if qk_l2norm else 0, 0)
     return shape, opt, (vs[0], nh, S, vs[-1])
 
 
@@ -396,8 +404,8 @@ def mamba2_causal_conv_fwd(x, weight, bias=None, silu=True, initial_state=None, 
         _want(final_state, "final_state", x.dtype, (b, W - 1, C))
     elif want_final_state:
         final_state = torch.empty((b, W - 1, C), device=x.device, dtype=x.dtype)
-    shape = mamba2_conv_shape(b, L, C, W, _rows(x, "x", 1), _rows(y, "y", 1), _dtype_code(x),
-                              MAMBA2_CONV_SILU if silu else 0)
+    shape = _conv_shape(b, L, C, W, _rows(x, "x", 1), _rows(y, "y", 1), _dtype_code(x),
+                        MAMBA2_CONV_SILU if silu else 0)
     rc = load_library().mamba2_causal_conv_fwd(shape, _at(x), _at(weight), _at(bias), _at(lengths), _at(initial_state),
                                                _at(y), _at(final_state), _on(stream, x))
     if rc:
@@ -418,8 +426,8 @@ def mamba2_causal_conv_step(x, weight, state_in=None, bias=None, silu=True, stat
         state_out = torch.empty(state, device=x.device, dtype=x.dtype)
     elif state_out is not state_in:
         _want(state_out, "state_out", x.dtype, state)
-    shape = mamba2_conv_shape(b, 1, C, W, _rows(x, "x", 1), _rows(y, "y", 1), _dtype_code(x),
-                              MAMBA2_CONV_SILU if silu else 0)
+    shape = _conv_shape(b, 1, C, W, _rows(x, "x", 1), _rows(y, "y", 1), _dtype_code(x),
+                        MAMBA2_CONV_SILU if silu else 0)
     rc = load_library().mamba2_causal_conv_step(shape, _at(x), _at(weight), _at(bias), _at(state_in), _at(state_out),
                                                 _at(y), _on(stream, x))
     if rc:
@@ -440,9 +448,9 @@ def mamba2_group_norm(x, weight, ngroups, z=None, bias=None, eps=1e-5, subtract_
     if z is not None:
         _like(x, z, "z")
     y = _like(x, y, "y")
-    shape = mamba2_norm_shape(x.numel() // C if C else 0, C, ngroups, _rows(x, "x", 1),
-                              0 if z is None else _rows(z, "z", 1), _rows(y, "y", 1), eps, _dtype_code(x),
-                              flags | MAMBA2_NORM_SUBTRACT_MEAN if subtract_mean else flags, 0)
+    shape = _norm_shape(x.numel() // C if C else 0, C, ngroups, _rows(x, "x", 1),
+                        0 if z is None else _rows(z, "z", 1), _rows(y, "y", 1), eps, _dtype_code(x),
+                        flags | MAMBA2_NORM_SUBTRACT_MEAN if subtract_mean else flags, 0)
     rc = load_library().mamba2_group_norm(shape, _at(x), _at(z), _at(weight), _at(bias), _at(y), _on(stream, x))
     if rc:
         _check("mamba2_group_norm", rc)

@@ -9,11 +9,12 @@ they come out of, since every operator takes a token stride.  ``prefill`` runs
 whole (ragged) sequences, ``step`` one token of each; both carry the
 convolution's last inputs and the fp32 state, which a later call continues from.
 
-Run ``python -m mamba_chunked_ssd_gb300.gated_delta_layer`` for a prompt and a few
-decoded tokens on random weights.
+Run ``python -m mamba_chunked_ssd_gb300.gated_delta_layer`` for a ragged batch of
+prompts and a few decoded tokens on random weights (``--help`` for the sizes).
 """
 from __future__ import annotations
 
+import argparse
 from dataclasses import dataclass
 
 import torch
@@ -88,15 +89,22 @@ class GatedDeltaLayer:
         return self._finish(y, z)
 
 
-def main():
-    layer = GatedDeltaLayer(1024, 16, 8, 64, 128)
-    u = torch.randn(2, 300, 1024, device="cuda").bfloat16()
-    out, carried = layer.prefill(u, lengths=torch.tensor([300, 120], dtype=torch.int32, device="cuda"))
-    token = out[:, 119]
-    for _ in range(4):
+def main(argv=None):
+    ap = argparse.ArgumentParser(description="A batch of prompts and a few decoded tokens through the layer.")
+    for name, default in (("batch", 2), ("tokens", 300), ("width", 1024), ("heads", 16), ("groups", 8),
+                          ("headdim", 64), ("dstate", 128), ("decode", 4)):
+        ap.add_argument(f"--{name}", type=int, default=default)
+    a = ap.parse_args(argv)
+    layer = GatedDeltaLayer(a.width, a.heads, a.groups, a.headdim, a.dstate)
+    u = torch.randn(a.batch, a.tokens, a.width, device="cuda").bfloat16()
+    # rows of every length from L down
+    n = torch.tensor([a.tokens - a.tokens * i // (2 * a.batch) for i in range(a.batch)], dtype=torch.int32, device="cuda")
+    out, carried = layer.prefill(u, lengths=n)
+    token = out[torch.arange(a.batch, device="cuda"), n.long() - 1]
+    for _ in range(a.decode):
         token = layer.step(token, carried)
     bd.mamba2_check_device_status()
-    print(f"prefill {tuple(out.shape)}, four tokens decoded, state {tuple(carried.state.shape)}, "
+    print(f"prefill {tuple(out.shape)}, {a.decode} tokens decoded, state {tuple(carried.state.shape)}, "
           f"last output's rms {token.float().square().mean().sqrt().item():.3f}")
 
 

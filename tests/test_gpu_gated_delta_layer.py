@@ -102,5 +102,5 @@ def test_ragged_prefill_is_its_rows(layer):
 
 
 def test_the_example_runs(capsys):
-    main()
-    assert "four tokens decoded" in capsys.readouterr().out
+    main([])
+    assert "4 tokens decoded" in capsys.readouterr().out
