@@ -116,6 +116,49 @@ def test_gdr_ragged_batch(H, l2norm):
         assert bool((y[i, n:] == 0).all())
 
 
+def test_gdr_ragged_batch_of_more_rows_than_threads():
+    """More rows than a block has threads to order them with."""
+    b, L = 1030, 40
+    d, h0 = gdr_inputs(b, L, 1, 1, 64, 64, BF16)
+    lengths = (torch.arange(b, device="cuda", dtype=torch.int32) * 7) % (L + 1)
+    y, fin = bd.mamba2_gdr_fwd(**d, initial_state=h0, lengths=lengths)
+    y_ref, fin_ref = ref.gdr(**d, scale=0.125, init=h0, lengths=lengths)
+    assert rel_err(np64(y), y_ref) <= TOL_Y[BF16] and rel_err(np64(fin), fin_ref) <= TOL_STATE
+
+
+@pytest.mark.parametrize("value,where", [("g", 70), ("beta", 70), ("k", 70), ("v", 70)])
+def test_gdr_nan_input_shows_from_its_token_on(value, where):
+    """A NaN in one head's input leaves the other heads and the tokens before it."""
+    d, h0 = gdr_inputs(1, 140, 2, 2, 128, 128, BF16)
+    clean, _ = bd.mamba2_gdr_fwd(**d, initial_state=h0)
+    d[value][0, where, 1] = NAN
+    y, fin = bd.mamba2_gdr_fwd(**d, initial_state=h0)
+    assert torch.equal(y[:, :, 0], clean[:, :, 0]) and torch.isfinite(fin[0, 0]).all()
+    start = where // 32 * 32  # a chunk's tokens share products with zeros in them
+    assert torch.equal(y[:, :start, 1], clean[:, :start, 1])
+    assert torch.isnan(y[0, where:, 1]).all() and torch.isnan(fin[0, 1]).all()
+
+
+def test_gdr_offsets_beyond_32_bits():
+    """v and y of more than 2^31 elements: the sequence's end, from the state that
+    enters it, against a call on the end alone."""
+    L, cut, nh, H = 540_000, 539_700, 64, 64
+    r = torch.Generator(device="cuda").manual_seed(1)
+    n = lambda *s: torch.randn(*s, generator=r, device="cuda", dtype=BF16)  # noqa: E731
+    q, k, v = n(1, L, 1, 64), n(1, L, 1, 64), n(1, L, nh, H)
+    g = -torch.rand(1, L, nh, generator=r, device="cuda")
+    beta = torch.rand(1, L, nh, generator=r, device="cuda")
+    assert v.numel() > 2 ** 31
+    y, fin = bd.mamba2_gdr_fwd(q, k, v, g, beta, qk_l2norm=True)
+    part = lambda t, s: t[:, s].contiguous()  # noqa: E731
+    # decays of e^-0.5 a token on average: nothing is left of what came 1000 tokens before
+    a, b = slice(cut - 3000, cut), slice(cut, L)
+    _, mid = bd.mamba2_gdr_fwd(*(part(t, a) for t in (q, k, v, g, beta)), qk_l2norm=True)
+    y2, fin2 = bd.mamba2_gdr_fwd(*(part(t, b) for t in (q, k, v, g, beta)), qk_l2norm=True, initial_state=mid)
+    assert rel_err(np64(y[:, cut:]), np64(y2)) <= TOL_Y[BF16]
+    assert rel_err(np64(fin), np64(fin2)) <= TOL_STATE
+
+
 @pytest.mark.parametrize("H", [64, 128, 40])
 def test_gdr_empty_sequences(H):
     d, h0 = gdr_inputs(2, 0, 2, 1, H, 128, BF16)
@@ -322,8 +365,18 @@ def test_conv_of_a_slice(off, dtype):
     assert bool((out[..., :off] == 7).all()) and bool((out[..., off + 64:] == 7).all())
 
 
+def test_conv_offsets_beyond_32_bits():
+    L, C = 70_000, 32_768
+    x = torch.randn(1, L, C, device="cuda", dtype=BF16)
+    w = torch.randn(C, 4, device="cuda")
+    assert x.numel() > 2 ** 31
+    y, fin = bd.mamba2_causal_conv_fwd(x, w)
+    tail, _ = bd.mamba2_causal_conv_fwd(x[:, -50:].contiguous(), w, initial_state=x[:, -53:-50].contiguous())
+    assert torch.equal(y[:, -50:], tail) and torch.equal(fin, x[:, -3:])
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
-@pytest.mark.parametrize("b,C,W", [(3, 64, 4), (1, 7, 4), (2, 1032, 3), (2, 8, 2), (1, 16, 8)])
+@pytest.mark.parametrize("b,C,W", [(300, 64, 4), (3, 64, 4), (1, 7, 4), (2, 1032, 3), (2, 8, 2), (1, 16, 8)])
 def test_conv_step_continues_a_sequence(b, C, W, dtype):
     x, w, bias, s0 = conv_inputs(b, 12, C, W, dtype)
     _, st = bd.mamba2_causal_conv_fwd(x[:, :5].contiguous(), w, bias=bias, initial_state=s0)
@@ -398,6 +451,25 @@ def test_norm_of_slices(off):
     y2 = bd.mamba2_group_norm(x.contiguous(), None, 2, z=z.contiguous(), mode="after")
     assert rel_err(np64(y), ref.norm(x, 2, z=z, mode="after")) <= TOL_ROUND[BF16]
     assert rel_err(np64(y2), np64(y)) <= TOL_ROUND[BF16]
+
+
+def test_norm_offsets_beyond_32_bits():
+    rows, C = 540_000, 4096
+    x = torch.randn(rows, C, device="cuda", dtype=BF16)
+    y = bd.mamba2_group_norm(x, None, 64, z=x, mode="after")
+    assert x.numel() > 2 ** 31
+    for at in (0, 524_287, 524_288, rows - 1):
+        row = x[at:at + 1].contiguous()
+        assert torch.equal(y[at:at + 1], bd.mamba2_group_norm(row, None, 64, z=row, mode="after"))
+
+
+@pytest.mark.parametrize("groups", [1, 2, 3, 7, 33, 100])
+def test_norm_row_and_group_counts(groups):
+    """Blocks that span several rows, several groups, and parts of either."""
+    for rows in (1, 2, 31, 257):
+        x = torch.randn(rows, groups * 48, device="cuda").bfloat16()
+        y = bd.mamba2_group_norm(x, None, groups)
+        assert rel_err(np64(y), ref.norm(x, groups)) <= TOL_ROUND[BF16]
 
 
 def test_norm_of_no_rows():
