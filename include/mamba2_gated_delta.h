@@ -63,10 +63,12 @@ typedef struct {
 
 /* Whole sequences.  initial_state NULL means zeros; final_state NULL means not
  * written.  No workspace.  State arithmetic is fp32 on both dtypes: with bf16
- * inputs of S = 64 or 128 and H = 64 or 128 the products run on the tensor
- * cores with the state and every intermediate of the state's recurrence as two
- * bf16 parts (about 16 bits); y's own products take one bf16 part.  Other
- * shapes run token by token in fp32. */
+ * inputs of S = 64 or 128 and H = 64 or 128, and q, k, v whose address and
+ * token stride are multiples of 16 bytes, the products run in chunks on the
+ * tensor cores: what is added to the fp32 state is made of three bf16 parts
+ * (24 bits) of every intermediate, from two parts (16 bits) of the state before
+ * it; y takes two parts of the corrections and the high part of the state.
+ * Everything else runs token by token in fp32. */
 MAMBA2_API mamba2_status mamba2_gdr_fwd(const mamba2_shape* shape, const mamba2_gdr_options* options, const void* q,
                                         const void* k, const void* v, const float* g, const float* beta,
                                         const int32_t* lengths, const float* initial_state, void* y,

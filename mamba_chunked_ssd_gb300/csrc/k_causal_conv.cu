@@ -8,7 +8,10 @@
 // tokens, and slides a window of the last W - 1 inputs through its registers, so a
 // token's input is loaded once per run (plus the W - 1 tokens before the run,
 // which the neighbouring run has just brought into L2).  The loads of the next
-// eight tokens are under way while eight are computed.
+// eight tokens are under way while eight are computed.  4 x 8192 tokens of 8192
+// channels in bf16, width 4, SiLU: 183 us, 5.9 TB/s (0.88 of a plain copy; 366 us
+// without the loads ahead).  One token of 256 sequences of these channels: 15 us of
+// which 5 are the bytes; the host's call takes as long.
 #include "gated_delta.cuh"
 
 namespace m2 {

@@ -9,6 +9,9 @@
 // and p = h^T q are formed together over the state that was read, so the block
 // meets once: with r and p,
 //   w = beta (v - a r),   y = scale (a p + (q . k) w),   h <- a h + k w^T.
+// 256 sequences of 64 heads of 64 columns, S 128: 168 us, 6.4 TB/s (0.96 of a plain
+// copy).  Blocks of 32 columns: a row of theirs is one 128-byte line, and a head of
+// one sequence still gives several blocks.
 #include "gated_delta.cuh"
 
 namespace m2 {
