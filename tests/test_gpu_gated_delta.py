@@ -139,6 +139,38 @@ def test_gdr_nan_input_shows_from_its_token_on(value, where):
     assert torch.isnan(y[0, where:, 1]).all() and torch.isnan(fin[0, 1]).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("b,nh,H", [(2, 4, 40), (1, 32, 40), (3, 32, 40), (2, 64, 33)])
+@pytest.mark.parametrize("S", [36, 65, 200])
+def test_gdr_token_by_token_widths(b, nh, H, S, dtype):
+    """Few and many heads (blocks of fewer or more columns), ragged, normalised,
+    heads that share q and k, lengths around the tiles' and passes' ends."""
+    L = 53
+    d, h0 = gdr_inputs(b, L, nh, nh // 4, H, S, dtype, seed=S, unit=False)
+    lengths = torch.tensor([L, 0, 34][:b], dtype=torch.int32, device="cuda")
+    check_gdr(d, h0, l2norm=True, lengths=lengths)
+
+
+@pytest.mark.parametrize("nh", [2, 32, 96])
+@pytest.mark.parametrize("value", ["g", "beta", "k", "v", "q"])
+def test_gdr_token_by_token_nan_input_shows_from_its_token_on(value, nh):
+    """Tokens that share a pass over the state: nothing of a later one's NaN
+    reaches the ones before it."""
+    for where in (20, 21, 22, 23):
+        d, h0 = gdr_inputs(1, 40, nh, nh, 40, 32, FP32)
+        clean, fin_clean = bd.mamba2_gdr_fwd(**d, initial_state=h0)
+        d[value][0, where, 1] = NAN
+        y, fin = bd.mamba2_gdr_fwd(**d, initial_state=h0)
+        others = [i for i in range(nh) if i != 1]
+        assert torch.equal(y[:, :, others], clean[:, :, others]) and torch.equal(fin[0, others], fin_clean[0, others])
+        assert torch.equal(y[:, :where, 1], clean[:, :where, 1])
+        if value == "q":
+            assert torch.isnan(y[0, where, 1]).all() and torch.equal(y[0, where + 1:, 1], clean[0, where + 1:, 1])
+            assert torch.equal(fin, fin_clean)
+        else:
+            assert torch.isnan(y[0, where:, 1]).all() and torch.isnan(fin[0, 1]).all()
+
+
 def test_gdr_offsets_beyond_32_bits():
     """v and y of more than 2^31 elements: the sequence's end, from the state that
     enters it, against a call on the end alone."""
