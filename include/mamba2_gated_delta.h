@@ -63,9 +63,9 @@ typedef struct {
 
 /* Whole sequences.  initial_state NULL means zeros; final_state NULL means not
  * written.  No workspace.  State arithmetic is fp32 on both dtypes: with bf16
- * inputs of S = 64 or 128 and H = 64 or 128, and q, k, v whose address and
- * token stride are multiples of 16 bytes, the products run in chunks on the
- * tensor cores: what is added to the fp32 state is made of three bf16 parts
+ * inputs of S and H up to 128, both multiples of 8, and q, k, v whose address
+ * and token stride are multiples of 16 bytes, the products run in chunks on the
+ * tensor cores (but for a few tokens of few heads): what is added to the fp32 state is made of three bf16 parts
  * (24 bits) of every intermediate, from two parts (16 bits) of the state before
  * it; y takes two parts of the corrections and the high part of the state.
  * Everything else runs token by token in fp32. */

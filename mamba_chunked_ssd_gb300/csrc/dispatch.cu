@@ -83,8 +83,18 @@ bool use_f32_tensor_cores(const Geom& g, bool bf16) {
     return f32_chunk_out_tensor_cores(g, bf16) && state_pass_split_fits(g);
 }
 
+// bf16 in chunks on the tensor cores where that kernel takes the shape, but a few tokens
+// of few heads token by token (us on the GPU, chunks / token by token: 16 tokens of 32 heads
+// of 128 columns, S 128, 8.5 / 6.7, 4 tokens 8.5 / 5.0; 64 tokens 11.4 / 16.2; 8 tokens of 256
+// heads 16.7 / 29.8; 16 tokens of 8 heads of 64, S 64, 7.5 / 4.3, 64 tokens 9.6 / 8.2, 1024
+// tokens 83 / 89).
+static bool few_tokens(const Geom& g) {
+    const int sms = sm_count();
+    return g.seqlen <= 16 && g.batch * g.nheads * ((g.headdim + 31) / 32) <= (sms > 0 ? sms : 152);
+}
+
 cudaError_t launch_gdr_fwd(const GdrArgs& a, bool bf16, cudaStream_t st) {
-    if (bf16 && gdr_chunk_tc_fits(a)) return launch_gdr_chunk_tc(a, st);
+    if (bf16 && gdr_chunk_tc_fits(a) && !few_tokens(a.g)) return launch_gdr_chunk_tc(a, st);
     return launch_gdr_recurrent(a, bf16, st);
 }
 

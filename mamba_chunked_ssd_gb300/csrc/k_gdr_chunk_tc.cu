@@ -13,8 +13,9 @@
 // q and k rows that are to be normalised stay as they are in shared memory:
 // their norms are factors of rows and columns of the products above.
 //
-// GB300 design.  One CTA owns one head of up to 128 columns (or two heads of 64
-// columns of one q/k group, NV = 2) and walks the chunks; the carried state and
+// GB300 design.  One CTA owns one head of up to 128 columns (or two heads of up to 64
+// columns of one q/k group, NV = 2; smaller states and heads are filled up with zeros:
+// 4 x 1024 tokens of 24 heads of 96 columns, S 96, 124 us, token by token 367) and walks the chunks; the carried state and
 // every intermediate stay on the chip, so q, k, v, g, beta are read once and y
 // is written once.  All products of the chain run transposed, with the head's
 // columns as the 128 rows of the MMA: the fp32 state h^T lives in tensor memory,
@@ -314,7 +315,8 @@ __device__ __forceinline__ void diag_norm(const float (&acc)[2][4], int lane, fl
     put(gid + 8, __frsqrt_rn((gid & 1 ? acc[1][3] : acc[1][2]) + eps));
 }
 
-template <int S, int H, int NV>
+// S x H: the state's size, or with PAD what its size is filled up to.
+template <int S, int H, int NV, bool PAD>
 __global__ void __launch_bounds__(kThreads, 1)
 k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                const __grid_constant__ CUtensorMap tm_v, const GdrTcParams p) {
@@ -414,9 +416,10 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const int q = warp & 3, part = warp >> 2;
         const int hv = NV == 2 ? q >> 1 : 0;
         const int colh = 32 * (NV == 2 ? (q & 1) : q) + lane;  // column of its head
-        const bool live = colh < H;
         const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16);
-        const int64_t sbase = (b * g.nheads + h0 + hv) * (int64_t)S * H + colh;
+        const int rows = PAD ? (int)g.dstate : S, cols = PAD ? (int)g.headdim : H;
+        const bool live = colh < cols;
+        const int64_t sbase = (b * g.nheads + h0 + hv) * (int64_t)rows * cols + colh;
         const int s0 = part * (S / 4), i0 = part * (kT / 4);  // this warp's state rows and tokens
         const uint32_t w_at = tl + (hv ? cR2 : cR) + i0;       // W of its head
         // this thread's column of V in a stage: 16-byte piece and place in it
@@ -427,7 +430,8 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             uint32_t r[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-                r[j] = (live && p.init) ? __float_as_uint(p.init[sbase + (int64_t)(s + j) * H]) : 0u;
+                r[j] = live && p.init && (!PAD || s + j < rows) ? __float_as_uint(p.init[sbase + (int64_t)(s + j) * cols])
+                                                                : 0u;
             tc::tmem_st16(tl + cH + s, r);
         }
         tc::tmem_wait_st();
@@ -542,7 +546,8 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 tc::tmem_ld16(tl + cH + s, r);
                 if (live) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) p.final_state[sbase + (int64_t)(s + j) * H] = __uint_as_float(r[j]);
+                    for (int j = 0; j < 16; ++j)
+                        if (!PAD || s + j < rows) p.final_state[sbase + (int64_t)(s + j) * cols] = __uint_as_float(r[j]);
                 }
             }
         }
@@ -552,13 +557,14 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const int q = warp & 3;
         const int hv = NV == 2 ? q >> 1 : 0;
         const int colh = 32 * (NV == 2 ? (q & 1) : q) + lane;
-        const bool live = colh < H;
+        const int cols = PAD ? (int)g.headdim : H;
+        const bool live = colh < cols;
         const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16);
         const uint32_t o_at = tl + (hv ? cO2 : cO);
-        const int64_t row = (int64_t)g.nheads * H;
+        const int64_t row = (int64_t)g.nheads * cols;
         const int odd = lane & 1;
         // lanes meet in pairs: the even one stores both columns of token i, the odd one of i + 1
-        __nv_bfloat16* y = p.y + (b * L + odd) * row + (int64_t)(h0 + hv) * H + (colh & ~1);
+        __nv_bfloat16* y = p.y + (b * L + odd) * row + (int64_t)(h0 + hv) * cols + (colh & ~1);
         if (lane == 0 && nc > 0) tc::mbar_arrive(&bars[kBarHReady]);  // no sum to be read yet
         for (int c = 0; c < nc; ++c) {
             const int buf = c % kBufs;
@@ -1045,7 +1051,7 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 
 bool aligned16(const void* p, int64_t stride) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0; }
 
-template <int S, int H, int NV>
+template <int S, int H, int NV, bool PAD>
 cudaError_t launch_k(const GdrArgs& a, cudaStream_t st) {
     const Geom& g = a.g;
     GdrTcParams p{};
@@ -1082,34 +1088,46 @@ cudaError_t launch_k(const GdrArgs& a, cudaStream_t st) {
         const uint64_t strides[3] = {width * 2, stride * 2, L * stride * 2};
         return make_tmap_bf16(m, base, 4, dims, strides, box);
     };
-    if (!map(&tm_q, a.q, S, g.ngroups, a.q_stride) || !map(&tm_k, a.k, S, g.ngroups, a.k_stride) ||
-        !map(&tm_v, a.v, H, g.nheads, a.v_stride))
+    if (!map(&tm_q, a.q, g.dstate, g.ngroups, a.q_stride) || !map(&tm_k, a.k, g.dstate, g.ngroups, a.k_stride) ||
+        !map(&tm_v, a.v, g.headdim, g.nheads, a.v_stride))
         return cudaErrorInvalidValue;
-    const cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(k_gdr_chunk_tc<S, H, NV>), smem);
+    const cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(k_gdr_chunk_tc<S, H, NV, PAD>), smem);
     if (e != cudaSuccess) return e;
-    k_gdr_chunk_tc<S, H, NV><<<dim3((unsigned)(g.nheads / NV), (unsigned)g.batch), kThreads, smem, st>>>(tm_q, tm_k, tm_v, p);
+    k_gdr_chunk_tc<S, H, NV, PAD><<<dim3((unsigned)(g.nheads / NV), (unsigned)g.batch), kThreads, smem, st>>>(tm_q, tm_k, tm_v, p);
     return cudaGetLastError();
+}
+
+template <bool PAD>
+cudaError_t launch_shape(const GdrArgs& a, bool wide, bool pairs, cudaStream_t st) {
+    if (a.g.dstate > 64) {
+        if (wide) return launch_k<128, 128, 1, PAD>(a, st);
+        return pairs ? launch_k<128, 64, 2, PAD>(a, st) : launch_k<128, 64, 1, PAD>(a, st);
+    }
+    if (wide) return launch_k<64, 128, 1, PAD>(a, st);
+    return pairs ? launch_k<64, 64, 2, PAD>(a, st) : launch_k<64, 64, 1, PAD>(a, st);
 }
 
 }  // namespace
 
-// bf16 shapes the kernel covers; TMA wants every row of q, k and v on a 16-byte
-// boundary.
+// bf16 shapes the kernel covers: states and heads of up to 128 rows and columns, filled up
+// to 64 or 128 with zeros by the TMA, which wants every row of q, k and v (and every head
+// of a row) on a 16-byte boundary.
 bool gdr_chunk_tc_fits(const GdrArgs& a) {
     const Geom& g = a.g;
-    if ((g.dstate != 64 && g.dstate != 128) || (g.headdim != 64 && g.headdim != 128)) return false;
+    if (g.dstate > 128 || g.headdim > 128 || g.dstate % 8 != 0 || g.headdim % 8 != 0) return false;
     if (g.seqlen >= ((int64_t)1 << 30) || g.nheads > 65535) return false;
     return aligned16(a.q, a.q_stride) && aligned16(a.k, a.k_stride) && aligned16(a.v, a.v_stride);
 }
 
+// Two heads of up to 64 columns to a CTA where there are more heads than SMs: a chunk of
+// two takes a sixth longer than one of one head (1024 tokens, S 128, us with one head to a CTA
+// / two: 64 heads 120 / 135, 128 heads 123 / 135, 256 heads 240 / 140).
 cudaError_t launch_gdr_chunk_tc(const GdrArgs& a, cudaStream_t st) {
-    const bool pairs = a.g.headdim == 64 && a.g.heads_per_group % 2 == 0;
-    if (a.g.dstate == 128) {
-        if (a.g.headdim == 128) return launch_k<128, 128, 1>(a, st);
-        return pairs ? launch_k<128, 64, 2>(a, st) : launch_k<128, 64, 1>(a, st);
-    }
-    if (a.g.headdim == 128) return launch_k<64, 128, 1>(a, st);
-    return pairs ? launch_k<64, 64, 2>(a, st) : launch_k<64, 64, 1>(a, st);
+    const int sms = sm_count();
+    const bool wide = a.g.headdim > 64;
+    const bool pairs = !wide && a.g.heads_per_group % 2 == 0 && a.g.batch * a.g.nheads > (sms > 0 ? sms : 152);
+    const bool pad = a.g.dstate % 64 != 0 || a.g.headdim % 64 != 0;
+    return pad ? launch_shape<true>(a, wide, pairs, st) : launch_shape<false>(a, wide, pairs, st);
 }
 
 }  // namespace m2

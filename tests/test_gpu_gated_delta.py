@@ -116,6 +116,46 @@ def test_gdr_ragged_batch(H, l2norm):
         assert bool((y[i, n:] == 0).all())
 
 
+@pytest.mark.parametrize("b,nh,G,L", [(2, 4, 2, 75), (11, 16, 4, 67), (200, 2, 2, 9), (10, 16, 16, 33)])
+@pytest.mark.parametrize("H,S", [(64, 128), (64, 64), (40, 128), (8, 72), (56, 96), (64, 8), (72, 128), (120, 40), (128, 96)])
+def test_gdr_sizes_and_numbers_of_heads(b, nh, G, L, H, S):
+    """States and heads that are filled up, few heads and enough for two to share
+    a block (where a group has two), ragged, with NaN past each row's end."""
+    d, h0 = gdr_inputs(b, L, nh, G, H, S, BF16, seed=H + S, unit=False)
+    lengths = (torch.arange(b, device="cuda", dtype=torch.int32) * 37 + L) % (L + 1)
+    clean = {n: t.clone() for n, t in d.items()}
+    for i, n in enumerate(lengths.tolist()):
+        for t in d.values():
+            t[i, n:] = NAN
+    scale = S ** -0.5
+    y, fin = Guarded((b, L, nh, H), BF16), Guarded((b, nh, S, H), FP32)
+    bd.mamba2_gdr_fwd(**d, scale=scale, qk_l2norm=True, initial_state=h0, lengths=lengths, y=y.t, final_state=fin.t)
+    bd.mamba2_check_device_status()
+    assert y.intact() and fin.intact()
+    y_ref, fin_ref = ref.gdr(**clean, scale=scale, l2norm=True, init=h0, lengths=lengths)
+    assert rel_err(np64(y.t), y_ref) <= TOL_Y[BF16]
+    assert rel_err(np64(fin.t), fin_ref) <= TOL_STATE
+
+
+@pytest.mark.parametrize("H", [64, 40])
+@pytest.mark.parametrize("case", ["equal_keys", "equal_keys_beta_2", "no_decay", "mixed_decay", "forget_all"])
+def test_gdr_hard_inputs_of_many_heads(H, case):
+    """The hard inputs below with two heads to a block."""
+    d, h0 = gdr_inputs(10, 190, 16, 4, H, 128, BF16, seed=6)
+    if case.startswith("equal_keys"):
+        d["k"][:] = d["k"][:, :1]
+        d["g"] *= 0.01
+        d["beta"][:] = 2.0 if case.endswith("2") else 1.0
+    if case == "no_decay":
+        d["g"][:] = 0
+    if case == "mixed_decay":
+        d["g"][:, ::3] = 0
+        d["g"][:, 1::3] = -90.0
+    if case == "forget_all":
+        d["g"][:, 100] = -float("inf")
+    check_gdr(d, h0, l2norm=case == "equal_keys_beta_2")
+
+
 def test_gdr_ragged_batch_of_more_rows_than_threads():
     """More rows than a block has threads to order them with."""
     b, L = 1030, 40
