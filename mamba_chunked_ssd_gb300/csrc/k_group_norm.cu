@@ -38,8 +38,8 @@ __device__ __forceinline__ float group_sum(float v, float* smem) {
 }
 
 // Blocks of an SM that the registers have to allow: 1024 threads for up to eight
-// channels to a thread (32768 x 4096 in groups of 64, gated: 132 us, 768 threads
-// 154), 768 for 16 (8192 x 4096 in one group, gated: 46 us, 1024 threads 53, 512 50).
+// channels to a thread (32768 x 4096 in groups of 64, gated: 130 us, 768 threads
+// 144), 768 for 16 (8192 x 4096 in one group, gated: 39 us, 1024 threads 49, 512 40).
 constexpr int min_blocks(int channels, int tpg) {
     return tpg > 256 || channels > 16 ? 1 : (channels <= 8 ? 1024 : 768) / (tpg > 32 ? tpg : kWarpBlock);
 }
