@@ -12,7 +12,7 @@
 // a thread, the weights stay in registers and a row's loads are under way while
 // the row before is summed.  32768 x 4096 in bf16, groups of 64, gated: 131 us, 6.2 TB/s
 // (0.92 of a plain copy; 217 us with a block to a row); 8192 x 4096 in one group,
-// gated first: 39 us, 5.2 TB/s (two block-wide sums a row).
+// gated first: 37 us, 5.4 TB/s (0.81; a block-wide sum a row).
 #include "gated_delta.cuh"
 #include "mamba2_gated_delta.h"
 
@@ -21,16 +21,18 @@ namespace {
 
 constexpr int kWarpBlock = 256;  // threads of a block whose groups stay inside warps
 
-// Sum over the group's threads.
+// Sum over the group's threads.  Block-wide, the partial sums go through one of two places in
+// turn, so that one barrier is enough: whoever writes a place has met, since it was read,
+// at the barrier of the sum between.
 template <int TPG>
-__device__ __forceinline__ float group_sum(float v, float* smem) {
+__device__ __forceinline__ float group_sum(float v, float (*smem)[32], int& turn) {
 #pragma unroll
     for (int m = (TPG < 32 ? TPG : 32) / 2; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-    if (TPG > 32) {
-        __syncthreads();  // the previous sum has been read
-        if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = v;
+    if constexpr (TPG > 32) {
+        turn ^= 1;
+        if ((threadIdx.x & 31) == 0) smem[turn][threadIdx.x >> 5] = v;
         __syncthreads();
-        v = smem[threadIdx.x & 31 & (TPG / 32 - 1)];
+        v = smem[turn][threadIdx.x & 31 & (TPG / 32 - 1)];
 #pragma unroll
         for (int m = TPG / 64; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
     }
@@ -39,9 +41,24 @@ __device__ __forceinline__ float group_sum(float v, float* smem) {
 
 // Blocks of an SM that the registers have to allow: 1024 threads for up to eight
 // channels to a thread (32768 x 4096 in groups of 64, gated: 130 us, 768 threads
-// 144), 768 for 16 (8192 x 4096 in one group, gated: 39 us, 1024 threads 49, 512 40).
+// 144), 768 for 16 (8192 x 4096 in one group, gated, without the ring below: 39 us, 1024 threads 49,
+// 512 40).
 constexpr int min_blocks(int channels, int tpg) {
     return tpg > 256 || channels > 16 ? 1 : (channels <= 8 ? 1024 : 768) / (tpg > 32 ? tpg : kWarpBlock);
+}
+
+// bf16 rows of groups that fill blocks come through a ring in shared memory, kRing rows ahead,
+// each thread copying what it reads itself: registers hold too few loads for block-wide
+// sums between them (us without / with, gated before: 2048 channels 36.6 / 33.8, 4096 36.7 /
+// 34.9, 8192 39.3 / 40.8, 16384 50 / 41; over 28 sizes and modes 6 % faster; two rows ahead
+// are 4 % slower).  In fp32 it is 5 % slower (1024 channels, gated after, 31.0 / 36.8).
+constexpr int kRing = 3;
+template <typename T>
+constexpr bool use_ring(int vec, int nv, int tpg) {
+    return tpg > 32 && sizeof(T) == 2 && vec == 8 && nv * vec <= 16 && nv * tpg <= 2048;
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 
 // VEC elements per load, NV loads per thread, TPG threads per group.  Groups
@@ -51,7 +68,8 @@ template <typename T, int VEC, int NV, int TPG>
 __global__ void __launch_bounds__(TPG > 32 ? TPG : kWarpBlock, min_blocks(NV * VEC, TPG))
 k_group_norm(const NormArgs a, int across) {
     using V = typename VecOf<T, VEC>::type;
-    __shared__ float smem[32];
+    __shared__ float smem[2][32];
+    int turn = 0;
     constexpr bool kKeep = NV * VEC <= 16;
     const int lane = threadIdx.x % TPG, slot = threadIdx.x / TPG;
     const int rows_per = TPG > 32 ? 1 : (kWarpBlock / TPG) >> across;
@@ -95,12 +113,41 @@ k_group_norm(const NormArgs a, int across) {
             }
         }
     };
-    load(row);
+    constexpr bool kUseRing = use_ring<T>(VEC, NV, TPG);
+    extern __shared__ __align__(16) uint4 ring[];  // [kRing][x and z][NV][TPG]
+    const int slots = gated ? 2 * NV : NV;
+    auto ahead = [&](int64_t r, int stage) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int j = lane + i * TPG;
+            const bool live = mine && r < a.rows && j < nvec;
+            const uint32_t dst = (uint32_t)__cvta_generic_to_shared(ring + (stage * slots + i) * TPG + lane);
+            const int64_t at = live ? (int64_t)j * VEC : 0, rr = live ? r : 0;
+            copy16(dst, x + rr * a.x_stride + at, live);
+            if (gated) copy16(dst + NV * TPG * 16, z + rr * a.z_stride + at, live);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int stage = 0;
+    if (kUseRing) {
+        for (int i = 0; i < kRing; ++i) ahead(row + i * step, i);
+    } else {
+        load(row);
+    }
     // every thread of the block walks as far (blocks larger than a warp meet at barriers)
     for (int64_t r0 = (int64_t)blockIdx.y * rows_per; r0 < a.rows; r0 += step, row += step) {
         float u[NV][VEC];
         V zc[NV];
         float s = 0.f;
+        if constexpr (kUseRing) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const V* from = reinterpret_cast<const V*>(ring + (stage * slots + i) * TPG + lane);
+                xr[i] = *from;
+                if (gated) zr[i] = from[NV * TPG];
+            }
+        }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             unpack<VEC>(xr[i], u[i], (const T*)nullptr);
@@ -114,9 +161,14 @@ k_group_norm(const NormArgs a, int across) {
 #pragma unroll
             for (int e = 0; e < VEC; ++e) s += u[i][e];
         }
-        if (kKeep) load(row + step);
+        if (kUseRing) {
+            ahead(row + kRing * step, stage);
+            if (++stage == kRing) stage = 0;
+        } else if (kKeep) {
+            load(row + step);
+        }
         float mean = 0.f;
-        if (a.flags & MAMBA2_NORM_SUBTRACT_MEAN) mean = group_sum<TPG>(s, smem) / (float)size;
+        if (a.flags & MAMBA2_NORM_SUBTRACT_MEAN) mean = group_sum<TPG>(s, smem, turn) / (float)size;
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -128,7 +180,7 @@ k_group_norm(const NormArgs a, int across) {
                 }
             }
         }
-        const float r = rsqrtf(group_sum<TPG>(ss, smem) / (float)size + a.eps);
+        const float r = rsqrtf(group_sum<TPG>(ss, smem, turn) / (float)size + a.eps);
         if (mine && row < a.rows) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -156,6 +208,7 @@ k_group_norm(const NormArgs a, int across) {
         }
         if (!kKeep) load(row + step);
     }
+    if (kUseRing) asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 template <typename T, int VEC, int NV, int TPG>
@@ -165,16 +218,23 @@ cudaError_t launch_n(const NormArgs& a, cudaStream_t st) {
     while ((2 << across) <= per && (1 << across) < a.ngroups) ++across;
     const int64_t gx = (a.ngroups + (1 << across) - 1) >> across, rows_per = per >> across;
     // as many blocks as fit on the GPU at once: each keeps its weights for its share of the rows
-    static const int resident = [] {
+    const bool gated = (a.flags & (MAMBA2_NORM_GATE_BEFORE | MAMBA2_NORM_GATE_AFTER)) != 0;
+    auto ring_bytes = [](bool z) { return use_ring<T>(VEC, NV, TPG) ? kRing * (z ? 2 : 1) * NV * TPG * 16 : 0; };
+    const cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(k_group_norm<T, VEC, NV, TPG>),
+                                                  ring_bytes(true));
+    if (e != cudaSuccess) return e;
+    auto count = [&](bool z) {
         int n = 0;
-        const cudaError_t e =
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_group_norm<T, VEC, NV, TPG>, block, 0);
-        return e == cudaSuccess && n > 0 ? n : 1;
-    }();
+        const cudaError_t err =
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_group_norm<T, VEC, NV, TPG>, block, ring_bytes(z));
+        return err == cudaSuccess && n > 0 ? n : 1;
+    };
+    static const int fit[2] = {count(false), count(true)};
+    const int resident = fit[gated];
     const int sms = sm_count();
     const int64_t want = (resident * (int64_t)(sms > 0 ? sms : 152) + gx - 1) / gx;
     const int64_t gy = imin64(imin64((a.rows + rows_per - 1) / rows_per, want < 1 ? 1 : want), 65535);
-    k_group_norm<T, VEC, NV, TPG><<<dim3((unsigned)gx, (unsigned)gy), block, 0, st>>>(a, across);
+    k_group_norm<T, VEC, NV, TPG><<<dim3((unsigned)gx, (unsigned)gy), block, ring_bytes(gated), st>>>(a, across);
     return cudaGetLastError();
 }
 
@@ -187,7 +247,7 @@ cudaError_t launch_v(const NormArgs& a, cudaStream_t st) {
     if (n <= 16 * K) return launch_n<T, VEC, K, 16>(a, st);
     if (n <= 32 * K) return launch_n<T, VEC, K, 32>(a, st);
     if (n <= 64 * K) return launch_n<T, VEC, 2 * K, 32>(a, st);
-    if (n <= 128 * K) return launch_n<T, VEC, K, 128>(a, st);
+    if (n <= 128 * K) return launch_n<T, VEC, 2 * K, 64>(a, st);
     if (n <= 256 * K) return launch_n<T, VEC, 2 * K, 128>(a, st);
     if (n <= 512 * K) return launch_n<T, VEC, 2 * K, 256>(a, st);
     if (n <= 1024 * K) return launch_n<T, VEC, 2 * K, 512>(a, st);

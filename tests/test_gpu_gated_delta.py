@@ -488,6 +488,36 @@ def test_norm(rows, groups, size, mode, dtype):
     assert rel_err(np64(y), ref.norm(x, groups, z=z, mode=mode)) <= TOL_ROUND[dtype]
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("mode", ["silu", "before"])
+@pytest.mark.parametrize("rows,groups,size", [
+    (9001, 1, 520), (4001, 3, 1000), (6007, 1, 1496), (3001, 1, 2056), (2999, 1, 4096), (1501, 1, 8192), (701, 1, 16384),
+])
+def test_norm_of_many_rows(rows, groups, size, mode, dtype):
+    """Every block walks down several rows, of a slice of a wider tensor; a NaN
+    stays in its row."""
+    r = torch.Generator(device="cuda").manual_seed(size)
+    C = groups * size
+    wide = (torch.randn(rows, 2 * C + 8, generator=r, device="cuda") + 0.5).to(dtype)
+    x, w = wide[:, :C], torch.randn(C, generator=r, device="cuda")
+    z = wide[:, C + 8:] if mode == "before" else None
+    bad = rows // 2
+    wide[bad, 5] = NAN
+    y = Guarded((rows, C), dtype)
+    bd.mamba2_group_norm(x, w, groups, z=z, mode=mode, subtract_mean=mode == "silu", y=y.t)
+    assert y.intact()
+    u = x.double() * torch.nn.functional.silu(z.double()) if z is not None else x.double()
+    u = u.reshape(rows, groups, size)
+    if mode == "silu":
+        u = u - u.mean(-1, keepdim=True)
+    u = (u / (u.square().mean(-1, keepdim=True) + 1e-5).sqrt()).reshape(rows, C) * w.double()
+    want = torch.nn.functional.silu(u) if mode == "silu" else u
+    keep = torch.arange(rows, device="cuda") != bad
+    assert torch.isnan(y.t[bad, :size]).all() and not torch.isnan(y.t[keep]).any()
+    err = (y.t[keep].double() - want[keep]).abs().amax() / want[keep].abs().amax()
+    assert float(err) <= TOL_ROUND[dtype]
+
+
 @pytest.mark.parametrize("size", [32768, 16400])
 def test_norm_of_the_largest_groups(size):
     x = torch.randn(2, size, device="cuda").bfloat16()
