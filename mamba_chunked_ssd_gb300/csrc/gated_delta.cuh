@@ -90,6 +90,8 @@ struct VecOf<__nv_bfloat16, 8> { using type = uint4; };
 template <>
 struct VecOf<__nv_bfloat16, 4> { using type = uint2; };
 template <>
+struct VecOf<__nv_bfloat16, 2> { using type = uint32_t; };
+template <>
 struct VecOf<__nv_bfloat16, 1> { using type = __nv_bfloat16; };
 
 template <int N>

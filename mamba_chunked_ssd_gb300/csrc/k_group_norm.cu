@@ -40,11 +40,11 @@ __device__ __forceinline__ float group_sum(float v, float (*smem)[32], int& turn
 }
 
 // Blocks of an SM that the registers have to allow: 1024 threads for up to eight
-// channels to a thread (32768 x 4096 in groups of 64, gated: 130 us, 768 threads
-// 144), 768 for 16 (8192 x 4096 in one group, gated, without the ring below: 39 us, 1024 threads 49,
+// channels to a thread (8192 x 2052 in fp32 in one group, gated: 41 us, 512 threads 55; 32768 x 4096 in groups of 64, gated: 130 us,
+// 768 threads 144), 768 for 16 (8192 x 4096 in one group, gated, without the ring below: 39 us, 1024 threads 49,
 // 512 40).
 constexpr int min_blocks(int channels, int tpg) {
-    return tpg > 256 || channels > 16 ? 1 : (channels <= 8 ? 1024 : 768) / (tpg > 32 ? tpg : kWarpBlock);
+    return tpg > 512 || channels > 16 ? 1 : (channels <= 8 ? 1024 : 768) / (tpg > 32 ? tpg : kWarpBlock);
 }
 
 // bf16 rows of groups that fill blocks come through a ring in shared memory, kRing rows ahead,
@@ -55,10 +55,14 @@ constexpr int min_blocks(int channels, int tpg) {
 constexpr int kRing = 3;
 template <typename T>
 constexpr bool use_ring(int vec, int nv, int tpg) {
-    return tpg > 32 && sizeof(T) == 2 && vec == 8 && nv * vec <= 16 && nv * tpg <= 2048;
+    return tpg > 32 && sizeof(T) == 2 && vec > 1 && nv * vec <= 16 && nv * tpg <= 2048;
 }
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool live) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(live ? 8 : 0) : "memory");
 }
 
 // VEC elements per load, NV loads per thread, TPG threads per group.  Groups
@@ -114,7 +118,8 @@ k_group_norm(const NormArgs a, int across) {
         }
     };
     constexpr bool kUseRing = use_ring<T>(VEC, NV, TPG);
-    extern __shared__ __align__(16) uint4 ring[];  // [kRing][x and z][NV][TPG]
+    extern __shared__ __align__(16) uint8_t ring_bytes[];  // [kRing][x and z][NV][TPG]
+    V* ring = reinterpret_cast<V*>(ring_bytes);
     const int slots = gated ? 2 * NV : NV;
     auto ahead = [&](int64_t r, int stage) {
 #pragma unroll
@@ -123,8 +128,8 @@ k_group_norm(const NormArgs a, int across) {
             const bool live = mine && r < a.rows && j < nvec;
             const uint32_t dst = (uint32_t)__cvta_generic_to_shared(ring + (stage * slots + i) * TPG + lane);
             const int64_t at = live ? (int64_t)j * VEC : 0, rr = live ? r : 0;
-            copy16(dst, x + rr * a.x_stride + at, live);
-            if (gated) copy16(dst + NV * TPG * 16, z + rr * a.z_stride + at, live);
+            copy_async<sizeof(V)>(dst, x + rr * a.x_stride + at, live);
+            if (gated) copy_async<sizeof(V)>(dst + NV * TPG * sizeof(V), z + rr * a.z_stride + at, live);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -143,7 +148,7 @@ k_group_norm(const NormArgs a, int across) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const V* from = reinterpret_cast<const V*>(ring + (stage * slots + i) * TPG + lane);
+                const V* from = ring + (stage * slots + i) * TPG + lane;
                 xr[i] = *from;
                 if (gated) zr[i] = from[NV * TPG];
             }
@@ -219,7 +224,7 @@ cudaError_t launch_n(const NormArgs& a, cudaStream_t st) {
     const int64_t gx = (a.ngroups + (1 << across) - 1) >> across, rows_per = per >> across;
     // as many blocks as fit on the GPU at once: each keeps its weights for its share of the rows
     const bool gated = (a.flags & (MAMBA2_NORM_GATE_BEFORE | MAMBA2_NORM_GATE_AFTER)) != 0;
-    auto ring_bytes = [](bool z) { return use_ring<T>(VEC, NV, TPG) ? kRing * (z ? 2 : 1) * NV * TPG * 16 : 0; };
+    auto ring_bytes = [](bool z) { return use_ring<T>(VEC, NV, TPG) ? kRing * (z ? 2 : 1) * NV * TPG * (int)sizeof(typename VecOf<T, VEC>::type) : 0; };
     const cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(k_group_norm<T, VEC, NV, TPG>),
                                                   ring_bytes(true));
     if (e != cudaSuccess) return e;
@@ -261,9 +266,16 @@ cudaError_t launch_t(const NormArgs& a, cudaStream_t st) {
     constexpr int VEC = 16 / sizeof(T);
     const uintptr_t p = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y) |
                         reinterpret_cast<uintptr_t>(a.z);
-    const bool vec = (a.channels / a.ngroups) % VEC == 0 && a.x_stride % VEC == 0 && a.y_stride % VEC == 0 &&
-                     a.z_stride % VEC == 0 && (p & 15) == 0;
-    return vec ? launch_v<T, VEC>(a, st) : launch_v<T, 1>(a, st);
+    auto fits = [&](int n) {
+        return (a.channels / a.ngroups) % n == 0 && a.x_stride % n == 0 && a.y_stride % n == 0 && a.z_stride % n == 0 &&
+               p % (n * sizeof(T)) == 0;
+    };
+    if (fits(VEC)) return launch_v<T, VEC>(a, st);
+    // (bf16, gated, us in fours / one by one: 16384 x 3200 in groups of 100 99 / 135, 16384 x 2400
+    // in groups of 300 81 / 181, 8192 x 2052 in one group 38 / 67)
+    if constexpr (VEC == 8)
+        if (fits(4)) return launch_v<T, 4>(a, st);
+    return launch_v<T, 1>(a, st);
 }
 
 }  // namespace
