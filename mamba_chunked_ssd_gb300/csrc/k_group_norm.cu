@@ -39,18 +39,19 @@ __device__ __forceinline__ float group_sum(float v, float (*smem)[32], int& turn
     return v;
 }
 
-// Blocks of an SM that the registers have to allow: 1024 threads for up to eight
-// channels to a thread (8192 x 2052 in fp32 in one group, gated: 41 us, 512 threads 55; 32768 x 4096 in groups of 64, gated: 130 us,
-// 768 threads 144), 768 for 16 (8192 x 4096 in one group, gated, without the ring below: 39 us, 1024 threads 49,
-// 512 40).
+// Blocks of an SM that the registers have to allow: 1024 threads for up to eight channels
+// to a thread (32768 x 4096 in groups of 64, gated: 130 us, 768 threads 144; 8192 x 2052 in
+// fp32 in one group, gated: 41 us, 512 threads 55) and in blocks of 512 (4096 x 8192 in bf16,
+// gated: 36 us, 512 threads 38), else 768 for 16 channels (8192 x 4096 in one group, gated,
+// without the ring below: 39 us, 1024 threads 49, 512 40).
 constexpr int min_blocks(int channels, int tpg) {
-    return tpg > 512 || channels > 16 ? 1 : (channels <= 8 ? 1024 : 768) / (tpg > 32 ? tpg : kWarpBlock);
+    return tpg > 512 || channels > 16 ? 1 : (channels <= 8 || tpg == 512 ? 1024 : 768) / (tpg > 32 ? tpg : kWarpBlock);
 }
 
 // bf16 rows of groups that fill blocks come through a ring in shared memory, kRing rows ahead,
 // each thread copying what it reads itself: registers hold too few loads for block-wide
 // sums between them (us without / with, gated before: 2048 channels 36.6 / 33.8, 4096 36.7 /
-// 34.9, 8192 39.3 / 40.8, 16384 50 / 41; over 28 sizes and modes 6 % faster; two rows ahead
+// 34.9, 16384 50 / 41; over 28 sizes and modes 6 % faster; two rows ahead
 // are 4 % slower).  In fp32 it is 5 % slower (1024 channels, gated after, 31.0 / 36.8).
 constexpr int kRing = 3;
 template <typename T>
