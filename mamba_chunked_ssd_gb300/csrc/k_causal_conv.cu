@@ -10,8 +10,8 @@
 // which the neighbouring run has just brought into L2).  The loads of the next
 // eight tokens are under way while eight are computed.  4 x 8192 tokens of 8192
 // channels in bf16, width 4, SiLU: 183 us, 5.9 TB/s (0.88 of a plain copy; 366 us
-// without the loads ahead).  One token of 256 sequences of these channels: 15 us of
-// which 5 are the bytes; the host's call takes as long.
+// without the loads ahead).  One token of 256 sequences of these channels: 5.0 us in
+// a graph, from L2 (alone the host's call is the time).
 #include "gated_delta.cuh"
 
 namespace m2 {
@@ -171,9 +171,7 @@ __global__ void __launch_bounds__(kThreads) k_causal_conv_step(const ConvArgs a,
 template <typename T, int VEC, int W>
 cudaError_t launch_w(const ConvArgs& a, bool step, cudaStream_t st) {
     const unsigned gx = (unsigned)((a.channels + (int64_t)kThreads * VEC - 1) / (kThreads * VEC));
-    constexpr bool whole = VEC * sizeof(T) < 16;  // the vectors of whole sequences, of one token, or single elements
-    constexpr bool token = VEC * sizeof(T) == 16 || VEC == 1;
-    if constexpr (token) {
+    if constexpr (VEC <= 2) {
         if (step) {
             // rows per thread: as many as leave eight blocks to an SM, at most 16
             const int sms = sm_count();
@@ -183,17 +181,15 @@ cudaError_t launch_w(const ConvArgs& a, bool step, cudaStream_t st) {
                 <<<dim3(gx, (unsigned)((a.batch + rows - 1) / rows)), kThreads, 0, st>>>(a, rows);
         }
     }
-    if constexpr (whole) {
-        if (!step) {
-            // Runs of 128 tokens (4 x 8192 x 8192: 180 us, 64: 186, 32: 197), halved down to 16 while there are
-            // fewer than four blocks to an SM.
-            const int sms = sm_count();
-            int run = kRun;
-            while (run > 16 && gx * a.batch * ((a.seqlen + run - 1) / run) < 4 * (int64_t)(sms > 0 ? sms : 152)) run /= 2;
-            const int64_t runs = (a.seqlen + run - 1) / run;
-            k_causal_conv<T, VEC, W>
-                <<<dim3(gx, (unsigned)imin64(runs, 65535), (unsigned)a.batch), kThreads, 0, st>>>(a, run);
-        }
+    if (!step) {
+        // Runs of 128 tokens (4 x 8192 x 8192: 180 us, 64: 186, 32: 197), halved down to 16 while there are
+        // fewer than four blocks to an SM.
+        const int sms = sm_count();
+        int run = kRun;
+        while (run > 16 && gx * a.batch * ((a.seqlen + run - 1) / run) < 4 * (int64_t)(sms > 0 ? sms : 152)) run /= 2;
+        const int64_t runs = (a.seqlen + run - 1) / run;
+        k_causal_conv<T, VEC, W>
+            <<<dim3(gx, (unsigned)imin64(runs, 65535), (unsigned)a.batch), kThreads, 0, st>>>(a, run);
     }
     return cudaGetLastError();
 }
@@ -213,20 +209,19 @@ cudaError_t launch_v(const ConvArgs& a, bool step, cudaStream_t st) {
 
 // The widest vectors on which every row of x and y starts, of up to 8 bytes over whole
 // sequences (registers for eight channels of weights, window and loads under way would
-// leave too few warps; 14 x 3053 x 820 channels in bf16: 34 us, 822 in pairs 42, one by one 62)
-// and of 16 bytes or single elements for one token.
+// leave too few warps; 14 x 3053 x 820 channels in bf16: 34 us, 822 in pairs 42, one by one 62),
+// and pairs for one token, whose weights then come in whole lines and not once for every
+// row (256 x 8192 in bf16: pairs 5.0 us, fours 5.4, eights 11.4, one by one 6.2; in fp32 7.2,
+// fours 7.7, one by one 7.4).
 template <typename T>
 cudaError_t launch_t(const ConvArgs& a, bool step, cudaStream_t st) {
-    constexpr int VEC = 16 / sizeof(T);
+    constexpr int VEC = 8 / sizeof(T);
     const uintptr_t p = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y);
     auto fits = [&](int n) {
         return a.channels % n == 0 && a.x_stride % n == 0 && a.y_stride % n == 0 && p % (n * sizeof(T)) == 0;
     };
-    if (step) return fits(VEC) ? launch_v<T, VEC>(a, true, st) : launch_v<T, 1>(a, true, st);
-    if (fits(VEC / 2)) return launch_v<T, VEC / 2>(a, false, st);
-    if constexpr (VEC == 8)
-        if (fits(2)) return launch_v<T, 2>(a, false, st);
-    return launch_v<T, 1>(a, false, st);
+    if (!step && fits(VEC)) return launch_v<T, VEC>(a, step, st);
+    return fits(2) ? launch_v<T, 2>(a, step, st) : launch_v<T, 1>(a, step, st);
 }
 
 }  // namespace
