@@ -4,36 +4,34 @@
 //
 // The state is read and written once, 8 S H bytes per (batch row, head), next
 // to a few hundred bytes of q, k, v: the step is bound by memory.  A block owns
-// 32 columns of one head's state (columns do not meet) and keeps them in
+// 16 to 64 columns of one head's state (columns do not meet) and keeps them in
 // registers, read before anything they wait for.  The two column sums r = h^T k
 // and p = h^T q are formed together over the state that was read, so the block
 // meets once: with r and p,
 //   w = beta (v - a r),   y = scale (a p + (q . k) w),   h <- a h + k w^T.
-// 256 sequences of 64 heads of 64 columns, S 128: 168 us, 6.4 TB/s (0.96 of a plain
-// copy).  Blocks of 32 columns: a row of theirs is one 128-byte line, and a head of
-// one sequence still gives several blocks.
+// 256 sequences of 64 heads of 64 columns, S 128: 155 us, 6.9 TB/s (1.03 of a plain
+// copy).
 #include "gated_delta.cuh"
 
 namespace m2 {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kCols = 32;  // columns of the state per block
 
 // VEC columns per thread (4, or 1 where H is no multiple of 4), RPT state rows
-// per thread; kCols / VEC threads span the columns, kRows row groups the rows.
-template <typename T, int VEC, int RPT>
+// per thread; COLS / VEC threads span the columns, kRows row groups the rows.
+template <typename T, int COLS, int VEC, int RPT>
 __global__ void __launch_bounds__(kThreads) k_gdr_step(const GdrArgs a) {
-    constexpr int kCt = kCols / VEC, kRows = kThreads / kCt;
+    constexpr int kCt = COLS / VEC, kRows = kThreads / kCt;
     using V = typename VecOf<float, VEC>::type;
-    __shared__ float s_q[256], s_k[256], s_red[4][3], s_part[4][kCols][2];
+    __shared__ float s_q[256], s_k[256], s_red[4][3], s_part[4][COLS][2];
     const Geom& g = a.g;
     const int S = (int)g.dstate, H = (int)g.headdim;
     const int64_t h = blockIdx.y, b = blockIdx.z;
     const int64_t grp = h / g.heads_per_group;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ct = tid % kCt, r0 = tid / kCt;
-    const int col = blockIdx.x * kCols + ct * VEC;
+    const int col = blockIdx.x * COLS + ct * VEC;
     const bool live = col < H;
     const int64_t base = (b * g.nheads + h) * (int64_t)S * H + col;
 
@@ -128,23 +126,32 @@ __global__ void __launch_bounds__(kThreads) k_gdr_step(const GdrArgs a) {
     }
 }
 
-template <typename T, int VEC>
-cudaError_t launch_v(const GdrArgs& a, cudaStream_t st) {
-    const dim3 grid((unsigned)((a.g.headdim + kCols - 1) / kCols), (unsigned)a.g.nheads, (unsigned)a.g.batch);
-    constexpr int kRows = kThreads / (kCols / VEC);
+template <typename T, int COLS, int VEC>
+cudaError_t launch_c(const GdrArgs& a, cudaStream_t st) {
+    const dim3 grid((unsigned)((a.g.headdim + COLS - 1) / COLS), (unsigned)a.g.nheads, (unsigned)a.g.batch);
+    constexpr int kRows = kThreads / (COLS / VEC);
     const int64_t S = a.g.dstate;
     if (S <= 64)
-        k_gdr_step<T, VEC, 64 / kRows><<<grid, kThreads, 0, st>>>(a);
+        k_gdr_step<T, COLS, VEC, 64 / kRows><<<grid, kThreads, 0, st>>>(a);
     else if (S <= 128)
-        k_gdr_step<T, VEC, 128 / kRows><<<grid, kThreads, 0, st>>>(a);
+        k_gdr_step<T, COLS, VEC, 128 / kRows><<<grid, kThreads, 0, st>>>(a);
     else
-        k_gdr_step<T, VEC, 256 / kRows><<<grid, kThreads, 0, st>>>(a);
+        k_gdr_step<T, COLS, VEC, 256 / kRows><<<grid, kThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 
+// Columns per block: 64 where that still gives eight blocks to an SM (more bytes under way
+// for each meeting of a block), 16 for narrow heads, else 32.  us with 16 / 32 / 64: 256
+// sequences of 64 heads of 64, S 128, 186 / 165 / 155; of 40, S 64, 100 / 79 / 71; of 8, S 128,
+// 40 / 55 / 87; one sequence of 32 heads of 128, S 128, 3.3 / 3.1 / 3.7.
 template <typename T>
 cudaError_t launch_t(const GdrArgs& a, cudaStream_t st) {
-    return a.g.headdim % 4 == 0 ? launch_v<T, 4>(a, st) : launch_v<T, 1>(a, st);
+    const int64_t H = a.g.headdim;
+    if (H % 4 != 0) return launch_c<T, 32, 1>(a, st);
+    if (H <= 16) return launch_c<T, 16, 4>(a, st);
+    const int sms = sm_count();
+    const bool many = a.g.batch * a.g.nheads * ((H + 63) / 64) >= 8 * (int64_t)(sms > 0 ? sms : 152);
+    return H > 32 && many ? launch_c<T, 64, 4>(a, st) : launch_c<T, 32, 4>(a, st);
 }
 
 }  // namespace

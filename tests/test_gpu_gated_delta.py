@@ -357,6 +357,15 @@ def test_gdr_step(b, nh, G, H, S, dtype):
     assert st2 is st and torch.equal(st, out.t) and torch.equal(y2, y.t)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("b,nh,G,H,S", [
+    (80, 16, 4, 64, 64), (1301, 1, 1, 40, 128), (650, 1, 1, 128, 96), (330, 2, 2, 100, 200), (3, 4, 2, 8, 128),
+    (2, 3, 1, 16, 64), (5, 2, 1, 12, 256), (1, 2, 1, 36, 40),
+])
+def test_gdr_step_of_many_sequences_and_narrow_heads(b, nh, G, H, S, dtype):
+    test_gdr_step(b, nh, G, H, S, dtype)
+
+
 def test_gdr_step_from_nothing_and_without_decay():
     d, h0 = gdr_inputs(2, 1, 2, 1, 64, 128, BF16)
     t = {n: x[:, 0].contiguous() for n, x in d.items()}
