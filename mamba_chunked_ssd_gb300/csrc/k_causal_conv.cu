@@ -7,11 +7,12 @@
 // by memory.  A thread owns the channels of one vector and a run of consecutive
 // tokens, and slides a window of the last W - 1 inputs through its registers, so a
 // token's input is loaded once per run (plus the W - 1 tokens before the run,
-// which the neighbouring run has just brought into L2).  The loads of the next
-// eight tokens are under way while eight are computed.  4 x 8192 tokens of 8192
-// channels in bf16, width 4, SiLU: 183 us, 5.9 TB/s (0.88 of a plain copy; 366 us
-// without the loads ahead).  One token of 256 sequences of these channels: 5.0 us in
-// a graph, from L2 (alone the host's call is the time).
+// which the neighbouring run has just brought into L2).  Inputs come through
+// shared memory, each thread's to its own place, two or three times eight tokens ahead.
+// 4 x 8192 tokens of 8192 channels in bf16, width 4, SiLU: 162 us, 6.6 TB/s (0.99 of a plain
+// copy; 366 us without loads ahead, 180 with eight in registers).  One token of 256
+// sequences of these channels: 5.0 us in a graph, from L2 (alone the host's call is the
+// time).
 #include "gated_delta.cuh"
 
 namespace m2 {
@@ -19,7 +20,11 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kRun = 128;  // tokens per thread, less where that leaves too few blocks
-constexpr int kAhead = 8;  // loads in flight per thread
+constexpr int kAhead = 8;
+// Groups of kAhead tokens under way per thread (4 x 8192 x 8192 in bf16: 3 162 us, 2 163, one in
+// registers 180; 16 x 1024 x 4096 46 / 50 / 55; 4 x 4096 x 8192 in fp32 177 / 170 / 172).
+template <typename T>
+constexpr int kDepthOf = sizeof(T) == 2 ? 3 : 2;
 
 // The weights of VEC neighbouring channels: one run of VEC W floats, in 16-byte
 // loads where that is whole ones.
@@ -100,23 +105,52 @@ __global__ void __launch_bounds__(kThreads, VEC * W <= 16 ? 5 : 1) k_causal_conv
                 *reinterpret_cast<V*>(yt) = pack<T, VEC>(s);
                 yt += a.y_stride;
             };
-            V next[kAhead];
             const int whole = m / kAhead;
-            if (whole > 0) {
+            if constexpr (sizeof(V) >= 4) {
+                constexpr int kDepth = kDepthOf<T>;
+                // the loads of the next kDepth times eight tokens are under way, each thread's to its own place
+                __shared__ V ring[kDepth * kAhead][kThreads];
+                auto ahead = [&](int k) {
+                    if (k < whole) {
+                        const T* from = x + (t0 + (int64_t)k * kAhead) * a.x_stride;
 #pragma unroll
-                for (int u = 0; u < kAhead; ++u) next[u] = *reinterpret_cast<const V*>(xt + u * a.x_stride);
-            }
-            for (int k = 0; k < whole; ++k) {
-                V in[kAhead];
+                        for (int u = 0; u < kAhead; ++u)
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(
+                                             (uint32_t)__cvta_generic_to_shared(&ring[k % kDepth * kAhead + u][threadIdx.x])),
+                                         "l"(from + u * a.x_stride), "n"(sizeof(V))
+                                         : "memory");
+                    }
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                };
+                for (int k = 0; k < kDepth; ++k) ahead(k);
+                for (int k = 0; k < whole; ++k) {
+                    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+                    V in[kAhead];
 #pragma unroll
-                for (int u = 0; u < kAhead; ++u) in[u] = next[u];
-                xt += kAhead * a.x_stride;
-                if (k + 1 < whole) {
+                    for (int u = 0; u < kAhead; ++u) in[u] = ring[k % kDepth * kAhead + u][threadIdx.x];
+#pragma unroll
+                    for (int u = 0; u < kAhead; ++u) token(in[u]);
+                    ahead(k + kDepth);
+                }
+                xt += (int64_t)whole * kAhead * a.x_stride;
+            } else {
+                V next[kAhead];
+                if (whole > 0) {
 #pragma unroll
                     for (int u = 0; u < kAhead; ++u) next[u] = *reinterpret_cast<const V*>(xt + u * a.x_stride);
                 }
+                for (int k = 0; k < whole; ++k) {
+                    V in[kAhead];
 #pragma unroll
-                for (int u = 0; u < kAhead; ++u) token(in[u]);
+                    for (int u = 0; u < kAhead; ++u) in[u] = next[u];
+                    xt += kAhead * a.x_stride;
+                    if (k + 1 < whole) {
+#pragma unroll
+                        for (int u = 0; u < kAhead; ++u) next[u] = *reinterpret_cast<const V*>(xt + u * a.x_stride);
+                    }
+#pragma unroll
+                    for (int u = 0; u < kAhead; ++u) token(in[u]);
+                }
             }
 #pragma unroll 1
             for (int u = whole * kAhead; u < m; ++u, xt += a.x_stride) token(*reinterpret_cast<const V*>(xt));
@@ -182,7 +216,7 @@ cudaError_t launch_w(const ConvArgs& a, bool step, cudaStream_t st) {
         }
     }
     if (!step) {
-        // Runs of 128 tokens (4 x 8192 x 8192: 180 us, 64: 186, 32: 197), halved down to 16 while there are
+        // Runs of 128 tokens (4 x 8192 x 8192: 162 us, 64: 162, 256: 166; width 8 110, 124, 105), halved down to 16 while there are
         // fewer than four blocks to an SM.
         const int sms = sm_count();
         int run = kRun;
@@ -209,7 +243,7 @@ cudaError_t launch_v(const ConvArgs& a, bool step, cudaStream_t st) {
 
 // The widest vectors on which every row of x and y starts, of up to 8 bytes over whole
 // sequences (registers for eight channels of weights, window and loads under way would
-// leave too few warps; 14 x 3053 x 820 channels in bf16: 34 us, 822 in pairs 42, one by one 62),
+// leave too few warps; 14 x 3053 channels in bf16: 820 33 us, 822 in pairs 37, 823 one by one 62),
 // and pairs for one token, whose weights then come in whole lines and not once for every
 // row (256 x 8192 in bf16: pairs 5.0 us, fours 5.4, eights 11.4, one by one 6.2; in fp32 7.2,
 // fours 7.7, one by one 7.4).
