@@ -10,8 +10,8 @@
 // it are summed from registers, in fp32 and a fixed order, without a second
 // read.  Threads keep their channels and walk down the rows: up to 16 channels to
 // a thread, the weights stay in registers and a row's loads are under way while
-// the row before is summed.  32768 x 4096 in bf16, groups of 64, gated: 131 us, 6.2 TB/s
-// (0.92 of a plain copy; 217 us with a block to a row); 8192 x 4096 in one group,
+// the row before is summed.  32768 x 4096 in bf16, groups of 64, gated: 129 us, 6.2 TB/s
+// (0.93 of a plain copy; 217 us with a block to a row); 8192 x 4096 in one group,
 // gated first: 37 us, 5.4 TB/s (0.81; a block-wide sum a row).
 #include "gated_delta.cuh"
 #include "mamba2_gated_delta.h"
@@ -48,20 +48,22 @@ constexpr int min_blocks(int channels, int tpg) {
     return tpg > 512 || channels > 16 ? 1 : (channels <= 8 || tpg == 512 ? 1024 : 768) / (tpg > 32 ? tpg : kWarpBlock);
 }
 
-// bf16 rows of groups that fill blocks come through a ring in shared memory, kRing rows ahead,
-// each thread copying what it reads itself: registers hold too few loads for block-wide
-// sums between them (us without / with, gated before: 2048 channels 36.6 / 33.8, 4096 36.7 /
-// 34.9, 16384 50 / 41; over 28 sizes and modes 6 % faster; two rows ahead
-// are 4 % slower).  In fp32 it is 5 % slower (1024 channels, gated after, 31.0 / 36.8).
-constexpr int kRing = 3;
+// bf16 rows come through a ring in shared memory, two or three rows ahead, each thread copying
+// what it reads itself: registers hold too few loads for the sums between them.  us without /
+// with: blocks, gated before, 2048 channels 36.6 / 33.8, 4096 36.7 / 34.9, 16384 50 / 41 (over
+// 28 sizes and modes 6 % faster; two rows ahead are 4 % slower); groups inside warps, 32768 x
+// 4096 in groups of 64, gated after 129 / 125, no gate 99 / 85 (three rows 131, 86), but in
+// 8-byte vectors 242 / 272.  In fp32 it is slower (1024 channels, gated after, 31 / 37).
+constexpr int ring_rows(int tpg) { return tpg > 32 ? 3 : 2; }
 template <typename T>
 constexpr bool use_ring(int vec, int nv, int tpg) {
-    return tpg > 32 && sizeof(T) == 2 && vec > 1 && nv * vec <= 16 && nv * tpg <= 2048;
+    return sizeof(T) == 2 && vec >= (tpg > 32 ? 4 : 8) && nv * vec <= 16 && nv * tpg <= 2048;
 }
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool live) {
     if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0)
+                     : "memory");
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(live ? 8 : 0) : "memory");
 }
@@ -119,7 +121,9 @@ k_group_norm(const NormArgs a, int across) {
         }
     };
     constexpr bool kUseRing = use_ring<T>(VEC, NV, TPG);
-    extern __shared__ __align__(16) uint8_t ring_bytes[];  // [kRing][x and z][NV][TPG]
+    constexpr int kRing = ring_rows(TPG);
+    extern __shared__ __align__(16) uint8_t ring_bytes[];  // [kRing][x and z][NV][threads]
+    constexpr int kBlk = TPG > 32 ? TPG : kWarpBlock;
     V* ring = reinterpret_cast<V*>(ring_bytes);
     const int slots = gated ? 2 * NV : NV;
     auto ahead = [&](int64_t r, int stage) {
@@ -127,10 +131,10 @@ k_group_norm(const NormArgs a, int across) {
         for (int i = 0; i < NV; ++i) {
             const int j = lane + i * TPG;
             const bool live = mine && r < a.rows && j < nvec;
-            const uint32_t dst = (uint32_t)__cvta_generic_to_shared(ring + (stage * slots + i) * TPG + lane);
+            const uint32_t dst = (uint32_t)__cvta_generic_to_shared(ring + (stage * slots + i) * kBlk + threadIdx.x);
             const int64_t at = live ? (int64_t)j * VEC : 0, rr = live ? r : 0;
             copy_async<sizeof(V)>(dst, x + rr * a.x_stride + at, live);
-            if (gated) copy_async<sizeof(V)>(dst + NV * TPG * sizeof(V), z + rr * a.z_stride + at, live);
+            if (gated) copy_async<sizeof(V)>(dst + NV * kBlk * sizeof(V), z + rr * a.z_stride + at, live);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -149,9 +153,9 @@ k_group_norm(const NormArgs a, int across) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const V* from = ring + (stage * slots + i) * TPG + lane;
+                const V* from = ring + (stage * slots + i) * kBlk + threadIdx.x;
                 xr[i] = *from;
-                if (gated) zr[i] = from[NV * TPG];
+                if (gated) zr[i] = from[NV * kBlk];
             }
         }
 #pragma unroll
@@ -225,7 +229,10 @@ cudaError_t launch_n(const NormArgs& a, cudaStream_t st) {
     const int64_t gx = (a.ngroups + (1 << across) - 1) >> across, rows_per = per >> across;
     // as many blocks as fit on the GPU at once: each keeps its weights for its share of the rows
     const bool gated = (a.flags & (MAMBA2_NORM_GATE_BEFORE | MAMBA2_NORM_GATE_AFTER)) != 0;
-    auto ring_bytes = [](bool z) { return use_ring<T>(VEC, NV, TPG) ? kRing * (z ? 2 : 1) * NV * TPG * (int)sizeof(typename VecOf<T, VEC>::type) : 0; };
+    auto ring_bytes = [](bool z) {
+        constexpr int row = NV * block * (int)sizeof(typename VecOf<T, VEC>::type);
+        return use_ring<T>(VEC, NV, TPG) ? ring_rows(TPG) * (z ? 2 : 1) * row : 0;
+    };
     const cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(k_group_norm<T, VEC, NV, TPG>),
                                                   ring_bytes(true));
     if (e != cudaSuccess) return e;
