@@ -255,7 +255,9 @@ cudaError_t launch_n(const NormArgs& a, cudaStream_t st) {
 template <typename T, int VEC>
 cudaError_t launch_v(const NormArgs& a, cudaStream_t st) {
     const int64_t n = a.channels / a.ngroups / VEC;
-    constexpr int K = VEC == 1 ? 8 : 1;  // single elements: more loads per thread
+    // single elements: more loads per thread (bf16, gated, us with 8 / 4 / 2: 65536 x 264 in groups of
+    // 33 58 / 51 / 80, 16384 x 1028 in groups of 257 86 / 45 / 49, 8192 x 2049 66 / 44 / 50)
+    constexpr int K = VEC == 1 ? 4 : 1;
     if (n <= 8 * K) return launch_n<T, VEC, K, 8>(a, st);
     if (n <= 16 * K) return launch_n<T, VEC, K, 16>(a, st);
     if (n <= 32 * K) return launch_n<T, VEC, K, 32>(a, st);

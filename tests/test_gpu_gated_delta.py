@@ -554,6 +554,17 @@ def test_norm_of_the_largest_groups(size):
     assert rel_err(np64(odd), ref.norm(x[:, :size - 1], 1)) <= TOL_ROUND[BF16]
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("size", [17, 65, 129, 257, 513, 1025, 4097, 16383, 32767])
+def test_norm_of_odd_groups(size, dtype):
+    r = torch.Generator().manual_seed(size)
+    x, w = torch.randn(7, 3 * size, generator=r).to(dtype).cuda(), torch.randn(3 * size, generator=r).cuda()
+    y = Guarded((7, 3 * size), dtype)
+    bd.mamba2_group_norm(x, w, 3, z=x, mode="after", subtract_mean=True, y=y.t)
+    assert y.intact()
+    assert rel_err(np64(y.t), ref.norm(x, 3, w, None, x, 1e-5, True, "after")) <= TOL_ROUND[dtype]
+
+
 def test_norm_far_from_zero():
     """A mean far larger than the spread: the squares are of the differences."""
     x = 1000 + torch.randn(4, 512, device="cuda")
