@@ -3,7 +3,7 @@
 //
 //   h <- a h + k (beta (v - a h^T k))^T,  y = scale h^T q,   a = e^g
 //
-// four tokens at a time.  Columns of the state do not meet, so a block owns 8 to 32
+// four tokens at a time.  Columns of the state do not meet, so a block owns 8 to 40
 // columns of one head for the whole sequence, and a column's rows lie in the registers
 // of eight lanes.  What bounds it is the chain from state to
 // state: the sum h^T k over the rows (registers, then three shuffles), the
@@ -377,14 +377,16 @@ cudaError_t launch_k(const GdrArgs& a, cudaStream_t st) {
 // memory's reads count, and two columns to a lane halve them.  1024 tokens in fp32, H 64,
 // us with 8 columns / 16 / 32 (two to a lane) to a block: S 64, 16 heads 93 / 105 / 135, 32
 // heads 123 / 107 / 135, 64 heads 272 / 178 / 135; S 256 207 / 268 / 327, 397 / 265 / 326,
-// 773 / 512 / 325.
+// 773 / 512 / 325.  40 columns where they leave fewer over than 32 (19 x 637 tokens of 24 heads
+// of 40 columns, S 128, fp32: 485 us, with 32 689).
 template <typename T, int RP>
 cudaError_t launch_rp(const GdrArgs& a, cudaStream_t st) {
     const int sms = sm_count();
     const int64_t fit = sms > 0 ? sms : 152, heads = a.g.batch * a.g.nheads;
     if (heads * ((a.g.headdim + 7) / 8) <= fit) return launch_k<T, RP, 8, 1>(a, st);
     if (heads * ((a.g.headdim + 15) / 16) <= fit) return launch_k<T, RP, 16, 1>(a, st);
-    return launch_k<T, RP, 32, 2>(a, st);
+    const auto blocks = [&](int n) { return (a.g.headdim + n - 1) / n * n; };
+    return blocks(40) < blocks(32) ? launch_k<T, RP, 40, 2>(a, st) : launch_k<T, RP, 32, 2>(a, st);
 }
 
 template <typename T>
