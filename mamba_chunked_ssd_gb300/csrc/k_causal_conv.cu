@@ -20,8 +20,11 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kRun = 128;  // tokens per thread, less where that leaves too few blocks
-constexpr int kAhead = 8;
-// Groups of kAhead tokens under way per thread (4 x 8192 x 8192 in bf16: 3 162 us, 2 163, one in
+// Tokens whose loads are issued together: 32 where a thread's are of 2 bytes and come through
+// registers (14 x 3053 tokens of 823 channels in bf16: 39 us, 16 49, 8 62).
+template <typename V>
+constexpr int kAheadOf = sizeof(V) < 4 ? 32 : 8;
+// Groups of these under way per thread (4 x 8192 x 8192 in bf16: 3 162 us, 2 163, one in
 // registers 180; 16 x 1024 x 4096 46 / 50 / 55; 4 x 4096 x 8192 in fp32 177 / 170 / 172).
 template <typename T>
 constexpr int kDepthOf = sizeof(T) == 2 ? 3 : 2;
@@ -53,6 +56,7 @@ __device__ __forceinline__ void load_weights(const float* weight, int64_t c, flo
 template <typename T, int VEC, int W>
 __global__ void __launch_bounds__(kThreads, VEC * W <= 16 ? 5 : 1) k_causal_conv(const ConvArgs a, int run) {
     using V = typename VecOf<T, VEC>::type;
+    constexpr int kAhead = kAheadOf<V>;
     const int64_t c = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * VEC;
     if (c >= a.channels) return;
     const int64_t b = blockIdx.z;
@@ -152,8 +156,20 @@ __global__ void __launch_bounds__(kThreads, VEC * W <= 16 ? 5 : 1) k_causal_conv
                     for (int u = 0; u < kAhead; ++u) token(in[u]);
                 }
             }
+            int left = m - whole * kAhead;
+            if (kAhead > 8) {
 #pragma unroll 1
-            for (int u = whole * kAhead; u < m; ++u, xt += a.x_stride) token(*reinterpret_cast<const V*>(xt));
+                for (; left >= 8; left -= 8) {
+                    V in[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) in[u] = *reinterpret_cast<const V*>(xt + u * a.x_stride);
+                    xt += 8 * a.x_stride;
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) token(in[u]);
+                }
+            }
+#pragma unroll 1
+            for (; left > 0; --left, xt += a.x_stride) token(*reinterpret_cast<const V*>(xt));
         }
         for (int64_t t = t0 + (m > 0 ? m : 0); t < t1; ++t) *reinterpret_cast<V*>(y + t * a.y_stride) = V{};
     }
@@ -216,11 +232,12 @@ cudaError_t launch_w(const ConvArgs& a, bool step, cudaStream_t st) {
         }
     }
     if (!step) {
-        // Runs of 128 tokens (4 x 8192 x 8192: 162 us, 64: 162, 256: 166; width 8 110, 124, 105), halved down to 16 while there are
-        // fewer than four blocks to an SM.
+        constexpr int least = VEC * sizeof(T) < 4 ? 32 : 16;
+        // Runs of 128 tokens (4 x 8192 x 8192: 162 us, 64: 162, 256: 166; width 8 110, 124, 105), halved down to
+        // 16 (or the 32 that are loaded together) while there are fewer than four blocks to an SM.
         const int sms = sm_count();
         int run = kRun;
-        while (run > 16 && gx * a.batch * ((a.seqlen + run - 1) / run) < 4 * (int64_t)(sms > 0 ? sms : 152)) run /= 2;
+        while (run > least && gx * a.batch * ((a.seqlen + run - 1) / run) < 4 * (int64_t)(sms > 0 ? sms : 152)) run /= 2;
         const int64_t runs = (a.seqlen + run - 1) / run;
         k_causal_conv<T, VEC, W>
             <<<dim3(gx, (unsigned)imin64(runs, 65535), (unsigned)a.batch), kThreads, 0, st>>>(a, run);
@@ -243,7 +260,7 @@ cudaError_t launch_v(const ConvArgs& a, bool step, cudaStream_t st) {
 
 // The widest vectors on which every row of x and y starts, of up to 8 bytes over whole
 // sequences (registers for eight channels of weights, window and loads under way would
-// leave too few warps; 14 x 3053 channels in bf16: 820 33 us, 822 in pairs 37, 823 one by one 62),
+// leave too few warps; 14 x 3053 tokens in bf16: 820 channels 33 us, 822 in pairs 37, 823 one by one 39),
 // and pairs for one token, whose weights then come in whole lines and not once for every
 // row (256 x 8192 in bf16: pairs 5.0 us, fours 5.4, eights 11.4, one by one 6.2; in fp32 7.2,
 // fours 7.7, one by one 7.4).
