@@ -15,14 +15,14 @@
 //
 // GB300 design.  One CTA owns one head of up to 128 columns (or two heads of up to 64
 // columns of one q/k group, NV = 2; smaller states and heads are filled up with zeros:
-// 4 x 1024 tokens of 24 heads of 96 columns, S 96, 124 us, token by token 367) and walks the chunks; the carried state and
-// every intermediate stay on the chip, so q, k, v, g, beta are read once and y
-// is written once.  All products of the chain run transposed, with the head's
-// columns as the 128 rows of the MMA: the fp32 state h^T lives in tensor memory,
-// and what is fed back (h, X, W) is read from there, converted, and written back
-// to tensor memory as the next product's left operand, while K, Q, N and P are
-// right operands in shared memory, straight from the TMA or as the scores' warps
-// wrote them.
+// 4 x 1024 tokens of 24 heads of 96 columns, S 96, 124 us, token by token 367) and
+// walks the chunks; the carried state and every intermediate stay on the chip, so q,
+// k, v, g, beta are read once and y is written once.  All products of the chain run
+// transposed, with the head's columns as the 128 rows of the MMA: the fp32 state h^T
+// lives in tensor memory, and what is fed back (h, X, W) is read from there,
+// converted, and written back to tensor memory as the next product's left operand,
+// while K, Q, N and P are right operands in shared memory, straight from the TMA or as
+// the scores' warps wrote them.
 //   warps 0-15   chain: h -> two bf16 parts and e^{G_last} h;  R = K h -> X;  W ->
 //                its parts (four per TMEM lane quadrant, a quarter of the columns
 //                each)
@@ -33,23 +33,22 @@
 //   warps 28-31  TMA producer of K and Q; TMA producer of V; issuers of the chain's
 //                products and of P W (a product takes its issuer 46 cycles or more
 //                however small it is, so P W would hold up the chain's)
-// What bounds it is the chain from state to state: three dependent products and
-// three conversions a chunk, about 3.5 us with two heads to a CTA and 3.0 with one,
-// whatever the memory could do.  4 x 8192 tokens of 64 heads of 64 columns, S 128,
-// 16 q/k groups: 903 us (0.93 TB/s of what has to move, 114 TFLOP/s of the recurrence's
-// arithmetic); 4 x 4096 of 32 heads of 128: 396 us (1.07 TB/s; DRAM 10 %, tensor
-// pipe 14 %, 0.57 instructions a cycle and scheduler); 1237 tokens alone: 119 us.
-// What enters the fp32 state is as good as fp32: N, X
-// and W take part in its products as three bf16 parts each (24 bits), h in the
-// correction R as two (16 bits; R's share of an error decays with the state's).
-// With two parts throughout, the state was 1e-6 to 3e-6 off on ordinary inputs
-// and 2e-3 where keys agree and beta is 2 (N's entries are +-2 there and W's sums
-// cancel).  The final state is 3e-7 to 5e-7 off, and up to 1.1e-6 in heads that hardly decay
-// (fp32 2e-7 to 3e-7): a third part of h brought that to 0.7e-6 and cost 15 % of the time
-// (4 x 4096: 396 -> 457 us), the rest is the tensor cores' accumulation, which rounds
-// towards zero.  P and W enter y as two parts: with keys that agree, P W sums
-// corrections that cancel, and one part lost 1.8 % of y's largest value.  Q h
-// takes h's high part.
+// What bounds it is the chain from state to state: three dependent products and three
+// conversions a chunk, about 3.5 us with two heads to a CTA and 3.0 with one, whatever
+// the memory could do.  4 x 8192 tokens of 64 heads of 64 columns, S 128, 16 q/k
+// groups: 903 us (0.93 TB/s of what has to move, 114 TFLOP/s of the recurrence's
+// arithmetic); 4 x 4096 of 32 heads of 128: 396 us (1.07 TB/s; DRAM 10 %, tensor pipe
+// 14 %, 0.57 instructions a cycle and scheduler); 1237 tokens alone: 119 us. What
+// enters the fp32 state is as good as fp32: N, X and W take part in its products as
+// three bf16 parts each (24 bits), h in the correction R as two (16 bits; R's share of
+// an error decays with the state's). With two parts throughout, the state was 1e-6 to
+// 3e-6 off on ordinary inputs and 2e-3 where keys agree and beta is 2 (N's entries are
+// +-2 there and W's sums cancel).  The final state is 3e-7 to 5e-7 off, and up to
+// 1.1e-6 in heads that hardly decay (fp32 2e-7 to 3e-7): a third part of h brought
+// that to 0.7e-6 and cost 15 % of the time (4 x 4096: 396 -> 457 us), the rest is the
+// tensor cores' accumulation, which rounds towards zero.  P and W enter y as two
+// parts: with keys that agree, P W sums corrections that cancel, and one part lost 1.8
+// % of y's largest value.  Q h takes h's high part.
 //
 // Chunks of 32 and not 64: N and P cost a chunk's square on the CUDA cores, and
 // with 64 tokens N (about 12000 cycles a chunk for four warps) held up a chain of
