@@ -38,8 +38,9 @@
 // the memory could do.  4 x 8192 tokens of 64 heads of 64 columns, S 128, 16 q/k
 // groups: 903 us (0.93 TB/s of what has to move, 114 TFLOP/s of the recurrence's
 // arithmetic); 4 x 4096 of 32 heads of 128: 396 us (1.07 TB/s; DRAM 10 %, tensor pipe
-// 14 %, 0.57 instructions a cycle and scheduler); 1237 tokens alone: 119 us. What
-// enters the fp32 state is as good as fp32: N, X and W take part in its products as
+// 14 %, 0.57 instructions a cycle and scheduler); 1237 tokens alone: 119 us
+// (some runs of the same binary take 1004 and 429 us for the first two, by where its code
+// comes to lie).  What enters the fp32 state is as good as fp32: N, X and W take part in its products as
 // three bf16 parts each (24 bits), h in the correction R as two (16 bits; R's share of
 // an error decays with the state's). With two parts throughout, the state was 1e-6 to
 // 3e-6 off on ordinary inputs and 2e-3 where keys agree and beta is 2 (N's entries are
