@@ -67,7 +67,7 @@ typedef struct {
  * and token stride are multiples of 16 bytes, the products run in chunks on the
  * tensor cores (but for a few tokens of few heads): what is added to the fp32 state is made of three bf16 parts
  * (24 bits) of every intermediate, from two parts (16 bits) of the state before
- * it; y takes two parts of the corrections and the high part of the state.
+ * it; y takes two parts (16 bits) of the corrections and of the state.
  * Everything else runs token by token in fp32. */
 MAMBA2_API mamba2_status mamba2_gdr_fwd(const mamba2_shape* shape, const mamba2_gdr_options* options, const void* q,
                                         const void* k, const void* v, const float* g, const float* beta,

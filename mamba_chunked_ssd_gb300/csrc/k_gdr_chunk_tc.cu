@@ -47,9 +47,12 @@
 // +-2 there and W's sums cancel).  The final state is 3e-7 to 5e-7 off, and up to
 // 1.1e-6 in heads that hardly decay (fp32 2e-7 to 3e-7): a third part of h brought
 // that to 0.7e-6 and cost 15 % of the time (4 x 4096: 396 -> 457 us), the rest is the
-// tensor cores' accumulation, which rounds towards zero.  P and W enter y as two
-// parts: with keys that agree, P W sums corrections that cancel, and one part lost 1.8
-// % of y's largest value.  Q h takes h's high part.
+// tensor cores' accumulation, which rounds towards zero.  P, W and h enter y as
+// two parts.  With keys that agree, P W sums corrections that cancel, and one part lost 1.8
+// % of y's largest value; and P W cancels against Q h where a token overwrites a larger
+// value, so Q h takes the h that R took (with h's high part alone, y of a token that
+// overwrites one 100 times its size was 10 % off; both parts cost 1 to 3 % of the time).
+// y is off by its rounding to bf16 alone, 1.658e-3 by norm.
 //
 // Chunks of 32 and not 64: N and P cost a chunk's square on the CUDA cores, and
 // with 64 tokens N (about 12000 cycles a chunk for four warps) held up a chain of
@@ -965,17 +968,19 @@ k_gdr_chunk_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     const uint32_t aK = tc::smem_u32(smem + st * kStage);
                     const uint64_t dK = tc::sdesc_sw128(aK, 16, 1024);
                     const uint64_t dKt = tc::sdesc_sw128(aK, 2 * kBox, 1024);
-                    // R | Q h from h's high part, R from its low part.  (The chain has waited for the scalars, and
-                    // their makers for K and Q, whose rows past the end they cleared.)
+                    // R | Q h from h's high part, then from its low part (Q h too: P W, made from this R, cancels
+                    // against it).  (The chain has waited for the scalars, and their makers for K and Q; K's rows
+                    // past the end they cleared.)
                     if (!thread_wait<false>(&bars[kBarHReady], ph, abort_flag)) { ok = false; break; }
                     tc::tc_fence_after();
 #pragma unroll 1
                     for (int x = 0; x < 2 * kBoxes; ++x) {
-                        const uint32_t id = x < kBoxes ? id_rq : id_t, box = x < kBoxes ? x : x - kBoxes;
+                        const uint32_t box = x < kBoxes ? x : x - kBoxes;
                         const uint64_t d = dK + box * (2 * kBox >> 4);
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            tc::mma_bf16_ts(tmem + cR, tmem + cHi + 32 * x + 8 * ks, d + 2 * ks, id, x > 0 || ks > 0);
+                            tc::mma_bf16_ts(tmem + cR, tmem + cHi + 32 * x + 8 * ks, d + 2 * ks, id_rq,
+                                            x > 0 || ks > 0);
                     }
                     tc::mma_commit(&bars[kBarRDone]);
                     // W = N X, N's parts times X's down to 2^-16 of hi hi; N's second block column only has
