@@ -266,7 +266,8 @@ def mamba2_ssd_step(x, dt, A, B, C, state_in=None, D=None, state_out=None, y=Non
 # The gated-delta-rule entry points are also called once a token, where the host
 # call is the time: they pass plain integers (ctypes makes the pointers), ask for
 # the raw stream, check a tensor's layout in as few attribute reads as will do, and
-# keep the structures that describe a call's sizes (never its tensors).
+# keep the structures that describe a call's sizes (never its tensors: what may come
+# as one, a scale or an eps, is a number before it is looked up).
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
@@ -342,8 +343,9 @@ def _gdr_args(q, k, v, g, beta, scale, qk_l2norm, l2_eps):
     _want(g, "g", torch.float32, rows), _want(beta, "beta", torch.float32, rows)
     S = qs[-1]
     shape = _gdr_shape(vs[0], vs[1] if len(vs) == 4 else 1, nh, vs[-1], S, qs[-2], 64, _dtype_code(v), 0)
-    opt = _gdr_options(_rows(q, "q", 2), _rows(k, "k", 2), _rows(v, "v", 2), S ** -0.5 if scale is None else scale,
-                       l2_eps, MAMBA2_GDR_QK_L2NORM if qk_l2norm else 0, 0)
+    opt = _gdr_options(_rows(q, "q", 2), _rows(k, "k", 2), _rows(v, "v", 2),
+                       S ** -0.5 if scale is None else float(scale), float(l2_eps),
+                       MAMBA2_GDR_QK_L2NORM if qk_l2norm else 0, 0)
     return shape, opt, (vs[0], nh, S, vs[-1])
 
 
@@ -449,7 +451,7 @@ def mamba2_group_norm(x, weight, ngroups, z=None, bias=None, eps=1e-5, subtract_
         _like(x, z, "z")
     y = _like(x, y, "y")
     shape = _norm_shape(x.numel() // C if C else 0, C, ngroups, _rows(x, "x", 1),
-                        0 if z is None else _rows(z, "z", 1), _rows(y, "y", 1), eps, _dtype_code(x),
+                        0 if z is None else _rows(z, "z", 1), _rows(y, "y", 1), float(eps), _dtype_code(x),
                         flags | MAMBA2_NORM_SUBTRACT_MEAN if subtract_mean else flags, 0)
     rc = load_library().mamba2_group_norm(shape, _at(x), _at(z), _at(weight), _at(bias), _at(y), _on(stream, x))
     if rc:
