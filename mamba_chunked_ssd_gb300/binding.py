@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 import re
 
@@ -267,7 +268,7 @@ def mamba2_ssd_step(x, dt, A, B, C, state_in=None, D=None, state_out=None, y=Non
 # call is the time: they pass plain integers (ctypes makes the pointers), ask for
 # the raw stream, check a tensor's layout in as few attribute reads as will do, and
 # keep the structures that describe a call's sizes (never its tensors: what may come
-# as one, a scale or an eps, is a number before it is looked up).
+# as one, a scale, an eps or a number of groups, is a number before it is looked up).
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
@@ -450,7 +451,7 @@ def mamba2_group_norm(x, weight, ngroups, z=None, bias=None, eps=1e-5, subtract_
     if z is not None:
         _like(x, z, "z")
     y = _like(x, y, "y")
-    shape = _norm_shape(x.numel() // C if C else 0, C, ngroups, _rows(x, "x", 1),
+    shape = _norm_shape(x.numel() // C if C else 0, C, operator.index(ngroups), _rows(x, "x", 1),
                         0 if z is None else _rows(z, "z", 1), _rows(y, "y", 1), float(eps), _dtype_code(x),
                         flags | MAMBA2_NORM_SUBTRACT_MEAN if subtract_mean else flags, 0)
     rc = load_library().mamba2_group_norm(shape, _at(x), _at(z), _at(weight), _at(bias), _at(y), _on(stream, x))

@@ -71,3 +71,13 @@ def test_an_eps_that_is_a_tensor_counts_by_its_value(lib):
         eps.fill_(value)
         bd.mamba2_group_norm(x, None, 2, eps=eps, y=Gpu(6, 8))
     assert [args[0].eps for _, args in lib.calls] == [0.5, 0.25]
+
+
+def test_a_number_of_groups_that_is_a_tensor_counts_by_its_value(lib):
+    groups, x = torch.tensor(2), Gpu(6, 8)
+    for value in (2, 4):
+        groups.fill_(value)
+        bd.mamba2_group_norm(x, None, groups, y=Gpu(6, 8))
+    assert [args[0].ngroups for _, args in lib.calls] == [2, 4]
+    with pytest.raises(TypeError):
+        bd.mamba2_group_norm(x, None, 2.0, y=Gpu(6, 8))
