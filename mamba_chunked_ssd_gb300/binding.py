@@ -336,6 +336,8 @@ _norm_shape = functools.lru_cache(maxsize=1024)(lambda *a: mamba2_norm_shape(*a)
 def _gdr_args(q, k, v, g, beta, scale, qk_l2norm, l2_eps):
     """The shape and options of a gated-delta-rule call; checks q, k, v, g, beta."""
     vs, qs, dt = v.shape, q.shape, v.dtype
+    if len(vs) not in (3, 4):
+        raise ValueError(f"v must have the dimensions (batch, [tokens,] heads, headdim), not {tuple(vs)}")
     rows, nh = vs[:-1], vs[-2]
     if qs != k.shape or len(qs) != len(vs) or qs[:-2] != vs[:-2]:
         raise ValueError(f"q and k must be {tuple(vs[:-2])} + (groups, state): got {tuple(qs)}, {tuple(k.shape)}")

@@ -81,3 +81,20 @@ def test_a_number_of_groups_that_is_a_tensor_counts_by_its_value(lib):
     assert [args[0].ngroups for _, args in lib.calls] == [2, 4]
     with pytest.raises(TypeError):
         bd.mamba2_group_norm(x, None, 2.0, y=Gpu(6, 8))
+
+
+@pytest.mark.parametrize("step", [False, True])
+@pytest.mark.parametrize("lead", [(), (2, 3, 5)])
+def test_tensors_with_too_few_or_too_many_dimensions_are_refused(lib, step, lead):
+    """With two dimensions heads would be taken for batch rows (and read behind the
+    tensors' ends); with five all but one token of a row would be left out."""
+    with pytest.raises(ValueError, match="dimensions"):
+        gdr(step, lead=lead)
+    assert lib.calls == []
+
+
+@pytest.mark.parametrize("step", [False, True])
+def test_a_single_token_with_and_without_its_dimension(lib, step):
+    gdr(step, lead=(3,)), gdr(step, lead=(3, 1))
+    for _, args in lib.calls:
+        assert (args[0].batch, args[0].seqlen, args[0].nheads) == (3, 1, 4)
