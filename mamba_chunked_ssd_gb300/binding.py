@@ -270,14 +270,19 @@ def mamba2_ssd_step(x, dt, A, B, C, state_in=None, D=None, state_out=None, y=Non
 # keep the structures that describe a call's sizes (never its tensors: what may come
 # as one, a scale, an eps or a number of groups, is a number before it is looked up).
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_gpu = torch._C._cuda_getDevice
 
 
 def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _on(stream, t):
-    return _raw_stream(t.device.index) if stream is None else stream.cuda_stream
+def _on(stream, gpu):
+    if stream is None:
+        return _raw_stream(gpu)
+    if stream.device.index != gpu:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{gpu}")
+    return stream.cuda_stream
 
 
 def _rows(t, name, inner):
@@ -310,20 +315,31 @@ def _rows(t, name, inner):
     return row
 
 
-def _want(t, name, dtype, shape):
-    """A contiguous CUDA tensor of this dtype and shape (or None)."""
-    if t is None or (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()):
+def _gpu(t, name):
+    """The index of a tensor's GPU, which has to be the current one: the launch goes there."""
+    gpu = t.get_device()
+    if gpu < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if gpu != _current_gpu():
+        raise ValueError(f"{name} is on cuda:{gpu}, but the current device is cuda:{_current_gpu()}")
+    return gpu
+
+
+def _want(t, name, dtype, shape, gpu):
+    """A contiguous tensor of this dtype and shape on this GPU (or None)."""
+    if t is None or (t.dtype is dtype and t.shape == shape and t.get_device() == gpu and t.is_contiguous()):
         return
-    raise ValueError(f"{name} must be a contiguous CUDA tensor, {dtype} {tuple(shape)}, "
+    raise ValueError(f"{name} must be a contiguous tensor on cuda:{gpu}, {dtype} {tuple(shape)}, "
                      f"not {t.dtype} {tuple(t.shape)} on {t.device} with strides {t.stride()}")
 
 
 def _like(t, given, name):
-    """The output for an input's dtype and shape: the given one, checked, or a new one."""
+    """The output for an input's dtype, shape and GPU: the given one, checked, or a new one."""
     if given is None:
         return torch.empty_like(t, memory_format=torch.contiguous_format)
-    if given.dtype is not t.dtype or given.shape != t.shape:
-        raise ValueError(f"{name} must be {t.dtype} {tuple(t.shape)}, not {given.dtype} {tuple(given.shape)}")
+    if given.dtype is not t.dtype or given.shape != t.shape or given.get_device() != t.get_device():
+        raise ValueError(f"{name} must be {t.dtype} {tuple(t.shape)} on {t.device}, "
+                         f"not {given.dtype} {tuple(given.shape)} on {given.device}")
     return given
 
 
@@ -334,7 +350,7 @@ _norm_shape = functools.lru_cache(maxsize=1024)(lambda *a: mamba2_norm_shape(*a)
 
 
 def _gdr_args(q, k, v, g, beta, scale, qk_l2norm, l2_eps):
-    """The shape and options of a gated-delta-rule call; checks q, k, v, g, beta."""
+    """The shape and options of a gated-delta-rule call, its state's shape and its GPU; checks q, k, v, g, beta."""
     vs, qs, dt = v.shape, q.shape, v.dtype
     if len(vs) not in (3, 4):
         raise ValueError(f"v must have the dimensions (batch, [tokens,] heads, headdim), not {tuple(vs)}")
@@ -343,13 +359,16 @@ def _gdr_args(q, k, v, g, beta, scale, qk_l2norm, l2_eps):
         raise ValueError(f"q and k must be {tuple(vs[:-2])} + (groups, state): got {tuple(qs)}, {tuple(k.shape)}")
     if q.dtype is not dt or k.dtype is not dt:
         raise TypeError("q, k and v must have one dtype")
-    _want(g, "g", torch.float32, rows), _want(beta, "beta", torch.float32, rows)
+    gpu = _gpu(v, "v")
+    if q.get_device() != gpu or k.get_device() != gpu:
+        raise ValueError(f"q and k must be on {v.device} as v is, not on {q.device} and {k.device}")
+    _want(g, "g", torch.float32, rows, gpu), _want(beta, "beta", torch.float32, rows, gpu)
     S = qs[-1]
     shape = _gdr_shape(vs[0], vs[1] if len(vs) == 4 else 1, nh, vs[-1], S, qs[-2], 64, _dtype_code(v), 0)
     opt = _gdr_options(_rows(q, "q", 2), _rows(k, "k", 2), _rows(v, "v", 2),
                        S ** -0.5 if scale is None else float(scale), float(l2_eps),
                        MAMBA2_GDR_QK_L2NORM if qk_l2norm else 0, 0)
-    return shape, opt, (vs[0], nh, S, vs[-1])
+    return shape, opt, (vs[0], nh, S, vs[-1]), gpu
 
 
 def mamba2_gdr_fwd(q, k, v, g, beta, scale=None, qk_l2norm=False, l2_eps=1e-6, initial_state=None, lengths=None,
@@ -358,17 +377,18 @@ def mamba2_gdr_fwd(q, k, v, g, beta, scale=None, qk_l2norm=False, l2_eps=1e-6, i
     [b, nh, S, H] fp32 or None).  q, k [b, L, G, S] and v [b, L, nh, H] may be
     slices of a wider tensor; g (log decay), beta [b, L, nh] fp32; scale
     defaults to S ** -0.5; lengths [b] int32 or None."""
-    shape, opt, state = _gdr_args(q, k, v, g, beta, scale, qk_l2norm, l2_eps)
-    _want(initial_state, "initial_state", torch.float32, state), _want(lengths, "lengths", torch.int32, state[:1])
+    shape, opt, state, gpu = _gdr_args(q, k, v, g, beta, scale, qk_l2norm, l2_eps)
+    _want(initial_state, "initial_state", torch.float32, state, gpu)
+    _want(lengths, "lengths", torch.int32, state[:1], gpu)
     if y is not None:
-        _want(y, "y", v.dtype, v.shape)
+        _want(y, "y", v.dtype, v.shape, gpu)
     y = _like(v, y, "y")
     if final_state is not None:
-        _want(final_state, "final_state", torch.float32, state)
+        _want(final_state, "final_state", torch.float32, state, gpu)
     elif want_final_state:
         final_state = torch.empty(state, device=v.device, dtype=torch.float32)
     rc = load_library().mamba2_gdr_fwd(shape, opt, _at(q), _at(k), _at(v), _at(g), _at(beta), _at(lengths),
-                                       _at(initial_state), _at(y), _at(final_state), _on(stream, v))
+                                       _at(initial_state), _at(y), _at(final_state), _on(stream, gpu))
     if rc:
         _check("mamba2_gdr_fwd", rc)
     return y, final_state
@@ -379,17 +399,17 @@ def mamba2_gdr_step(q, k, v, g, beta, state_in=None, scale=None, qk_l2norm=False
     """One token of the gated delta rule: q, k [b, G, S], v [b, nh, H], g, beta
     [b, nh], state [b, nh, S, H] fp32.  Returns (y [b, nh, H], state_out).  Pass
     state_out=state_in to update the state in place."""
-    shape, opt, state = _gdr_args(q, k, v, g, beta, scale, qk_l2norm, l2_eps)
-    _want(state_in, "state_in", torch.float32, state)
+    shape, opt, state, gpu = _gdr_args(q, k, v, g, beta, scale, qk_l2norm, l2_eps)
+    _want(state_in, "state_in", torch.float32, state, gpu)
     if y is not None:
-        _want(y, "y", v.dtype, v.shape)
+        _want(y, "y", v.dtype, v.shape, gpu)
     y = _like(v, y, "y")
     if state_out is None:
         state_out = torch.empty(state, device=v.device, dtype=torch.float32)
     elif state_out is not state_in:
-        _want(state_out, "state_out", torch.float32, state)
+        _want(state_out, "state_out", torch.float32, state, gpu)
     rc = load_library().mamba2_gdr_step(shape, opt, _at(q), _at(k), _at(v), _at(g), _at(beta), _at(state_in),
-                                        _at(state_out), _at(y), _on(stream, v))
+                                        _at(state_out), _at(y), _on(stream, gpu))
     if rc:
         _check("mamba2_gdr_step", rc)
     return y, state_out
@@ -401,18 +421,19 @@ def mamba2_causal_conv_fwd(x, weight, bias=None, silu=True, initial_state=None, 
     slice), weight [C, W] and bias [C] fp32, states [b, W - 1, C] in x's dtype.
     Returns (y [b, L, C], final_state or None)."""
     b, L, C = x.shape
-    W = weight.shape[-1]
-    _want(weight, "weight", torch.float32, (C, W)), _want(bias, "bias", torch.float32, (C,))
-    _want(initial_state, "initial_state", x.dtype, (b, W - 1, C)), _want(lengths, "lengths", torch.int32, (b,))
+    W, gpu = weight.shape[-1], _gpu(x, "x")
+    _want(weight, "weight", torch.float32, (C, W), gpu), _want(bias, "bias", torch.float32, (C,), gpu)
+    _want(initial_state, "initial_state", x.dtype, (b, W - 1, C), gpu)
+    _want(lengths, "lengths", torch.int32, (b,), gpu)
     y = _like(x, y, "y")
     if final_state is not None:
-        _want(final_state, "final_state", x.dtype, (b, W - 1, C))
+        _want(final_state, "final_state", x.dtype, (b, W - 1, C), gpu)
     elif want_final_state:
         final_state = torch.empty((b, W - 1, C), device=x.device, dtype=x.dtype)
     shape = _conv_shape(b, L, C, W, _rows(x, "x", 1), _rows(y, "y", 1), _dtype_code(x),
                         MAMBA2_CONV_SILU if silu else 0)
     rc = load_library().mamba2_causal_conv_fwd(shape, _at(x), _at(weight), _at(bias), _at(lengths), _at(initial_state),
-                                               _at(y), _at(final_state), _on(stream, x))
+                                               _at(y), _at(final_state), _on(stream, gpu))
     if rc:
         _check("mamba2_causal_conv_fwd", rc)
     return y, final_state
@@ -422,19 +443,19 @@ def mamba2_causal_conv_step(x, weight, state_in=None, bias=None, silu=True, stat
     """One token of the convolution: x [b, C], state [b, W - 1, C] in x's dtype.
     Returns (y [b, C], state_out); state_out=state_in updates in place."""
     b, C = x.shape
-    W = weight.shape[-1]
+    W, gpu = weight.shape[-1], _gpu(x, "x")
     state = (b, W - 1, C)
-    _want(weight, "weight", torch.float32, (C, W)), _want(bias, "bias", torch.float32, (C,))
-    _want(state_in, "state_in", x.dtype, state)
+    _want(weight, "weight", torch.float32, (C, W), gpu), _want(bias, "bias", torch.float32, (C,), gpu)
+    _want(state_in, "state_in", x.dtype, state, gpu)
     y = _like(x, y, "y")
     if state_out is None:
         state_out = torch.empty(state, device=x.device, dtype=x.dtype)
     elif state_out is not state_in:
-        _want(state_out, "state_out", x.dtype, state)
+        _want(state_out, "state_out", x.dtype, state, gpu)
     shape = _conv_shape(b, 1, C, W, _rows(x, "x", 1), _rows(y, "y", 1), _dtype_code(x),
                         MAMBA2_CONV_SILU if silu else 0)
     rc = load_library().mamba2_causal_conv_step(shape, _at(x), _at(weight), _at(bias), _at(state_in), _at(state_out),
-                                                _at(y), _on(stream, x))
+                                                _at(y), _on(stream, gpu))
     if rc:
         _check("mamba2_causal_conv_step", rc)
     return y, state_out
@@ -445,8 +466,8 @@ def mamba2_group_norm(x, weight, ngroups, z=None, bias=None, eps=1e-5, subtract_
     """Group norm of each row of x [.., C] over its ngroups groups of channels:
     mode "none", "silu" (SiLU of the result), "before" or "after" (a gate
     SiLU(z) before or after the norm).  weight, bias [C] fp32 or None."""
-    C = x.shape[-1]
-    _want(weight, "weight", torch.float32, (C,)), _want(bias, "bias", torch.float32, (C,))
+    C, gpu = x.shape[-1], _gpu(x, "x")
+    _want(weight, "weight", torch.float32, (C,), gpu), _want(bias, "bias", torch.float32, (C,), gpu)
     flags = NORM_MODES.get(mode)
     if flags is None:
         raise ValueError(f"mode must be one of {sorted(NORM_MODES)}, not {mode!r}")
@@ -456,7 +477,7 @@ def mamba2_group_norm(x, weight, ngroups, z=None, bias=None, eps=1e-5, subtract_
     shape = _norm_shape(x.numel() // C if C else 0, C, operator.index(ngroups), _rows(x, "x", 1),
                         0 if z is None else _rows(z, "z", 1), _rows(y, "y", 1), float(eps), _dtype_code(x),
                         flags | MAMBA2_NORM_SUBTRACT_MEAN if subtract_mean else flags, 0)
-    rc = load_library().mamba2_group_norm(shape, _at(x), _at(z), _at(weight), _at(bias), _at(y), _on(stream, x))
+    rc = load_library().mamba2_group_norm(shape, _at(x), _at(z), _at(weight), _at(bias), _at(y), _on(stream, gpu))
     if rc:
         _check("mamba2_group_norm", rc)
     return y

@@ -39,6 +39,7 @@ def lib(monkeypatch):
     rec = Recorder()
     monkeypatch.setattr(bd, "load_library", lambda: rec)
     monkeypatch.setattr(bd, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(bd, "_current_gpu", lambda: 0, raising=False)
     return rec
 
 
@@ -98,3 +99,61 @@ def test_a_single_token_with_and_without_its_dimension(lib, step):
     gdr(step, lead=(3,)), gdr(step, lead=(3, 1))
     for _, args in lib.calls:
         assert (args[0].batch, args[0].seqlen, args[0].nheads) == (3, 1, 4)
+
+
+def conv(step=False, device=None, **kw):
+    b, C, W = 2, 8, 4
+    at = lambda name, *s: Gpu(*s, device=(device or {}).get(name, 0))  # noqa: E731
+    first, last = ("state_in", "state_out") if step else ("initial_state", "final_state")
+    lead = (b,) if step else (b, 5)
+    t = {"x": at("x", *lead, C), "weight": at("weight", C, W), "bias": at("bias", C), "y": at("y", *lead, C),
+         first: at(first, b, W - 1, C), last: at(last, b, W - 1, C)}
+    return (bd.mamba2_causal_conv_step if step else bd.mamba2_causal_conv_fwd)(**t, **kw)
+
+
+def norm(device=None, **kw):
+    at = lambda name, *s: Gpu(*s, device=(device or {}).get(name, 0))  # noqa: E731
+    return bd.mamba2_group_norm(at("x", 6, 8), at("weight", 8), 2, z=at("z", 6, 8), bias=at("bias", 8), y=at("y", 6, 8),
+                                mode="after", **kw)
+
+
+CALLS = {"gdr_fwd": (gdr, "q k v g beta y initial_state final_state"),
+         "gdr_step": (lambda **kw: gdr(True, **kw), "q k v g beta y state_in state_out"),
+         "conv_fwd": (conv, "x weight bias y initial_state final_state"),
+         "conv_step": (lambda **kw: conv(True, **kw), "x weight bias y state_in state_out"),
+         "norm": (norm, "x weight bias z y")}
+
+
+@pytest.mark.parametrize("call,names", CALLS.values(), ids=CALLS)
+def test_tensors_on_another_gpu_are_refused(lib, monkeypatch, call, names):
+    """One tensor on another GPU than the rest, and all of them on another one than
+    the current: a launch would get addresses that are not its device's."""
+    call()
+    assert len(lib.calls) == 1
+    for name in names.split():
+        with pytest.raises(ValueError, match="cuda:"):
+            call(device={name: 1})
+    with pytest.raises(ValueError, match="current device"):
+        call(device=dict.fromkeys(names.split(), 1))
+    assert len(lib.calls) == 1
+    monkeypatch.setattr(bd, "_current_gpu", lambda: 1)
+    call(device=dict.fromkeys(names.split(), 1))
+    assert len(lib.calls) == 2
+
+
+@pytest.mark.parametrize("call", [c for c, _ in CALLS.values()], ids=CALLS)
+def test_a_stream_of_another_gpu_is_refused(lib, call):
+    class Stream:
+        cuda_stream, device = 7, torch.device("cuda", 0)
+    call(stream=Stream())
+    assert lib.calls[0][1][-1] == 7
+    Stream.device = torch.device("cuda", 1)
+    with pytest.raises(ValueError, match="stream"):
+        call(stream=Stream())
+
+
+def test_lengths_on_another_gpu_are_refused(lib):
+    for call in (gdr, conv):
+        call(lengths=Gpu(2, dtype=torch.int32))
+        with pytest.raises(ValueError, match="lengths"):
+            call(lengths=Gpu(2, dtype=torch.int32, device=1))
