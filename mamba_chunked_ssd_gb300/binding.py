@@ -119,13 +119,24 @@ def _check(fn: str, rc: int):
         raise Mamba2Error(fn, rc, text)
 
 
+_current_gpu = torch._C._cuda_getDevice
+
+
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    """A tensor's address, on the current GPU: the launch goes there."""
+    if t is None:
+        return None
+    if t.get_device() != _current_gpu():
+        raise ValueError(f"a tensor is on {t.device}, but the current device is cuda:{_current_gpu()}")
+    return ctypes.c_void_p(t.data_ptr())
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    if stream.device.index != _current_gpu():
+        raise ValueError(f"the stream is on {stream.device}, but the current device is cuda:{_current_gpu()}")
+    return ctypes.c_void_p(stream.cuda_stream)
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -270,7 +281,6 @@ def mamba2_ssd_step(x, dt, A, B, C, state_in=None, D=None, state_out=None, y=Non
 # keep the structures that describe a call's sizes (never its tensors: what may come
 # as one, a scale, an eps or a number of groups, is a number before it is looked up).
 _raw_stream = torch._C._cuda_getCurrentRawStream
-_current_gpu = torch._C._cuda_getDevice
 
 
 def _at(t):
