@@ -2,8 +2,8 @@
 
 Each function has the name of the C entry point it calls and takes torch
 tensors that already live on the GPU; it passes their data pointers, the
-shape and the current CUDA stream to the library and allocates any missing
-output with ``torch.empty``.  No step of the forward pass runs in Python: if
+shape and the current CUDA stream (or the ``stream`` it is given) to the library
+and allocates any missing output with ``torch.empty`` on that stream.  No step of the forward pass runs in Python: if
 the library is missing the import fails loudly, there is no fallback.
 
 Layouts and semantics are those of include/mamba2_ssd.h ("Accelerating
@@ -139,6 +139,15 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _new(shape, dtype, device, stream):
+    """An output or workspace from the pool of the call's stream: memory that was freed
+    on another one may still be in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.bfloat16:
         return MAMBA2_BF16
@@ -167,7 +176,7 @@ def mamba2_chunk_cumsum(dt, A, chunk_size, G=None, stream=None):
     b, L, nh = dt.shape
     shape = make_shape(b, L, nh, 1, 1, 1, int(chunk_size), MAMBA2_F32)
     if G is None:
-        G = torch.empty(b, nh, L, device=dt.device, dtype=torch.float32)
+        G = _new((b, nh, L), torch.float32, dt.device, stream)
     _check("mamba2_chunk_cumsum", load_library().mamba2_chunk_cumsum(
         ctypes.byref(shape), _ptr(dt), _ptr(A), _ptr(G), _stream(stream)))
     return G
@@ -181,11 +190,9 @@ def mamba2_state_pass(x, dt, B, G, chunk_size, initial_state=None, chunk_states=
     shape = shape_of(x, B, chunk_size)
     nc = -(-shape.seqlen // shape.chunk_size)
     if chunk_states is None:
-        chunk_states = torch.empty(shape.batch, shape.nheads, nc, shape.dstate, shape.headdim,
-                                   device=x.device, dtype=x.dtype)
+        chunk_states = _new((shape.batch, shape.nheads, nc, shape.dstate, shape.headdim), x.dtype, x.device, stream)
     if final_state is None and want_final_state:
-        final_state = torch.empty(shape.batch, shape.nheads, shape.dstate, shape.headdim,
-                                  device=x.device, dtype=torch.float32)
+        final_state = _new((shape.batch, shape.nheads, shape.dstate, shape.headdim), torch.float32, x.device, stream)
     _check("mamba2_state_pass", load_library().mamba2_state_pass(
         ctypes.byref(shape), _ptr(x), _ptr(dt), _ptr(B), _ptr(G), _ptr(initial_state),
         _ptr(chunk_states), _ptr(final_state), _stream(stream)))
@@ -199,7 +206,7 @@ def mamba2_chunk_out(x, dt, B, C, G, chunk_states, chunk_size, D=None, y=None, s
         _need(t, n)
     shape = shape_of(x, B, chunk_size)
     if y is None:
-        y = torch.empty_like(x)
+        y = _new(x.shape, x.dtype, x.device, stream)
     _check("mamba2_chunk_out", load_library().mamba2_chunk_out(
         ctypes.byref(shape), _ptr(x), _ptr(dt), _ptr(B), _ptr(C), _ptr(D), _ptr(G),
         _ptr(chunk_states), _ptr(y), _stream(stream)))
@@ -222,13 +229,12 @@ def mamba2_ssd_fwd(x, dt, A, B, C, chunk_size, D=None, initial_state=None, y=Non
         _need(t, n)
     shape = shape_of(x, B, chunk_size)
     if y is None:
-        y = torch.empty_like(x)
+        y = _new(x.shape, x.dtype, x.device, stream)
     if final_state is None and want_final_state:
-        final_state = torch.empty(shape.batch, shape.nheads, shape.dstate, shape.headdim,
-                                  device=x.device, dtype=torch.float32)
+        final_state = _new((shape.batch, shape.nheads, shape.dstate, shape.headdim), torch.float32, x.device, stream)
     ws_bytes = mamba2_ssd_fwd_workspace_size(shape)
     if workspace is None:
-        workspace = torch.empty(max(ws_bytes, 1), device=x.device, dtype=torch.uint8)
+        workspace = _new(max(ws_bytes, 1), torch.uint8, x.device, stream)
     _check("mamba2_ssd_fwd", load_library().mamba2_ssd_fwd(
         ctypes.byref(shape), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
         _ptr(initial_state), _ptr(y), _ptr(final_state), _ptr(workspace),
@@ -246,10 +252,9 @@ def mamba2_ssd_fwd_noalloc(x, dt, A, B, C, chunk_size, D=None, initial_state=Non
         _need(t, n)
     shape = shape_of(x, B, chunk_size)
     if y is None:
-        y = torch.empty_like(x)
+        y = _new(x.shape, x.dtype, x.device, stream)
     if final_state is None and want_final_state:
-        final_state = torch.empty(shape.batch, shape.nheads, shape.dstate, shape.headdim,
-                                  device=x.device, dtype=torch.float32)
+        final_state = _new((shape.batch, shape.nheads, shape.dstate, shape.headdim), torch.float32, x.device, stream)
     _check("mamba2_ssd_fwd_noalloc", load_library().mamba2_ssd_fwd_noalloc(
         ctypes.byref(shape), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
         _ptr(initial_state), _ptr(y), _ptr(final_state), _stream(stream)))
@@ -266,9 +271,9 @@ def mamba2_ssd_step(x, dt, A, B, C, state_in=None, D=None, state_out=None, y=Non
     b, nh, H = x.shape
     shape = make_shape(b, 1, nh, H, B.shape[2], B.shape[1], 1, _dtype_code(x))
     if y is None:
-        y = torch.empty_like(x)
+        y = _new(x.shape, x.dtype, x.device, stream)
     if state_out is None:
-        state_out = torch.empty(b, nh, B.shape[2], H, device=x.device, dtype=torch.float32)
+        state_out = _new((b, nh, B.shape[2], H), torch.float32, x.device, stream)
     _check("mamba2_ssd_step", load_library().mamba2_ssd_step(
         ctypes.byref(shape), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
         _ptr(state_in), _ptr(state_out), _ptr(y), _stream(stream)))
@@ -343,10 +348,10 @@ def _want(t, name, dtype, shape, gpu):
                      f"not {t.dtype} {tuple(t.shape)} on {t.device} with strides {t.stride()}")
 
 
-def _like(t, given, name):
+def _like(t, given, name, stream=None):
     """The output for an input's dtype, shape and GPU: the given one, checked, or a new one."""
     if given is None:
-        return torch.empty_like(t, memory_format=torch.contiguous_format)
+        return _new(t.shape, t.dtype, t.device, stream)
     if given.dtype is not t.dtype or given.shape != t.shape or given.get_device() != t.get_device():
         raise ValueError(f"{name} must be {t.dtype} {tuple(t.shape)} on {t.device}, "
                          f"not {given.dtype} {tuple(given.shape)} on {given.device}")
@@ -392,11 +397,11 @@ def mamba2_gdr_fwd(q, k, v, g, beta, scale=None, qk_l2norm=False, l2_eps=1e-6, i
     _want(lengths, "lengths", torch.int32, state[:1], gpu)
     if y is not None:
         _want(y, "y", v.dtype, v.shape, gpu)
-    y = _like(v, y, "y")
+    y = _like(v, y, "y", stream)
     if final_state is not None:
         _want(final_state, "final_state", torch.float32, state, gpu)
     elif want_final_state:
-        final_state = torch.empty(state, device=v.device, dtype=torch.float32)
+        final_state = _new(state, torch.float32, v.device, stream)
     rc = load_library().mamba2_gdr_fwd(shape, opt, _at(q), _at(k), _at(v), _at(g), _at(beta), _at(lengths),
                                        _at(initial_state), _at(y), _at(final_state), _on(stream, gpu))
     if rc:
@@ -413,9 +418,9 @@ def mamba2_gdr_step(q, k, v, g, beta, state_in=None, scale=None, qk_l2norm=False
     _want(state_in, "state_in", torch.float32, state, gpu)
     if y is not None:
         _want(y, "y", v.dtype, v.shape, gpu)
-    y = _like(v, y, "y")
+    y = _like(v, y, "y", stream)
     if state_out is None:
-        state_out = torch.empty(state, device=v.device, dtype=torch.float32)
+        state_out = _new(state, torch.float32, v.device, stream)
     elif state_out is not state_in:
         _want(state_out, "state_out", torch.float32, state, gpu)
     rc = load_library().mamba2_gdr_step(shape, opt, _at(q), _at(k), _at(v), _at(g), _at(beta), _at(state_in),
@@ -435,11 +440,11 @@ def mamba2_causal_conv_fwd(x, weight, bias=None, silu=True, initial_state=None, 
     _want(weight, "weight", torch.float32, (C, W), gpu), _want(bias, "bias", torch.float32, (C,), gpu)
     _want(initial_state, "initial_state", x.dtype, (b, W - 1, C), gpu)
     _want(lengths, "lengths", torch.int32, (b,), gpu)
-    y = _like(x, y, "y")
+    y = _like(x, y, "y", stream)
     if final_state is not None:
         _want(final_state, "final_state", x.dtype, (b, W - 1, C), gpu)
     elif want_final_state:
-        final_state = torch.empty((b, W - 1, C), device=x.device, dtype=x.dtype)
+        final_state = _new((b, W - 1, C), x.dtype, x.device, stream)
     shape = _conv_shape(b, L, C, W, _rows(x, "x", 1), _rows(y, "y", 1), _dtype_code(x),
                         MAMBA2_CONV_SILU if silu else 0)
     rc = load_library().mamba2_causal_conv_fwd(shape, _at(x), _at(weight), _at(bias), _at(lengths), _at(initial_state),
@@ -457,9 +462,9 @@ def mamba2_causal_conv_step(x, weight, state_in=None, bias=None, silu=True, stat
     state = (b, W - 1, C)
     _want(weight, "weight", torch.float32, (C, W), gpu), _want(bias, "bias", torch.float32, (C,), gpu)
     _want(state_in, "state_in", x.dtype, state, gpu)
-    y = _like(x, y, "y")
+    y = _like(x, y, "y", stream)
     if state_out is None:
-        state_out = torch.empty(state, device=x.device, dtype=x.dtype)
+        state_out = _new(state, x.dtype, x.device, stream)
     elif state_out is not state_in:
         _want(state_out, "state_out", x.dtype, state, gpu)
     shape = _conv_shape(b, 1, C, W, _rows(x, "x", 1), _rows(y, "y", 1), _dtype_code(x),
@@ -483,7 +488,7 @@ def mamba2_group_norm(x, weight, ngroups, z=None, bias=None, eps=1e-5, subtract_
         raise ValueError(f"mode must be one of {sorted(NORM_MODES)}, not {mode!r}")
     if z is not None:
         _like(x, z, "z")
-    y = _like(x, y, "y")
+    y = _like(x, y, "y", stream)
     shape = _norm_shape(x.numel() // C if C else 0, C, operator.index(ngroups), _rows(x, "x", 1),
                         0 if z is None else _rows(z, "z", 1), _rows(y, "y", 1), float(eps), _dtype_code(x),
                         flags | MAMBA2_NORM_SUBTRACT_MEAN if subtract_mean else flags, 0)

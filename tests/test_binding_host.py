@@ -53,3 +53,41 @@ def test_tensors_and_streams_of_another_gpu_are_refused(lib, monkeypatch, name):
         call(stream=Stream(1))
     monkeypatch.setattr(bd, "_current_gpu", lambda: 1)
     assert call(dict.fromkeys(names, 1), Stream(1)) == 2
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_outputs_and_workspace_that_are_not_given_come_from_the_stream_of_the_call(lib, monkeypatch, name):  # noqa: F811
+    under, made, stream = [], [], Stream()
+
+    class Under:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            under.append(self.s)
+
+        def __exit__(self, *a):
+            under.pop()
+
+    real = torch.empty
+
+    def empty(shape, dtype=None, device=None):
+        made.append(under[-1] if under else None)
+        t = Gpu(1)
+        t.t = real(shape, dtype=dtype)
+        return t
+
+    out = {"mamba2_chunk_cumsum": ["G"], "mamba2_state_pass": ["chunk_states", "final_state"], "mamba2_chunk_out": ["y"],
+           "mamba2_ssd_fwd": ["y", "final_state", "workspace"], "mamba2_ssd_fwd_noalloc": ["y", "final_state"],
+           "mamba2_ssd_step": ["y", "state_out"]}[name]
+    t = tensors([n for n in CALLS[name].split() if n not in out], {})
+    if name == "mamba2_ssd_step":
+        for n in ("x", "dt", "B", "C"):
+            t[n].t = t[n].t[:, 0].contiguous()
+            t[n].shape = t[n].t.shape
+    else:
+        t["chunk_size"] = 4
+    monkeypatch.setattr(torch.cuda, "stream", Under)
+    monkeypatch.setattr(torch, "empty", empty)
+    getattr(bd, name)(**t, stream=stream)
+    assert made == [stream] * len(out) and not under

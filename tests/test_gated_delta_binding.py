@@ -43,8 +43,9 @@ def lib(monkeypatch):
     return rec
 
 
-def gdr(step=False, lead=None, device=None, **kw):
-    """A call of the rule with every tensor given; `device` puts single ones on other GPUs."""
+def gdr(step=False, lead=None, device=None, drop=(), **kw):
+    """A call of the rule with every tensor given but those in `drop`; `device` puts
+    single ones on other GPUs."""
     lead = ((2,) if step else (2, 5)) if lead is None else lead
     at = lambda name, *s: Gpu(*s, device=(device or {}).get(name, 0))  # noqa: E731
     t = {"q": at("q", *lead, 2, 16), "k": at("k", *lead, 2, 16), "v": at("v", *lead, 4, 8),
@@ -52,6 +53,7 @@ def gdr(step=False, lead=None, device=None, **kw):
     b = lead[0] if lead else 4
     first, last = ("state_in", "state_out") if step else ("initial_state", "final_state")
     t.update({"y": at("y", *lead, 4, 8), first: at(first, b, 4, 16, 8), last: at(last, b, 4, 16, 8)})
+    t = {n: x for n, x in t.items() if n not in drop}
     return (bd.mamba2_gdr_step if step else bd.mamba2_gdr_fwd)(**t, **kw)
 
 
@@ -101,20 +103,21 @@ def test_a_single_token_with_and_without_its_dimension(lib, step):
         assert (args[0].batch, args[0].seqlen, args[0].nheads) == (3, 1, 4)
 
 
-def conv(step=False, device=None, **kw):
+def conv(step=False, device=None, drop=(), **kw):
     b, C, W = 2, 8, 4
     at = lambda name, *s: Gpu(*s, device=(device or {}).get(name, 0))  # noqa: E731
     first, last = ("state_in", "state_out") if step else ("initial_state", "final_state")
     lead = (b,) if step else (b, 5)
     t = {"x": at("x", *lead, C), "weight": at("weight", C, W), "bias": at("bias", C), "y": at("y", *lead, C),
          first: at(first, b, W - 1, C), last: at(last, b, W - 1, C)}
+    t = {n: x for n, x in t.items() if n not in drop}
     return (bd.mamba2_causal_conv_step if step else bd.mamba2_causal_conv_fwd)(**t, **kw)
 
 
-def norm(device=None, **kw):
+def norm(device=None, drop=(), **kw):
     at = lambda name, *s: Gpu(*s, device=(device or {}).get(name, 0))  # noqa: E731
-    return bd.mamba2_group_norm(at("x", 6, 8), at("weight", 8), 2, z=at("z", 6, 8), bias=at("bias", 8), y=at("y", 6, 8),
-                                mode="after", **kw)
+    return bd.mamba2_group_norm(at("x", 6, 8), at("weight", 8), 2, z=at("z", 6, 8), bias=at("bias", 8),
+                                y=None if "y" in drop else at("y", 6, 8), mode="after", **kw)
 
 
 CALLS = {"gdr_fwd": (gdr, "q k v g beta y initial_state final_state"),
@@ -157,3 +160,38 @@ def test_lengths_on_another_gpu_are_refused(lib):
         call(lengths=Gpu(2, dtype=torch.int32))
         with pytest.raises(ValueError, match="lengths"):
             call(lengths=Gpu(2, dtype=torch.int32, device=1))
+
+
+@pytest.mark.parametrize("call", [c for c, _ in CALLS.values()], ids=CALLS)
+def test_outputs_that_are_not_given_come_from_the_stream_of_the_call(lib, monkeypatch, call):
+    """Memory from the current stream's pool may still be in use there, and a kernel
+    on another stream does not wait for that."""
+    class Stream:
+        cuda_stream, device = 7, torch.device("cuda", 0)
+
+    under, made = [], []
+
+    class Under:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            under.append(self.stream)
+
+        def __exit__(self, *a):
+            under.pop()
+
+    def empty(*shape, dtype=None, device=None):
+        made.append(under[-1] if under else None)
+        return Gpu(*shape[0] if len(shape) == 1 and not isinstance(shape[0], int) else shape, dtype=dtype)
+
+    monkeypatch.setattr(torch.cuda, "stream", Under)
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(torch, "empty_like", lambda t, memory_format=None: empty(t.shape, dtype=t.dtype))
+    outputs = ("y", "final_state", "state_out")
+    stream = Stream()
+    call(stream=stream, drop=outputs)
+    assert made and all(s is stream for s in made) and not under
+    count = len(made)
+    call(drop=outputs)
+    assert made[count:] == [None] * count
