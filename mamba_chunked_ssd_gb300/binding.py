@@ -350,6 +350,8 @@ def _want(t, name, dtype, shape, gpu):
 
 def _like(t, given, name, stream=None):
     """The output for an input's dtype, shape and GPU: the given one, checked, or a new one."""
+    if given is None and stream is None:
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
     if given is None:
         return _new(t.shape, t.dtype, t.device, stream)
     if given.dtype is not t.dtype or given.shape != t.shape or given.get_device() != t.get_device():
