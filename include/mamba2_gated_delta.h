@@ -61,14 +61,22 @@ typedef struct {
     int32_t reserved; /* must be 0 */
 } mamba2_gdr_options;
 
-/* Whole sequences.  initial_state NULL means zeros; final_state NULL means not
+/* As for mamba2_ssd.h's calls: S and H up to 256, batch and nheads up to 65535,
+ * else MAMBA2_ERR_UNSUPPORTED; so are tensors of more than 2^40 elements, strides
+ * included.
+ *
+ * Whole sequences.  initial_state NULL means zeros; final_state NULL means not
  * written.  No workspace.  State arithmetic is fp32 on both dtypes: with bf16
  * inputs of S and H up to 128, both multiples of 8, and q, k, v whose address
  * and token stride are multiples of 16 bytes, the products run in chunks on the
  * tensor cores (but for a few tokens of few heads): what is added to the fp32 state is made of three bf16 parts
  * (24 bits) of every intermediate, from two parts (16 bits) of the state before
  * it; y takes two parts (16 bits) of the corrections and of the state.
- * Everything else runs token by token in fp32. */
+ * Everything else runs token by token in fp32.  What is not finite: a NaN or an
+ * infinity in a token's k, v or beta, or a NaN in its g, shows in its head's y from
+ * that token on and in its final state; in chunks also, as NaN, in y of up to 15
+ * tokens before it (those of its 16, counted from the sequence's start), since a
+ * zero weight on a later token is a factor there.  In q it stays in its token. */
 MAMBA2_API mamba2_status mamba2_gdr_fwd(const mamba2_shape* shape, const mamba2_gdr_options* options, const void* q,
                                         const void* k, const void* v, const float* g, const float* beta,
                                         const int32_t* lengths, const float* initial_state, void* y,
@@ -96,7 +104,8 @@ MAMBA2_API mamba2_status mamba2_gdr_step(const mamba2_shape* shape, const mamba2
  *   initial_state, final_state [b, W - 1, C] dtype: the W - 1 inputs before
  *                the first token, and the last W - 1 inputs, oldest first
  *                (initial_state NULL means zeros, final_state NULL not written)
- *   lengths      [b]            int32, as above */
+ *   lengths      [b]            int32, as above
+ * At most 65535 rows, 2^30 tokens and 2^30 channels. */
 enum { MAMBA2_CONV_SILU = 1 };
 
 typedef struct {
@@ -128,7 +137,8 @@ MAMBA2_API mamba2_status mamba2_causal_conv_step(const mamba2_conv_shape* shape,
  * At most one of GATE_BEFORE, GATE_AFTER and SILU.  Statistics in fp32.
  *   x, z, y  [rows, channels] dtype; z only with a gate, else NULL
  *   weight, bias [channels] fp32; NULL means 1 and 0
- * channels % ngroups == 0, at most 32768 channels to a group. */
+ * channels % ngroups == 0, at most 32768 channels to a group, rows x ngroups below
+ * 2^31 and rows x channels up to 2^40. */
 enum {
     MAMBA2_NORM_SUBTRACT_MEAN = 1,
     MAMBA2_NORM_GATE_BEFORE = 2,

@@ -9,8 +9,9 @@
 // token's input is loaded once per run (plus the W - 1 tokens before the run,
 // which the neighbouring run has just brought into L2).  Inputs come through
 // shared memory, each thread's to its own place, two or three times eight tokens ahead.
-// 4 x 8192 tokens of 8192 channels in bf16, width 4, SiLU: 162 us, 6.6 TB/s (0.99 of a plain
-// copy; 366 us without loads ahead, 180 with eight in registers).  One token of 256
+// 4 x 8192 tokens of 8192 channels in bf16, width 4, SiLU: 165 us, 6.5 TB/s (0.97 of a plain
+// copy; 366 us without loads ahead, 180 with eight in registers; 162 where the variants
+// below were compared).  One token of 256
 // sequences of these channels: 5.0 us in a graph, from L2 (alone the host's call is the
 // time).
 #include "gated_delta.cuh"

@@ -36,18 +36,20 @@
 // What bounds it is the chain from state to state: three dependent products and three
 // conversions a chunk, about 3.5 us with two heads to a CTA and 3.0 with one, whatever
 // the memory could do.  4 x 8192 tokens of 64 heads of 64 columns, S 128, 16 q/k
-// groups: 903 us (0.93 TB/s of what has to move, 114 TFLOP/s of the recurrence's
-// arithmetic); 4 x 4096 of 32 heads of 128: 396 us (1.07 TB/s; DRAM 10 %, tensor pipe
-// 14 %, 0.57 instructions a cycle and scheduler); 1237 tokens alone: 119 us
-// (some runs of the same binary take 1004 and 429 us for the first two, by where its code
-// comes to lie).  What enters the fp32 state is as good as fp32: N, X and W take part in its products as
-// three bf16 parts each (24 bits), h in the correction R as two (16 bits; R's share of
-// an error decays with the state's). With two parts throughout, the state was 1e-6 to
+// groups: 907 us (0.93 TB/s of what has to move, 114 TFLOP/s of the recurrence's
+// arithmetic); 4 x 4096 of 32 heads of 128: 406 us (1.04 TB/s; DRAM 10 %, tensor pipe
+// 15 %, 0.56 instructions a cycle and scheduler); 1237 tokens alone: 119 us
+// (before Q h took h's second part, 902, 395 and 119, and in some runs of the same binary
+// 1004 and 429 for the first two; why is not shown).
+//
+// Precision.  What enters the fp32 state is as good as fp32: N, X and W take part in its
+// products as three bf16 parts each (24 bits), h in the correction R as two (16 bits; R's
+// share of an error decays with the state's). With two parts throughout, the state was 1e-6 to
 // 3e-6 off on ordinary inputs and 2e-3 where keys agree and beta is 2 (N's entries are
-// +-2 there and W's sums cancel).  The final state is 3e-7 to 5e-7 off, and up to
-// 1.1e-6 in heads that hardly decay (fp32 2e-7 to 3e-7): a third part of h brought
-// that to 0.7e-6 and cost 15 % of the time (4 x 4096: 396 -> 457 us), the rest is the
-// tensor cores' accumulation, which rounds towards zero.  P, W and h enter y as
+// +-2 there and W's sums cancel).  The final state is 4e-7 to 6e-7 off, and up to
+// 1.1e-6 in heads that hardly decay (fp32 2e-7 to 4e-7): a third part of h brought
+// that to 0.7e-6 and cost 15 % of the time (4 x 4096, when it was tried: 396 -> 457 us),
+// the rest is the tensor cores' accumulation, which rounds towards zero.  P, W and h enter y as
 // two parts.  With keys that agree, P W sums corrections that cancel, and one part lost 1.8
 // % of y's largest value; and P W cancels against Q h where a token overwrites a larger
 // value, so Q h takes the h that R took (with h's high part alone, y of a token that
@@ -67,8 +69,8 @@
 //
 // G is summed in fixed point and kept as an integer and a fraction, so that
 // G_i - G_j is good to 2^-22 even behind a token that forgets everything.
-// Log2 decays of a token are clamped to +-160, beyond which fp32 has only 0 and
-// infinity.
+// A token's g is clamped to +-112 (162 in log2), beyond which e^g is 0 or infinity in
+// fp32.
 #include "gated_delta.cuh"
 #include "tc_ptx.cuh"
 #include "tmap_host.cuh"

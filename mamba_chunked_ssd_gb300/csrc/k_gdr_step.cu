@@ -9,8 +9,8 @@
 // and p = h^T q are formed together over the state that was read, so the block
 // meets once: with r and p,
 //   w = beta (v - a r),   y = scale (a p + (q . k) w),   h <- a h + k w^T.
-// 256 sequences of 64 heads of 64 columns, S 128: 155 us, 6.9 TB/s (1.03 of a plain
-// copy).
+// 256 sequences of 64 heads of 64 columns, S 128: 158 us, 6.9 TB/s (1.02 of a plain
+// copy; 155 where the blocks' widths below were compared).
 #include "gated_delta.cuh"
 
 namespace m2 {

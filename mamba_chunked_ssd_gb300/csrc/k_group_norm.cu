@@ -52,8 +52,9 @@ constexpr int min_blocks(int channels, int tpg) {
 // what it reads itself: registers hold too few loads for the sums between them.  us without /
 // with: blocks, gated before, 2048 channels 36.6 / 33.8, 4096 36.7 / 34.9, 16384 50 / 41 (over
 // 28 sizes and modes 6 % faster; two rows ahead are 4 % slower); groups inside warps, 32768 x
-// 4096 in groups of 64, gated after 129 / 125, no gate 99 / 85 (three rows 131, 86), but in
-// 8-byte vectors 242 / 272.  In fp32 it is slower (1024 channels, gated after, 31 / 37).
+// 4096 in groups of 64, gated after 129 / 125 (where they were compared in turn; 129 with
+// the ring in later runs), no gate 99 / 85 (three rows 131, 86), but in 8-byte vectors
+// 242 / 272.  In fp32 it is slower (1024 channels, gated after, 31 / 37).
 constexpr int ring_rows(int tpg) { return tpg > 32 ? 3 : 2; }
 template <typename T>
 constexpr bool use_ring(int vec, int nv, int tpg) {

@@ -71,3 +71,42 @@ def test_y_of_a_token_that_overwrites_a_far_larger_value(b, nh, G, H, S):
     y_ref, _ = ref.gdr(k, k, v, zeros, zeros + 1, 1.0, l2norm=True)
     token = np.linalg.norm(np64(y) - y_ref, axis=-1) / np.linalg.norm(y_ref, axis=-1)
     assert token.max() <= 2.0 ** -9 + 150 * 2.0 ** -16
+
+
+NAN = float("nan")
+
+
+@pytest.mark.parametrize("b,nh,G,H,S", SHAPES)
+@pytest.mark.parametrize("where", [31, 70, 85])
+@pytest.mark.parametrize("value,bad", [("k", NAN), ("v", NAN), ("g", NAN), ("beta", NAN), ("v", float("inf"))])
+def test_what_is_not_finite_reaches_back_no_further_than_its_16_tokens(b, nh, G, H, S, where, value, bad):
+    """The last head's (or group's) token `where`: the tokens before its block of 16
+    and the heads of other groups keep their results bit for bit."""
+    d, h0 = gdr_inputs(b, 100, nh, G, H, S, BF16, seed=where)
+    clean, fin_clean = bd.mamba2_gdr_fwd(**d, initial_state=h0)
+    d[value][-1, where, -1] = bad
+    y, fin = bd.mamba2_gdr_fwd(**d, initial_state=h0)
+    bd.mamba2_check_device_status()
+    start = where // 16 * 16
+    assert torch.equal(y[-1, :start], clean[-1, :start]) and torch.equal(y[:-1], clean[:-1])
+    others = nh - (nh // G if value == "k" else 1)
+    assert torch.equal(y[-1, :, :others], clean[-1, :, :others])
+    assert torch.equal(fin[-1, :others], fin_clean[-1, :others])
+    columns = y[-1, where:, others:]
+    assert not torch.isfinite(columns).any()
+
+
+@pytest.mark.parametrize("b,nh,G,H,S", SHAPES)
+@pytest.mark.parametrize("l2norm", [False, True])
+@pytest.mark.parametrize("bad", [NAN, float("inf")])
+def test_a_query_that_is_not_finite_stays_in_its_token(b, nh, G, H, S, l2norm, bad):
+    d, h0 = gdr_inputs(b, 100, nh, G, H, S, BF16, seed=3)
+    clean, fin_clean = bd.mamba2_gdr_fwd(**d, initial_state=h0, qk_l2norm=l2norm)
+    where, others = 45, nh - nh // G
+    d["q"][-1, where, -1, S // 2] = bad
+    y, fin = bd.mamba2_gdr_fwd(**d, initial_state=h0, qk_l2norm=l2norm)
+    bd.mamba2_check_device_status()
+    assert torch.equal(fin, fin_clean)
+    assert not torch.isfinite(y[-1, where, others:]).any()
+    y[-1, where, others:] = clean[-1, where, others:]
+    assert torch.equal(y, clean)
