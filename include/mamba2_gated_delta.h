@@ -105,7 +105,7 @@ MAMBA2_API mamba2_status mamba2_gdr_step(const mamba2_shape* shape, const mamba2
  *                the first token, and the last W - 1 inputs, oldest first
  *                (initial_state NULL means zeros, final_state NULL not written)
  *   lengths      [b]            int32, as above
- * At most 65535 rows, 2^30 tokens and 2^30 channels. */
+ * At most 65535 batch rows, 2^30 tokens and 2^30 channels. */
 enum { MAMBA2_CONV_SILU = 1 };
 
 typedef struct {
