@@ -8,8 +8,9 @@ the library is missing the import fails loudly, there is no fallback.
 
 Layouts and semantics are those of include/mamba2_ssd.h ("Accelerating
 Mamba-2 with High-Performance Forward Pass Kernels in NVIDIA CUDA Tile",
-§Kernel 1-3) and, for the gated delta rule, the causal convolution and the
-group norm, of include/mamba2_gated_delta.h.
+§Kernel 1-3), for the gated delta rule, the causal convolution and the group
+norm of include/mamba2_gated_delta.h, and for the gated linear recurrence, the
+block norm and the gradients of include/mamba2_gated_linear.h.
 """
 from __future__ import annotations
 
@@ -24,6 +25,7 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmamba2ssd.so")
 HEADER = os.path.join(os.path.dirname(_PKG), "include", "mamba2_ssd.h")
+HEADER_GATED_LINEAR = os.path.join(os.path.dirname(_PKG), "include", "mamba2_gated_linear.h")
 HEADER_GATED_DELTA = os.path.join(os.path.dirname(_PKG), "include", "mamba2_gated_delta.h")
 
 MAMBA2_F32, MAMBA2_BF16 = 0, 1
@@ -32,6 +34,8 @@ MAMBA2_CONV_SILU = 1
 MAMBA2_NORM_SUBTRACT_MEAN, MAMBA2_NORM_GATE_BEFORE, MAMBA2_NORM_GATE_AFTER, MAMBA2_NORM_SILU = 1, 2, 4, 8
 NORM_MODES = {"none": 0, "before": MAMBA2_NORM_GATE_BEFORE, "after": MAMBA2_NORM_GATE_AFTER,
               "silu": MAMBA2_NORM_SILU}
+MAMBA2_GLR_CHUNK = 64
+MAMBA2_BLOCK_NORM_POST, MAMBA2_BLOCK_NORM_PRE = 1, 2
 STATUS = {0: "MAMBA2_OK", 1: "MAMBA2_ERR_INVALID_ARG", 2: "MAMBA2_ERR_UNSUPPORTED",
           3: "MAMBA2_ERR_CUDA", 4: "MAMBA2_ERR_TIMEOUT"}
 
@@ -67,6 +71,30 @@ class mamba2_norm_shape(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class mamba2_glr_shape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64), ("r_stride", ctypes.c_int64), ("i_stride", ctypes.c_int64),
+                ("z_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("flags", ctypes.c_int32)]
+
+
+class mamba2_glr_grad_strides(ctypes.Structure):
+    _fields_ = [("dx_stride", ctypes.c_int64), ("dr_stride", ctypes.c_int64), ("di_stride", ctypes.c_int64),
+                ("dz_stride", ctypes.c_int64)]
+
+
+class mamba2_block_norm_shape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("channels", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+                ("z_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64),
+                ("residual_out_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64), ("eps", ctypes.c_float),
+                ("dtype", ctypes.c_int32), ("residual_dtype", ctypes.c_int32), ("flags", ctypes.c_int32)]
+
+
+class mamba2_block_norm_grad_strides(ctypes.Structure):
+    _fields_ = [("dx_stride", ctypes.c_int64), ("dz_stride", ctypes.c_int64),
+                ("dresidual_out_stride", ctypes.c_int64), ("dresidual_stride", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -81,6 +109,9 @@ def load_library(path: str = LIB_PATH):
     lib = ctypes.CDLL(path)
     P, S = ctypes.c_void_p, ctypes.POINTER(mamba2_shape)
     O, V, N = (ctypes.POINTER(t) for t in (mamba2_gdr_options, mamba2_conv_shape, mamba2_norm_shape))
+    R, RG, B, BG = (ctypes.POINTER(t) for t in (mamba2_glr_shape, mamba2_glr_grad_strides, mamba2_block_norm_shape,
+                                               mamba2_block_norm_grad_strides))
+    Z = ctypes.c_size_t
     sig = {
         "mamba2_chunk_cumsum": (ctypes.c_int, [S, P, P, P, P]),
         "mamba2_state_pass": (ctypes.c_int, [S, P, P, P, P, P, P, P, P]),
@@ -95,6 +126,15 @@ def load_library(path: str = LIB_PATH):
         "mamba2_causal_conv_fwd": (ctypes.c_int, [V, P, P, P, P, P, P, P, P]),
         "mamba2_causal_conv_step": (ctypes.c_int, [V, P, P, P, P, P, P, P]),
         "mamba2_group_norm": (ctypes.c_int, [N, P, P, P, P, P, P]),
+        "mamba2_glr_fwd": (ctypes.c_int, [R] + [P] * 11),
+        "mamba2_glr_bwd_workspace_size": (Z, [R]),
+        "mamba2_glr_bwd": (ctypes.c_int, [R, RG] + [P] * 16 + [Z, P]),
+        "mamba2_glr_step": (ctypes.c_int, [R] + [P] * 9),
+        "mamba2_causal_conv_bwd_workspace_size": (Z, [V]),
+        "mamba2_causal_conv_bwd": (ctypes.c_int, [V, ctypes.c_int64] + [P] * 12 + [Z, P]),
+        "mamba2_block_norm_fwd": (ctypes.c_int, [B] + [P] * 9),
+        "mamba2_block_norm_bwd_workspace_size": (Z, [B]),
+        "mamba2_block_norm_bwd": (ctypes.c_int, [B, BG] + [P] * 15 + [Z, P]),
         "mamba2_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_int64, P]),
         "mamba2_check_device_status": (ctypes.c_int, [P]),
         "mamba2_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -498,6 +538,264 @@ def mamba2_group_norm(x, weight, ngroups, z=None, bias=None, eps=1e-5, subtract_
     if rc:
         _check("mamba2_group_norm", rc)
     return y
+
+
+# The recurrent block's entry points.  A gradient that is given goes where it lies (a slice of a
+# wider tensor is fine); one that is not given comes back as a new tensor.
+_glr_shape = functools.lru_cache(maxsize=1024)(lambda *a: mamba2_glr_shape(*a))
+_glr_grad_strides = functools.lru_cache(maxsize=1024)(lambda *a: mamba2_glr_grad_strides(*a))
+_block_norm_shape = functools.lru_cache(maxsize=1024)(lambda *a: mamba2_block_norm_shape(*a))
+_block_norm_grad_strides = functools.lru_cache(maxsize=1024)(lambda *a: mamba2_block_norm_grad_strides(*a))
+# bytes of a call's workspace: they follow from its sizes and the GPU
+_workspace_sizes = {}
+
+
+def _workspace(fn, shape, given, t, gpu, stream):
+    """The workspace of a call: the given one, checked, or a new one."""
+    key = (fn, bytes(shape), gpu)
+    need = _workspace_sizes.get(key)
+    if need is None:
+        if len(_workspace_sizes) >= 4096:
+            _workspace_sizes.clear()
+        need = _workspace_sizes[key] = int(getattr(load_library(), fn + "_workspace_size")(shape))
+    if given is None:
+        return _new(max(need, 1), torch.uint8, t.device, stream), need
+    if given.get_device() != gpu or not given.is_contiguous() or given.numel() * given.element_size() < need:
+        raise ValueError(f"workspace must be a contiguous tensor of at least {need} bytes on {t.device}")
+    return given, need
+
+
+def _tensors(names, tensors, like, gpu):
+    """Every tensor that is given has like's dtype, shape and GPU."""
+    for name, t in zip(names, tensors):
+        if t is not None and (t.dtype is not like.dtype or t.shape != like.shape or t.get_device() != gpu):
+            raise ValueError(f"{name} must be {like.dtype} {tuple(like.shape)} on cuda:{gpu}, "
+                             f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _strides(t, name, inner=1):
+    return 0 if t is None else _rows(t, name, inner)
+
+
+def _glr_args(x, r, i, z, A, y, dims):
+    """The shape of a recurrence's call and its GPU; y: the output, or its gradient."""
+    if len(x.shape) != dims:
+        raise ValueError(f"x must have {dims} dimensions, not {tuple(x.shape)}")
+    gpu = _gpu(x, "x")
+    _tensors(("r", "i", "z", "y"), (r, i, z, y), x, gpu)
+    if r is None or i is None:
+        raise ValueError("r and i must be given")
+    C = x.shape[-1]
+    _want(A, "A", torch.float32, (C,), gpu)
+    return _glr_shape(x.shape[0], x.shape[1] if dims == 3 else 1, C, _rows(x, "x", 1), _rows(r, "r", 1),
+                      _rows(i, "i", 1), _strides(z, "z"), _rows(y, "y", 1), _dtype_code(x), 0), gpu
+
+
+def mamba2_glr_fwd(x, r, i, A, z=None, initial_state=None, lengths=None, y=None, final_state=None,
+                   want_final_state=True, chunk_states=None, want_chunk_states=False, stream=None):
+    """The gated linear recurrence over whole sequences: x, r, i (and z) [b, L, C]
+    (slices of a wider tensor are fine), A [C] fp32, states [b, C] fp32, lengths
+    [b] int32 or None.  Returns (y [b, L, C], final_state or None, chunk_states
+    or None): chunk_states [b, ceil(L / 64), C] fp32 is what mamba2_glr_bwd
+    starts from."""
+    gpu = _gpu(x, "x")
+    y = _like(x, y, "y", stream)
+    shape, gpu = _glr_args(x, r, i, z, A, y, 3)
+    b, L, C = x.shape
+    _want(initial_state, "initial_state", torch.float32, (b, C), gpu)
+    _want(lengths, "lengths", torch.int32, (b,), gpu)
+    if final_state is not None:
+        _want(final_state, "final_state", torch.float32, (b, C), gpu)
+    elif want_final_state:
+        final_state = _new((b, C), torch.float32, x.device, stream)
+    chunks = (b, -(-L // MAMBA2_GLR_CHUNK), C)
+    if chunk_states is not None:
+        _want(chunk_states, "chunk_states", torch.float32, chunks, gpu)
+    elif want_chunk_states:
+        chunk_states = _new(chunks, torch.float32, x.device, stream)
+    rc = load_library().mamba2_glr_fwd(shape, _at(x), _at(r), _at(i), _at(z), _at(A), _at(lengths), _at(initial_state),
+                                       _at(y), _at(chunk_states), _at(final_state), _on(stream, gpu))
+    if rc:
+        _check("mamba2_glr_fwd", rc)
+    return y, final_state, chunk_states
+
+
+def mamba2_glr_bwd(dy, x, r, i, A, chunk_states, z=None, dfinal_state=None, lengths=None, dx=None, dr=None, di=None,
+                   dz=None, dA=None, dinitial_state=None, want_dinitial_state=True, workspace=None, stream=None):
+    """Gradients of a mamba2_glr_fwd call from dy [b, L, C] and dfinal_state
+    [b, C] fp32 or None, with that call's chunk_states.  Returns (dx, dr, di,
+    dz or None, dA [C] fp32, dinitial_state [b, C] fp32 or None)."""
+    shape, gpu = _glr_args(x, r, i, z, A, dy, 3)
+    b, L, C = x.shape
+    _want(chunk_states, "chunk_states", torch.float32, (b, -(-L // MAMBA2_GLR_CHUNK), C), gpu)
+    if chunk_states is None:
+        raise ValueError("chunk_states must be given")
+    _want(dfinal_state, "dfinal_state", torch.float32, (b, C), gpu)
+    _want(lengths, "lengths", torch.int32, (b,), gpu)
+    if dz is not None and z is None:
+        raise ValueError("dz is the gradient of z, which is not given")
+    dx, dr, di = _like(x, dx, "dx", stream), _like(x, dr, "dr", stream), _like(x, di, "di", stream)
+    dz = None if z is None else _like(x, dz, "dz", stream)
+    if dA is not None:
+        _want(dA, "dA", torch.float32, (C,), gpu)
+    else:
+        dA = _new((C,), torch.float32, x.device, stream)
+    if dinitial_state is not None:
+        _want(dinitial_state, "dinitial_state", torch.float32, (b, C), gpu)
+    elif want_dinitial_state:
+        dinitial_state = _new((b, C), torch.float32, x.device, stream)
+    grads = _glr_grad_strides(_rows(dx, "dx", 1), _rows(dr, "dr", 1), _rows(di, "di", 1), _strides(dz, "dz"))
+    ws, size = _workspace("mamba2_glr_bwd", shape, workspace, x, gpu, stream)
+    rc = load_library().mamba2_glr_bwd(shape, grads, _at(dy), _at(x), _at(r), _at(i), _at(z), _at(A), _at(lengths),
+                                       _at(chunk_states), _at(dfinal_state), _at(dx), _at(dr), _at(di), _at(dz),
+                                       _at(dA), _at(dinitial_state), _at(ws), size, _on(stream, gpu))
+    if rc:
+        _check("mamba2_glr_bwd", rc)
+    return dx, dr, di, dz, dA, dinitial_state
+
+
+def mamba2_glr_step(x, r, i, A, z=None, state_in=None, state_out=None, y=None, stream=None):
+    """One token of the gated linear recurrence: x, r, i (and z) [b, C], state
+    [b, C] fp32.  Returns (y [b, C], state_out).  Pass state_out=state_in to
+    update the state in place."""
+    gpu = _gpu(x, "x")
+    y = _like(x, y, "y", stream)
+    shape, gpu = _glr_args(x, r, i, z, A, y, 2)
+    _want(state_in, "state_in", torch.float32, x.shape, gpu)
+    if state_out is None:
+        state_out = _new(x.shape, torch.float32, x.device, stream)
+    elif state_out is not state_in:
+        _want(state_out, "state_out", torch.float32, x.shape, gpu)
+    rc = load_library().mamba2_glr_step(shape, _at(x), _at(r), _at(i), _at(z), _at(A), _at(state_in), _at(state_out),
+                                        _at(y), _on(stream, gpu))
+    if rc:
+        _check("mamba2_glr_step", rc)
+    return y, state_out
+
+
+def mamba2_causal_conv_bwd(dy, x, weight, bias=None, silu=True, initial_state=None, lengths=None, dfinal_state=None,
+                           dx=None, dweight=None, dbias=None, dinitial_state=None, want_dinitial_state=True,
+                           workspace=None, stream=None):
+    """Gradients of a mamba2_causal_conv_fwd call from dy [b, L, C] and
+    dfinal_state [b, W - 1, C] or None.  Returns (dx, dweight [C, W] fp32, dbias
+    [C] fp32 or None without a bias, dinitial_state or None)."""
+    b, L, C = x.shape
+    W, gpu = weight.shape[-1], _gpu(x, "x")
+    state = (b, W - 1, C)
+    _tensors(("dy",), (dy,), x, gpu)
+    _want(weight, "weight", torch.float32, (C, W), gpu), _want(bias, "bias", torch.float32, (C,), gpu)
+    _want(initial_state, "initial_state", x.dtype, state, gpu)
+    _want(dfinal_state, "dfinal_state", x.dtype, state, gpu)
+    _want(lengths, "lengths", torch.int32, (b,), gpu)
+    dx = _like(x, dx, "dx", stream)
+    if dweight is not None:
+        _want(dweight, "dweight", torch.float32, (C, W), gpu)
+    else:
+        dweight = _new((C, W), torch.float32, x.device, stream)
+    if dbias is not None:
+        _want(dbias, "dbias", torch.float32, (C,), gpu)
+    elif bias is not None:
+        dbias = _new((C,), torch.float32, x.device, stream)
+    if dinitial_state is not None:
+        _want(dinitial_state, "dinitial_state", x.dtype, state, gpu)
+    elif want_dinitial_state:
+        dinitial_state = _new(state, x.dtype, x.device, stream)
+    shape = _conv_shape(b, L, C, W, _rows(x, "x", 1), _rows(dy, "dy", 1), _dtype_code(x),
+                        MAMBA2_CONV_SILU if silu else 0)
+    ws, size = _workspace("mamba2_causal_conv_bwd", shape, workspace, x, gpu, stream)
+    rc = load_library().mamba2_causal_conv_bwd(shape, _rows(dx, "dx", 1), _at(dy), _at(x), _at(weight), _at(bias),
+                                               _at(lengths), _at(initial_state), _at(dfinal_state), _at(dx),
+                                               _at(dweight), _at(dbias), _at(dinitial_state), _at(ws), size,
+                                               _on(stream, gpu))
+    if rc:
+        _check("mamba2_causal_conv_bwd", rc)
+    return dx, dweight, dbias, dinitial_state
+
+
+def _block_norm_args(x, z, weights, gpu):
+    """The number of channels; checks z and the weights."""
+    C = x.shape[-1]
+    _tensors(("z",), (z,), x, gpu)
+    for name, w in weights:
+        _want(w, name, torch.float32, (C,), gpu)
+    return C
+
+
+def mamba2_block_norm_fwd(x, residual=None, z=None, post_weight=None, scale=None, pre_weight=None, eps=1e-5, post=True,
+                          pre=True, residual_out=None, residual_dtype=None, y=None, stream=None):
+    """The norms after and before a block with its gate and the residual sum: x
+    (and z) [.., C], residual [.., C] in x's dtype or fp32, weights [C] fp32 or
+    None.  Returns (residual_out, y or None without pre): residual_out = residual +
+    scale (post_weight N(x)) SiLU(z), y = pre_weight N(residual_out).  Pass
+    residual_out=residual to update the residual in place; residual_dtype is for
+    calls that give neither (x's dtype else)."""
+    gpu = _gpu(x, "x")
+    C = _block_norm_args(x, z, (("post_weight", post_weight), ("scale", scale), ("pre_weight", pre_weight)), gpu)
+    if residual_out is None:
+        dt = residual.dtype if residual is not None else residual_dtype or x.dtype
+        residual_out = _new(x.shape, dt, x.device, stream)
+    for name, t in (("residual", residual), ("residual_out", residual_out)):
+        if t is not None and (t.dtype is not residual_out.dtype or t.shape != x.shape or t.get_device() != gpu):
+            raise ValueError(f"{name} must be {residual_out.dtype} {tuple(x.shape)} on cuda:{gpu}, "
+                             f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+    if pre:
+        y = _like(x, y, "y", stream)
+    elif y is not None:
+        raise ValueError("y comes from the norm before the next block, which is not asked for")
+    shape = _block_norm_shape(x.numel() // C if C else 0, C, _rows(x, "x", 1), _strides(z, "z"),
+                              _strides(residual, "residual"), _rows(residual_out, "residual_out", 1),
+                              _strides(y, "y"), float(eps), _dtype_code(x), _dtype_code(residual_out),
+                              (MAMBA2_BLOCK_NORM_POST if post else 0) | (MAMBA2_BLOCK_NORM_PRE if pre else 0))
+    rc = load_library().mamba2_block_norm_fwd(shape, _at(x), _at(z), _at(residual), _at(post_weight), _at(scale),
+                                              _at(pre_weight), _at(residual_out), _at(y), _on(stream, gpu))
+    if rc:
+        _check("mamba2_block_norm_fwd", rc)
+    return residual_out, y
+
+
+def mamba2_block_norm_bwd(dresidual_out, dy, x, residual_out=None, z=None, post_weight=None, scale=None, pre_weight=None,
+                          eps=1e-5, post=True, pre=True, dx=None, dz=None, dresidual=None, residual_dtype=None,
+                          want_dresidual=True, workspace=None, stream=None):
+    """Gradients of a mamba2_block_norm_fwd call from those of its outputs:
+    dresidual_out [.., C] in the residual's dtype or None, dy [.., C] (None
+    without pre); residual_out (with pre) as the call wrote it.  Returns (dx, dz
+    or None, dresidual or None, dpost_weight, dscale, dpre_weight [C] fp32, None
+    for a weight that is not given).  Pass dresidual=dresidual_out to update it
+    in place; residual_dtype is for calls that give neither (x's dtype else)."""
+    gpu = _gpu(x, "x")
+    C = _block_norm_args(x, z, (("post_weight", post_weight), ("scale", scale), ("pre_weight", pre_weight)), gpu)
+    _tensors(("dy",), (dy,), x, gpu)
+    if (dy is None or residual_out is None) if pre else dy is not None:
+        raise ValueError("dy and residual_out must be given with the norm before the next block, dy only with it")
+    if not pre:
+        residual_out = None
+    if dz is not None and z is None:
+        raise ValueError("dz is the gradient of z, which is not given")
+    known = next((t.dtype for t in (residual_out, dresidual_out, dresidual) if t is not None), residual_dtype or x.dtype)
+    if dresidual is None and want_dresidual:
+        dresidual = _new(x.shape, known, x.device, stream)
+    for name, t in (("residual_out", residual_out), ("dresidual_out", dresidual_out), ("dresidual", dresidual)):
+        if t is not None and (t.dtype is not known or t.shape != x.shape or t.get_device() != gpu):
+            raise ValueError(f"{name} must be {known} {tuple(x.shape)} on cuda:{gpu}, "
+                             f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+    dx = _like(x, dx, "dx", stream)
+    dz = None if z is None else _like(x, dz, "dz", stream)
+    weights = [None if w is None else _new((C,), torch.float32, x.device, stream)
+               for w in (post_weight, scale, pre_weight)]
+    code = MAMBA2_BF16 if known == torch.bfloat16 else MAMBA2_F32 if known == torch.float32 else -1
+    shape = _block_norm_shape(x.numel() // C if C else 0, C, _rows(x, "x", 1), _strides(z, "z"), 0,
+                              _strides(residual_out, "residual_out"), _strides(dy, "dy"), float(eps), _dtype_code(x),
+                              code, (MAMBA2_BLOCK_NORM_POST if post else 0) | (MAMBA2_BLOCK_NORM_PRE if pre else 0))
+    grads = _block_norm_grad_strides(_rows(dx, "dx", 1), _strides(dz, "dz"), _strides(dresidual_out, "dresidual_out"),
+                                     _strides(dresidual, "dresidual"))
+    ws, size = _workspace("mamba2_block_norm_bwd", shape, workspace, x, gpu, stream)
+    rc = load_library().mamba2_block_norm_bwd(shape, grads, _at(dresidual_out), _at(dy), _at(x), _at(z),
+                                              _at(residual_out), _at(post_weight), _at(scale), _at(pre_weight),
+                                              _at(dx), _at(dz), _at(dresidual), *map(_at, weights), _at(ws), size,
+                                              _on(stream, gpu))
+    if rc:
+        _check("mamba2_block_norm_bwd", rc)
+    return dx, dz, dresidual, *weights
 
 
 def mamba2_selftest_wait_timeout(limit_ns: int, stream=None):
