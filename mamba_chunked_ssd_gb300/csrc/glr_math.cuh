@@ -6,16 +6,15 @@
 #include "gated_linear.cuh"
 #include "tc_ptx.cuh"
 
+
 namespace m2 {
 namespace glr {
 
 using namespace tc;
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kTok = 8;                  // tokens of a warp
-constexpr int kTile = kWarps * kTok;     // tokens of a block's step
-constexpr int kStrip = 64;               // channels of a block: two to a lane
+constexpr int kGroups = 8;               // groups of lanes in a block, each with its own tokens
+constexpr int kTok = 8;                  // tokens of a group
+constexpr int kTile = kGroups * kTok;    // tokens of a block's step
 static_assert(kTile == MAMBA2_GLR_CHUNK, "a chunk state is the state that enters a tile");
 
 __device__ __forceinline__ float2 f2(float v) { return make_float2(v, v); }
@@ -44,34 +43,55 @@ __device__ __forceinline__ float2 sigmoid2(float2 x) {
     return make_float2(rcp_approx(d.x), rcp_approx(d.y));
 }
 
-// a = e^la and m = 1 - a^2 of la <= 0.  With la = n ln 2 + y, |y| <= ln 2 / 2, the Taylor
-// polynomial p of e^y - 1 to y^7 (remainder 2e-8 of p) gives e^la - 1 = 2^n p + (2^n - 1)
-// without cancellation, so that m keeps its precision for a next to 1, where it sets the
-// state's scale, and a is e^la rounded: an error of a that is the same for every token would be
-// multiplied by the recurrence's memory 1 / (1 - a).  Below -87 a is 1.6e-38.
+// a = e^la and m = 1 - a^2 of la <= 0.  A polynomial p of e^la - 1 keeps m's precision for a
+// next to 1, where m sets the state's scale, and gives an a that is e^la rounded: an error of a that is the
+// same for every token would be multiplied by the recurrence's memory 1 / (1 - a).  p / la to la^6
+// by a Remez exchange for the relative error on -1 .. 0 (2.7e-9).  WIDE, where A is below -1:
+// la = n ln 2 + y, |y| <= ln 2 / 2, and e^la - 1 = 2^n p + (2^n - 1) without cancellation, p / y
+// to y^5 (1.1e-8); below -87 a is 1.6e-38.
+template <bool WIDE>
 __device__ __forceinline__ void decay2(float2 la, float2& a, float2& m) {
-    la.x = max_nan(la.x, -87.f), la.y = max_nan(la.y, -87.f);
-    const float2 big = f2(12582912.f);  // 1.5 2^23: its sum with a small number is rounded to a whole one
-    const float2 t = fma2(la, f2(kLog2e), big);
-    const float2 y = fma2(add2(t, f2(-12582912.f)), f2(-0.693147180559945f), la);
-    float2 p = fma2(y, f2(1.f / 5040.f), f2(1.f / 720.f));
-    p = fma2(p, y, f2(1.f / 120.f));
-    p = fma2(p, y, f2(1.f / 24.f));
-    p = fma2(p, y, f2(1.f / 6.f));
-    p = fma2(p, y, f2(0.5f));
-    p = fma2(p, y, f2(1.f));
-    p = mul2(p, y);
-    // 2^n from the bits that hold n
-    const float2 s = make_float2(__uint_as_float((__float_as_uint(t.x) << 23) + 0x3f800000u),
-                                 __uint_as_float((__float_as_uint(t.y) << 23) + 0x3f800000u));
-    a = fma2(s, p, s);
-    const float2 e = fma2(s, p, add2(s, f2(-1.f)));  // a - 1
-    m = mul2(e, fma2(e, f2(-1.f), f2(-2.f)));        // -e (e + 2)
+    float2 e;  // a - 1
+    if constexpr (!WIDE) {
+        e = fma2(la, f2(0.00012913094542454928f), f2(0.001301126554608345f));
+        e = fma2(e, la, f2(0.008276209235191345f));
+        e = fma2(e, la, f2(0.04164746776223183f));
+        e = fma2(e, la, f2(0.16666366159915924f));
+        e = fma2(e, la, f2(0.49999985098838806f));
+        e = fma2(e, la, f2(1.f));
+        e = mul2(e, la);
+        a = add2(e, f2(1.f));
+    } else {
+        la.x = max_nan(la.x, -87.f), la.y = max_nan(la.y, -87.f);
+        // 1.5 2^23 + 127: its sum with a small number is rounded to a whole one, and ends in the bits of 2^n
+        constexpr float kBig = 12582912.f + 127.f;
+        const float2 t = fma2(la, f2(kLog2e), f2(kBig));
+        const float2 y = fma2(add2(t, f2(-kBig)), f2(-0.693147180559945f), la);
+        float2 p = fma2(y, f2(0.0013888872927054763f), f2(0.008369109593331814f));
+        p = fma2(p, y, f2(0.041667137295007706f));
+        p = fma2(p, y, f2(0.16666506230831146f));
+        p = fma2(p, y, f2(0.5f));
+        p = fma2(p, y, f2(1.f));
+        p = mul2(p, y);
+        const float2 s =
+            make_float2(__uint_as_float(__float_as_uint(t.x) << 23), __uint_as_float(__float_as_uint(t.y) << 23));
+        a = fma2(s, p, s);
+        e = fma2(s, p, add2(s, f2(-1.f)));
+    }
+    m = mul2(e, fma2(e, f2(-1.f), f2(-2.f)));  // -e (e + 2)
 }
 
+// sqrt(m)
+__device__ __forceinline__ float2 sqrt2(float2 m) {
+    float2 r;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(m.x));
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(m.y));
+    return r;
+}
 // 1 / sqrt(m), finite at m = 0 (where log a, which it meets, is 0 too).
 __device__ __forceinline__ float2 rsqrt2(float2 m) {
-    return make_float2(rsqrt_approx(fmaxf(m.x, 1e-36f)), rsqrt_approx(fmaxf(m.y, 1e-36f)));
+    m = add2(m, f2(1e-36f));
+    return make_float2(rsqrt_approx(m.x), rsqrt_approx(m.y));
 }
 
 // A pair of neighbouring channels as it lies in memory.
@@ -95,75 +115,91 @@ struct Pair<float> {
 // How rows lie: on 16 bytes with whole 16-byte pieces of channels, on a pair of channels, or on an element.
 enum Rows { kRows16, kRowsPair, kRowsOne };
 
-// One sequence tensor of a block: its strip of channels, its batch row.
-template <typename T>
-struct Seq {
-    const T* p;  // channel 0 of the strip, token 0
-    int64_t stride;
-};
+// One sequence tensor's tokens on their way to shared memory.  LANES lanes are a group with two channels each of
+// the strip's and eight tokens; the 32 / LANES groups of a warp lie side by side in its place, [8 tokens]
+// [group][2 LANES channels] T, which its lanes fill together, tile after tile, `step` tokens apart: by cp.async
+// (waited for with its group, then __syncwarp), or by plain loads where rows start on single
+// bf16 elements.  What is not there becomes 0 in tiles that a row ends in.
+template <typename T, Rows ROWS, int LANES>
+struct Walk {
+    static constexpr int kStrip = 2 * LANES, kSub = 32 / LANES, kPlace = kTok * kSub * kStrip;
+    static constexpr int kPer = ROWS == kRows16 ? 16 / (int)sizeof(T) : ROWS == kRowsPair ? 2 : 1;  // channels of a copy
+    static constexpr int kAcross = kStrip / kPer, kCopies = kPlace / kPer / 32;
+    static constexpr int kBytes = kPer * (int)sizeof(T);
+    const T* next;  // of this lane's first copy
 
-// The tokens t .. t + 7 (those before n) of a strip with `have` channels into a warp's place in
-// shared memory, [8][64] T; what is not there becomes 0.  A warp's lanes fill the place
-// together: cp.async (waited for with its group, then __syncwarp), or plain loads where rows
-// start on single bf16 elements.
-template <typename T, Rows ROWS>
-__device__ __forceinline__ void fetch(T* place, const Seq<T>& s, int64_t t, int64_t n, int have, int lane) {
-    if constexpr (ROWS == kRows16) {
-        constexpr int per = 16 / sizeof(T), across = kStrip / per, at_once = 32 / across;
-        const int c = lane % across * per;
-#pragma unroll
-        for (int k = 0; k < kTok / at_once; ++k) {
-            const int row = lane / across + k * at_once;
-            const bool live = t + row < n && c < have;
-            const T* from = live ? s.p + (t + row) * s.stride + c : s.p;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(place + row * kStrip + c)),
-                         "l"(from), "r"(live ? 16 : 0)
-                         : "memory");
-        }
-    } else if constexpr (ROWS == kRowsPair) {
-        constexpr int bytes = 2 * sizeof(T);
-#pragma unroll
-        for (int row = 0; row < kTok; ++row) {
-            const bool live = t + row < n && 2 * lane < have;
-            const T* from = live ? s.p + (t + row) * s.stride + 2 * lane : s.p;
-            asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(
-                             smem_u32(place + row * kStrip + 2 * lane)),
-                         "l"(from), "n"(bytes), "r"(live ? bytes : 0)
-                         : "memory");
-        }
-    } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int row = 0; row < kTok; ++row)
-#pragma unroll
-            for (int c = lane; c < kStrip; c += 32) {
-                const bool live = t + row < n && c < have;
-                const T* from = live ? s.p + (t + row) * s.stride + c : s.p;
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(place + row * kStrip + c)),
-                             "l"(from), "r"(live ? 4 : 0)
-                             : "memory");
-            }
-    } else {
-        T v[kTok][2];
-#pragma unroll
-        for (int row = 0; row < kTok; ++row)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int c = lane + 32 * k;
-                v[row][k] = t + row < n && c < have ? s.p[(t + row) * s.stride + c] : from_f32<T>(0.f);
-            }
-#pragma unroll
-        for (int row = 0; row < kTok; ++row)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) place[row * kStrip + lane + 32 * k] = v[row][k];
+    // copy k of this lane: its group of the warp, token and channel
+    static __device__ __forceinline__ int sub(int lane, int k) { return (lane + 32 * k) / kAcross % kSub; }
+    static __device__ __forceinline__ int token(int lane, int k) { return (lane + 32 * k) / (kAcross * kSub); }
+    static __device__ __forceinline__ int channel(int lane, int k) { return (lane + 32 * k) % kAcross * kPer; }
+
+    __device__ __forceinline__ void start(const void* base, int64_t row, int64_t stride, int64_t c0, int64_t t, int lane) {
+        next = static_cast<const T*>(base) + (row + t + token(lane, 0) + sub(lane, 0) * kTok) * stride + c0 +
+               channel(lane, 0);
     }
-}
+    // t: the warp's first token; -1: nothing is there.  base: the tensor, for copies of nothing
+    __device__ __forceinline__ void fetch(T* place, const void* base, int64_t stride, int t, int n, int step, int have, int lane) {
+        if (ROWS != kRowsOne && t >= 0 && t + kTok * kSub <= n) {
+            if constexpr (ROWS != kRowsOne) {
+                // from copy to copy a fixed number of tokens on (one warp's copies span whole tokens)
+                static_assert(32 % (kAcross * kSub) == 0 || kAcross * kSub % 32 == 0, "");
+                const uint32_t to = smem_u32(place) + lane * kBytes;
+#pragma unroll
+                for (int k = 0; k < kCopies; ++k) {
+                    const T* from = next + (token(lane, k) - token(lane, 0) + (sub(lane, k) - sub(lane, 0)) * kTok) * stride +
+                                    (channel(lane, k) - channel(lane, 0));
+                    if (channel(lane, k) < have) {
+                        if constexpr (kBytes == 16)
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + k * 32 * kBytes), "l"(from)
+                                         : "memory");
+                        else
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to + k * 32 * kBytes),
+                                         "l"(from), "n"(kBytes)
+                                         : "memory");
+                    }
+                }
+            }
+        } else {
+            // (copies of single bf16 elements: eight loads at once)
+            constexpr int kAtOnce = kCopies < 8 ? kCopies : 8;
+#pragma unroll
+            for (int k0 = 0; k0 < kCopies; k0 += kAtOnce) {
+                T v[kAtOnce];
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i) {
+                    const int k = k0 + i, row = token(lane, k) + sub(lane, k) * kTok;
+                    const bool live = t >= 0 && t + row < n && channel(lane, k) < have;
+                    const T* from = next + (token(lane, k) - token(lane, 0) + (sub(lane, k) - sub(lane, 0)) * kTok) * stride +
+                                    (channel(lane, k) - channel(lane, 0));
+                    if (!live) from = static_cast<const T*>(base);
+                    T* to = place + (lane + 32 * k) * kPer;
+                    if constexpr (kBytes == 16)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from),
+                                     "r"(live ? 16 : 0)
+                                     : "memory");
+                    else if constexpr (kBytes >= 4)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(to)), "l"(from),
+                                     "n"(kBytes), "r"(live ? kBytes : 0)
+                                     : "memory");
+                    else
+                        v[i] = live ? *from : from_f32<T>(0.f);
+                }
+                if constexpr (kBytes < 4) {
+#pragma unroll
+                    for (int i = 0; i < kAtOnce; ++i) place[lane + 32 * (k0 + i)] = v[i];
+                }
+            }
+        }
+        next += (int64_t)step * stride;
+    }
+};
 __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void wait_for() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A pair of channels of a row to memory; `have` of the strip's channels are there.
+// A pair of channels to memory; `have` of the strip's channels are there.
 template <typename T, bool ODD>
 __device__ __forceinline__ void store(T* row, float2 v, int lane, int have) {
     if constexpr (!ODD) {
@@ -173,6 +209,27 @@ __device__ __forceinline__ void store(T* row, float2 v, int lane, int have) {
         if (2 * lane + 1 < have) row[2 * lane + 1] = from_f32<T>(v.y);
     }
 }
+
+// A lane's pairs of channels of a group's tokens, one after another (`step` elements apart).
+// ALL: every lane's channels are there.
+template <typename T, bool ODD>
+struct Rows1 {
+    T* to;
+    int64_t step;
+    __device__ __forceinline__ void start(void* base, int64_t row, int64_t stride, int64_t c0, int64_t t, int lane, int dir) {
+        to = static_cast<T*>(base) + (row + t) * stride + c0 + 2 * lane;
+        step = dir * stride;
+    }
+    template <bool ALL>
+    __device__ __forceinline__ void put(float2 v, int lane, int have, bool live) {
+        if constexpr (ALL && !ODD) {
+            *reinterpret_cast<typename Pair<T>::raw*>(to) = Pair<T>::put(v);
+        } else {
+            if (live) store<T, ODD>(to - 2 * lane, v, lane, have);
+        }
+        to += step;
+    }
+};
 
 // fp32 values of a pair of channels, of which `have` of the strip's are there.
 __device__ __forceinline__ float2 load_pair(const float* p, int lane, int have) {
@@ -202,22 +259,26 @@ inline Rows rows_of(const void* const* p, const int64_t* strides, int count, int
     return all % 16 == 0 ? kRows16 : all % (2 * bytes) == 0 ? kRowsPair : kRowsOne;
 }
 
-// Blocks that split a sequence: doubled up to 8, while there are fewer than four to an SM and tiles for them.
-inline int glr_cluster(int64_t strips, int64_t tiles) {
-    const int sms = sm_count();
-    int K = 1;
-    while (K < 8 && 2 * K <= tiles && strips * K < 4 * (int64_t)(sms > 0 ? sms : 152)) K *= 2;
-    return K;
+// Blocks that split a sequence, of which `per_sm` fit on an SM at once: eight or four while all
+// of them are there at once and have a tile each, else one (an exchange between blocks costs more than it
+// gives where strips alone fill half of the GPU).  1 x 4096 tokens, forward / backward, us with 1, 4 and 8:
+// 32 strips 52, 38, 28 / 104, 46, 34; 64 strips 52, 44, 36 / 108, 56, 67; 100 strips 54, 52, 56 / 112, 65, 71;
+// 128 strips 54, 56, 61 / 114, 104, 95.
+inline int glr_cluster(int64_t strips, int64_t tiles, int per_sm) {
+    const int64_t sms = sm_count() > 0 ? sm_count() : 152;
+    if (tiles >= 8 && 8 * strips <= per_sm * sms) return 8;
+    return tiles >= 4 && 4 * strips <= 3 * sms ? 4 : 1;
 }
 
 // A block for each strip of each batch row, or K of them as a cluster.
 template <typename Args>
-cudaError_t launch_strips(void (*kernel)(Args, int), const Args& a, int64_t strips, int K, int bytes, cudaStream_t st) {
+cudaError_t launch_strips(void (*kernel)(Args, int), const Args& a, int64_t strips, int K, int threads,
+                          int bytes, cudaStream_t st) {
     const cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kernel), bytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(strips * K), (unsigned)a.batch);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = (size_t)bytes;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];

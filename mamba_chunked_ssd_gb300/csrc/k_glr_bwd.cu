@@ -3,14 +3,18 @@
 //
 //   dh_t = dy_t [SiLU(z_t)] + a_{t+1} dh_{t+1}          dz = dy h SiLU'(z)
 //   dx   = dh s sigmoid(i)                              di = dx x (1 - sigmoid(i))
-//   E    = la dL/dla = dh (la a h_{t-1} - la a^2 / s v) dr = E (1 - sigmoid(r)),  dA = sum E / A
+//   E    = la dL/dla = dh la a (h_{t-1} - a / s v)     dr = E (1 - sigmoid(r)),  dA = sum E / A
 //
-// (la / s is finite where s vanishes, d la is not.)  Everything is read once and written once:
-// a block walks its strip of 64 channels backwards in tiles of 64 tokens, a warp with eight
+// (la / s is finite where s vanishes, dL/dla is not.)  Everything is read once and written once:
+// a block walks its strip of 32 channels backwards in tiles of 64 tokens, a group of 16 lanes with eight
 // tokens of each.  The states inside a tile come from the chunk state that enters it, which the forward
-// pass kept, by the same exchange of maps as there; the maps of the gradients, c -> A (c + ..)
+// pass kept, by the same exchange of maps as there; the maps of the gradients, c -> A c + R
 // from the other end, go through the same barrier.  What both halves need stays in
-// registers, or in the places of inputs that have been used.
+// registers or in shared memory, in the places of inputs that have been used where they fit.
+// About 60 instructions an element in 16 (gated 12) warps of an SM bound it next to memory: 16 x 1024 x 4096 in bf16 196 us,
+// 4.8 TB/s, gated 243 us, 5.0 TB/s; 4 x 4096 x 4096 220 us, gated 298.
+#include <type_traits>
+
 #include "glr_math.cuh"
 
 namespace m2 {
@@ -19,12 +23,18 @@ namespace {
 using namespace glr;
 
 constexpr int kStages = 2;
-
+constexpr int kLanes = 16;
+// Warps of an SM: as many as shared memory allows (4 x 4096 x 4096 in bf16: with 16 220 us, with 12 of more
+// registers each 259; gated, where 16 do not fit, 298).
 template <typename T, bool GATED>
-constexpr int smem_bytes() {
-    return kStages * kWarps * (4 + GATED) * kTok * kStrip * (int)sizeof(T) +
-           2 * kWarps * 32 * (int)(sizeof(float4) + sizeof(float2)) + 2 * 8 * 32 * (int)sizeof(float4) +
-           (GATED && sizeof(T) == 2 ? kThreads * kTok * (int)sizeof(float2) : 0);
+constexpr int kWarpsOf = sizeof(T) == 2 && !GATED ? 16 : 12;
+constexpr int kPerSm = 3;  // blocks of an SM that a split of sequences counts on
+
+template <typename T, bool GATED, int LANES>
+constexpr int smem_bytes(bool cluster) {
+    return kStages * kGroups * LANES * 2 * (4 + GATED) * kTok * (int)sizeof(T) +
+           (4 * kGroups + (cluster ? 2 * 8 : 0)) * LANES * (int)sizeof(float4) +
+           (sizeof(T) == 2 ? (2 + GATED) * kGroups * LANES * kTok * (int)sizeof(float2) : 0);
 }
 
 // Two fp32 values in the places of two raw pairs (one of them where a raw pair is fp32).
@@ -37,182 +47,223 @@ __device__ __forceinline__ float2 unstash(const uint32_t* p, const uint32_t* q) 
 __device__ __forceinline__ void stash(float2* p, float2*, float2 v) { *p = v; }
 __device__ __forceinline__ float2 unstash(const float2* p, const float2*) { return *p; }
 
-template <typename T, Rows ROWS, bool GATED>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) k_glr_bwd(const GlrBwdArgs a, int K) {
-    constexpr int NT = 4 + GATED, kPlace = kTok * kStrip, S = kStages;
+template <typename T, Rows ROWS, bool GATED, int LANES, bool CLUSTER>
+__global__ void __launch_bounds__(kGroups* LANES, kWarpsOf<T, GATED> * 32 / (kGroups * LANES)) k_glr_bwd(const GlrBwdArgs a, int K) {
+    using W = Walk<T, ROWS, LANES>;
+    constexpr int NT = 4 + GATED, S = kStages, kSub = W::kSub, kPlace = W::kPlace, kStrip = W::kStrip;
+    constexpr int kWarps = kGroups / kSub, kThreads = kGroups * LANES;
     constexpr bool kOdd = ROWS == kRowsOne;
     using P = Pair<T>;
     using Raw = typename P::raw;
     extern __shared__ __align__(16) uint8_t smem[];
-    float4(*sums)[kWarps][32] = reinterpret_cast<float4(*)[kWarps][32]>(smem);
-    float4(*parts)[8][32] = reinterpret_cast<float4(*)[8][32]>(smem + 2 * kWarps * 32 * sizeof(float4));
-    float2(*rsums)[kWarps][32] =
-        reinterpret_cast<float2(*)[kWarps][32]>(smem + (2 * kWarps + 2 * 8) * 32 * sizeof(float4));
-    uint8_t* rest = smem + (2 * kWarps + 2 * 8) * 32 * sizeof(float4) + 2 * kWarps * 32 * sizeof(float2);
-    T* ring = reinterpret_cast<T*>(rest);
-    // the factors of dz, where z's places do not hold them
-    float2* dzs = reinterpret_cast<float2*>(rest + kStages * kWarps * NT * kPlace * sizeof(T)) + threadIdx.x;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int rank = K > 1 ? (int)cluster_rank() : 0;
+    using Maps = float4[kGroups][LANES];
+    Maps* sums = reinterpret_cast<Maps*>(smem);   // of the states
+    Maps* rsums = sums + 2;                       // of the gradients
+    float4(*parts)[8][LANES] = reinterpret_cast<float4(*)[8][LANES]>(rsums + 2);
+    T* ring = reinterpret_cast<T*>(parts + (CLUSTER ? 2 : 0));
+    // what does not fit where bf16 inputs lay: each thread's uo, w and factors of dz
+    float2* kept = reinterpret_cast<float2*>(ring + kStages * kWarps * NT * kPlace) + threadIdx.x;
+    if (!CLUSTER) K = 1;
+    const int warp = threadIdx.x / 32, group = threadIdx.x / LANES, lane = threadIdx.x % LANES, wl = threadIdx.x % 32;
+    const int rank = CLUSTER ? (int)cluster_rank() : 0;
     const int64_t b = blockIdx.y, c0 = (int64_t)(blockIdx.x / K) * kStrip;
     const int have = (int)imin64(a.channels - c0, kStrip);
-    const int64_t L = a.seqlen, n = row_length(a.lengths, b, L), tiles = (n + kTile - 1) / kTile;
-    const Seq<T> in[5] = {{static_cast<const T*>(a.x) + b * L * a.x_stride + c0, a.x_stride},
-                          {static_cast<const T*>(a.r) + b * L * a.r_stride + c0, a.r_stride},
-                          {static_cast<const T*>(a.i) + b * L * a.i_stride + c0, a.i_stride},
-                          {static_cast<const T*>(a.dy) + b * L * a.dy_stride + c0, a.dy_stride},
-                          {GATED ? static_cast<const T*>(a.z) + b * L * a.z_stride + c0 : nullptr, a.z_stride}};
+    const int L = (int)a.seqlen, n = __shfl_sync(0xffffffffu, (int)row_length(a.lengths, b, L), 0), tiles = (n + kTile - 1) / kTile;
+    const int step = K * kTile;
+    int g = tiles - 1 - rank;                              // the tile that is computed (below 0: none)
+    int ta = g * kTile + warp * kSub * kTok;               // the warp's first token of the tile that is fetched
+    W in[NT];
+    in[0].start(a.x, b * L, a.x_stride, c0, ta, wl);
+    in[1].start(a.r, b * L, a.r_stride, c0, ta, wl);
+    in[2].start(a.i, b * L, a.i_stride, c0, ta, wl);
+    in[3].start(a.dy, b * L, a.dy_stride, c0, ta, wl);
+    if (GATED) in[NT - 1].start(a.z, b * L, a.z_stride, c0, ta, wl);
     T* dx = static_cast<T*>(a.dx) + b * L * a.dx_stride + c0;
     T* dr = static_cast<T*>(a.dr) + b * L * a.dr_stride + c0;
     T* di = static_cast<T*>(a.di) + b * L * a.di_stride + c0;
     T* dz = GATED ? static_cast<T*>(a.dz) + b * L * a.dz_stride + c0 : nullptr;
-    const float* states = a.chunk_states + b * ((L + kTile - 1) / kTile) * a.channels + c0;
+    const float* states = a.chunk_states + (b * ((L + kTile - 1) / kTile)) * a.channels + c0;
     const float2 A = load_pair(a.A + c0, lane, have);
     float2 carry = a.dfinal ? load_pair(a.dfinal + b * a.channels + c0, lane, have) : f2(0.f);
     float2 total = f2(0.f);
-
-    // the tile of a step (below 0: none) and this warp's first token in it
-    auto tile_of = [&](int64_t step) { return tiles - 1 - (step * K + rank); };
-    auto ahead = [&](int64_t step, int stage) {
-        const int64_t g = tile_of(step), t = (g < 0 ? 0 : g) * kTile + warp * kTok;
+    const int64_t strides[5] = {a.x_stride, a.r_stride, a.i_stride, a.dy_stride, a.z_stride};
+    const void* bases[5] = {a.x, a.r, a.i, a.dy, a.z};
+    auto ahead = [&](int stage) {
 #pragma unroll
         for (int q = 0; q < NT; ++q)
-            fetch<T, ROWS>(ring + ((stage * kWarps + warp) * NT + q) * kPlace, in[q], t, g < 0 ? 0 : n, have, lane);
+            in[q].fetch(ring + ((stage * kWarps + warp) * NT + q) * kPlace, bases[q], strides[q], ta, n, -step, have, wl);
+        ta = ta < 0 ? -1 : ta - step;
         commit();
     };
-    if (K > 1) cluster_sync();  // the others' shared memory is there
-    for (int s = 0; s < S; ++s) ahead(s, s);
-    const int64_t steps = (tiles + K - 1) / K;
-    int stage = 0, buf = 0;
-    for (int64_t j = 0; j < steps; ++j) {
-        const int64_t g = tile_of(j), t = (g < 0 ? 0 : g) * kTile + warp * kTok;
-        const int live = g < 0 ? 0 : (int)imin64(n - t < 0 ? 0 : n - t, kTok);  // this warp's tokens
-        float2 h = g < 0 ? f2(0.f) : load_pair(states + g * a.channels, lane, have);
-        wait_for<S - 1>();
-        __syncwarp();
-        Raw* px = reinterpret_cast<Raw*>(ring + (stage * kWarps + warp) * NT * kPlace) + lane;
-        Raw *pr = px + kTok * 32, *pi = px + 2 * kTok * 32, *pd = px + 3 * kTok * 32, *pz = px + 4 * kTok * 32;
-        float2 f[kTok], s[kTok], c2[kTok], oi[kTok];  // a; s sigmoid(i); -la a^2 / s v; 1 - sigmoid(i)
-        float2 PA = f2(1.f), PB = f2(0.f), PR = f2(0.f);
+    if (CLUSTER) cluster_sync();  // the others' shared memory is there
+    for (int s = 0; s < S; ++s) ahead(s);
+    const int steps = (tiles + K - 1) / K;
+    auto walk = [&](auto wide) {
+        int stage = 0, buf = 0;
+        float2 before = g < 0 ? f2(0.f) : load_pair(states + (int64_t)g * a.channels, lane, have);
+        for (int j = 0; j < steps; ++j, g -= K) {
+            const int t = g * kTile + group * kTok;
+            const int live = g < 0 ? 0 : min(max(n - t, 0), kTok);  // this group's tokens
+            float2 h = before;  // the state that enters the tile; the next one's is on its way
+            if (g >= K) before = load_pair(states + (int64_t)(g - K) * a.channels, lane, have);
+            wait_for<S - 1>();
+            __syncwarp();
+            Raw* px = reinterpret_cast<Raw*>(ring + (stage * kWarps + warp) * NT * kPlace) + wl;
+            Raw *pr = px + kTok * 32, *pi = px + 2 * kTok * 32, *pd = px + 3 * kTok * 32, *pz = px + 4 * kTok * 32;
+            // The second half needs a, s sigmoid(i), u = s v; sigmoid(r), u (1 - sigmoid(i)), a v / s, and the
+            // gradient of h; the latter lie in shared memory (registers for them would leave too few warps).
+            auto keep = [&](Raw* at, int which, int k, float2 v) {
+                if constexpr (sizeof(T) == 2) kept[(which * kTok + k) * kThreads] = v;
+                else *reinterpret_cast<float2*>(at + k * 32) = v;
+            };
+            auto take = [&](const Raw* at, int which, int k) {
+                if constexpr (sizeof(T) == 2) return kept[(which * kTok + k) * kThreads];
+                else return *reinterpret_cast<const float2*>(at + k * 32);
+            };
+            float2 f[kTok], s[kTok], u[kTok];
+            float2 PA = f2(1.f), PB = f2(0.f), PR = f2(0.f);
+            auto factors = [&](auto whole) {
 #pragma unroll
-        for (int k = 0; k < kTok; ++k) {
-            const float2 x = P::get(px[k * 32]);
-            float2 sr = sigmoid2(P::get(pr[k * 32]));
-            const float2 si = sigmoid2(P::get(pi[k * 32]));
-            const float2 la = mul2(A, sr);
-            float2 m;
-            decay2(la, f[k], m);
-            const float2 q = rsqrt2(m);
-            s[k] = mul2(mul2(m, q), si);
-            oi[k] = fma2(si, f2(-1.f), f2(1.f));
-            const float2 ap = mul2(f[k], q);
-            c2[k] = mul2(mul2(mul2(mul2(ap, ap), mul2(la, f2(-1.f))), s[k]), x);
-            float2 gy = P::get(pd[k * 32]);
-            if (GATED) {
-                const float2 z = P::get(pz[k * 32]), sz = sigmoid2(z);
-                const float2 d = mul2(gy, sz);
-                gy = mul2(d, z);
-                const float2 dzc = fma2(gy, fma2(sz, f2(-1.f), f2(1.f)), d);
-                stash(pd + k * 32, pz + k * 32, gy);
-                if (sizeof(T) == 2) dzs[k * kThreads] = dzc;
-                else *reinterpret_cast<float2*>(pz + k * 32) = dzc;
-            }
-            if (k >= live) f[k] = f2(1.f), s[k] = c2[k] = sr = gy = f2(0.f);
-            stash(pr + k * 32, pi + k * 32, sr);
-            PB = fma2(f[k], PB, mul2(s[k], x));
-            PA = mul2(PA, f[k]);
-            PR = fma2(PA, gy, PR);
-        }
-        sums[buf][warp][lane] = make_float4(PA.x, PA.y, PB.x, PB.y);
-        rsums[buf][warp][lane] = PR;
-        __syncthreads();
-        // the state before this warp's tokens
-        for (int w = 0; w < warp; ++w) {
-            const float4 v = sums[buf][w][lane];
-            h = fma2(make_float2(v.x, v.y), h, make_float2(v.z, v.w));
-        }
-        // the gradient map of the tile's tokens behind this warp's, and of the whole tile
-        float2 QA = f2(1.f), QR = f2(0.f), c;
-        PA = f2(1.f), PR = f2(0.f);
+                for (int k = 0; k < kTok; ++k) {
+                    const float2 x = P::get(px[k * 32]);
+                    float2 sr = sigmoid2(P::get(pr[k * 32]));
+                    const float2 si = sigmoid2(P::get(pi[k * 32])), v = mul2(si, x);
+                    float2 m;
+                    decay2<decltype(wide)::value>(mul2(A, sr), f[k], m);
+                    const float2 q = rsqrt2(m), mq = mul2(m, q);
+                    s[k] = mul2(mq, si);
+                    u[k] = mul2(mq, v);
+                    float2 w = mul2(mul2(f[k], q), v);
+                    float2 gy = P::get(pd[k * 32]);
+                    if (GATED) {
+                        const float2 z = P::get(pz[k * 32]), sz = sigmoid2(z);
+                        const float2 d = mul2(gy, sz);
+                        gy = mul2(d, z);
+                        const float2 dzc = fma2(gy, fma2(sz, f2(-1.f), f2(1.f)), d);
+                        stash(pd + k * 32, pz + k * 32, gy);
+                        keep(pz, 2, k, dzc);
+                    }
+                    if (!decltype(whole)::value && k >= live) f[k] = f2(1.f), s[k] = u[k] = w = sr = gy = f2(0.f);
+                    keep(px, 0, k, fma2(mul2(u[k], f2(-1.f)), si, u[k]));
+                    stash(pr + k * 32, pi + k * 32, sr);
+                    keep(pi, 1, k, w);
+                    PB = fma2(f[k], PB, u[k]);
+                    PA = mul2(PA, f[k]);
+                    PR = fma2(PA, gy, PR);
+                }
+            };
+            if (live == kTok) factors(std::true_type{});
+            else factors(std::false_type{});
+            sums[buf][group][lane] = make_float4(PA.x, PA.y, PB.x, PB.y);
+            rsums[buf][group][lane] = make_float4(PA.x, PA.y, PR.x, PR.y);
+            __syncthreads();
+            // the state before this group's tokens
 #pragma unroll
-        for (int w = kWarps - 1; w >= 0; --w) {
-            if (w == warp) QA = PA, QR = PR;
-            const float2 fa = *reinterpret_cast<const float2*>(&sums[buf][w][lane]);
-            PR = fma2(fa, PR, rsums[buf][w][lane]), PA = mul2(PA, fa);
-        }
-        if (K == 1) {
-            c = carry;
-            carry = fma2(PA, carry, PR);
-        } else {
-            if (warp < K) store_remote(&parts[buf][rank][lane], warp, make_float4(PA.x, PA.y, PR.x, PR.y));
-            cluster_sync();
-            for (int q = 0; q < K; ++q) {
-                if (q == rank) c = carry;
-                const float4 v = parts[buf][q][lane];
-                carry = fma2(make_float2(v.x, v.y), carry, make_float2(v.z, v.w));
+            for (int w = 0; w < kGroups - 1; ++w)
+                if (w < group) {
+                    const float4 v = sums[buf][w][lane];
+                    h = fma2(make_float2(v.x, v.y), h, make_float2(v.z, v.w));
+                }
+            // the gradient that comes back to its last one, and the one that leaves the tile
+            float2 c = carry;
+            if constexpr (CLUSTER) {
+                PA = f2(1.f), PR = f2(0.f);
+#pragma unroll
+                for (int w = kGroups - 1; w >= 0; --w) {
+                    const float4 v = rsums[buf][w][lane];
+                    const float2 fa = make_float2(v.x, v.y);
+                    PR = fma2(fa, PR, make_float2(v.z, v.w)), PA = mul2(PA, fa);
+                }
+                if (group < K) store_remote(&parts[buf][rank][lane], group, make_float4(PA.x, PA.y, PR.x, PR.y));
+                cluster_sync();
+                for (int q = 0; q < K; ++q) {
+                    if (q == rank) c = carry;
+                    const float4 v = parts[buf][q][lane];
+                    carry = fma2(make_float2(v.x, v.y), carry, make_float2(v.z, v.w));
+                }
+#pragma unroll
+                for (int w = kGroups - 1; w > 0; --w)
+                    if (w > group) {
+                        const float4 v = rsums[buf][w][lane];
+                        c = fma2(make_float2(v.x, v.y), c, make_float2(v.z, v.w));
+                    }
+            } else {
+#pragma unroll
+                for (int w = kGroups - 1; w >= 0; --w) {
+                    if (w == group) c = carry;
+                    const float4 v = rsums[buf][w][lane];
+                    carry = fma2(make_float2(v.x, v.y), carry, make_float2(v.z, v.w));
+                }
             }
-        }
-        c = fma2(QA, c, QR);
-        buf ^= 1;
+            buf ^= 1;
 
-        float2 hp[kTok];  // the state before each token
+            Rows1<T, kOdd> ox, orr, oi, oz;
+            if (GATED) oz.start(a.dz, b * L, a.dz_stride, c0, t, lane, 1);
+            ox.start(a.dx, b * L, a.dx_stride, c0, t + kTok - 1, lane, -1);
+            orr.start(a.dr, b * L, a.dr_stride, c0, t + kTok - 1, lane, -1);
+            oi.start(a.di, b * L, a.di_stride, c0, t + kTok - 1, lane, -1);
+            float2 e8 = f2(0.f);
+            auto tokens = [&](auto all) {
+                constexpr bool kAll = decltype(all)::value;
 #pragma unroll
-        for (int k = 0; k < kTok; ++k) {
-            hp[k] = h;
-            h = fma2(f[k], h, mul2(s[k], P::get(px[k * 32])));
-            if (GATED) {
-                const float2 dzc = sizeof(T) == 2 ? dzs[k * kThreads] : *reinterpret_cast<const float2*>(pz + k * 32);
-                if (k < live) store<T, kOdd>(dz + (t + k) * a.dz_stride, mul2(dzc, h), lane, have);
-            }
-        }
-        float2 e8 = f2(0.f);
+                for (int k = 0; k < kTok; ++k) {
+                    const float2 last = h;
+                    h = fma2(f[k], h, u[k]);
+                    u[k] = last;
+                    if (GATED) oz.template put<kAll>(mul2(take(pz, 2, k), h), lane, have, k < live);
+                }
 #pragma unroll
-        for (int k = kTok - 1; k >= 0; --k) {
-            float2 dh = GATED ? unstash(pd + k * 32, pz + k * 32) : P::get(pd[k * 32]);
-            if (k >= live) dh = f2(0.f);
-            dh = add2(dh, c);
-            const float2 sr = unstash(pr + k * 32, pi + k * 32);
-            const float2 e = mul2(dh, fma2(mul2(mul2(A, sr), f[k]), hp[k], c2[k]));
-            e8 = add2(e8, e);
-            const float2 gx = mul2(dh, s[k]);
-            c = mul2(f[k], dh);
-            if (k < live) {
-                store<T, kOdd>(dx + (t + k) * a.dx_stride, gx, lane, have);
-                store<T, kOdd>(dr + (t + k) * a.dr_stride, mul2(e, fma2(sr, f2(-1.f), f2(1.f))), lane, have);
-                store<T, kOdd>(di + (t + k) * a.di_stride, mul2(mul2(gx, P::get(px[k * 32])), oi[k]), lane, have);
-            }
+                for (int k = kTok - 1; k >= 0; --k) {
+                    float2 dh = GATED ? unstash(pd + k * 32, pz + k * 32) : P::get(pd[k * 32]);
+                    if (!kAll && k >= live) dh = f2(0.f);
+                    dh = add2(dh, c);
+                    const float2 sr = unstash(pr + k * 32, pi + k * 32);
+                    const float2 e = mul2(mul2(dh, mul2(mul2(A, sr), f[k])), fma2(take(pi, 1, k), f2(-1.f), u[k]));
+                    e8 = add2(e8, e);
+                    c = mul2(f[k], dh);
+                    ox.template put<kAll>(mul2(dh, s[k]), lane, have, k < live);
+                    orr.template put<kAll>(fma2(mul2(e, f2(-1.f)), sr, e), lane, have, k < live);
+                    oi.template put<kAll>(mul2(dh, take(px, 0, k)), lane, have, k < live);
+                }
+            };
+            if (live == kTok && have == kStrip) tokens(std::true_type{});
+            else tokens(std::false_type{});
+            total = add2(total, e8);
+            __syncwarp();  // the places have been read
+            ahead(stage);
+            if (++stage == S) stage = 0;
         }
-        total = add2(total, e8);
-        __syncwarp();  // the places have been read
-        ahead(j + S, stage);
-        if (++stage == S) stage = 0;
-    }
+    };
+    if (__syncthreads_and(A.x >= -1.f && A.y >= -1.f)) walk(std::false_type{});
+    else walk(std::true_type{});
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (rank == 0 && warp == 0 && a.dinit) store<float, true>(a.dinit + b * a.channels + c0, carry, lane, have);
-    for (int64_t t = n + rank * kWarps + warp; t < L; t += K * kWarps) {
+    if (rank == 0 && group == 0 && a.dinit) store<float, true>(a.dinit + b * a.channels + c0, carry, lane, have);
+    for (int64_t t = n + rank * kGroups + group; t < L; t += K * kGroups) {
         store<T, kOdd>(dx + t * a.dx_stride, f2(0.f), lane, have);
         store<T, kOdd>(dr + t * a.dr_stride, f2(0.f), lane, have);
         store<T, kOdd>(di + t * a.di_stride, f2(0.f), lane, have);
         if (GATED) store<T, kOdd>(dz + t * a.dz_stride, f2(0.f), lane, have);
     }
     __syncthreads();
-    rsums[0][warp][lane] = total;
+    float2* part = reinterpret_cast<float2*>(smem) + lane;
+    part[group * LANES] = total;
     __syncthreads();
-    if (warp == 0) {
+    if (group == 0) {
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) total = add2(total, rsums[0][w][lane]);
+        for (int w = 1; w < kGroups; ++w) total = add2(total, part[w * LANES]);
         store<float, true>(a.partials + (b * K + rank) * a.channels + c0, total, lane, have);
     }
 }
 
-int64_t strips_of(int64_t channels) { return (channels + kStrip - 1) / kStrip; }
+int64_t strips_of(int64_t channels) { return (channels + 2 * kLanes - 1) / (2 * kLanes); }
 
 template <typename T, Rows ROWS, bool GATED>
 cudaError_t launch(const GlrBwdArgs& a, cudaStream_t st) {
-    constexpr int bytes = smem_bytes<T, GATED>();
     const int64_t strips = strips_of(a.channels);
-    const int K = glr_cluster(strips * a.batch, (a.seqlen + kTile - 1) / kTile);
-    const cudaError_t e = launch_strips(k_glr_bwd<T, ROWS, GATED>, a, strips, K, bytes, st);
+    const int K = glr_cluster(strips * a.batch, (a.seqlen + kTile - 1) / kTile, kPerSm);
+    const cudaError_t e = launch_strips(
+        K > 1 ? k_glr_bwd<T, ROWS, GATED, kLanes, true> : k_glr_bwd<T, ROWS, GATED, kLanes, false>, a, strips, K,
+        kGroups * kLanes, smem_bytes<T, GATED, kLanes>(K > 1), st);
     if (e != cudaSuccess) return e;
     return launch_sum_rows(a.partials, a.batch * K, {a.dA, a.channels}, {}, {}, a.A, st);
 }
@@ -232,7 +283,7 @@ cudaError_t launch_t(const GlrBwdArgs& a, cudaStream_t st) {
 }  // namespace
 
 int64_t glr_bwd_partials(int64_t batch, int64_t seqlen, int64_t channels) {
-    return batch * glr_cluster(strips_of(channels) * batch, (seqlen + kTile - 1) / kTile);
+    return batch * glr_cluster(strips_of(channels) * batch, (seqlen + kTile - 1) / kTile, kPerSm);
 }
 
 cudaError_t launch_glr_bwd(const GlrBwdArgs& a, bool bf16, cudaStream_t st) {

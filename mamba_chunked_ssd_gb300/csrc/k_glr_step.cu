@@ -29,8 +29,8 @@ __global__ void __launch_bounds__(kBlock) k_glr_step(const GlrArgs a) {
     const float2 A = load_pair(a.A + c, 0, have);
     float2 h = a.init ? load_pair(a.init + b * a.channels + c, 0, have) : f2(0.f);
     float2 f, m;
-    decay2(mul2(A, sigmoid2(r)), f, m);
-    h = fma2(f, h, mul2(mul2(mul2(m, rsqrt2(m)), sigmoid2(i)), x));
+    decay2<true>(mul2(A, sigmoid2(r)), f, m);
+    h = fma2(f, h, mul2(mul2(sqrt2(m), sigmoid2(i)), x));
     store<float, true>(a.final_state + b * a.channels + c, h, 0, have);
     if (GATED) {
         const float2 z = pair(a.z, a.z_stride);
