@@ -780,8 +780,10 @@ def mamba2_block_norm_bwd(dresidual_out, dy, x, residual_out=None, z=None, post_
                              f"not {t.dtype} {tuple(t.shape)} on {t.device}")
     dx = _like(x, dx, "dx", stream)
     dz = None if z is None else _like(x, dz, "dz", stream)
-    weights = [None if w is None else _new((C,), torch.float32, x.device, stream)
-               for w in (post_weight, scale, pre_weight)]
+    given = [w is not None for w in (post_weight, scale, pre_weight)]
+    new = iter(_new((sum(given), C), torch.float32, x.device, stream).unbind(0) if any(given) and C % 4 == 0 else
+               [_new((C,), torch.float32, x.device, stream) for g in given if g])
+    weights = [next(new) if g else None for g in given]
     code = MAMBA2_BF16 if known == torch.bfloat16 else MAMBA2_F32 if known == torch.float32 else -1
     shape = _block_norm_shape(x.numel() // C if C else 0, C, _rows(x, "x", 1), _strides(z, "z"), 0,
                               _strides(residual_out, "residual_out"), _strides(dy, "dy"), float(eps), _dtype_code(x),

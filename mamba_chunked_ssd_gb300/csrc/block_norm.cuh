@@ -1,12 +1,18 @@
-// block_norm.cuh — what the block norm's forward and backward kernels share: sums over a
-// row whose channels lie with the threads of a warp, of a block or of a cluster's blocks,
-// and rows on their way to the thread that reads them.
+// block_norm.cuh — what the block norm's forward and backward kernels share: how rows come
+// to the threads that keep them, and sums over a row whose channels lie with a block's
+// threads or with those of a cluster's blocks.
 #pragma once
 
 #include "glr_math.cuh"
 
 namespace m2 {
 namespace bnorm {
+
+using glr::add2;
+using glr::f2;
+using glr::fma2;
+using glr::mul2;
+using glr::sigmoid2;
 
 constexpr int kPer = 8;  // channels of a thread
 
@@ -20,26 +26,25 @@ struct Plan {
     int Q, threads;
     int64_t walkers;
 };
-// `resident`: threads of an SM at once.
-inline Plan plan_of(int64_t rows, int64_t channels, int resident) {
+// `most`: threads of a block; `resident`: threads of an SM at once.
+inline Plan plan_of(int64_t rows, int64_t channels, int most, int resident) {
     Plan p = {1, 32, 1};
-    while (p.Q * 512 * kPer < channels) p.Q *= 2;
-    while (p.threads < 512 && p.threads * kPer < channels) p.threads *= 2;
+    while (p.Q * (int64_t)most * kPer < channels) p.Q *= 2;
+    p.threads = (int)((share_of(channels, p.Q) / kPer + 31) / 32 * 32);
     const int sms = sm_count();
     int64_t per_sm = resident / p.threads;
-    if (per_sm > 32) per_sm = 32;
+    per_sm = per_sm < 1 ? 1 : per_sm > 32 ? 32 : per_sm;
     const int64_t fit = per_sm * (int64_t)(sms > 0 ? sms : 152) / p.Q;
     p.walkers = imin64(rows, fit < 1 ? 1 : fit);
     return p;
 }
 template <typename Args>
-cudaError_t launch_rows(void (*kernel)(Args, int), const Args& a, const Plan& p, int threads, int bytes,
-                        cudaStream_t st) {
+cudaError_t launch_rows(void (*kernel)(Args, int), const Args& a, const Plan& p, int bytes, cudaStream_t st) {
     const cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kernel), bytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.walkers * p.Q));
-    cfg.blockDim = dim3((unsigned)threads);
+    cfg.blockDim = dim3((unsigned)p.threads);
     cfg.dynamicSmemBytes = (size_t)bytes;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -56,109 +61,235 @@ cudaError_t launch_rows(void (*kernel)(Args, int), const Args& a, const Plan& p,
 // writes a place has met, since it was read, at the barrier of the sum between.
 template <int N>
 struct Sums {
-    float warp[2][32][N];
+    float warp[2][N][32];
     float block[2][8][N];
 };
 
-// Sums of N values over TPG threads (a warp, or a block, which then is all of its threads)
-// and over the Q blocks of a cluster, in a fixed order.
-template <int TPG, int N>
-__device__ __forceinline__ void group_sums(float (&v)[N], Sums<N>& s, int& turn, int Q, int rank) {
+// The sum over a cluster's blocks of values that all threads of a block have.
+template <int N>
+__device__ __forceinline__ void cluster_sums(float (&v)[N], Sums<N>& s, int turn, int Q, int rank) {
+    if (threadIdx.x < Q) {
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1)
+        for (int k = 0; k < N; ++k) {
+            uint32_t at;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                         : "=r"(at)
+                         : "r"(tc::smem_u32(&s.block[turn][rank][k])), "r"(threadIdx.x));
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v[k]) : "memory");
+        }
+    }
+    glr::cluster_sync();
 #pragma unroll
-        for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], m);
-    if constexpr (TPG > 32) {
-        constexpr int warps = TPG / 32;
+    for (int k = 0; k < N; ++k) {
+        v[k] = 0.f;
+        for (int q = 0; q < Q; ++q) v[k] += s.block[turn][q][k];
+    }
+}
+
+// A value's sum over a block's threads and over the Q blocks of a cluster, in a fixed order.
+__device__ __forceinline__ void group_sums(float (&v)[1], Sums<1>& s, int& turn, int Q, int rank) {
+    float x = v[0];
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+    const int warps = blockDim.x / 32, lane = threadIdx.x & 31;
+    if (warps > 1 || Q > 1) {
         turn ^= 1;
-        const int lane = threadIdx.x & 31;
-        if (lane == 0) {
-#pragma unroll
-            for (int k = 0; k < N; ++k) s.warp[turn][threadIdx.x >> 5][k] = v[k];
-        }
+        if (lane == 0) s.warp[turn][0][threadIdx.x >> 5] = x;
         __syncthreads();
+        x = lane < warps ? s.warp[turn][0][lane] : 0.f;
 #pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = s.warp[turn][lane & (warps - 1)][k];
+        for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+    }
+    v[0] = x;
+    if (Q > 1) cluster_sums(v, s, turn, Q, rank);
+}
+// Three at once (and a fourth that is 0): half of the lanes go on with two of them, a quarter with each.
+// Blocks of up to 16 warps.
+__device__ __forceinline__ void group_sums(float (&v)[3], Sums<3>& s, int& turn, int Q, int rank) {
+    const int lane = threadIdx.x & 31, warps = blockDim.x / 32;
+    const bool high = lane & 16, odd = lane & 8;
+    float a = (high ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, high ? v[0] : v[2], 16);
+    const float b = (high ? 0.f : v[1]) + __shfl_xor_sync(0xffffffffu, high ? v[1] : 0.f, 16);
+    a = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);  // lanes 8 k .. 8 k + 7: value k
 #pragma unroll
-        for (int m = warps / 2; m > 0; m >>= 1)
+    for (int m = 4; m > 0; m >>= 1) a += __shfl_xor_sync(0xffffffffu, a, m);
+    if (warps > 1 || Q > 1) {
+        turn ^= 1;
+        const int k = lane >> 3, w = lane & 7;
+        if (w == 0 && k < 3) s.warp[turn][k][threadIdx.x >> 5] = a;
+        __syncthreads();
+        const float* from = s.warp[turn][k < 3 ? k : 2];
+        a = (w < warps ? from[w] : 0.f) + (w + 8 < warps ? from[w + 8] : 0.f);
 #pragma unroll
-            for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], m);
-        if (Q > 1) {
-            if (threadIdx.x < Q) {
+        for (int m = 4; m > 0; m >>= 1) a += __shfl_xor_sync(0xffffffffu, a, m);
+    }
 #pragma unroll
-                for (int k = 0; k < N; ++k) {
-                    uint32_t at;
-                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                                 : "=r"(at)
-                                 : "r"(tc::smem_u32(&s.block[turn][rank][k])), "r"(threadIdx.x));
-                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v[k]) : "memory");
-                }
+    for (int k = 0; k < 3; ++k) v[k] = __shfl_sync(0xffffffffu, a, 8 * k);
+    if (Q > 1) cluster_sums(v, s, turn, Q, rank);
+}
+
+// How a thread's eight channels lie: in groups of GRP neighbouring ones, group i the (threadIdx + i blockDim)-th
+// of the block's.  GRP > 1: rows start on a group's bytes and have whole groups, and a thread copies what it
+// reads itself.  GRP = 1: rows lie in shared memory as they do in memory, from the 16-byte boundary
+// before their start; the threads' copies of 16 bytes (of single elements at a row's ends) are there for all
+// after a barrier.  (16384 x 2050 in bf16, gated, backward: groups of two 267 us, as whole rows 308.)
+template <int GRP>
+__device__ __forceinline__ int channel(int i) {
+    return GRP * ((int)threadIdx.x + i / GRP * (int)blockDim.x) + i % GRP;
+}
+
+template <int BYTES>
+struct Word;
+template <>
+struct Word<16> { using type = uint4; };
+template <>
+struct Word<8> { using type = uint2; };
+template <>
+struct Word<4> { using type = uint32_t; };
+template <>
+struct Word<2> { using type = uint16_t; };
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
+    if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES) : "memory");
+}
+
+// A walker's rows of one input.
+template <typename E, int GRP>
+struct RowIn {
+    static constexpr int kGroups = kPer / GRP, kBytes = GRP * (int)sizeof(E);
+    static constexpr bool kOwn = GRP > 1;
+    using Unit = typename Word<kBytes>::type;
+    const E* next;  // kOwn: this thread's first channel of the row that is fetched next; else the block's first
+    // an element at a row's end that is too small for an asynchronous copy, on its way to its place
+    Unit* edge_to;
+    Unit edge;
+
+    static __host__ __device__ __forceinline__ int place_bytes(int threads) {
+        return threads * kPer * (int)sizeof(E) + (kOwn ? 0 : 32);
+    }
+    __device__ __forceinline__ void start(const void* base, int64_t row, int64_t stride, int64_t c0) {
+        next = static_cast<const E*>(base) + row * stride + c0 + (kOwn ? GRP * (int)threadIdx.x : 0);
+        edge_to = nullptr;
+    }
+    // zeros in the places of channels that are not there, which are never written again
+    static __device__ __forceinline__ void clear(uint8_t* place, int n) {
+        if constexpr (kOwn) {
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i)
+                if (channel<GRP>(i * GRP) >= n)
+                    *reinterpret_cast<Unit*>(place + (i * blockDim.x + threadIdx.x) * kBytes) = {};
+        }
+    }
+    __device__ __forceinline__ void fetch(uint8_t* place, int n, int64_t step) {
+        const int tid = threadIdx.x;
+        if constexpr (kOwn) {
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i)
+                if (channel<GRP>(i * GRP) < n)
+                    copy_async<kBytes>(tc::smem_u32(place + (i * blockDim.x + tid) * kBytes), next + i * GRP * (int)blockDim.x);
+        } else {
+            // the row's first elements up to the boundary, whole pieces of 16 bytes, the last elements
+            constexpr int per = 16 / (int)sizeof(E);
+            const int skip = (int)(reinterpret_cast<uintptr_t>(next) & 15);
+            const int head = min(((16 - skip) & 15) / (int)sizeof(E), n), whole = (n - head) / per, tail = head + whole * per;
+            E* to = reinterpret_cast<E*>(place + skip);
+            for (int k = tid; k < whole; k += blockDim.x) copy_async<16>(tc::smem_u32(to + head + k * per), next + head + k * per);
+            const int end = tid < per ? tid : tail + tid - per;  // this thread's element at an end
+            if (tid < per ? tid < head : tid < 2 * per && end < n) {
+                if constexpr (sizeof(E) == 4) copy_async<4>(tc::smem_u32(to + end), next + end);
+                else edge = reinterpret_cast<const Unit*>(next)[end], edge_to = reinterpret_cast<Unit*>(to + end);
             }
-            glr::cluster_sync();
+        }
+        next += step;
+    }
+    // before a barrier that comes before the row's use
+    __device__ __forceinline__ void finish() {
+        if constexpr (kBytes < 4) {
+            if (edge_to) *edge_to = edge;
+            edge_to = nullptr;
+        }
+    }
+    // `row`: the row's first channel in memory (but kOwn); zeros where there is no channel
+    static __device__ __forceinline__ void read(const uint8_t* place, const E* row, int n, float2 (&f)[4]) {
+        if constexpr (kOwn) {
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-                v[k] = 0.f;
-                for (int q = 0; q < Q; ++q) v[k] += s.block[turn][q][k];
+            for (int i = 0; i < kGroups; ++i) {
+                const Unit v = *reinterpret_cast<const Unit*>(place + (i * blockDim.x + threadIdx.x) * kBytes);
+                const auto* p = reinterpret_cast<const typename glr::Pair<E>::raw*>(&v);
+#pragma unroll
+                for (int k = 0; k < GRP / 2; ++k) f[i * GRP / 2 + k] = glr::Pair<E>::get(p[k]);
+            }
+        } else {
+            const E* from = reinterpret_cast<const E*>(place + (reinterpret_cast<uintptr_t>(row) & 15));
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int c = channel<GRP>(i);
+                const float v = c < n ? to_f32(from[c]) : 0.f;
+                if (i % 2) f[i / 2].y = v;
+                else f[i / 2].x = v;
             }
         }
     }
-}
-
-// N elements that start on their own size (up to 16 bytes: their pieces' size) as fp32, and back.
-template <typename R, int N>
-struct Piece {
-    static constexpr int kPer = 16 / sizeof(R) < N ? 16 / (int)sizeof(R) : N;
-    typename VecOf<R, kPer>::type v[N / kPer];
 };
-template <typename R, int N>
-__device__ __forceinline__ void load_piece(Piece<R, N>& p, const R* from) {
+
+// A walker's rows of one output.
+template <typename E, int GRP>
+struct RowOut {
+    E* next;  // as RowIn's
+    __device__ __forceinline__ void start(void* base, int64_t row, int64_t stride, int64_t c0) {
+        next = static_cast<E*>(base) + row * stride + c0 + (GRP > 1 ? GRP * (int)threadIdx.x : 0);
+    }
+    __device__ __forceinline__ void write(int n, const float2 (&f)[4], int64_t step) {
+        if constexpr (GRP > 1) {
 #pragma unroll
-    for (int k = 0; k < N / Piece<R, N>::kPer; ++k)
-        p.v[k] = reinterpret_cast<const typename VecOf<R, Piece<R, N>::kPer>::type*>(from)[k];
-}
-template <typename R, int N>
-__device__ __forceinline__ void widen(const Piece<R, N>& p, float (&f)[N]) {
-    constexpr int per = Piece<R, N>::kPer;
+            for (int i = 0; i < kPer / GRP; ++i) {
+                typename Word<GRP * sizeof(E)>::type v;
+                auto* p = reinterpret_cast<typename glr::Pair<E>::raw*>(&v);
 #pragma unroll
-    for (int k = 0; k < N / per; ++k) {
-        float g[per];
-        unpack<per>(p.v[k], g, (const R*)nullptr);
+                for (int k = 0; k < GRP / 2; ++k) p[k] = glr::Pair<E>::put(f[i * GRP / 2 + k]);
+                if (channel<GRP>(i * GRP) < n) *reinterpret_cast<decltype(v)*>(next + i * GRP * (int)blockDim.x) = v;
+            }
+        } else {
 #pragma unroll
-        for (int e = 0; e < per; ++e) f[k * per + e] = g[e];
+            for (int i = 0; i < kPer; ++i) {
+                const int c = channel<GRP>(i);
+                if (c < n) next[c] = from_f32<E>(i % 2 ? f[i / 2].y : f[i / 2].x);
+            }
+        }
+        next += step;
+    }
+};
+
+// A thread's values of a row of fp32 weights (`none` without one), and its sums to such a row.
+template <int GRP>
+__device__ __forceinline__ void load_weight(const float* w, int n, float none, float2 (&f)[4]) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int c = channel<GRP>(i);
+        const float v = w && c < n ? w[c] : none;
+        if (i % 2) f[i / 2].y = v;
+        else f[i / 2].x = v;
     }
 }
-template <typename R, int N>
-__device__ __forceinline__ void store_piece(R* to, const float (&f)[N]) {
-    constexpr int per = Piece<R, N>::kPer;
+template <int GRP>
+__device__ __forceinline__ void store_weight(float* w, int n, const float2 (&f)[4]) {
 #pragma unroll
-    for (int k = 0; k < N / per; ++k) {
-        float g[per];
-#pragma unroll
-        for (int e = 0; e < per; ++e) g[e] = f[k * per + e];
-        reinterpret_cast<typename VecOf<R, per>::type*>(to)[k] = pack<R, per>(g);
+    for (int i = 0; i < kPer; ++i) {
+        const int c = channel<GRP>(i);
+        if (c < n) w[c] = i % 2 ? f[i / 2].y : f[i / 2].x;
     }
 }
 
-// An aligned piece into shared memory, waited for with its group.
-template <typename R, int N>
-__device__ __forceinline__ void copy_piece(Piece<R, N>* to, const R* from) {
-    constexpr int bytes = sizeof(Piece<R, N>) < 16 ? (int)sizeof(Piece<R, N>) : 16;
-#pragma unroll
-    for (int k = 0; k < (int)sizeof(Piece<R, N>) / bytes; ++k) {
-        const uint32_t dst = tc::smem_u32(reinterpret_cast<uint8_t*>(to) + k * bytes);
-        const uint8_t* src = reinterpret_cast<const uint8_t*>(from) + k * bytes;
-        if constexpr (bytes == 16)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-        else
-            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(bytes) : "memory");
-    }
-}
+__device__ __forceinline__ float sum_of(const float2& v) { return v.x + v.y; }
 
-// sigmoid of a gate: the hardware's exponential and reciprocal for bf16, exact functions else.
-template <typename T>
-__device__ __forceinline__ float sigmoid(float z) {
-    if (sizeof(T) == 2) return rcp_approx(1.f + ex2_approx(-kLog2e * z));
-    return 1.f / (1.f + expf(-z));
+// The widest groups that a call's rows allow: `t` and `r`, all addresses and strides in bytes of the two dtypes' tensors
+// or-ed together.  Eight channels only where both are bf16 (16 bytes of fp32 are four).
+inline int group_of(uint64_t t, uint64_t r, int64_t channels, int t_bytes, int r_bytes) {
+    for (int g = t_bytes == 2 && r_bytes == 2 ? 8 : 4; g > 1; g /= 2)
+        if (channels % g == 0 && t % (uint64_t)(g * t_bytes) == 0 && r % (uint64_t)(g * r_bytes) == 0) return g;
+    return 1;
 }
 
 }  // namespace bnorm

@@ -4,8 +4,10 @@
 //
 // Bound by memory: x, z and res are read once, out and y are written once.  A thread has eight
 // channels, which it keeps while it walks down the rows, so that the weights stay in its
-// registers, where the row stays for both sums; rows of more than 4096 channels are split
-// between the blocks of a cluster.  Rows come through shared memory, two ahead.
+// registers, where the row stays for both sums; rows of more than 8192 channels are split
+// between the blocks of a cluster.  Rows come through shared memory, one ahead.  The two sums a row and 37
+// instructions an element bound it next to memory: 32768 x 4096 in bf16, gated, 221 us, 6.1 TB/s; 65536 x 1024 124 us, 5.4;
+// 8192 x 4096 with an fp32 residual 76 us, 5.3.
 #include "block_norm.cuh"
 
 namespace m2 {
@@ -13,157 +15,137 @@ namespace {
 
 using namespace bnorm;
 
-constexpr int kRing = 3;
+// Rows under way (32768 x 4096 in bf16, gated: two 226 us, three or four 235; in fp32 two are 196 KB for blocks of
+// 1024 threads).
+template <typename T>
+constexpr int ring_rows() { return 2; }
+constexpr int kMost = 1024;  // threads of a block, and of an SM (64 registers each)
 
-template <typename T, typename R, int VEC, int TPG>
-__global__ void __launch_bounds__(TPG, 1024 / TPG) k_block_norm(const BlockNormArgs a, int Q) {
-    constexpr int NV = kPer / VEC;
-    constexpr bool kUseRing = VEC > 1;
-    using PT = Piece<T, VEC>;
-    using PR = Piece<R, VEC>;
+template <typename T, typename R, int GRP, bool GATED>
+__global__ void __launch_bounds__(kMost, 1) k_block_norm(const BlockNormArgs a, int Q) {
+    constexpr int kRing = ring_rows<T>();
+    using InT = RowIn<T, GRP>;
+    using InR = RowIn<R, GRP>;
     __shared__ Sums<1> smem;
     int turn = 0;
     extern __shared__ __align__(16) uint8_t ring[];
     const int rank = Q > 1 ? (int)glr::cluster_rank() : 0;
-    const int64_t walker = blockIdx.x / Q, walkers = gridDim.x / Q;
-    const int64_t share = share_of(a.channels, Q), cb = rank * share;  // this block's channels
-    const int nvec = (int)((imin64(a.channels - cb, share) + VEC - 1) / VEC);
-    const T* x = static_cast<const T*>(a.x) + cb;
-    const T* z = a.z ? static_cast<const T*>(a.z) + cb : nullptr;
-    const R* res = a.res ? static_cast<const R*>(a.res) + cb : nullptr;
-    R* out = static_cast<R*>(a.out) + cb;
-    T* y = a.pre ? static_cast<T*>(a.y) + cb : nullptr;
-    const float count = (float)a.channels;
+    const uint32_t rows = (uint32_t)a.rows, walker = blockIdx.x / Q, walkers = gridDim.x / Q;  // (rows < 2^31)
+    const int64_t c0 = rank * share_of(a.channels, Q);
+    const int n = (int)imin64(a.channels - c0, share_of(a.channels, Q));  // this block's channels
+    const int bx = InT::place_bytes(blockDim.x), at_res = GATED ? 2 * bx : bx;
+    const int per_row = at_res + (a.res ? InR::place_bytes(blockDim.x) : 0);
+    const float inv = 1.f / (float)a.channels;
 
-    float w1[NV][VEC], w2[NV][VEC];
+    float2 w1[4], w2[4], sc[4];
+    load_weight<GRP>(a.post_weight ? a.post_weight + c0 : nullptr, n, 1.f, w1);
+    load_weight<GRP>(a.scale ? a.scale + c0 : nullptr, n, 1.f, sc);
+    load_weight<GRP>(a.pre_weight ? a.pre_weight + c0 : nullptr, n, 1.f, w2);
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const int j = threadIdx.x + i * TPG;
-            const int64_t c = cb + (int64_t)j * VEC + e;
-            w1[i][e] = (a.post_weight && j < nvec ? a.post_weight[c] : 1.f) * (a.scale && j < nvec ? a.scale[c] : 1.f);
-            w2[i][e] = a.pre_weight && j < nvec ? a.pre_weight[c] : 1.f;
-        }
+    for (int i = 0; i < 4; ++i) w1[i] = mul2(w1[i], sc[i]);
 
-    // a thread's places of a stage: its pieces of x, z and res
-    auto place = [&](int stage, int i) {
-        return ring + (stage * NV + i) * TPG * (int)(2 * sizeof(PT) + sizeof(PR));
-    };
-    auto ahead = [&](int64_t row, int stage) {
-        if constexpr (kUseRing) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int j = threadIdx.x + i * TPG;
-                if (row < a.rows && j < nvec) {
-                    const int64_t c = (int64_t)j * VEC;
-                    PT* p = reinterpret_cast<PT*>(place(stage, i));
-                    copy_piece(p + threadIdx.x, x + row * a.x_stride + c);
-                    if (z) copy_piece(p + TPG + threadIdx.x, z + row * a.z_stride + c);
-                    if (res) copy_piece(reinterpret_cast<PR*>(p + 2 * TPG) + threadIdx.x, res + row * a.res_stride + c);
-                }
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
+    InT x, z;
+    InR res;
+    z.edge_to = nullptr, res.edge_to = nullptr;
+    x.start(a.x, walker, a.x_stride, c0);
+    if (GATED) z.start(a.z, walker, a.z_stride, c0);
+    if (a.res) res.start(a.res, walker, a.res_stride, c0);
+    const int64_t sx = walkers * a.x_stride, sz = walkers * a.z_stride, sr = walkers * a.res_stride;
+    uint32_t coming = walker;  // the row that is fetched next
+    auto ahead = [&](int stage) {
+        if (coming < rows) {
+            uint8_t* at = ring + stage * per_row;
+            x.fetch(at, n, sx);
+            if (GATED) z.fetch(at + bx, n, sz);
+            if (a.res) res.fetch(at + at_res, n, sr);
         }
+        coming += walkers;
+        glr::commit();
     };
+    for (int k = 0; k < kRing; ++k) {
+        uint8_t* at = ring + k * per_row;
+        InT::clear(at, n);
+        if (GATED) InT::clear(at + bx, n);
+        if (a.res) InR::clear(at + at_res, n);
+    }
     if (Q > 1) glr::cluster_sync();  // the others' shared memory is there
-    for (int k = 0; k < kRing; ++k) ahead(walker + k * walkers, k);
+    auto finish = [&] { x.finish(), z.finish(), res.finish(); };
+    for (int k = 0; k < kRing; ++k) ahead(k), finish();
+    RowOut<R, GRP> out;
+    RowOut<T, GRP> y;
+    out.start(a.out, walker, a.out_stride, c0);
+    if (a.pre) y.start(a.y, walker, a.y_stride, c0);
+    const int64_t so = walkers * a.out_stride, sy = walkers * a.y_stride;
     int stage = 0;
-    for (int64_t row = walker; row < a.rows; row += walkers) {
-        if (kUseRing) asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
-        PT vx[NV], vz[NV];
-        PR vr[NV];
+    for (uint32_t row = walker; row < rows; row += walkers) {
+        glr::wait_for<kRing - 1>();
+        finish();
+        if (!InT::kOwn) __syncthreads();  // the other threads' copies are there too
+        const uint8_t* at = ring + stage * per_row;
+        auto first = [&](auto* base, int64_t stride) { return base + row * stride + c0; };
+        float2 f[4], g[4], v[4];
+        InT::read(at, first(static_cast<const T*>(a.x), a.x_stride), n, f);
+        if (GATED) InT::read(at + bx, first(static_cast<const T*>(a.z), a.z_stride), n, g);
+        if (a.res) {
+            InR::read(at + at_res, first(static_cast<const R*>(a.res), a.res_stride), n, v);
+        } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int j = threadIdx.x + i * TPG;
-            vx[i] = vz[i] = PT{};
-            vr[i] = PR{};
-            if (j >= nvec) continue;
-            if constexpr (kUseRing) {
-                const PT* p = reinterpret_cast<const PT*>(place(stage, i));
-                vx[i] = p[threadIdx.x];
-                if (z) vz[i] = p[TPG + threadIdx.x];
-                if (res) vr[i] = reinterpret_cast<const PR*>(p + 2 * TPG)[threadIdx.x];
-            } else {
-                const int64_t c = (int64_t)j * VEC;
-                load_piece(vx[i], x + row * a.x_stride + c);
-                if (z) load_piece(vz[i], z + row * a.z_stride + c);
-                if (res) load_piece(vr[i], res + row * a.res_stride + c);
-            }
+            for (int i = 0; i < 4; ++i) v[i] = f2(0.f);
         }
-        ahead(row + kRing * walkers, stage);
+        if (!InT::kOwn) __syncthreads();  // (the place is read)
+        ahead(stage);
         if (++stage == kRing) stage = 0;
         float k1 = 1.f;
         if (a.post) {
-            float ss[1] = {0.f};
+            float2 s = f2(0.f);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                float f[VEC];
-                widen(vx[i], f);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) ss[0] = fmaf(f[e], f[e], ss[0]);
-            }
-            group_sums<TPG, 1>(ss, smem, turn, Q, rank);
-            k1 = rsqrtf(ss[0] / count + a.eps);
+            for (int i = 0; i < 4; ++i) s = fma2(f[i], f[i], s);
+            float ss[1] = {sum_of(s)};
+            group_sums(ss, smem, turn, Q, rank);
+            k1 = rsqrtf(fmaf(ss[0], inv, a.eps));
         }
-        float v[NV][VEC], ss[1] = {0.f};
+        float2 s = f2(0.f);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int j = threadIdx.x + i * TPG;
-            float f[VEC], g[VEC];
-            widen(vx[i], f), widen(vz[i], g), widen(vr[i], v[i]);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                float p = f[e] * k1 * w1[i][e];
-                if (z) p *= g[e] * sigmoid<T>(g[e]);
-                v[i][e] += p;
-                ss[0] = fmaf(v[i][e], v[i][e], ss[0]);  // (0 where there is no channel)
-            }
-            if (j < nvec) store_piece(out + row * a.out_stride + (int64_t)j * VEC, v[i]);
+        for (int i = 0; i < 4; ++i) {
+            float2 p = mul2(mul2(f[i], f2(k1)), w1[i]);
+            if (GATED) p = mul2(mul2(p, g[i]), sigmoid2(g[i]));
+            v[i] = add2(v[i], p);
+            s = fma2(v[i], v[i], s);  // (0 where there is no channel)
         }
+        out.write(n, v, so);
         if (a.pre) {
-            group_sums<TPG, 1>(ss, smem, turn, Q, rank);
-            const float k2 = rsqrtf(ss[0] / count + a.eps);
+            float ss[1] = {sum_of(s)};
+            group_sums(ss, smem, turn, Q, rank);
+            const float k2 = rsqrtf(fmaf(ss[0], inv, a.eps));
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int j = threadIdx.x + i * TPG;
-                if (j >= nvec) continue;
-                float o[VEC];
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) o[e] = v[i][e] * k2 * w2[i][e];
-                store_piece(y + row * a.y_stride + (int64_t)j * VEC, o);
-            }
+            for (int i = 0; i < 4; ++i) v[i] = mul2(mul2(v[i], f2(k2)), w2[i]);
+            y.write(n, v, sy);
         }
     }
-    if (kUseRing) asm volatile("cp.async.wait_all;" ::: "memory");
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-template <typename T, typename R, int VEC, int TPG>
-cudaError_t launch_n(const BlockNormArgs& a, const Plan& p, cudaStream_t st) {
-    const int bytes = VEC > 1 ? kRing * TPG * kPer * (2 * (int)sizeof(T) + (int)sizeof(R)) : 0;
-    return launch_rows(k_block_norm<T, R, VEC, TPG>, a, p, TPG, bytes, st);
-}
-
-template <typename T, typename R, int VEC>
-cudaError_t launch_v(const BlockNormArgs& a, cudaStream_t st) {
-    const Plan p = plan_of(a.rows, a.channels, 1024);
-    switch (p.threads) {
-        case 32: return launch_n<T, R, VEC, 32>(a, p, st);
-        case 64: return launch_n<T, R, VEC, 64>(a, p, st);
-        case 128: return launch_n<T, R, VEC, 128>(a, p, st);
-        case 256: return launch_n<T, R, VEC, 256>(a, p, st);
-        default: return launch_n<T, R, VEC, 512>(a, p, st);
-    }
+template <typename T, typename R, int GRP>
+cudaError_t launch_g(const BlockNormArgs& a, cudaStream_t st) {
+    const Plan p = plan_of(a.rows, a.channels, kMost, kMost);
+    const int bx = RowIn<T, GRP>::place_bytes(p.threads), br = RowIn<R, GRP>::place_bytes(p.threads);
+    const int bytes = ring_rows<T>() * (bx * (a.z ? 2 : 1) + (a.res ? br : 0));
+    return launch_rows(a.z ? k_block_norm<T, R, GRP, true> : k_block_norm<T, R, GRP, false>, a, p, bytes, st);
 }
 
 template <typename T, typename R>
 cudaError_t launch_t(const BlockNormArgs& a, cudaStream_t st) {
-    const uint64_t p = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y) |
-                       reinterpret_cast<uintptr_t>(a.z) | reinterpret_cast<uintptr_t>(a.res) |
-                       reinterpret_cast<uintptr_t>(a.out);
-    const uint64_t s = (uint64_t)((a.x_stride | (a.y ? a.y_stride : 0) | (a.z ? a.z_stride : 0) | a.channels) * sizeof(T)) |
+    const uint64_t t = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.z) |
+                       (uint64_t)((a.x_stride | (a.y ? a.y_stride : 0) | (a.z ? a.z_stride : 0)) * sizeof(T));
+    const uint64_t r = reinterpret_cast<uintptr_t>(a.res) | reinterpret_cast<uintptr_t>(a.out) |
                        (uint64_t)((a.out_stride | (a.res ? a.res_stride : 0)) * sizeof(R));
-    return (p | s) % 16 == 0 ? launch_v<T, R, 16 / sizeof(T)>(a, st) : launch_v<T, R, 1>(a, st);
+    switch (group_of(t, r, a.channels, sizeof(T), sizeof(R))) {
+        case 8:
+            if constexpr (sizeof(R) == 2) return launch_g<T, R, 8>(a, st);
+        case 4: return launch_g<T, R, 4>(a, st);
+        case 2: return launch_g<T, R, 2>(a, st);
+        default: return launch_g<T, R, 1>(a, st);
+    }
 }
 
 }  // namespace

@@ -10,8 +10,12 @@
 // Two sums over a row's threads: x^2, r^2 and w2 dy r together, then w1 q k1 x.
 // A thread has eight channels, which it keeps while it walks down the rows: weights, and the sums
 // over the rows, stay in its registers; the sums of all walkers are added up by a second kernel.  Rows of
-// more than 4096 channels are split between the blocks of a cluster.  Rows come through
-// shared memory, one or two ahead.
+// more than 4096 channels are split between the blocks of a cluster, which wait for one another twice a row.
+// Rows come through shared memory, one or two ahead.  About 65 instructions an element and one block of 512
+// threads to an SM, which waits at two barriers a row, bound it next to memory: 32768 x 4096 in bf16, gated, 392 us, 5.5
+// TB/s; 8192 x 4096 with an fp32 residual 110 us, 5.5 TB/s; 4096 x 8192 218 us, 2.5 TB/s.  (Two rows at a
+// time, for half as many barriers: 581 us, their inputs take the registers; blocks of 256 threads and
+// clusters from 2048 channels on 716.)
 #include "block_norm.cuh"
 
 namespace m2 {
@@ -22,220 +26,181 @@ using namespace bnorm;
 // Rows under way: three, two in fp32 (a ring of 164 KB for blocks of 512 threads).
 template <typename T>
 constexpr int ring_rows() { return sizeof(T) == 2 ? 3 : 2; }
-constexpr int kResident = 512;  // threads of an SM at once
-// Bytes of a thread's places in the ring, a row.
-template <typename T, typename R>
-constexpr int place_bytes() {
-    return kPer * (3 * (int)sizeof(T) + 2 * (int)sizeof(R));
-}
+constexpr int kMost = 512;  // threads of a block, and of an SM (128 registers each)
 
-template <typename T, typename R, int VEC, int TPG>
-__global__ void __launch_bounds__(TPG, kResident / TPG) k_block_norm_bwd(const BlockNormBwdArgs a, int Q) {
-    constexpr int NV = kPer / VEC, kRing = ring_rows<T>();
-    constexpr bool kUseRing = VEC > 1;
+template <typename T, typename R, int GRP, bool GATED>
+__global__ void __launch_bounds__(kMost, 1) k_block_norm_bwd(const BlockNormBwdArgs a, int Q) {
+    constexpr int kRing = ring_rows<T>();
     __shared__ Sums<3> smem3;
     __shared__ Sums<1> smem1;
     int turn3 = 0, turn1 = 0;
     extern __shared__ __align__(16) uint8_t ring[];
     const int rank = Q > 1 ? (int)glr::cluster_rank() : 0;
-    const int64_t walker = blockIdx.x / Q, walkers = gridDim.x / Q;
-    const int64_t share = share_of(a.channels, Q), cb = rank * share;  // this block's channels
-    const int nvec = (int)((imin64(a.channels - cb, share) + VEC - 1) / VEC);
-    const T* x = static_cast<const T*>(a.x) + cb;
-    const T* z = a.z ? static_cast<const T*>(a.z) + cb : nullptr;
-    const T* dy = a.pre ? static_cast<const T*>(a.dy) + cb : nullptr;
-    const R* r = a.pre ? static_cast<const R*>(a.out) + cb : nullptr;
-    const R* dr = a.dout ? static_cast<const R*>(a.dout) + cb : nullptr;
-    T* dx = static_cast<T*>(a.dx) + cb;
-    T* dz = a.z ? static_cast<T*>(a.dz) + cb : nullptr;
-    R* dres = a.dres ? static_cast<R*>(a.dres) + cb : nullptr;
-    const float count = (float)a.channels;
+    using InT = RowIn<T, GRP>;
+    using InR = RowIn<R, GRP>;
+    const uint32_t rows = (uint32_t)a.rows, walker = blockIdx.x / Q, walkers = gridDim.x / Q;  // (rows < 2^31)
+    const int64_t c0 = rank * share_of(a.channels, Q);
+    const int n = (int)imin64(a.channels - c0, share_of(a.channels, Q));  // this block's channels
+    // places of a row: x, [z], [dy, r], [dr]
+    const int bx = InT::place_bytes(blockDim.x), br = InR::place_bytes(blockDim.x);
+    const int at_dy = GATED ? 2 * bx : bx, at_r = at_dy + bx, at_dr = a.pre ? at_r + br : at_dy;
+    const int per_row = at_dr + (a.dout ? br : 0);
+    const float inv = 1.f / (float)a.channels;
 
-    float w1[NV][VEC], w2[NV][VEC], sc[NV][VEC], s1[NV][VEC], s2[NV][VEC], s3[NV][VEC];
+    float2 w1[4], w2[4], sc[4], s1[4], s2[4], s3[4];
+    load_weight<GRP>(a.post_weight ? a.post_weight + c0 : nullptr, n, 1.f, w1);
+    load_weight<GRP>(a.scale ? a.scale + c0 : nullptr, n, 1.f, sc);
+    load_weight<GRP>(a.pre_weight ? a.pre_weight + c0 : nullptr, n, 1.f, w2);
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const int j = threadIdx.x + i * TPG;
-            const int64_t c = cb + (int64_t)j * VEC + e;
-            w1[i][e] = a.post_weight && j < nvec ? a.post_weight[c] : 1.f;
-            w2[i][e] = a.pre_weight && j < nvec ? a.pre_weight[c] : 1.f;
-            sc[i][e] = a.scale && j < nvec ? a.scale[c] : 1.f;
-            s1[i][e] = s2[i][e] = s3[i][e] = 0.f;
-        }
+    for (int i = 0; i < 4; ++i) s1[i] = s2[i] = s3[i] = f2(0.f);
 
-    struct Row {
-        Piece<T, VEC> x, z, dy;
-        Piece<R, VEC> r, dr;
-    };
-    auto ahead = [&](int64_t row, int stage) {
-        if constexpr (kUseRing) {
-            uint8_t* at = ring + stage * TPG * NV * (int)sizeof(Row);
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int j = threadIdx.x + i * TPG;
-                if (row < a.rows && j < nvec) {
-                    const int64_t c = (int64_t)j * VEC;
-                    auto to = [&](auto* p, int before) {
-                        return reinterpret_cast<decltype(p)>(at + before * TPG * NV) + i * TPG + threadIdx.x;
-                    };
-                    constexpr int t = sizeof(Piece<T, VEC>), u = sizeof(Piece<R, VEC>);
-                    copy_piece(to((Piece<T, VEC>*)nullptr, 0), x + row * a.x_stride + c);
-                    if (z) copy_piece(to((Piece<T, VEC>*)nullptr, t), z + row * a.z_stride + c);
-                    if (dy) copy_piece(to((Piece<T, VEC>*)nullptr, 2 * t), dy + row * a.dy_stride + c);
-                    if (r) copy_piece(to((Piece<R, VEC>*)nullptr, 3 * t), r + row * a.out_stride + c);
-                    if (dr) copy_piece(to((Piece<R, VEC>*)nullptr, 3 * t + u), dr + row * a.dout_stride + c);
-                }
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
+    InT x, z, dy;
+    InR r, dr;
+    z.edge_to = dy.edge_to = nullptr, r.edge_to = dr.edge_to = nullptr;
+    x.start(a.x, walker, a.x_stride, c0);
+    if (GATED) z.start(a.z, walker, a.z_stride, c0);
+    if (a.pre) dy.start(a.dy, walker, a.dy_stride, c0), r.start(a.out, walker, a.out_stride, c0);
+    if (a.dout) dr.start(a.dout, walker, a.dout_stride, c0);
+    const int64_t sx = walkers * a.x_stride, sz = walkers * a.z_stride, sdy = walkers * a.dy_stride,
+                  sr = walkers * a.out_stride, sdr = walkers * a.dout_stride;
+    uint32_t coming = walker;  // the row that is fetched next
+    auto ahead = [&](int stage) {
+        if (coming < rows) {
+            uint8_t* at = ring + stage * per_row;
+            x.fetch(at, n, sx);
+            if (GATED) z.fetch(at + bx, n, sz);
+            if (a.pre) dy.fetch(at + at_dy, n, sdy), r.fetch(at + at_r, n, sr);
+            if (a.dout) dr.fetch(at + at_dr, n, sdr);
         }
+        coming += walkers;
+        glr::commit();
     };
-    auto take = [&](Row& v, int64_t row, int stage, int i) {
-        const int j = threadIdx.x + i * TPG;
-        v = Row{};
-        if (j >= nvec) return;
-        if constexpr (kUseRing) {
-            const uint8_t* at = ring + stage * TPG * NV * (int)sizeof(Row);
-            auto from = [&](auto* p, int before) {
-                return reinterpret_cast<decltype(p)>(at + before * TPG * NV) + i * TPG + threadIdx.x;
-            };
-            constexpr int t = sizeof(Piece<T, VEC>), u = sizeof(Piece<R, VEC>);
-            v.x = *from((const Piece<T, VEC>*)nullptr, 0);
-            if (z) v.z = *from((const Piece<T, VEC>*)nullptr, t);
-            if (dy) v.dy = *from((const Piece<T, VEC>*)nullptr, 2 * t);
-            if (r) v.r = *from((const Piece<R, VEC>*)nullptr, 3 * t);
-            if (dr) v.dr = *from((const Piece<R, VEC>*)nullptr, 3 * t + u);
-        } else {
-            const int64_t c = (int64_t)j * VEC;
-            load_piece(v.x, x + row * a.x_stride + c);
-            if (z) load_piece(v.z, z + row * a.z_stride + c);
-            if (dy) load_piece(v.dy, dy + row * a.dy_stride + c);
-            if (r) load_piece(v.r, r + row * a.out_stride + c);
-            if (dr) load_piece(v.dr, dr + row * a.dout_stride + c);
-        }
-    };
+    for (int k = 0; k < kRing; ++k) {
+        uint8_t* at = ring + k * per_row;
+        InT::clear(at, n);
+        if (GATED) InT::clear(at + bx, n);
+        if (a.pre) InT::clear(at + at_dy, n), InR::clear(at + at_r, n);
+        if (a.dout) InR::clear(at + at_dr, n);
+    }
+    tc::griddep_launch_dependents();  // the sum over the walkers may be launched; it waits for this grid's end
     if (Q > 1) glr::cluster_sync();  // the others' shared memory is there
-    for (int k = 0; k < kRing; ++k) ahead(walker + k * walkers, k);
+    auto finish = [&] { x.finish(), z.finish(), dy.finish(), r.finish(), dr.finish(); };
+    for (int k = 0; k < kRing; ++k) ahead(k), finish();
+    RowOut<T, GRP> dx, dz;
+    RowOut<R, GRP> dres;
+    dx.start(a.dx, walker, a.dx_stride, c0);
+    if (GATED) dz.start(a.dz, walker, a.dz_stride, c0);
+    if (a.dres) dres.start(a.dres, walker, a.dres_stride, c0);
+    const int64_t tx = walkers * a.dx_stride, tz = walkers * a.dz_stride, tr = walkers * a.dres_stride;
     int stage = 0;
-    for (int64_t row = walker; row < a.rows; row += walkers) {
-        if (kUseRing) asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
-        Row v[NV];
-        float sums[3] = {0.f, 0.f, 0.f};
+    for (uint32_t row = walker; row < rows; row += walkers) {
+        glr::wait_for<kRing - 1>();
+        finish();
+        if (!InT::kOwn) __syncthreads();  // the other threads' copies are there too
+        const uint8_t* at = ring + stage * per_row;
+        auto first = [&](auto* base, int64_t stride) { return base + row * stride + c0; };
+        float2 fx[4], fz[4], fd[4], fr[4], D[4];
+        InT::read(at, first(static_cast<const T*>(a.x), a.x_stride), n, fx);
+        if (GATED) InT::read(at + bx, first(static_cast<const T*>(a.z), a.z_stride), n, fz);
+        if (a.pre) {
+            InT::read(at + at_dy, first(static_cast<const T*>(a.dy), a.dy_stride), n, fd);
+            InR::read(at + at_r, first(static_cast<const R*>(a.out), a.out_stride), n, fr);
+        } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            take(v[i], row, stage, i);
-            float fx[VEC], fr[VEC], fd[VEC];
-            widen(v[i].x, fx), widen(v[i].r, fr), widen(v[i].dy, fd);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                sums[0] = fmaf(fx[e], fx[e], sums[0]);
-                sums[1] = fmaf(fr[e], fr[e], sums[1]);
-                sums[2] = fmaf(fd[e] * w2[i][e], fr[e], sums[2]);
-            }
+            for (int i = 0; i < 4; ++i) fd[i] = fr[i] = f2(0.f);
         }
-        ahead(row + kRing * walkers, stage);
+        if (a.dout) {
+            InR::read(at + at_dr, first(static_cast<const R*>(a.dout), a.dout_stride), n, D);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) D[i] = f2(0.f);
+        }
+        if (!InT::kOwn) __syncthreads();  // (the place is read)
+        ahead(stage);
         if (++stage == kRing) stage = 0;
-        group_sums<TPG, 3>(sums, smem3, turn3, Q, rank);
-        const float k1 = a.post ? rsqrtf(sums[0] / count + a.eps) : 1.f;
-        const float k2 = a.pre ? rsqrtf(sums[1] / count + a.eps) : 0.f;
-        const float m2 = k2 * k2 * (sums[2] / count);
-        float q[NV][VEC], last[1] = {0.f};
+        float k1 = 1.f, k2 = 0.f, m2 = 0.f;
+        if (a.post || a.pre) {
+            float2 s[3] = {f2(0.f), f2(0.f), f2(0.f)};
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int j = threadIdx.x + i * TPG;
-            const int64_t c = (int64_t)j * VEC;
-            float fx[VEC], fz[VEC], fr[VEC], fd[VEC], D[VEC], oz[VEC];
-            widen(v[i].x, fx), widen(v[i].z, fz), widen(v[i].r, fr), widen(v[i].dy, fd), widen(v[i].dr, D);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                s3[i][e] = fmaf(fd[e] * k2, fr[e], s3[i][e]);
-                D[e] = fmaf(k2, fmaf(-m2, fr[e], fd[e] * w2[i][e]), D[e]);
-                const float xh = fx[e] * k1, n = xh * w1[i][e];
-                float g = 1.f, dn = D[e] * sc[i][e];
-                if (z) {
-                    const float sg = sigmoid<T>(fz[e]);
-                    g = fz[e] * sg;
-                    oz[e] = dn * n * fmaf(g, 1.f - sg, sg);
-                }
-                s2[i][e] = fmaf(D[e], n * g, s2[i][e]);
-                dn *= g;
-                s1[i][e] = fmaf(dn, xh, s1[i][e]);
-                q[i][e] = dn * w1[i][e];
-                last[0] = fmaf(q[i][e], xh, last[0]);
+            for (int i = 0; i < 4; ++i) {
+                s[0] = fma2(fx[i], fx[i], s[0]);
+                s[1] = fma2(fr[i], fr[i], s[1]);
+                s[2] = fma2(mul2(fd[i], w2[i]), fr[i], s[2]);
             }
-            if (j < nvec) {
-                if (dres) store_piece(dres + row * a.dres_stride + c, D);
-                if (z) store_piece(dz + row * a.dz_stride + c, oz);
-            }
+            float sums[3] = {sum_of(s[0]), sum_of(s[1]), sum_of(s[2])};
+            group_sums(sums, smem3, turn3, Q, rank);
+            if (a.post) k1 = rsqrtf(fmaf(sums[0], inv, a.eps));
+            if (a.pre) k2 = rsqrtf(fmaf(sums[1], inv, a.eps));
+            m2 = -k2 * k2 * (sums[2] * inv);
         }
+        float2 last = f2(0.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            s3[i] = fma2(mul2(fd[i], f2(k2)), fr[i], s3[i]);
+            D[i] = fma2(f2(k2), fma2(f2(m2), fr[i], mul2(fd[i], w2[i])), D[i]);
+            fx[i] = mul2(fx[i], f2(k1));
+            float2 v = mul2(fx[i], w1[i]), dn = mul2(D[i], sc[i]);
+            if (GATED) {
+                const float2 sg = sigmoid2(fz[i]), g = mul2(fz[i], sg);
+                fz[i] = mul2(mul2(dn, v), fma2(g, fma2(sg, f2(-1.f), f2(1.f)), sg));  // dz
+                v = mul2(v, g), dn = mul2(dn, g);
+            }
+            s2[i] = fma2(D[i], v, s2[i]);
+            s1[i] = fma2(dn, fx[i], s1[i]);
+            fd[i] = mul2(dn, w1[i]);
+            last = fma2(fd[i], fx[i], last);
+        }
+        if (a.dres) dres.write(n, D, tr);
+        if (GATED) dz.write(n, fz, tz);
         float m1 = 0.f;
         if (a.post) {
-            group_sums<TPG, 1>(last, smem1, turn1, Q, rank);
-            m1 = k1 * (last[0] / count);
+            float sums[1] = {sum_of(last)};
+            group_sums(sums, smem1, turn1, Q, rank);
+            m1 = -sums[0] * inv;
         }
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int j = threadIdx.x + i * TPG;
-            if (j >= nvec) continue;
-            float fx[VEC], o[VEC];
-            widen(v[i].x, fx);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) o[e] = k1 * fmaf(-m1, fx[e], q[i][e]);
-            store_piece(dx + row * a.dx_stride + (int64_t)j * VEC, o);
-        }
+        for (int i = 0; i < 4; ++i) fd[i] = mul2(f2(k1), fma2(f2(m1), fx[i], fd[i]));
+        dx.write(n, fd, tx);
     }
-    if (kUseRing) asm volatile("cp.async.wait_all;" ::: "memory");
-    float* part = a.partials + walker * 3 * a.channels + cb;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int j = threadIdx.x + i * TPG;
-        if (j >= nvec) continue;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const int64_t c = (int64_t)j * VEC + e;
-            part[c] = s1[i][e], part[a.channels + c] = s2[i][e], part[2 * a.channels + c] = s3[i][e];
-        }
-    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    float* part = a.partials + (int64_t)walker * 3 * a.channels + c0;
+    store_weight<GRP>(part, n, s1);
+    store_weight<GRP>(part + a.channels, n, s2);
+    store_weight<GRP>(part + 2 * a.channels, n, s3);
 }
 
-template <typename T, typename R, int VEC, int TPG>
-cudaError_t launch_n(const BlockNormBwdArgs& a, const Plan& p, cudaStream_t st) {
-    const int bytes = VEC > 1 ? ring_rows<T>() * TPG * place_bytes<T, R>() : 0;
-    const cudaError_t e = launch_rows(k_block_norm_bwd<T, R, VEC, TPG>, a, p, TPG, bytes, st);
-    if (e != cudaSuccess) return e;
-    if (!a.dpost && !a.dscale && !a.dpre) return cudaSuccess;
+template <typename T, typename R, int GRP>
+cudaError_t launch_g(const BlockNormBwdArgs& a, cudaStream_t st) {
+    const Plan p = plan_of(a.rows, a.channels, kMost, kMost);
+    const int bx = RowIn<T, GRP>::place_bytes(p.threads), br = RowIn<R, GRP>::place_bytes(p.threads);
+    const int bytes = ring_rows<T>() * (bx * (1 + (a.z != nullptr) + a.pre) + br * (a.pre + (a.dout != nullptr)));
+    const cudaError_t e =
+        launch_rows(a.z ? k_block_norm_bwd<T, R, GRP, true> : k_block_norm_bwd<T, R, GRP, false>, a, p, bytes, st);
+    if (e != cudaSuccess || (!a.dpost && !a.dscale && !a.dpre)) return e;
     return launch_sum_rows(a.partials, p.walkers, {a.dpost, a.channels}, {a.dscale, a.channels}, {a.dpre, a.channels},
                            nullptr, st);
 }
 
-template <typename T, typename R, int VEC>
-cudaError_t launch_v(const BlockNormBwdArgs& a, cudaStream_t st) {
-    const Plan p = plan_of(a.rows, a.channels, kResident);
-    switch (p.threads) {
-        case 32: return launch_n<T, R, VEC, 32>(a, p, st);
-        case 64: return launch_n<T, R, VEC, 64>(a, p, st);
-        case 128: return launch_n<T, R, VEC, 128>(a, p, st);
-        case 256: return launch_n<T, R, VEC, 256>(a, p, st);
-        default: return launch_n<T, R, VEC, 512>(a, p, st);
-    }
-}
-
 template <typename T, typename R>
 cudaError_t launch_t(const BlockNormBwdArgs& a, cudaStream_t st) {
-    constexpr int VEC = 16 / sizeof(T);
-    const void* ptr[] = {a.x, a.z, a.dy, a.dx, a.dz, a.out, a.dout, a.dres};
-    uint64_t all = (uint64_t)a.channels * sizeof(T);
-    for (const void* p : ptr) all |= reinterpret_cast<uintptr_t>(p);
-    all |= (uint64_t)((a.x_stride | a.dx_stride | (a.z ? a.z_stride | a.dz_stride : 0) | (a.dy ? a.dy_stride : 0)) * sizeof(T));
-    all |= (uint64_t)(((a.out ? a.out_stride : 0) | (a.dout ? a.dout_stride : 0) | (a.dres ? a.dres_stride : 0)) * sizeof(R));
-    if (all % 16 == 0) return launch_v<T, R, VEC>(a, st);
-    return launch_v<T, R, 1>(a, st);
+    uint64_t t = 0, r = 0;
+    for (const void* p : {a.x, a.z, a.dy, (const void*)a.dx, (const void*)a.dz}) t |= reinterpret_cast<uintptr_t>(p);
+    for (const void* p : {a.out, a.dout, (const void*)a.dres}) r |= reinterpret_cast<uintptr_t>(p);
+    t |= (uint64_t)((a.x_stride | a.dx_stride | (a.z ? a.z_stride | a.dz_stride : 0) | (a.dy ? a.dy_stride : 0)) * sizeof(T));
+    r |= (uint64_t)(((a.out ? a.out_stride : 0) | (a.dout ? a.dout_stride : 0) | (a.dres ? a.dres_stride : 0)) * sizeof(R));
+    switch (group_of(t, r, a.channels, sizeof(T), sizeof(R))) {
+        case 8:
+            if constexpr (sizeof(R) == 2) return launch_g<T, R, 8>(a, st);
+        case 4: return launch_g<T, R, 4>(a, st);
+        case 2: return launch_g<T, R, 2>(a, st);
+        default: return launch_g<T, R, 1>(a, st);
+    }
 }
 
 }  // namespace
 
 int64_t block_norm_bwd_partials(int64_t rows, int64_t channels) {
-    return plan_of(rows, channels, kResident).walkers * 3 * channels;
+    return plan_of(rows, channels, kMost, kMost).walkers * 3 * channels;
 }
 
 cudaError_t launch_block_norm_bwd(const BlockNormBwdArgs& a, bool bf16, bool res_bf16, cudaStream_t st) {

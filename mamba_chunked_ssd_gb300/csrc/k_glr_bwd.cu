@@ -95,6 +95,7 @@ __global__ void __launch_bounds__(kGroups* LANES, kWarpsOf<T, GATED> * 32 / (kGr
         ta = ta < 0 ? -1 : ta - step;
         commit();
     };
+    griddep_launch_dependents();  // the sum of the blocks' parts of dA may be launched; it waits for this grid's end
     if (CLUSTER) cluster_sync();  // the others' shared memory is there
     for (int s = 0; s < S; ++s) ahead(s);
     const int steps = (tiles + K - 1) / K;

@@ -1,6 +1,8 @@
 // k_sum_rows.cu — sums over the rows of a matrix of partial sums, the last step of
 // the gradients of weights.  Eight threads take every eighth row of a column each.
+// It is launched while the kernel that writes the matrix runs, and waits for its end.
 #include "gated_linear.cuh"
+#include "tc_ptx.cuh"
 
 namespace m2 {
 namespace {
@@ -13,6 +15,7 @@ k_sum_rows(const float* partials, int64_t rows, int64_t cols, SumOut o0, SumOut 
     const int x = threadIdx.x % kCols, g = threadIdx.x / kCols;
     const int64_t c = (int64_t)blockIdx.x * kCols + x;
     float s = 0.f;
+    tc::griddep_wait();
     if (c < cols) {
 #pragma unroll 8
         for (int64_t k = g; k < rows; k += kGroups) s += partials[k * cols + c];
@@ -38,8 +41,17 @@ cudaError_t launch_sum_rows(const float* partials, int64_t rows, SumOut o0, SumO
                             cudaStream_t st) {
     const int64_t cols = o0.len + o1.len + o2.len;
     if (cols == 0) return cudaSuccess;
-    k_sum_rows<<<(unsigned)((cols + kCols - 1) / kCols), kCols * kGroups, 0, st>>>(partials, rows, cols, o0, o1, o2, by);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((cols + kCols - 1) / kCols));
+    cfg.blockDim = dim3(kCols * kGroups);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t launched = cudaLaunchKernelEx(&cfg, k_sum_rows, partials, rows, cols, o0, o1, o2, by);
+    return launched == cudaSuccess ? cudaGetLastError() : (cudaGetLastError(), launched);
 }
 
 }  // namespace m2
