@@ -44,8 +44,8 @@ extern "C" {
  * final_state (and chunk_states past them) the state after them, and nothing
  * there is read into a result.  Gates and states are fp32 for both dtypes.
  * r_t = -infinity keeps the state (to fp32's rounding).  At most 65535 batch
- * rows, 2^30 tokens and 2^30 channels; tensors of more than 2^40 elements,
- * strides included, are MAMBA2_ERR_UNSUPPORTED, too. */
+ * rows, 2^30 tokens, 2^30 channels and 2^33 states of all batch rows; tensors of
+ * more than 2^40 elements, strides included, are MAMBA2_ERR_UNSUPPORTED, too. */
 enum { MAMBA2_GLR_CHUNK = 64 };
 
 typedef struct {

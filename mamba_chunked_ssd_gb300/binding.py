@@ -565,30 +565,38 @@ def _workspace(fn, shape, given, t, gpu, stream):
     return given, need
 
 
-def _tensors(names, tensors, like, gpu):
-    """Every tensor that is given has like's dtype, shape and GPU."""
+def _same(t, shape, dtype, gpu):
+    """Whether a tensor (None passes) has this shape and dtype and is on this GPU."""
+    return t is None or (t.dtype is dtype and t.shape == shape and t.get_device() == gpu)
+
+
+def _refuse(names, tensors, shape, dtype, gpu):
+    """Names the first tensor that is another one than _same asks for."""
     for name, t in zip(names, tensors):
-        if t is not None and (t.dtype is not like.dtype or t.shape != like.shape or t.get_device() != gpu):
-            raise ValueError(f"{name} must be {like.dtype} {tuple(like.shape)} on cuda:{gpu}, "
+        if not _same(t, shape, dtype, gpu):
+            raise ValueError(f"{name} must be {dtype} {tuple(shape)} on cuda:{gpu}, "
                              f"not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _strides(t, name, inner=1):
-    return 0 if t is None else _rows(t, name, inner)
+def _stride(t, name):
+    """_rows of a tensor that is known to be on the GPU, or 0 for None."""
+    return 0 if t is None or t.is_contiguous() else _rows(t, name, 1)
 
 
-def _glr_args(x, r, i, z, A, y, dims):
-    """The shape of a recurrence's call and its GPU; y: the output, or its gradient."""
-    if len(x.shape) != dims:
-        raise ValueError(f"x must have {dims} dimensions, not {tuple(x.shape)}")
-    gpu = _gpu(x, "x")
-    _tensors(("r", "i", "z", "y"), (r, i, z, y), x, gpu)
+def _glr_args(x, r, i, z, A, y, dims, gpu):
+    """The shape of a recurrence's call on this GPU; y: the output, or its gradient."""
+    shape, dt = x.shape, x.dtype
+    if len(shape) != dims:
+        raise ValueError(f"x must have {dims} dimensions, not {tuple(shape)}")
     if r is None or i is None:
         raise ValueError("r and i must be given")
-    C = x.shape[-1]
+    if not (_same(r, shape, dt, gpu) and _same(i, shape, dt, gpu) and _same(z, shape, dt, gpu) and
+            _same(y, shape, dt, gpu)):
+        _refuse(("r", "i", "z", "y"), (r, i, z, y), shape, dt, gpu)
+    C = shape[-1]
     _want(A, "A", torch.float32, (C,), gpu)
-    return _glr_shape(x.shape[0], x.shape[1] if dims == 3 else 1, C, _rows(x, "x", 1), _rows(r, "r", 1),
-                      _rows(i, "i", 1), _strides(z, "z"), _rows(y, "y", 1), _dtype_code(x), 0), gpu
+    return _glr_shape(shape[0], shape[1] if dims == 3 else 1, C, _stride(x, "x"), _stride(r, "r"), _stride(i, "i"),
+                      _stride(z, "z"), _stride(y, "y"), _dtype_code(x), 0)
 
 
 def mamba2_glr_fwd(x, r, i, A, z=None, initial_state=None, lengths=None, y=None, final_state=None,
@@ -599,8 +607,9 @@ def mamba2_glr_fwd(x, r, i, A, z=None, initial_state=None, lengths=None, y=None,
     or None): chunk_states [b, ceil(L / 64), C] fp32 is what mamba2_glr_bwd
     starts from."""
     gpu = _gpu(x, "x")
-    y = _like(x, y, "y", stream)
-    shape, gpu = _glr_args(x, r, i, z, A, y, 3)
+    if y is None:
+        y = _like(x, y, "y", stream)
+    shape = _glr_args(x, r, i, z, A, y, 3, gpu)
     b, L, C = x.shape
     _want(initial_state, "initial_state", torch.float32, (b, C), gpu)
     _want(lengths, "lengths", torch.int32, (b,), gpu)
@@ -625,8 +634,11 @@ def mamba2_glr_bwd(dy, x, r, i, A, chunk_states, z=None, dfinal_state=None, leng
     """Gradients of a mamba2_glr_fwd call from dy [b, L, C] and dfinal_state
     [b, C] fp32 or None, with that call's chunk_states.  Returns (dx, dr, di,
     dz or None, dA [C] fp32, dinitial_state [b, C] fp32 or None)."""
-    shape, gpu = _glr_args(x, r, i, z, A, dy, 3)
+    gpu = _gpu(x, "x")
+    shape = _glr_args(x, r, i, z, A, dy, 3, gpu)
     b, L, C = x.shape
+    if dy is None:
+        raise ValueError("dy must be given")
     _want(chunk_states, "chunk_states", torch.float32, (b, -(-L // MAMBA2_GLR_CHUNK), C), gpu)
     if chunk_states is None:
         raise ValueError("chunk_states must be given")
@@ -644,7 +656,7 @@ def mamba2_glr_bwd(dy, x, r, i, A, chunk_states, z=None, dfinal_state=None, leng
         _want(dinitial_state, "dinitial_state", torch.float32, (b, C), gpu)
     elif want_dinitial_state:
         dinitial_state = _new((b, C), torch.float32, x.device, stream)
-    grads = _glr_grad_strides(_rows(dx, "dx", 1), _rows(dr, "dr", 1), _rows(di, "di", 1), _strides(dz, "dz"))
+    grads = _glr_grad_strides(_stride(dx, "dx"), _stride(dr, "dr"), _stride(di, "di"), _stride(dz, "dz"))
     ws, size = _workspace("mamba2_glr_bwd", shape, workspace, x, gpu, stream)
     rc = load_library().mamba2_glr_bwd(shape, grads, _at(dy), _at(x), _at(r), _at(i), _at(z), _at(A), _at(lengths),
                                        _at(chunk_states), _at(dfinal_state), _at(dx), _at(dr), _at(di), _at(dz),
@@ -659,8 +671,9 @@ def mamba2_glr_step(x, r, i, A, z=None, state_in=None, state_out=None, y=None, s
     [b, C] fp32.  Returns (y [b, C], state_out).  Pass state_out=state_in to
     update the state in place."""
     gpu = _gpu(x, "x")
-    y = _like(x, y, "y", stream)
-    shape, gpu = _glr_args(x, r, i, z, A, y, 2)
+    if y is None:
+        y = _like(x, y, "y", stream)
+    shape = _glr_args(x, r, i, z, A, y, 2, gpu)
     _want(state_in, "state_in", torch.float32, x.shape, gpu)
     if state_out is None:
         state_out = _new(x.shape, torch.float32, x.device, stream)
@@ -682,7 +695,8 @@ def mamba2_causal_conv_bwd(dy, x, weight, bias=None, silu=True, initial_state=No
     b, L, C = x.shape
     W, gpu = weight.shape[-1], _gpu(x, "x")
     state = (b, W - 1, C)
-    _tensors(("dy",), (dy,), x, gpu)
+    if dy is None or not _same(dy, x.shape, x.dtype, gpu):
+        raise ValueError(f"dy must be {x.dtype} {tuple(x.shape)} on cuda:{gpu}")
     _want(weight, "weight", torch.float32, (C, W), gpu), _want(bias, "bias", torch.float32, (C,), gpu)
     _want(initial_state, "initial_state", x.dtype, state, gpu)
     _want(dfinal_state, "dfinal_state", x.dtype, state, gpu)
@@ -700,10 +714,9 @@ def mamba2_causal_conv_bwd(dy, x, weight, bias=None, silu=True, initial_state=No
         _want(dinitial_state, "dinitial_state", x.dtype, state, gpu)
     elif want_dinitial_state:
         dinitial_state = _new(state, x.dtype, x.device, stream)
-    shape = _conv_shape(b, L, C, W, _rows(x, "x", 1), _rows(dy, "dy", 1), _dtype_code(x),
-                        MAMBA2_CONV_SILU if silu else 0)
+    shape = _conv_shape(b, L, C, W, _stride(x, "x"), _stride(dy, "dy"), _dtype_code(x), MAMBA2_CONV_SILU if silu else 0)
     ws, size = _workspace("mamba2_causal_conv_bwd", shape, workspace, x, gpu, stream)
-    rc = load_library().mamba2_causal_conv_bwd(shape, _rows(dx, "dx", 1), _at(dy), _at(x), _at(weight), _at(bias),
+    rc = load_library().mamba2_causal_conv_bwd(shape, _stride(dx, "dx"), _at(dy), _at(x), _at(weight), _at(bias),
                                                _at(lengths), _at(initial_state), _at(dfinal_state), _at(dx),
                                                _at(dweight), _at(dbias), _at(dinitial_state), _at(ws), size,
                                                _on(stream, gpu))
@@ -712,12 +725,14 @@ def mamba2_causal_conv_bwd(dy, x, weight, bias=None, silu=True, initial_state=No
     return dx, dweight, dbias, dinitial_state
 
 
-def _block_norm_args(x, z, weights, gpu):
+def _block_norm_args(x, z, post_weight, scale, pre_weight, gpu):
     """The number of channels; checks z and the weights."""
-    C = x.shape[-1]
-    _tensors(("z",), (z,), x, gpu)
-    for name, w in weights:
-        _want(w, name, torch.float32, (C,), gpu)
+    shape = x.shape
+    C = shape[-1]
+    if not _same(z, shape, x.dtype, gpu):
+        _refuse(("z",), (z,), shape, x.dtype, gpu)
+    _want(post_weight, "post_weight", torch.float32, (C,), gpu), _want(scale, "scale", torch.float32, (C,), gpu)
+    _want(pre_weight, "pre_weight", torch.float32, (C,), gpu)
     return C
 
 
@@ -730,21 +745,20 @@ def mamba2_block_norm_fwd(x, residual=None, z=None, post_weight=None, scale=None
     residual_out=residual to update the residual in place; residual_dtype is for
     calls that give neither (x's dtype else)."""
     gpu = _gpu(x, "x")
-    C = _block_norm_args(x, z, (("post_weight", post_weight), ("scale", scale), ("pre_weight", pre_weight)), gpu)
+    C = _block_norm_args(x, z, post_weight, scale, pre_weight, gpu)
     if residual_out is None:
         dt = residual.dtype if residual is not None else residual_dtype or x.dtype
         residual_out = _new(x.shape, dt, x.device, stream)
-    for name, t in (("residual", residual), ("residual_out", residual_out)):
-        if t is not None and (t.dtype is not residual_out.dtype or t.shape != x.shape or t.get_device() != gpu):
-            raise ValueError(f"{name} must be {residual_out.dtype} {tuple(x.shape)} on cuda:{gpu}, "
-                             f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+    dt = residual_out.dtype
+    if not (_same(residual, x.shape, dt, gpu) and _same(residual_out, x.shape, dt, gpu)):
+        _refuse(("residual", "residual_out"), (residual, residual_out), x.shape, dt, gpu)
     if pre:
         y = _like(x, y, "y", stream)
     elif y is not None:
         raise ValueError("y comes from the norm before the next block, which is not asked for")
-    shape = _block_norm_shape(x.numel() // C if C else 0, C, _rows(x, "x", 1), _strides(z, "z"),
-                              _strides(residual, "residual"), _rows(residual_out, "residual_out", 1),
-                              _strides(y, "y"), float(eps), _dtype_code(x), _dtype_code(residual_out),
+    shape = _block_norm_shape(x.numel() // C if C else 0, C, _stride(x, "x"), _stride(z, "z"),
+                              _stride(residual, "residual"), _stride(residual_out, "residual_out"),
+                              _stride(y, "y"), float(eps), _dtype_code(x), _dtype_code(residual_out),
                               (MAMBA2_BLOCK_NORM_POST if post else 0) | (MAMBA2_BLOCK_NORM_PRE if pre else 0))
     rc = load_library().mamba2_block_norm_fwd(shape, _at(x), _at(z), _at(residual), _at(post_weight), _at(scale),
                                               _at(pre_weight), _at(residual_out), _at(y), _on(stream, gpu))
@@ -763,8 +777,9 @@ def mamba2_block_norm_bwd(dresidual_out, dy, x, residual_out=None, z=None, post_
     for a weight that is not given).  Pass dresidual=dresidual_out to update it
     in place; residual_dtype is for calls that give neither (x's dtype else)."""
     gpu = _gpu(x, "x")
-    C = _block_norm_args(x, z, (("post_weight", post_weight), ("scale", scale), ("pre_weight", pre_weight)), gpu)
-    _tensors(("dy",), (dy,), x, gpu)
+    C = _block_norm_args(x, z, post_weight, scale, pre_weight, gpu)
+    if not _same(dy, x.shape, x.dtype, gpu):
+        _refuse(("dy",), (dy,), x.shape, x.dtype, gpu)
     if (dy is None or residual_out is None) if pre else dy is not None:
         raise ValueError("dy and residual_out must be given with the norm before the next block, dy only with it")
     if not pre:
@@ -774,22 +789,20 @@ def mamba2_block_norm_bwd(dresidual_out, dy, x, residual_out=None, z=None, post_
     known = next((t.dtype for t in (residual_out, dresidual_out, dresidual) if t is not None), residual_dtype or x.dtype)
     if dresidual is None and want_dresidual:
         dresidual = _new(x.shape, known, x.device, stream)
-    for name, t in (("residual_out", residual_out), ("dresidual_out", dresidual_out), ("dresidual", dresidual)):
-        if t is not None and (t.dtype is not known or t.shape != x.shape or t.get_device() != gpu):
-            raise ValueError(f"{name} must be {known} {tuple(x.shape)} on cuda:{gpu}, "
-                             f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+    if not (_same(residual_out, x.shape, known, gpu) and _same(dresidual_out, x.shape, known, gpu) and
+            _same(dresidual, x.shape, known, gpu)):
+        _refuse(("residual_out", "dresidual_out", "dresidual"), (residual_out, dresidual_out, dresidual), x.shape, known,
+                gpu)
     dx = _like(x, dx, "dx", stream)
     dz = None if z is None else _like(x, dz, "dz", stream)
-    given = [w is not None for w in (post_weight, scale, pre_weight)]
-    new = iter(_new((sum(given), C), torch.float32, x.device, stream).unbind(0) if any(given) and C % 4 == 0 else
-               [_new((C,), torch.float32, x.device, stream) for g in given if g])
-    weights = [next(new) if g else None for g in given]
+    weights = [None if w is None else _new((C,), torch.float32, x.device, stream)
+               for w in (post_weight, scale, pre_weight)]
     code = MAMBA2_BF16 if known == torch.bfloat16 else MAMBA2_F32 if known == torch.float32 else -1
-    shape = _block_norm_shape(x.numel() // C if C else 0, C, _rows(x, "x", 1), _strides(z, "z"), 0,
-                              _strides(residual_out, "residual_out"), _strides(dy, "dy"), float(eps), _dtype_code(x),
+    shape = _block_norm_shape(x.numel() // C if C else 0, C, _stride(x, "x"), _stride(z, "z"), 0,
+                              _stride(residual_out, "residual_out"), _stride(dy, "dy"), float(eps), _dtype_code(x),
                               code, (MAMBA2_BLOCK_NORM_POST if post else 0) | (MAMBA2_BLOCK_NORM_PRE if pre else 0))
-    grads = _block_norm_grad_strides(_rows(dx, "dx", 1), _strides(dz, "dz"), _strides(dresidual_out, "dresidual_out"),
-                                     _strides(dresidual, "dresidual"))
+    grads = _block_norm_grad_strides(_stride(dx, "dx"), _stride(dz, "dz"), _stride(dresidual_out, "dresidual_out"),
+                                     _stride(dresidual, "dresidual"))
     ws, size = _workspace("mamba2_block_norm_bwd", shape, workspace, x, gpu, stream)
     rc = load_library().mamba2_block_norm_bwd(shape, grads, _at(dresidual_out), _at(dy), _at(x), _at(z),
                                               _at(residual_out), _at(post_weight), _at(scale), _at(pre_weight),

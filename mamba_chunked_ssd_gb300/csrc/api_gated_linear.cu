@@ -9,6 +9,7 @@ namespace {
 
 constexpr int64_t kMaxElements = (int64_t)1 << 40;  // of a tensor, strides included
 constexpr int64_t kMaxCount = (int64_t)1 << 30;     // tokens, channels
+constexpr int64_t kMaxStates = (int64_t)1 << 33;     // of the recurrence: a launch has a block for 32
 constexpr size_t kWorkspaceAlign = 256;
 
 bool is_dtype(int32_t d) { return d == MAMBA2_F32 || d == MAMBA2_BF16; }
@@ -93,6 +94,7 @@ mamba2_status check_glr(const mamba2_glr_shape* s) {
     if (s->batch > 65535 || s->seqlen > kMaxCount || s->channels > kMaxCount) return MAMBA2_ERR_UNSUPPORTED;
     const int64_t rows = s->batch * s->seqlen;
     if (rows > 0 && s->channels > kMaxElements / rows) return MAMBA2_ERR_UNSUPPORTED;
+    if (s->batch * s->channels > kMaxStates) return MAMBA2_ERR_UNSUPPORTED;
     return MAMBA2_OK;
 }
 int64_t chunks_of(const mamba2_glr_shape& s) { return (s.seqlen + MAMBA2_GLR_CHUNK - 1) / MAMBA2_GLR_CHUNK; }
@@ -179,7 +181,7 @@ mamba2_status mamba2_glr_step(const mamba2_glr_shape* shape, const void* x, cons
 
 size_t mamba2_glr_bwd_workspace_size(const mamba2_glr_shape* s) {
     if (check_glr(s) != MAMBA2_OK || s->batch == 0 || s->seqlen == 0) return 0;
-    return rounded(glr_bwd_partials(s->batch, s->seqlen, s->channels) * s->channels);
+    return rounded(s->batch * s->channels);  // each batch row's part of A dA
 }
 
 mamba2_status mamba2_glr_bwd(const mamba2_glr_shape* s, const mamba2_glr_grad_strides* grad_strides, const void* dy,

@@ -21,6 +21,7 @@ struct GlrArgs {
     void* y;
     float* chunk_states;  // may be null
     float* final_state;   // may be null (not in the step)
+    int64_t first;        // strip of channels (of all batch rows) that clusters start with, and single blocks end before
 };
 
 struct GlrBwdArgs {
@@ -42,7 +43,8 @@ struct GlrBwdArgs {
     void* dz;
     float* dA;
     float* dinit;     // may be null
-    float* partials;  // glr_bwd_partials() rows of channels
+    float* partials;    // [batch, channels]: each row's part of A dA
+    int64_t first;    // as GlrArgs'
 };
 
 struct ConvBwdArgs {
@@ -114,8 +116,6 @@ cudaError_t launch_sum_rows(const float* partials, int64_t rows, SumOut o0, SumO
 
 cudaError_t launch_glr_fwd(const GlrArgs& a, bool bf16, cudaStream_t st);
 cudaError_t launch_glr_step(const GlrArgs& a, bool bf16, cudaStream_t st);
-// Rows of `channels` floats that the backward pass keeps dA's parts in.
-int64_t glr_bwd_partials(int64_t batch, int64_t seqlen, int64_t channels);
 cudaError_t launch_glr_bwd(const GlrBwdArgs& a, bool bf16, cudaStream_t st);
 
 // Floats of dweight's and dbias's parts.

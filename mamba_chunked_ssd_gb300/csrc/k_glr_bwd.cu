@@ -28,7 +28,6 @@ constexpr int kLanes = 16;
 // registers each 259; gated, where 16 do not fit, 298).
 template <typename T, bool GATED>
 constexpr int kWarpsOf = sizeof(T) == 2 && !GATED ? 16 : 12;
-constexpr int kPerSm = 3;  // blocks of an SM that a split of sequences counts on
 
 template <typename T, bool GATED, int LANES>
 constexpr int smem_bytes(bool cluster) {
@@ -62,11 +61,18 @@ __global__ void __launch_bounds__(kGroups* LANES, kWarpsOf<T, GATED> * 32 / (kGr
     float4(*parts)[8][LANES] = reinterpret_cast<float4(*)[8][LANES]>(rsums + 2);
     T* ring = reinterpret_cast<T*>(parts + (CLUSTER ? 2 : 0));
     // what does not fit where bf16 inputs lay: each thread's uo, w and factors of dz
-    float2* kept = reinterpret_cast<float2*>(ring + kStages * kWarps * NT * kPlace) + threadIdx.x;
+    float2* kept = reinterpret_cast<float2*>(ring + S * kWarps * NT * kPlace) + threadIdx.x;
     if (!CLUSTER) K = 1;
     const int warp = threadIdx.x / 32, group = threadIdx.x / LANES, lane = threadIdx.x % LANES, wl = threadIdx.x % 32;
     const int rank = CLUSTER ? (int)cluster_rank() : 0;
-    const int64_t b = blockIdx.y, c0 = (int64_t)(blockIdx.x / K) * kStrip;
+    // the strip and its batch row: of the grid's two dimensions, or counted through all rows
+    int64_t b = blockIdx.y, c0 = (int64_t)blockIdx.x * kStrip;
+    if constexpr (CLUSTER) {
+        const int64_t per_row = (a.channels + kStrip - 1) / kStrip, strip = a.first + blockIdx.x / K;
+        b = strip / per_row, c0 = strip % per_row * kStrip;
+    } else if (b * gridDim.x + blockIdx.x >= a.first) {
+        return;  // (the clusters take those)
+    }
     const int have = (int)imin64(a.channels - c0, kStrip);
     const int L = (int)a.seqlen, n = __shfl_sync(0xffffffffu, (int)row_length(a.lengths, b, L), 0), tiles = (n + kTile - 1) / kTile;
     const int step = K * kTile;
@@ -95,7 +101,7 @@ __global__ void __launch_bounds__(kGroups* LANES, kWarpsOf<T, GATED> * 32 / (kGr
         ta = ta < 0 ? -1 : ta - step;
         commit();
     };
-    griddep_launch_dependents();  // the sum of the blocks' parts of dA may be launched; it waits for this grid's end
+    griddep_launch_dependents();  // (what is launched beside this takes other strips, or waits for this grid's end)
     if (CLUSTER) cluster_sync();  // the others' shared memory is there
     for (int s = 0; s < S; ++s) ahead(s);
     const int steps = (tiles + K - 1) / K;
@@ -245,6 +251,7 @@ __global__ void __launch_bounds__(kGroups* LANES, kWarpsOf<T, GATED> * 32 / (kGr
         store<T, kOdd>(di + t * a.di_stride, f2(0.f), lane, have);
         if (GATED) store<T, kOdd>(dz + t * a.dz_stride, f2(0.f), lane, have);
     }
+    // the blocks' parts of A dA, in the order of their groups and ranks
     __syncthreads();
     float2* part = reinterpret_cast<float2*>(smem) + lane;
     part[group * LANES] = total;
@@ -252,21 +259,28 @@ __global__ void __launch_bounds__(kGroups* LANES, kWarpsOf<T, GATED> * 32 / (kGr
     if (group == 0) {
 #pragma unroll
         for (int w = 1; w < kGroups; ++w) total = add2(total, part[w * LANES]);
-        store<float, true>(a.partials + (b * K + rank) * a.channels + c0, total, lane, have);
     }
+    if constexpr (CLUSTER) {
+        if (group == 0) store_remote(&parts[0][rank][lane], 0, make_float4(total.x, total.y, 0.f, 0.f));
+        cluster_sync();
+        if (rank == 0 && group == 0) {
+            total = f2(0.f);
+            for (int q = 0; q < K; ++q) total = add2(total, make_float2(parts[0][q][lane].x, parts[0][q][lane].y));
+        }
+    }
+    if (rank == 0 && group == 0) store<float, true>(a.partials + b * a.channels + c0, total, lane, have);
+    if (CLUSTER) griddep_wait();
 }
-
-int64_t strips_of(int64_t channels) { return (channels + 2 * kLanes - 1) / (2 * kLanes); }
 
 template <typename T, Rows ROWS, bool GATED>
 cudaError_t launch(const GlrBwdArgs& a, cudaStream_t st) {
-    const int64_t strips = strips_of(a.channels);
-    const int K = glr_cluster(strips * a.batch, (a.seqlen + kTile - 1) / kTile, kPerSm);
-    const cudaError_t e = launch_strips(
-        K > 1 ? k_glr_bwd<T, ROWS, GATED, kLanes, true> : k_glr_bwd<T, ROWS, GATED, kLanes, false>, a, strips, K,
-        kGroups * kLanes, smem_bytes<T, GATED, kLanes>(K > 1), st);
+    const int64_t per_row = (a.channels + 2 * kLanes - 1) / (2 * kLanes);
+    const cudaError_t e =
+        launch_all(k_glr_bwd<T, ROWS, GATED, kLanes, false>, k_glr_bwd<T, ROWS, GATED, kLanes, true>, a, per_row,
+                   kWarpsOf<T, GATED> * 32 / (kGroups * kLanes), kGroups * kLanes, smem_bytes<T, GATED, kLanes>(false),
+                   smem_bytes<T, GATED, kLanes>(true), st);
     if (e != cudaSuccess) return e;
-    return launch_sum_rows(a.partials, a.batch * K, {a.dA, a.channels}, {}, {}, a.A, st);
+    return launch_sum_rows(a.partials, a.batch, {a.dA, a.channels}, {}, {}, a.A, st);
 }
 
 template <typename T>
@@ -282,10 +296,6 @@ cudaError_t launch_t(const GlrBwdArgs& a, cudaStream_t st) {
 }
 
 }  // namespace
-
-int64_t glr_bwd_partials(int64_t batch, int64_t seqlen, int64_t channels) {
-    return batch * glr_cluster(strips_of(channels) * batch, (seqlen + kTile - 1) / kTile, kPerSm);
-}
 
 cudaError_t launch_glr_bwd(const GlrBwdArgs& a, bool bf16, cudaStream_t st) {
     return bf16 ? launch_t<__nv_bfloat16>(a, st) : launch_t<float>(a, st);

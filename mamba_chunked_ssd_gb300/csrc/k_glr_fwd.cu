@@ -52,7 +52,14 @@ __global__ void __launch_bounds__(kGroups* LANES, kWarpsOf * 32 / (kGroups * LAN
     if (!CLUSTER) K = 1;
     const int warp = threadIdx.x / 32, group = threadIdx.x / LANES, lane = threadIdx.x % LANES, wl = threadIdx.x % 32;
     const int rank = CLUSTER ? (int)cluster_rank() : 0;
-    const int64_t b = blockIdx.y, c0 = (int64_t)(blockIdx.x / K) * kStrip;
+    // the strip and its batch row: of the grid's two dimensions, or counted through all rows
+    int64_t b = blockIdx.y, c0 = (int64_t)blockIdx.x * kStrip;
+    if constexpr (CLUSTER) {
+        const int64_t per_row = (a.channels + kStrip - 1) / kStrip, strip = a.first + blockIdx.x / K;
+        b = strip / per_row, c0 = strip % per_row * kStrip;
+    } else if (b * gridDim.x + blockIdx.x >= a.first) {
+        return;  // (the clusters take those)
+    }
     const int have = (int)imin64(a.channels - c0, kStrip);
     const int L = (int)a.seqlen, n = __shfl_sync(0xffffffffu, (int)row_length(a.lengths, b, L), 0), tiles = (n + kTile - 1) / kTile;
     const int step = K * kTile;
@@ -76,6 +83,7 @@ __global__ void __launch_bounds__(kGroups* LANES, kWarpsOf * 32 / (kGroups * LAN
         ta += step;
         commit();
     };
+    griddep_launch_dependents();  // (what is launched beside this takes other strips)
     if (CLUSTER) cluster_sync();  // the others' shared memory is there
     for (int s = 0; s < S; ++s) ahead(s);
     const int steps = (tiles + K - 1) / K;
@@ -172,15 +180,16 @@ __global__ void __launch_bounds__(kGroups* LANES, kWarpsOf * 32 / (kGroups * LAN
         for (int64_t g = tiles + rank * kGroups + group; g < nc; g += K * kGroups)
             store<float, true>(a.chunk_states + (b * nc + g) * a.channels + c0, carry, lane, have);
     }
+    if (CLUSTER) griddep_wait();
 }
 
 template <typename T, Rows ROWS, bool GATED>
 cudaError_t launch(const GlrArgs& a, cudaStream_t st) {
     constexpr int LANES = kLanes;
-    const int64_t strips = (a.channels + 2 * LANES - 1) / (2 * LANES), tiles = (a.seqlen + kTile - 1) / kTile;
-    const int K = glr_cluster(strips * a.batch, tiles, kWarpsOf * 32 / (kGroups * LANES));
-    return launch_strips(K > 1 ? k_glr_fwd<T, ROWS, GATED, LANES, true> : k_glr_fwd<T, ROWS, GATED, LANES, false>, a, strips,
-                         K, kGroups * LANES, smem_bytes<T, GATED, LANES>(K > 1), st);
+    const int64_t per_row = (a.channels + 2 * LANES - 1) / (2 * LANES);
+    return launch_all(k_glr_fwd<T, ROWS, GATED, LANES, false>, k_glr_fwd<T, ROWS, GATED, LANES, true>, a, per_row,
+                      kWarpsOf * 32 / (kGroups * LANES), kGroups * LANES, smem_bytes<T, GATED, LANES>(false),
+                      smem_bytes<T, GATED, LANES>(true), st);
 }
 
 template <typename T>

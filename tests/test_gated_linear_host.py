@@ -73,6 +73,7 @@ def glr_bwd(lib, ptr=None, grads=None, bytes_=1 << 40, **kw):
     (dict(dtype=2), INVALID), (dict(flags=1), INVALID), (dict(batch=-1), INVALID), (dict(channels=0), INVALID),
     (dict(x_stride=63), INVALID), (dict(y_stride=-64), INVALID), (dict(r_stride=1 << 40), UNSUPPORTED),
     (dict(batch=65536), UNSUPPORTED), (dict(channels=(1 << 30) + 1), UNSUPPORTED),
+    (dict(batch=9, channels=1 << 30), UNSUPPORTED),
 ])
 def test_glr_refusals(lib, f, kw, code):
     assert f(lib, **kw) == code

@@ -134,6 +134,38 @@ def test_glr_few_and_many_strips(b, L, C, dtype):
     check_glr(d, h0)
 
 
+@pytest.mark.parametrize("gated", [False, True])
+def test_glr_strips_that_are_left_over(gated):
+    """More strips than the GPU takes at once, a few of them left over: those are split between the blocks of
+    clusters, beside the others.  Every channel is one of a sequence that is known; a row of them ends early."""
+    L, C = 64 * 64 + 9, 32 * 40
+    b = 15 if not gated else 12
+    n = gen(3)
+    base = {k: n(1, L, 32).cuda() for k in ("x", "r", "i", "z", "dy")}
+    A = (-torch.exp(n(32))).cuda()
+    wide = {k: t.to(BF16).repeat(b, 1, C // 32).contiguous() for k, t in base.items()}
+    lengths = torch.full((b,), L, dtype=torch.int32, device="cuda")
+    lengths[-1] = 4000
+    z = wide["z"] if gated else None
+    y, fin, cs = bd.mamba2_glr_fwd(wide["x"], wide["r"], wide["i"], A.repeat(C // 32), z=z, lengths=lengths,
+                                   want_chunk_states=True)
+    grads = bd.mamba2_glr_bwd(wide["dy"], wide["x"], wide["r"], wide["i"], A.repeat(C // 32), cs, z=z, lengths=lengths)
+    bd.mamba2_check_device_status()
+    one = {k: t.to(BF16) for k, t in base.items()}
+    for rows, m in ((slice(0, b - 1), L), (slice(b - 1, b), 4000)):
+        part = {k: t[:, :m].contiguous() for k, t in one.items()}
+        z1 = part["z"] if gated else None
+        y1, fin1, cs1 = bd.mamba2_glr_fwd(part["x"], part["r"], part["i"], A, z=z1, want_chunk_states=True)
+        want = bd.mamba2_glr_bwd(part["dy"], part["x"], part["r"], part["i"], A, cs1, z=z1)
+        close(y[rows, :m], y1.repeat(b, 1, C // 32)[rows].cpu(), TOL[BF16], name="y")
+        close(fin[rows], fin1.repeat(b, C // 32)[rows].cpu(), TOL[FP32], name="state")
+        for got, w, name in zip(grads[:4], want[:4], ("dx", "dr", "di", "dz")):
+            if w is not None:
+                close(got[rows, :m], w.repeat(b, 1, C // 32)[rows].cpu(), TOL[BF16], name=name)
+                assert bool((got[rows, m:] == 0).all())
+        close(grads[5][rows], want[5].repeat(b, C // 32)[rows].cpu(), TOL[FP32], name="dinit")
+
+
 @BOTH
 @pytest.mark.parametrize("C", [64, 37])
 @pytest.mark.parametrize("gated", [False, True])
