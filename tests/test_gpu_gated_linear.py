@@ -139,7 +139,7 @@ def test_glr_strips_that_are_left_over(gated):
     """More strips than the GPU takes at once, a few of them left over: those are split between the blocks of
     clusters, beside the others.  Every channel is one of a sequence that is known; a row of them ends early."""
     L, C = 64 * 64 + 9, 32 * 40
-    b = 15 if not gated else 12
+    b = 16
     n = gen(3)
     base = {k: n(1, L, 32).cuda() for k in ("x", "r", "i", "z", "dy")}
     A = (-torch.exp(n(32))).cuda()
