@@ -11,9 +11,9 @@
 // A thread has eight channels, which it keeps while it walks down the rows: weights, and the sums
 // over the rows, stay in its registers; the sums of all walkers are added up by a second kernel.  Rows of
 // more than 4096 channels are split between the blocks of a cluster, which wait for one another twice a row.
-// Rows come through shared memory, one or two ahead.  About 65 instructions an element and one block of 512
-// threads to an SM, which waits at two barriers a row, bound it next to memory: 32768 x 4096 in bf16, gated, 392 us, 5.5
-// TB/s; 8192 x 4096 with an fp32 residual 110 us, 5.5 TB/s; 4096 x 8192 218 us, 2.5 TB/s.  (Two rows at a
+// Rows come through shared memory, one or two ahead.  About 55 instructions an element and one block of 512
+// threads to an SM, which waits at two barriers a row, bound it next to memory: 32768 x 4096 in bf16, gated, 349 us, 6.2
+// TB/s; 8192 x 4096 with an fp32 residual 110 us, 5.5 TB/s; 4096 x 8192 212 us, 2.5 TB/s.  (Two rows at a
 // time, for half as many barriers: 581 us, their inputs take the registers; blocks of 256 threads and
 // clusters from 2048 channels on 716.)
 #include "block_norm.cuh"
@@ -28,8 +28,10 @@ template <typename T>
 constexpr int ring_rows() { return sizeof(T) == 2 ? 3 : 2; }
 constexpr int kMost = 512;  // threads of a block, and of an SM (128 registers each)
 
-template <typename T, typename R, int GRP, bool GATED>
+// FULL: both norms and both gradients of residuals are there.
+template <typename T, typename R, int GRP, bool GATED, bool FULL>
 __global__ void __launch_bounds__(kMost, 1) k_block_norm_bwd(const BlockNormBwdArgs a, int Q) {
+    const bool pre = FULL || a.pre, post = FULL || a.post, dout = FULL || a.dout, has_dres = FULL || a.dres;
     constexpr int kRing = ring_rows<T>();
     __shared__ Sums<3> smem3;
     __shared__ Sums<1> smem1;
@@ -43,8 +45,8 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm_bwd(const BlockNormBwdA
     const int n = (int)imin64(a.channels - c0, share_of(a.channels, Q));  // this block's channels
     // places of a row: x, [z], [dy, r], [dr]
     const int bx = InT::place_bytes(blockDim.x), br = InR::place_bytes(blockDim.x);
-    const int at_dy = GATED ? 2 * bx : bx, at_r = at_dy + bx, at_dr = a.pre ? at_r + br : at_dy;
-    const int per_row = at_dr + (a.dout ? br : 0);
+    const int at_dy = GATED ? 2 * bx : bx, at_r = at_dy + bx, at_dr = pre ? at_r + br : at_dy;
+    const int per_row = at_dr + (dout ? br : 0);
     const float inv = 1.f / (float)a.channels;
 
     float2 w1[4], w2[4], sc[4], s1[4], s2[4], s3[4];
@@ -59,8 +61,8 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm_bwd(const BlockNormBwdA
     z.edge_to = dy.edge_to = nullptr, r.edge_to = dr.edge_to = nullptr;
     x.start(a.x, walker, a.x_stride, c0);
     if (GATED) z.start(a.z, walker, a.z_stride, c0);
-    if (a.pre) dy.start(a.dy, walker, a.dy_stride, c0), r.start(a.out, walker, a.out_stride, c0);
-    if (a.dout) dr.start(a.dout, walker, a.dout_stride, c0);
+    if (pre) dy.start(a.dy, walker, a.dy_stride, c0), r.start(a.out, walker, a.out_stride, c0);
+    if (dout) dr.start(a.dout, walker, a.dout_stride, c0);
     const int64_t sx = walkers * a.x_stride, sz = walkers * a.z_stride, sdy = walkers * a.dy_stride,
                   sr = walkers * a.out_stride, sdr = walkers * a.dout_stride;
     uint32_t coming = walker;  // the row that is fetched next
@@ -69,8 +71,8 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm_bwd(const BlockNormBwdA
             uint8_t* at = ring + stage * per_row;
             x.fetch(at, n, sx);
             if (GATED) z.fetch(at + bx, n, sz);
-            if (a.pre) dy.fetch(at + at_dy, n, sdy), r.fetch(at + at_r, n, sr);
-            if (a.dout) dr.fetch(at + at_dr, n, sdr);
+            if (pre) dy.fetch(at + at_dy, n, sdy), r.fetch(at + at_r, n, sr);
+            if (dout) dr.fetch(at + at_dr, n, sdr);
         }
         coming += walkers;
         glr::commit();
@@ -79,8 +81,8 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm_bwd(const BlockNormBwdA
         uint8_t* at = ring + k * per_row;
         InT::clear(at, n);
         if (GATED) InT::clear(at + bx, n);
-        if (a.pre) InT::clear(at + at_dy, n), InR::clear(at + at_r, n);
-        if (a.dout) InR::clear(at + at_dr, n);
+        if (pre) InT::clear(at + at_dy, n), InR::clear(at + at_r, n);
+        if (dout) InR::clear(at + at_dr, n);
     }
     tc::griddep_launch_dependents();  // the sum over the walkers may be launched; it waits for this grid's end
     if (Q > 1) glr::cluster_sync();  // the others' shared memory is there
@@ -90,7 +92,7 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm_bwd(const BlockNormBwdA
     RowOut<R, GRP> dres;
     dx.start(a.dx, walker, a.dx_stride, c0);
     if (GATED) dz.start(a.dz, walker, a.dz_stride, c0);
-    if (a.dres) dres.start(a.dres, walker, a.dres_stride, c0);
+    if (has_dres) dres.start(a.dres, walker, a.dres_stride, c0);
     const int64_t tx = walkers * a.dx_stride, tz = walkers * a.dz_stride, tr = walkers * a.dres_stride;
     int stage = 0;
     for (uint32_t row = walker; row < rows; row += walkers) {
@@ -102,14 +104,14 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm_bwd(const BlockNormBwdA
         float2 fx[4], fz[4], fd[4], fr[4], D[4];
         InT::read(at, first(static_cast<const T*>(a.x), a.x_stride), n, fx);
         if (GATED) InT::read(at + bx, first(static_cast<const T*>(a.z), a.z_stride), n, fz);
-        if (a.pre) {
+        if (pre) {
             InT::read(at + at_dy, first(static_cast<const T*>(a.dy), a.dy_stride), n, fd);
             InR::read(at + at_r, first(static_cast<const R*>(a.out), a.out_stride), n, fr);
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) fd[i] = fr[i] = f2(0.f);
         }
-        if (a.dout) {
+        if (dout) {
             InR::read(at + at_dr, first(static_cast<const R*>(a.dout), a.dout_stride), n, D);
         } else {
 #pragma unroll
@@ -119,7 +121,7 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm_bwd(const BlockNormBwdA
         ahead(stage);
         if (++stage == kRing) stage = 0;
         float k1 = 1.f, k2 = 0.f, m2 = 0.f;
-        if (a.post || a.pre) {
+        if (post || pre) {
             float2 s[3] = {f2(0.f), f2(0.f), f2(0.f)};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -129,8 +131,8 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm_bwd(const BlockNormBwdA
             }
             float sums[3] = {sum_of(s[0]), sum_of(s[1]), sum_of(s[2])};
             group_sums(sums, smem3, turn3, Q, rank);
-            if (a.post) k1 = rsqrtf(fmaf(sums[0], inv, a.eps));
-            if (a.pre) k2 = rsqrtf(fmaf(sums[1], inv, a.eps));
+            if (post) k1 = rsqrtf(fmaf(sums[0], inv, a.eps));
+            if (pre) k2 = rsqrtf(fmaf(sums[1], inv, a.eps));
             m2 = -k2 * k2 * (sums[2] * inv);
         }
         float2 last = f2(0.f);
@@ -150,10 +152,10 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm_bwd(const BlockNormBwdA
             fd[i] = mul2(dn, w1[i]);
             last = fma2(fd[i], fx[i], last);
         }
-        if (a.dres) dres.write(n, D, tr);
+        if (has_dres) dres.write(n, D, tr);
         if (GATED) dz.write(n, fz, tz);
         float m1 = 0.f;
-        if (a.post) {
+        if (post) {
             float sums[1] = {sum_of(last)};
             group_sums(sums, smem1, turn1, Q, rank);
             m1 = -sums[0] * inv;
@@ -169,13 +171,22 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm_bwd(const BlockNormBwdA
     store_weight<GRP>(part + 2 * a.channels, n, s3);
 }
 
+// (In bf16, 32768 x 4096, gated: 351 us, without it 390; narrow groups are bound by their loads.)
+template <typename T, typename R, int GRP>
+auto pick(const BlockNormBwdArgs& a) {
+    if constexpr (GRP >= 4)
+        if (a.pre && a.post && a.dout && a.dres)
+            return a.z ? k_block_norm_bwd<T, R, GRP, true, true> : k_block_norm_bwd<T, R, GRP, false, true>;
+    return a.z ? k_block_norm_bwd<T, R, GRP, true, false> : k_block_norm_bwd<T, R, GRP, false, false>;
+}
+
 template <typename T, typename R, int GRP>
 cudaError_t launch_g(const BlockNormBwdArgs& a, cudaStream_t st) {
     const Plan p = plan_of(a.rows, a.channels, kMost, kMost);
     const int bx = RowIn<T, GRP>::place_bytes(p.threads), br = RowIn<R, GRP>::place_bytes(p.threads);
     const int bytes = ring_rows<T>() * (bx * (1 + (a.z != nullptr) + a.pre) + br * (a.pre + (a.dout != nullptr)));
     const cudaError_t e =
-        launch_rows(a.z ? k_block_norm_bwd<T, R, GRP, true> : k_block_norm_bwd<T, R, GRP, false>, a, p, bytes, st);
+        launch_rows(pick<T, R, GRP>(a), a, p, bytes, st);
     if (e != cudaSuccess || (!a.dpost && !a.dscale && !a.dpre)) return e;
     return launch_sum_rows(a.partials, p.walkers, {a.dpost, a.channels}, {a.dscale, a.channels}, {a.dpre, a.channels},
                            nullptr, st);

@@ -10,8 +10,8 @@
 // run reads W - 1 tokens of the next one too.  Inputs come through shared memory, each thread's
 // to its own place, 16 tokens ahead.  Sums over a run stay in registers and go to a row of
 // partial sums, which a second kernel adds up.  About 22 instructions an element (19 of them packed multiplications
-// and additions of two) in 16 warps of an SM bound it next to memory: 4 x 8192 x 8192 in bf16 295 us, 5.5
-// TB/s; 4 x 4096 x 8192 in fp32 263 us, 6.1 TB/s.  (Vectors of four bytes, with 24 to 32 warps: 347 to 357 us.)
+// and additions of two) in 16 warps of an SM bound it next to memory: 4 x 8192 x 8192 in bf16 282 us, 5.7
+// TB/s; 4 x 4096 x 8192 in fp32 259 us, 6.2 TB/s.  (Vectors of four bytes, with 24 to 32 warps: 347 to 357 us.)
 #include "glr_math.cuh"
 
 namespace m2 {
@@ -45,7 +45,7 @@ __device__ __forceinline__ typename VecOf<T, VEC>::type narrow(const float2 (&f)
     return pack<T, VEC>(v);
 }
 
-template <typename T, int VEC, int W>
+template <typename T, int VEC, int W, bool SILU>
 __global__ void __launch_bounds__(kThreads, per_sm(W)) k_causal_conv_bwd(const ConvBwdArgs a, int64_t run) {
     using V = typename VecOf<T, VEC>::type;
     constexpr int N2 = (VEC + 1) / 2;
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(W)) k_causal_conv_bwd(const C
             widen<T, VEC>(dv, ds[0]);
 #pragma unroll
             for (int i = 0; i < N2; ++i) {
-                if (a.silu) {
+                if (SILU) {
                     float2 p = bias[i];
 #pragma unroll
                     for (int w = 0; w < W; ++w) p = fma2(wt[w][i], xs[w][i], p);
@@ -253,7 +253,9 @@ cudaError_t launch_w(const ConvBwdArgs& a, cudaStream_t st) {
     int64_t R = runs_of(a.batch, a.seqlen, gx, W);
     const int64_t run = (a.seqlen + R - 1) / R;
     R = (a.seqlen + run - 1) / run;
-    k_causal_conv_bwd<T, VEC, W><<<dim3((unsigned)gx, (unsigned)R, (unsigned)a.batch), kThreads, 0, st>>>(a, run);
+    const dim3 grid((unsigned)gx, (unsigned)R, (unsigned)a.batch);
+    if (a.silu) k_causal_conv_bwd<T, VEC, W, true><<<grid, kThreads, 0, st>>>(a, run);
+    else k_causal_conv_bwd<T, VEC, W, false><<<grid, kThreads, 0, st>>>(a, run);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_sum_rows(a.partials, R * a.batch, {a.dweight, a.channels * W}, {a.dbias, a.channels}, {}, nullptr, st);
