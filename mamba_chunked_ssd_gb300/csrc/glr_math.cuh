@@ -300,17 +300,18 @@ cudaError_t launch_strips(void (*kernel)(Args, int), const Args& a, dim3 grid, i
     return launched == cudaSuccess ? cudaGetLastError() : (cudaGetLastError(), launched);
 }
 
-// All of a call's strips, `per_row` of each batch row: `one` takes them alone, `some` as clusters.  Where strips are more than
-// the GPU's places for them, the few that are left over when every SM has as many would keep a few SMs for as long as
-// all others: they are split, while the last of the others end (4 x 4096 x 4096 in bf16, gated, backward 298 -> 258 us,
-// 8 x 2048 x 2560 155 -> 126, 10 x 1024 x 2048 85 -> 71; where all have places, 4 x 4096 x 4096 218 -> 241).
+// All of a call's strips, `per_row` of each batch row: `one` takes them alone, `some` as clusters.  Where strips are a little
+// more than the GPU's places for them, the few that are left over when every SM has as many would keep a few SMs for
+// as long as all others: they are split, while the last of the others end (4 x 4096 x 4096 in bf16, gated, backward
+// 298 -> 258 us, 8 x 2048 x 2560 155 -> 126, 10 x 1024 x 2048 85 -> 71; but where all have places, 4 x 4096 x 4096,
+// 218 -> 241, and where places are taken three times, 16 x 2048 x 4096 forward, 183 -> 196).
 template <typename Args>
 cudaError_t launch_all(void (*one)(Args, int), void (*some)(Args, int), Args a, int64_t per_row, int per_sm, int threads,
                        int bytes_one, int bytes_some, cudaStream_t st) {
     const int64_t tiles = (a.seqlen + kTile - 1) / kTile, sms = sm_count() > 0 ? sm_count() : 152, places = per_sm * sms;
     const int64_t strips = a.batch * per_row, left = strips % sms;
     const int K = glr_cluster(strips, tiles, per_sm);
-    const bool split = strips > places && left > 0 && 8 * left <= places && tiles >= 16;
+    const bool split = strips > places && strips < 2 * places && left > 0 && 8 * left <= places && tiles >= 16;
     a.first = K > 1 ? 0 : split ? strips - left : strips;
     if (K == 1) {
         const cudaError_t e = launch_strips(one, a, dim3((unsigned)per_row, (unsigned)a.batch), 1, threads, bytes_one, false, st);
