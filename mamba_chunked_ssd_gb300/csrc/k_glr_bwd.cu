@@ -105,8 +105,9 @@ __global__ void __launch_bounds__(kGroups* LANES, kWarpsOf<T, GATED> * 32 / (kGr
     if (CLUSTER) cluster_sync();  // the others' shared memory is there
     for (int s = 0; s < S; ++s) ahead(s);
     const int steps = (tiles + K - 1) / K;
+    int buf = 0;
     auto walk = [&](auto wide) {
-        int stage = 0, buf = 0;
+        int stage = 0;
         float2 before = g < 0 ? f2(0.f) : load_pair(states + (int64_t)g * a.channels, lane, have);
         for (int j = 0; j < steps; ++j, g -= K) {
             const int t = g * kTile + group * kTok;
@@ -261,11 +262,12 @@ __global__ void __launch_bounds__(kGroups* LANES, kWarpsOf<T, GATED> * 32 / (kGr
         for (int w = 1; w < kGroups; ++w) total = add2(total, part[w * LANES]);
     }
     if constexpr (CLUSTER) {
-        if (group == 0) store_remote(&parts[0][rank][lane], 0, make_float4(total.x, total.y, 0.f, 0.f));
+        // (the places that the last step did not use: the first block may still be reading those)
+        if (group == 0) store_remote(&parts[buf][rank][lane], 0, make_float4(total.x, total.y, 0.f, 0.f));
         cluster_sync();
         if (rank == 0 && group == 0) {
             total = f2(0.f);
-            for (int q = 0; q < K; ++q) total = add2(total, make_float2(parts[0][q][lane].x, parts[0][q][lane].y));
+            for (int q = 0; q < K; ++q) total = add2(total, make_float2(parts[buf][q][lane].x, parts[buf][q][lane].y));
         }
     }
     if (rank == 0 && group == 0) store<float, true>(a.partials + b * a.channels + c0, total, lane, have);
