@@ -21,6 +21,7 @@ struct GlrArgs {
     void* y;
     float* chunk_states;  // may be null
     float* final_state;   // may be null (not in the step)
+    unsigned int* status = nullptr;  // the device's status word, for clusters
     int64_t first;        // strip of channels (of all batch rows) that clusters start with, and single blocks end before
 };
 

@@ -252,6 +252,42 @@ __device__ __forceinline__ void store_remote(const void* here, uint32_t rank, fl
                  : "memory");
 }
 
+// The same as a message: it counts on `bar` in that block, and nothing waits for what was stored before it, as the
+// cluster's barrier does for y on its way to memory (forward, 1 x 4096 x 1024 in bf16: 24 us, with the barrier 28;
+// backward, whose registers are all taken, 40 with messages and 34 with the barrier).
+__device__ __forceinline__ void send(const void* here, uint64_t* bar, uint32_t rank, float4 v) {
+    uint32_t at, count;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(here)), "r"(rank));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(count) : "r"(smem_u32(bar)), "r"(rank));
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(at),
+                 "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(count)
+                 : "memory");
+}
+
+// What a block of a cluster needs to take messages: two barriers in turn, and whether a wait has run out (the status word
+// says so, and later waits end at once).
+struct Mail {
+    uint64_t bars[2];
+    int abort;
+    int pad;
+};
+__device__ __forceinline__ void open_mail(Mail& m) {  // (a cluster_sync has to follow)
+    if (threadIdx.x == 0) {
+        mbar_init(&m.bars[0], 1), mbar_init(&m.bars[1], 1);
+        fence_barrier_init();
+        m.abort = 0;
+    }
+}
+// All threads, after the sends of exchange `count` (from 0): until `bytes` have come to this block.
+__device__ __forceinline__ void take_mail(Mail& m, uint32_t count, uint32_t bytes, unsigned int* status) {
+    uint64_t* bar = &m.bars[count & 1];
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, bytes);
+    if (!mbar_wait(bar, (count >> 1) & 1, &m.abort)) {
+        m.abort = 1;
+        if (status) atomicExch(status, kStatusTimeout);
+    }
+}
+
 // How all of a call's rows lie (pointers that are null do not count).
 inline Rows rows_of(const void* const* p, const int64_t* strides, int count, int64_t channels, int bytes) {
     uint64_t all = (uint64_t)channels * bytes;
@@ -259,15 +295,15 @@ inline Rows rows_of(const void* const* p, const int64_t* strides, int count, int
     return all % 16 == 0 ? kRows16 : all % (2 * bytes) == 0 ? kRowsPair : kRowsOne;
 }
 
-// Blocks that split a sequence, of which `per_sm` fit on an SM at once: eight or four while all
-// of them are there at once and have a tile each, else one (an exchange between blocks costs more than it
-// gives where strips alone fill half of the GPU).  1 x 4096 tokens, forward / backward, us with 1, 4 and 8:
-// 32 strips 52, 38, 28 / 104, 46, 34; 64 strips 52, 44, 36 / 108, 56, 67; 100 strips 54, 52, 56 / 112, 65, 71;
-// 128 strips 54, 56, 61 / 114, 104, 95.
-inline int glr_cluster(int64_t strips, int64_t tiles, int per_sm) {
-    const int64_t sms = sm_count() > 0 ? sm_count() : 152;
-    if (tiles >= 8 && 8 * strips <= per_sm * sms) return 8;
-    return tiles >= 4 && 4 * strips <= 3 * sms ? 4 : 1;
+// Blocks that split a sequence: eight or four while they are at most three to an SM and have a tile each,
+// else one (an exchange between blocks costs more than it gives where strips alone fill half of the GPU).
+// 1 x 4096 tokens in bf16, us with 1, 4 and 8.  Forward: 32 strips 50, 28, 24; 64 strips 52, 34, 31 (gated 63, 38, 48);
+// 100 strips 52, 38, 44; 128 strips 52, 45, 50 (gated 63, 64, 69).  Backward: 32 strips 104, 46, 34; 64 strips
+// 108, 56, 67; 100 strips 112, 65, 71; 128 strips 114, 104, 95.
+inline int glr_cluster(int64_t strips, int64_t tiles) {
+    const int64_t most = 3 * (int64_t)(sm_count() > 0 ? sm_count() : 152);
+    if (tiles >= 8 && 8 * strips <= most) return 8;
+    return tiles >= 4 && 4 * strips <= most ? 4 : 1;
 }
 
 // `beside`: the kernel may start while the one before it ends (of other strips), for whose end it waits before its own.
@@ -310,7 +346,7 @@ cudaError_t launch_all(void (*one)(Args, int), void (*some)(Args, int), Args a, 
                        int bytes_one, int bytes_some, cudaStream_t st) {
     const int64_t tiles = (a.seqlen + kTile - 1) / kTile, sms = sm_count() > 0 ? sm_count() : 152, places = per_sm * sms;
     const int64_t strips = a.batch * per_row, left = strips % sms;
-    const int K = glr_cluster(strips, tiles, per_sm);
+    const int K = glr_cluster(strips, tiles);
     const bool split = strips > places && strips < 2 * places && left > 0 && 8 * left <= places && tiles >= 16;
     a.first = K > 1 ? 0 : split ? strips - left : strips;
     if (K == 1) {

@@ -8,7 +8,7 @@
 // the groups exchange these maps through shared memory, one barrier a tile, and each then runs its
 // tokens from the state that enters them.  Inputs come through shared memory, each warp's to its own
 // place, tiles ahead.  Where strips are too few to fill the GPU, the blocks of a cluster take a
-// sequence's tiles in turn and exchange their tiles' maps through distributed shared memory.
+// sequence's tiles in turn and send one another their tiles' maps.
 // About 32 instructions an element (a third of them the gates', the rest the decay's, the exchange's and
 // the loads') leave 60 % of the issue slots used by 16 warps of 128 registers: that is what bounds it next to
 // memory.  16 x 2048 x 4096 in bf16: 183 us, 5.9 TB/s; 4 x 8192 x 4096, 512 strips of which some SMs have three
@@ -33,7 +33,7 @@ constexpr int kWarpsOf = 16;
 template <typename T, bool GATED, int LANES>
 constexpr int smem_bytes(bool cluster) {
     return kStages<T> * kGroups * LANES * 2 * (3 + GATED) * kTok * (int)sizeof(T) +
-           (2 * kGroups + (cluster ? 2 * 8 : 0)) * LANES * (int)sizeof(float4);
+           (2 * kGroups + (cluster ? 2 * 8 : 0)) * LANES * (int)sizeof(float4) + (cluster ? (int)sizeof(Mail) + 8 : 0);
 }
 
 // CLUSTER: K blocks take a sequence's tiles in turn, else K is 1.
@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(kGroups* LANES, kWarpsOf * 32 / (kGroups * LAN
     float4(*sums)[kGroups][LANES] = reinterpret_cast<float4(*)[kGroups][LANES]>(smem);
     float4(*parts)[8][LANES] = reinterpret_cast<float4(*)[8][LANES]>(sums + 2);
     T* ring = reinterpret_cast<T*>(parts + (CLUSTER ? 2 : 0));
+    Mail& mail = *reinterpret_cast<Mail*>(ring + S * kWarps * NT * kPlace);  // (behind the ring; of clusters)
     if (!CLUSTER) K = 1;
     const int warp = threadIdx.x / 32, group = threadIdx.x / LANES, lane = threadIdx.x % LANES, wl = threadIdx.x % 32;
     const int rank = CLUSTER ? (int)cluster_rank() : 0;
@@ -84,7 +85,10 @@ __global__ void __launch_bounds__(kGroups* LANES, kWarpsOf * 32 / (kGroups * LAN
         commit();
     };
     griddep_launch_dependents();  // (what is launched beside this takes other strips)
-    if (CLUSTER) cluster_sync();  // the others' shared memory is there
+    if constexpr (CLUSTER) {
+        open_mail(mail);
+        cluster_sync();  // the others' shared memory is there
+    }
     for (int s = 0; s < S; ++s) ahead(s);
     const int steps = (tiles + K - 1) / K;
     auto walk = [&](auto wide) {
@@ -126,8 +130,8 @@ __global__ void __launch_bounds__(kGroups* LANES, kWarpsOf * 32 / (kGroups * LAN
                     const float2 sa = make_float2(s.x, s.y);
                     PB = fma2(sa, PB, make_float2(s.z, s.w)), PA = mul2(PA, sa);
                 }
-                if (group < K) store_remote(&parts[buf][rank][lane], group, make_float4(PA.x, PA.y, PB.x, PB.y));
-                cluster_sync();
+                if (group < K) send(&parts[buf][rank][lane], &mail.bars[buf], group, make_float4(PA.x, PA.y, PB.x, PB.y));
+                take_mail(mail, j, K * LANES * (int)sizeof(float4), a.status);
                 for (int q = 0; q < K; ++q) {
                     if (q == rank) start = carry;
                     const float4 s = parts[buf][q][lane];
@@ -180,11 +184,15 @@ __global__ void __launch_bounds__(kGroups* LANES, kWarpsOf * 32 / (kGroups * LAN
         for (int64_t g = tiles + rank * kGroups + group; g < nc; g += K * kGroups)
             store<float, true>(a.chunk_states + (b * nc + g) * a.channels + c0, carry, lane, have);
     }
-    if (CLUSTER) griddep_wait();
+    if constexpr (CLUSTER) {
+        cluster_sync();  // nobody sends to a block that is gone
+        griddep_wait();
+    }
 }
 
 template <typename T, Rows ROWS, bool GATED>
-cudaError_t launch(const GlrArgs& a, cudaStream_t st) {
+cudaError_t launch(GlrArgs a, cudaStream_t st) {
+    a.status = device_status_word();
     constexpr int LANES = kLanes;
     const int64_t per_row = (a.channels + 2 * LANES - 1) / (2 * LANES);
     return launch_all(k_glr_fwd<T, ROWS, GATED, LANES, false>, k_glr_fwd<T, ROWS, GATED, LANES, true>, a, per_row,
