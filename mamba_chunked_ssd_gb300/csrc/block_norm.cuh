@@ -26,10 +26,15 @@ struct Plan {
     int Q, threads;
     int64_t walkers;
 };
-// `most`: threads of a block; `resident`: threads of an SM at once.
-inline Plan plan_of(int64_t rows, int64_t channels, int most, int resident) {
+// `most`: threads of a block, and of an SM at once.  Rows of one block where it has places for them; else, as long as eight
+// take a row, blocks of half as many threads: while one waits for its cluster the SM has another.  In bf16, gated, backward
+// 4096 x 8192 141 us, with blocks of 512 threads 153, 2048 x 8200 101 and 119; forward 2048 x 8200 52, with blocks of
+// 1024 threads 65, 2048 x 16384 79 and 83; but backward 16384 x 4096 one block of 512 threads 187, two of 256 251.
+inline Plan plan_of(int64_t rows, int64_t channels, int most) {
     Plan p = {1, 32, 1};
-    while (p.Q * (int64_t)most * kPer < channels) p.Q *= 2;
+    const int resident = most;
+    if (channels > most * kPer && channels <= 8 * (most / 2) * kPer) most /= 2;
+    while (p.Q * (int64_t)most * kPer < channels) ++p.Q;
     p.threads = (int)((share_of(channels, p.Q) / kPer + 31) / 32 * 32);
     const int sms = sm_count();
     int64_t per_sm = resident / p.threads;
@@ -38,12 +43,13 @@ inline Plan plan_of(int64_t rows, int64_t channels, int most, int resident) {
     p.walkers = imin64(rows, fit < 1 ? 1 : fit);
     return p;
 }
+// (`p.walkers` may become less.)
 template <typename Args>
-cudaError_t launch_rows(void (*kernel)(Args, int), const Args& a, const Plan& p, int bytes, cudaStream_t st) {
+cudaError_t launch_rows(void (*kernel)(Args, int), const Args& a, Plan& p, int64_t rows, int bytes, cudaStream_t st) {
     const cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kernel), bytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.walkers * p.Q));
+    cfg.gridDim = dim3((unsigned)p.Q);
     cfg.blockDim = dim3((unsigned)p.threads);
     cfg.dynamicSmemBytes = (size_t)bytes;
     cfg.stream = st;
@@ -53,47 +59,59 @@ cudaError_t launch_rows(void (*kernel)(Args, int), const Args& a, const Plan& p,
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.Q > 1 ? 1 : 0;
+    int there = 0;  // clusters that find places: they do not reach across the GPU's parts, which have odd numbers of SMs
+    if (p.Q > 2 && p.walkers < rows) {
+        if (cudaOccupancyMaxActiveClusters(&there, kernel, &cfg) == cudaSuccess && there > 0)
+            p.walkers = imin64(p.walkers, there);
+        else cudaGetLastError();
+    }
+    cfg.gridDim = dim3((unsigned)(p.walkers * p.Q));
     const cudaError_t launched = cudaLaunchKernelEx(&cfg, kernel, a, p.Q);
     return launched == cudaSuccess ? cudaGetLastError() : (cudaGetLastError(), launched);
 }
 
-// Places for partial sums; two of each in turn, so that one barrier a sum is enough: who
-// writes a place has met, since it was read, at the barrier of the sum between.
+// Places for partial sums; two of each in turn, so that one barrier a sum is enough: who writes or sends to a place
+// has met, since it was read, at the barrier (and the messages) of the sum between.
 template <int N>
 struct Sums {
     float warp[2][N][32];
     float block[2][8][N];
+    glr::Mail mail;
 };
 
-// The sum over a cluster's blocks of values that all threads of a block have.
+// The blocks that share a row, and this one's place among them.
+template <bool CLUSTER>
+struct Share {
+    int blocks, rank;
+    unsigned int* status;
+    __device__ __forceinline__ int Q() const { return CLUSTER ? blocks : 1; }
+};
+
+// The sum over a cluster's blocks of values that all threads of a block have; `count`: how many came before.
 template <int N>
-__device__ __forceinline__ void cluster_sums(float (&v)[N], Sums<N>& s, int turn, int Q, int rank) {
-    if (threadIdx.x < Q) {
+__device__ __forceinline__ void cluster_sums(float (&v)[N], Sums<N>& s, int count, const Share<true>& by) {
+    float(*part)[N] = s.block[count & 1];
+    if (threadIdx.x < by.Q()) {
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            uint32_t at;
-            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                         : "=r"(at)
-                         : "r"(tc::smem_u32(&s.block[turn][rank][k])), "r"(threadIdx.x));
-            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v[k]) : "memory");
-        }
+        for (int k = 0; k < N; ++k) glr::send(&part[by.rank][k], &s.mail.bars[count & 1], threadIdx.x, v[k]);
     }
-    glr::cluster_sync();
+    glr::take_mail(s.mail, count, by.Q() * N * (int)sizeof(float), by.status);
 #pragma unroll
     for (int k = 0; k < N; ++k) {
         v[k] = 0.f;
-        for (int q = 0; q < Q; ++q) v[k] += s.block[turn][q][k];
+        for (int q = 0; q < by.Q(); ++q) v[k] += part[q][k];
     }
 }
 
 // A value's sum over a block's threads and over the Q blocks of a cluster, in a fixed order.
-__device__ __forceinline__ void group_sums(float (&v)[1], Sums<1>& s, int& turn, int Q, int rank) {
+template <bool CLUSTER>
+__device__ __forceinline__ void group_sums(float (&v)[1], Sums<1>& s, int& count, const Share<CLUSTER>& by) {
     float x = v[0];
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
     const int warps = blockDim.x / 32, lane = threadIdx.x & 31;
-    if (warps > 1 || Q > 1) {
-        turn ^= 1;
+    if (warps > 1 || CLUSTER) {
+        const int turn = count & 1;
         if (lane == 0) s.warp[turn][0][threadIdx.x >> 5] = x;
         __syncthreads();
         x = lane < warps ? s.warp[turn][0][lane] : 0.f;
@@ -101,11 +119,13 @@ __device__ __forceinline__ void group_sums(float (&v)[1], Sums<1>& s, int& turn,
         for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
     }
     v[0] = x;
-    if (Q > 1) cluster_sums(v, s, turn, Q, rank);
+    if constexpr (CLUSTER) cluster_sums(v, s, count, by);
+    ++count;
 }
 // Three at once (and a fourth that is 0): half of the lanes go on with two of them, a quarter with each.
 // Blocks of up to 16 warps.
-__device__ __forceinline__ void group_sums(float (&v)[3], Sums<3>& s, int& turn, int Q, int rank) {
+template <bool CLUSTER>
+__device__ __forceinline__ void group_sums(float (&v)[3], Sums<3>& s, int& count, const Share<CLUSTER>& by) {
     const int lane = threadIdx.x & 31, warps = blockDim.x / 32;
     const bool high = lane & 16, odd = lane & 8;
     float a = (high ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, high ? v[0] : v[2], 16);
@@ -113,8 +133,8 @@ __device__ __forceinline__ void group_sums(float (&v)[3], Sums<3>& s, int& turn,
     a = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);  // lanes 8 k .. 8 k + 7: value k
 #pragma unroll
     for (int m = 4; m > 0; m >>= 1) a += __shfl_xor_sync(0xffffffffu, a, m);
-    if (warps > 1 || Q > 1) {
-        turn ^= 1;
+    if (warps > 1 || CLUSTER) {
+        const int turn = count & 1;
         const int k = lane >> 3, w = lane & 7;
         if (w == 0 && k < 3) s.warp[turn][k][threadIdx.x >> 5] = a;
         __syncthreads();
@@ -125,7 +145,8 @@ __device__ __forceinline__ void group_sums(float (&v)[3], Sums<3>& s, int& turn,
     }
 #pragma unroll
     for (int k = 0; k < 3; ++k) v[k] = __shfl_sync(0xffffffffu, a, 8 * k);
-    if (Q > 1) cluster_sums(v, s, turn, Q, rank);
+    if constexpr (CLUSTER) cluster_sums(v, s, count, by);
+    ++count;
 }
 
 // How a thread's eight channels lie: in groups of GRP neighbouring ones, group i the (threadIdx + i blockDim)-th

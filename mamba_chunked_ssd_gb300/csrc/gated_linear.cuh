@@ -80,6 +80,7 @@ struct BlockNormArgs {
     void* y;  // with the norm before
     float eps;
     bool post, pre;
+    unsigned int* status = nullptr;  // the device's status word, for clusters
 };
 
 struct BlockNormBwdArgs {
@@ -103,6 +104,7 @@ struct BlockNormBwdArgs {
     float eps;
     bool post, pre;
     float* partials;
+    unsigned int* status = nullptr;  // the device's status word, for clusters
 };
 
 // out[c] = sum over k < rows of partials[k, c] (/ by[c]), for up to three outputs that lie side by

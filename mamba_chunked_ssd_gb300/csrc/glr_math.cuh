@@ -263,6 +263,13 @@ __device__ __forceinline__ void send(const void* here, uint64_t* bar, uint32_t r
                  "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(count)
                  : "memory");
 }
+__device__ __forceinline__ void send(const void* here, uint64_t* bar, uint32_t rank, float v) {
+    uint32_t at, count;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(here)), "r"(rank));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(count) : "r"(smem_u32(bar)), "r"(rank));
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(at), "f"(v), "r"(count)
+                 : "memory");
+}
 
 // What a block of a cluster needs to take messages: two barriers in turn, and whether a wait has run out (the status word
 // says so, and later waits end at once).

@@ -21,15 +21,18 @@ template <typename T>
 constexpr int ring_rows() { return 2; }
 constexpr int kMost = 1024;  // threads of a block, and of an SM (64 registers each)
 
-template <typename T, typename R, int GRP, bool GATED>
+// CLUSTER: Q blocks share a row, else Q is 1.
+template <typename T, typename R, int GRP, bool GATED, bool CLUSTER>
 __global__ void __launch_bounds__(kMost, 1) k_block_norm(const BlockNormArgs a, int Q) {
     constexpr int kRing = ring_rows<T>();
     using InT = RowIn<T, GRP>;
     using InR = RowIn<R, GRP>;
     __shared__ Sums<1> smem;
-    int turn = 0;
-    extern __shared__ __align__(16) uint8_t ring[];
-    const int rank = Q > 1 ? (int)glr::cluster_rank() : 0;
+    int count = 0;
+    extern __shared__ __align__(128) uint8_t ring[];
+    if (!CLUSTER) Q = 1;
+    const int rank = CLUSTER ? (int)glr::cluster_rank() : 0;
+    const Share<CLUSTER> by = {Q, rank, a.status};
     const uint32_t rows = (uint32_t)a.rows, walker = blockIdx.x / Q, walkers = gridDim.x / Q;  // (rows < 2^31)
     const int64_t c0 = rank * share_of(a.channels, Q);
     const int n = (int)imin64(a.channels - c0, share_of(a.channels, Q));  // this block's channels
@@ -68,7 +71,10 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm(const BlockNormArgs a, 
         if (GATED) InT::clear(at + bx, n);
         if (a.res) InR::clear(at + at_res, n);
     }
-    if (Q > 1) glr::cluster_sync();  // the others' shared memory is there
+    if constexpr (CLUSTER) {
+        glr::open_mail(smem.mail);
+        glr::cluster_sync();  // the others' shared memory is there
+    }
     auto finish = [&] { x.finish(), z.finish(), res.finish(); };
     for (int k = 0; k < kRing; ++k) ahead(k), finish();
     RowOut<R, GRP> out;
@@ -101,7 +107,7 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm(const BlockNormArgs a, 
 #pragma unroll
             for (int i = 0; i < 4; ++i) s = fma2(f[i], f[i], s);
             float ss[1] = {sum_of(s)};
-            group_sums(ss, smem, turn, Q, rank);
+            group_sums(ss, smem, count, by);
             k1 = rsqrtf(fmaf(ss[0], inv, a.eps));
         }
         float2 s = f2(0.f);
@@ -115,7 +121,7 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm(const BlockNormArgs a, 
         out.write(n, v, so);
         if (a.pre) {
             float ss[1] = {sum_of(s)};
-            group_sums(ss, smem, turn, Q, rank);
+            group_sums(ss, smem, count, by);
             const float k2 = rsqrtf(fmaf(ss[0], inv, a.eps));
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = mul2(mul2(v[i], f2(k2)), w2[i]);
@@ -123,14 +129,18 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm(const BlockNormArgs a, 
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    if constexpr (CLUSTER) glr::cluster_sync();  // nobody sends to a block that is gone
 }
 
 template <typename T, typename R, int GRP>
-cudaError_t launch_g(const BlockNormArgs& a, cudaStream_t st) {
-    const Plan p = plan_of(a.rows, a.channels, kMost, kMost);
+cudaError_t launch_g(BlockNormArgs a, cudaStream_t st) {
+    Plan p = plan_of(a.rows, a.channels, kMost);
+    if (p.Q > 1) a.status = device_status_word();
     const int bx = RowIn<T, GRP>::place_bytes(p.threads), br = RowIn<R, GRP>::place_bytes(p.threads);
     const int bytes = ring_rows<T>() * (bx * (a.z ? 2 : 1) + (a.res ? br : 0));
-    return launch_rows(a.z ? k_block_norm<T, R, GRP, true> : k_block_norm<T, R, GRP, false>, a, p, bytes, st);
+    if (p.Q > 1)
+        return launch_rows(a.z ? k_block_norm<T, R, GRP, true, true> : k_block_norm<T, R, GRP, false, true>, a, p, a.rows, bytes, st);
+    return launch_rows(a.z ? k_block_norm<T, R, GRP, true, false> : k_block_norm<T, R, GRP, false, false>, a, p, a.rows, bytes, st);
 }
 
 template <typename T, typename R>

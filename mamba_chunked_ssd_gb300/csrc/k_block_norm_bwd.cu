@@ -10,10 +10,10 @@
 // Two sums over a row's threads: x^2, r^2 and w2 dy r together, then w1 q k1 x.
 // A thread has eight channels, which it keeps while it walks down the rows: weights, and the sums
 // over the rows, stay in its registers; the sums of all walkers are added up by a second kernel.  Rows of
-// more than 4096 channels are split between the blocks of a cluster, which wait for one another twice a row.
+// more than 4096 channels are split between the blocks of a cluster, which send one another their sums, twice a row.
 // Rows come through shared memory, one or two ahead.  About 55 instructions an element and one block of 512
 // threads to an SM, which waits at two barriers a row, bound it next to memory: 32768 x 4096 in bf16, gated, 349 us, 6.2
-// TB/s; 8192 x 4096 with an fp32 residual 110 us, 5.5 TB/s; 4096 x 8192 212 us, 2.5 TB/s.  (Two rows at a
+// TB/s; 8192 x 4096 with an fp32 residual 107 us, 5.6 TB/s; 4096 x 8192 142 us, 3.8 TB/s.  (Two rows at a
 // time, for half as many barriers: 581 us, their inputs take the registers; blocks of 256 threads and
 // clusters from 2048 channels on 716.)
 #include "block_norm.cuh"
@@ -28,16 +28,18 @@ template <typename T>
 constexpr int ring_rows() { return sizeof(T) == 2 ? 3 : 2; }
 constexpr int kMost = 512;  // threads of a block, and of an SM (128 registers each)
 
-// FULL: both norms and both gradients of residuals are there.
-template <typename T, typename R, int GRP, bool GATED, bool FULL>
+// CLUSTER: Q blocks share a row, else Q is 1.  FULL: both norms and both gradients of residuals are there.
+template <typename T, typename R, int GRP, bool GATED, bool CLUSTER, bool FULL>
 __global__ void __launch_bounds__(kMost, 1) k_block_norm_bwd(const BlockNormBwdArgs a, int Q) {
     const bool pre = FULL || a.pre, post = FULL || a.post, dout = FULL || a.dout, has_dres = FULL || a.dres;
     constexpr int kRing = ring_rows<T>();
     __shared__ Sums<3> smem3;
     __shared__ Sums<1> smem1;
-    int turn3 = 0, turn1 = 0;
-    extern __shared__ __align__(16) uint8_t ring[];
-    const int rank = Q > 1 ? (int)glr::cluster_rank() : 0;
+    int count3 = 0, count1 = 0;
+    extern __shared__ __align__(128) uint8_t ring[];
+    if (!CLUSTER) Q = 1;
+    const int rank = CLUSTER ? (int)glr::cluster_rank() : 0;
+    const Share<CLUSTER> by = {Q, rank, a.status};
     using InT = RowIn<T, GRP>;
     using InR = RowIn<R, GRP>;
     const uint32_t rows = (uint32_t)a.rows, walker = blockIdx.x / Q, walkers = gridDim.x / Q;  // (rows < 2^31)
@@ -85,7 +87,10 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm_bwd(const BlockNormBwdA
         if (dout) InR::clear(at + at_dr, n);
     }
     tc::griddep_launch_dependents();  // the sum over the walkers may be launched; it waits for this grid's end
-    if (Q > 1) glr::cluster_sync();  // the others' shared memory is there
+    if constexpr (CLUSTER) {
+        glr::open_mail(smem3.mail), glr::open_mail(smem1.mail);
+        glr::cluster_sync();  // the others' shared memory is there
+    }
     auto finish = [&] { x.finish(), z.finish(), dy.finish(), r.finish(), dr.finish(); };
     for (int k = 0; k < kRing; ++k) ahead(k), finish();
     RowOut<T, GRP> dx, dz;
@@ -130,7 +135,7 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm_bwd(const BlockNormBwdA
                 s[2] = fma2(mul2(fd[i], w2[i]), fr[i], s[2]);
             }
             float sums[3] = {sum_of(s[0]), sum_of(s[1]), sum_of(s[2])};
-            group_sums(sums, smem3, turn3, Q, rank);
+            group_sums(sums, smem3, count3, by);
             if (post) k1 = rsqrtf(fmaf(sums[0], inv, a.eps));
             if (pre) k2 = rsqrtf(fmaf(sums[1], inv, a.eps));
             m2 = -k2 * k2 * (sums[2] * inv);
@@ -157,7 +162,7 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm_bwd(const BlockNormBwdA
         float m1 = 0.f;
         if (post) {
             float sums[1] = {sum_of(last)};
-            group_sums(sums, smem1, turn1, Q, rank);
+            group_sums(sums, smem1, count1, by);
             m1 = -sums[0] * inv;
         }
 #pragma unroll
@@ -169,24 +174,25 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm_bwd(const BlockNormBwdA
     store_weight<GRP>(part, n, s1);
     store_weight<GRP>(part + a.channels, n, s2);
     store_weight<GRP>(part + 2 * a.channels, n, s3);
+    if constexpr (CLUSTER) glr::cluster_sync();  // nobody sends to a block that is gone
 }
 
 // (In bf16, 32768 x 4096, gated: 351 us, without it 390; narrow groups are bound by their loads.)
-template <typename T, typename R, int GRP>
+template <typename T, typename R, int GRP, bool CLUSTER>
 auto pick(const BlockNormBwdArgs& a) {
     if constexpr (GRP >= 4)
         if (a.pre && a.post && a.dout && a.dres)
-            return a.z ? k_block_norm_bwd<T, R, GRP, true, true> : k_block_norm_bwd<T, R, GRP, false, true>;
-    return a.z ? k_block_norm_bwd<T, R, GRP, true, false> : k_block_norm_bwd<T, R, GRP, false, false>;
+            return a.z ? k_block_norm_bwd<T, R, GRP, true, CLUSTER, true> : k_block_norm_bwd<T, R, GRP, false, CLUSTER, true>;
+    return a.z ? k_block_norm_bwd<T, R, GRP, true, CLUSTER, false> : k_block_norm_bwd<T, R, GRP, false, CLUSTER, false>;
 }
 
 template <typename T, typename R, int GRP>
-cudaError_t launch_g(const BlockNormBwdArgs& a, cudaStream_t st) {
-    const Plan p = plan_of(a.rows, a.channels, kMost, kMost);
+cudaError_t launch_g(BlockNormBwdArgs a, cudaStream_t st) {
+    Plan p = plan_of(a.rows, a.channels, kMost);
+    if (p.Q > 1) a.status = device_status_word();
     const int bx = RowIn<T, GRP>::place_bytes(p.threads), br = RowIn<R, GRP>::place_bytes(p.threads);
     const int bytes = ring_rows<T>() * (bx * (1 + (a.z != nullptr) + a.pre) + br * (a.pre + (a.dout != nullptr)));
-    const cudaError_t e =
-        launch_rows(pick<T, R, GRP>(a), a, p, bytes, st);
+    const cudaError_t e = launch_rows(p.Q > 1 ? pick<T, R, GRP, true>(a) : pick<T, R, GRP, false>(a), a, p, a.rows, bytes, st);
     if (e != cudaSuccess || (!a.dpost && !a.dscale && !a.dpre)) return e;
     return launch_sum_rows(a.partials, p.walkers, {a.dpost, a.channels}, {a.dscale, a.channels}, {a.dpre, a.channels},
                            nullptr, st);
@@ -211,7 +217,7 @@ cudaError_t launch_t(const BlockNormBwdArgs& a, cudaStream_t st) {
 }  // namespace
 
 int64_t block_norm_bwd_partials(int64_t rows, int64_t channels) {
-    return plan_of(rows, channels, kMost, kMost).walkers * 3 * channels;
+    return plan_of(rows, channels, kMost).walkers * 3 * channels;
 }
 
 cudaError_t launch_block_norm_bwd(const BlockNormBwdArgs& a, bool bf16, bool res_bf16, cudaStream_t st) {
