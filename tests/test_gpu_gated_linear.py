@@ -493,6 +493,24 @@ def test_block_norm_numbers_of_rows(rows, C, dtype, rdtype):
 
 
 @DTYPES
+@pytest.mark.parametrize("rows,C", [(400, 8200), (260, 16400)])
+def test_block_norm_rows_of_clusters_captured_and_replayed(rows, C, dtype, rdtype):
+    """More rows than clusters at once, each with many exchanges; a replay gives what the calls gave, bit for bit."""
+    d, res, dr, dy = norm_inputs(rows, C, dtype, rdtype, seed=C)
+    out, y, got = check_norm(d, res, dr, dy)
+    names = ("residual_out", "y", "dx", "dz", "dresidual", "dpost_weight", "dscale", "dpre_weight")
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=stream):
+        out2, y2 = bd.mamba2_block_norm_fwd(**d, residual=res)
+        got2 = bd.mamba2_block_norm_bwd(dr, dy, residual_out=out2, **d)
+    graph.replay()
+    torch.cuda.synchronize()
+    for name, a, b in zip(names, (out2, y2, *got2), (out, y, *got)):
+        assert torch.equal(a, b), name
+
+
+@DTYPES
 @pytest.mark.parametrize("C", [40, 1001, 4608])
 @pytest.mark.parametrize("gated,post,pre,scale", [(a, b, c, s) for a in (0, 1) for b in (0, 1) for c in (0, 1)
                                                   for s in (0, 1)])
