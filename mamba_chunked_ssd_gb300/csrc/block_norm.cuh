@@ -152,8 +152,8 @@ __device__ __forceinline__ void group_sums(float (&v)[3], Sums<3>& s, int& count
 // How a thread's eight channels lie: in groups of GRP neighbouring ones, group i the (threadIdx + i blockDim)-th
 // of the block's.  GRP > 1: rows start on a group's bytes and have whole groups, and a thread copies what it
 // reads itself.  GRP = 1: rows lie in shared memory as they do in memory, from the 16-byte boundary
-// before their start; the threads' copies of 16 bytes (of single elements at a row's ends) are there for all
-// after a barrier.  (16384 x 2050 in bf16, gated, backward: groups of two 267 us, as whole rows 308.)
+// before their start; the threads' copies are there for all after a barrier.  (In bf16, gated, backward: 16384 x 2050 in
+// groups of two 228 us, 16384 x 2051 as whole rows 323.)
 template <int GRP>
 __device__ __forceinline__ int channel(int i) {
     return GRP * ((int)threadIdx.x + i / GRP * (int)blockDim.x) + i % GRP;
@@ -176,6 +176,11 @@ __device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
     else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES) : "memory");
 }
 
+// 16 bytes, of which `bytes` are read and the others are zero.
+__device__ __forceinline__ void copy_piece(uint32_t to, const void* from, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
+
 // A walker's rows of one input.
 template <typename E, int GRP>
 struct RowIn {
@@ -183,16 +188,14 @@ struct RowIn {
     static constexpr bool kOwn = GRP > 1;
     using Unit = typename Word<kBytes>::type;
     const E* next;  // kOwn: this thread's first channel of the row that is fetched next; else the block's first
-    // an element at a row's end that is too small for an asynchronous copy, on its way to its place
-    Unit* edge_to;
-    Unit edge;
+    bool first;  // (bf16, not kOwn) the row that is fetched next is less than 16 bytes behind the tensor's start
 
     static __host__ __device__ __forceinline__ int place_bytes(int threads) {
         return threads * kPer * (int)sizeof(E) + (kOwn ? 0 : 32);
     }
     __device__ __forceinline__ void start(const void* base, int64_t row, int64_t stride, int64_t c0) {
         next = static_cast<const E*>(base) + row * stride + c0 + (kOwn ? GRP * (int)threadIdx.x : 0);
-        edge_to = nullptr;
+        first = (row * stride + c0) * (int64_t)sizeof(E) < 16;
     }
     // zeros in the places of channels that are not there, which are never written again
     static __device__ __forceinline__ void clear(uint8_t* place, int n) {
@@ -210,27 +213,31 @@ struct RowIn {
             for (int i = 0; i < kGroups; ++i)
                 if (channel<GRP>(i * GRP) < n)
                     copy_async<kBytes>(tc::smem_u32(place + (i * blockDim.x + tid) * kBytes), next + i * GRP * (int)blockDim.x);
-        } else {
+        } else if constexpr (sizeof(E) == 4) {
             // the row's first elements up to the boundary, whole pieces of 16 bytes, the last elements
-            constexpr int per = 16 / (int)sizeof(E);
+            constexpr int per = 4;
             const int skip = (int)(reinterpret_cast<uintptr_t>(next) & 15);
-            const int head = min(((16 - skip) & 15) / (int)sizeof(E), n), whole = (n - head) / per, tail = head + whole * per;
-            E* to = reinterpret_cast<E*>(place + skip);
-            for (int k = tid; k < whole; k += blockDim.x) copy_async<16>(tc::smem_u32(to + head + k * per), next + head + k * per);
+            const int head = min(((16 - skip) & 15) / 4, n), whole = (n - head) / per, tail = head + whole * per;
+            const uint32_t to = tc::smem_u32(place + skip);
+            for (int k = tid; k < whole; k += blockDim.x) copy_async<16>(to + 4 * (head + k * per), next + head + k * per);
             const int end = tid < per ? tid : tail + tid - per;  // this thread's element at an end
-            if (tid < per ? tid < head : tid < 2 * per && end < n) {
-                if constexpr (sizeof(E) == 4) copy_async<4>(tc::smem_u32(to + end), next + end);
-                else edge = reinterpret_cast<const Unit*>(next)[end], edge_to = reinterpret_cast<Unit*>(to + end);
-            }
+            if (tid < per ? tid < head : tid < 2 * per && end < n) copy_async<4>(to + 4 * end, next + end);
+        } else {
+            // Single elements are too small for an asynchronous copy: pieces of 16 bytes, of which the first begins up to 14
+            // bytes before the row (in the tensor, or between its rows), and the last is read as far as the row goes.  Where
+            // the first would begin before the tensor, its elements are stored.  (16384 x 2051 in bf16, gated, forward /
+            // backward: 128 / 323 us, with a load and a store for each element of a row's ends 181 / 419.)
+            const int from = (int)(reinterpret_cast<uintptr_t>(next) & 15), to = from + n * (int)sizeof(E);
+            const uint8_t* at = reinterpret_cast<const uint8_t*>(next) - from;
+            const bool single = first && from;
+            for (int k = single ? tid + 1 : tid; k < to / 16; k += blockDim.x)
+                copy_async<16>(tc::smem_u32(place + 16 * k), at + 16 * k);
+            if (tid == 0 && to % 16 && !(single && to < 16))
+                copy_piece(tc::smem_u32(place + to / 16 * 16), at + to / 16 * 16, to % 16);
+            if (single && tid < min((16 - from) / (int)sizeof(E), n)) reinterpret_cast<E*>(place + from)[tid] = next[tid];
+            first = false;
         }
         next += step;
-    }
-    // before a barrier that comes before the row's use
-    __device__ __forceinline__ void finish() {
-        if constexpr (kBytes < 4) {
-            if (edge_to) *edge_to = edge;
-            edge_to = nullptr;
-        }
     }
     // `row`: the row's first channel in memory (but kOwn); zeros where there is no channel
     static __device__ __forceinline__ void read(const uint8_t* place, const E* row, int n, float2 (&f)[4]) {

@@ -49,7 +49,6 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm(const BlockNormArgs a, 
 
     InT x, z;
     InR res;
-    z.edge_to = nullptr, res.edge_to = nullptr;
     x.start(a.x, walker, a.x_stride, c0);
     if (GATED) z.start(a.z, walker, a.z_stride, c0);
     if (a.res) res.start(a.res, walker, a.res_stride, c0);
@@ -75,8 +74,7 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm(const BlockNormArgs a, 
         glr::open_mail(smem.mail);
         glr::cluster_sync();  // the others' shared memory is there
     }
-    auto finish = [&] { x.finish(), z.finish(), res.finish(); };
-    for (int k = 0; k < kRing; ++k) ahead(k), finish();
+    for (int k = 0; k < kRing; ++k) ahead(k);
     RowOut<R, GRP> out;
     RowOut<T, GRP> y;
     out.start(a.out, walker, a.out_stride, c0);
@@ -85,7 +83,6 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm(const BlockNormArgs a, 
     int stage = 0;
     for (uint32_t row = walker; row < rows; row += walkers) {
         glr::wait_for<kRing - 1>();
-        finish();
         if (!InT::kOwn) __syncthreads();  // the other threads' copies are there too
         const uint8_t* at = ring + stage * per_row;
         auto first = [&](auto* base, int64_t stride) { return base + row * stride + c0; };

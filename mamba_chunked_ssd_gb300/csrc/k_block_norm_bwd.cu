@@ -60,7 +60,6 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm_bwd(const BlockNormBwdA
 
     InT x, z, dy;
     InR r, dr;
-    z.edge_to = dy.edge_to = nullptr, r.edge_to = dr.edge_to = nullptr;
     x.start(a.x, walker, a.x_stride, c0);
     if (GATED) z.start(a.z, walker, a.z_stride, c0);
     if (pre) dy.start(a.dy, walker, a.dy_stride, c0), r.start(a.out, walker, a.out_stride, c0);
@@ -91,8 +90,7 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm_bwd(const BlockNormBwdA
         glr::open_mail(smem3.mail), glr::open_mail(smem1.mail);
         glr::cluster_sync();  // the others' shared memory is there
     }
-    auto finish = [&] { x.finish(), z.finish(), dy.finish(), r.finish(), dr.finish(); };
-    for (int k = 0; k < kRing; ++k) ahead(k), finish();
+    for (int k = 0; k < kRing; ++k) ahead(k);
     RowOut<T, GRP> dx, dz;
     RowOut<R, GRP> dres;
     dx.start(a.dx, walker, a.dx_stride, c0);
@@ -102,7 +100,6 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm_bwd(const BlockNormBwdA
     int stage = 0;
     for (uint32_t row = walker; row < rows; row += walkers) {
         glr::wait_for<kRing - 1>();
-        finish();
         if (!InT::kOwn) __syncthreads();  // the other threads' copies are there too
         const uint8_t* at = ring + stage * per_row;
         auto first = [&](auto* base, int64_t stride) { return base + row * stride + c0; };
