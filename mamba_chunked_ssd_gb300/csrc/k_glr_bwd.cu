@@ -12,7 +12,7 @@
 // from the other end, go through the same barrier.  What both halves need stays in
 // registers or in shared memory, in the places of inputs that have been used where they fit.
 // About 60 instructions an element in 16 (gated 12) warps of an SM bound it next to memory: 16 x 1024 x 4096 in bf16 196 us,
-// 4.8 TB/s, gated 243 us, 5.0 TB/s; 4 x 4096 x 4096 220 us, gated 298.
+// 4.8 TB/s, gated 243 us, 5.0 TB/s; 4 x 4096 x 4096 216 us, gated 258.
 #include <type_traits>
 
 #include "glr_math.cuh"
