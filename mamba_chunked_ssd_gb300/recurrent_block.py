@@ -110,8 +110,8 @@ def main(argv=None):
     block = RecurrentBlock(a.width, a.channels)
     n = torch.randn(a.batch, a.tokens, a.width, device="cuda").bfloat16()
     res = torch.randn(a.batch, a.tokens, a.width, device="cuda")
-    # rows of every length from L down
-    m = torch.tensor([a.tokens - a.tokens * k // (2 * a.batch) for k in range(a.batch)], dtype=torch.int32, device="cuda")
+    # rows of lengths between L and about half of it
+    m = torch.tensor([a.tokens - a.tokens * k // (2 * a.batch + 1) for k in range(a.batch)], dtype=torch.int32, device="cuda")
     nxt, out, carried, kept = block.forward(n, res, lengths=m, keep=True)
     dn, _, _, dw = block.backward(kept, torch.ones_like(nxt), torch.zeros_like(out))
     last = torch.arange(a.batch, device="cuda"), m.long() - 1
