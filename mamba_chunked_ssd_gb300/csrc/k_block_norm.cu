@@ -6,8 +6,9 @@
 // channels, which it keeps while it walks down the rows, so that the weights stay in its
 // registers, where the row stays for both sums; rows of more than 8192 channels are split
 // between the blocks of a cluster.  Rows come through shared memory, one ahead.  The two sums a row and 37
-// instructions an element bound it next to memory: 32768 x 4096 in bf16, gated, 221 us, 6.1 TB/s; 65536 x 1024 124 us, 5.4;
-// 8192 x 4096 with an fp32 residual 76 us, 5.3.
+// instructions an element bound it next to memory: 32768 x 4096 in bf16, gated, 224 us, 6.0 TB/s; 65536 x 1024 123 us, 5.5;
+// 8192 x 4096 with an fp32 residual 75 us, 5.4.  The rings start on a line of 128 bytes: 64 bytes off it 16384 x 8192, gated,
+// takes 219 us for 209, 32768 x 2560 149 for 146, but 32768 x 4096 223 for 227 and 32768 x 2048 in fp32 207 for 213.
 #include "block_norm.cuh"
 
 namespace m2 {

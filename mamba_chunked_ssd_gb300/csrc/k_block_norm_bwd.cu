@@ -12,10 +12,10 @@
 // over the rows, stay in its registers; the sums of all walkers are added up by a second kernel.  Rows of
 // more than 4096 channels are split between the blocks of a cluster, which send one another their sums, twice a row.
 // Rows come through shared memory, one or two ahead.  About 55 instructions an element and one block of 512
-// threads to an SM, which waits at two barriers a row, bound it next to memory: 32768 x 4096 in bf16, gated, 349 us, 6.2
+// threads to an SM, which waits at two barriers a row, bound it next to memory: 32768 x 4096 in bf16, gated, 350 us, 6.1
 // TB/s; 8192 x 4096 with an fp32 residual 107 us, 5.6 TB/s; 4096 x 8192 142 us, 3.8 TB/s.  (Two rows at a
 // time, for half as many barriers: 581 us, their inputs take the registers; blocks of 256 threads and
-// clusters from 2048 channels on 716.)
+// clusters from 2048 channels on 716; rings 48 bytes off a line of 128 429.)
 #include "block_norm.cuh"
 
 namespace m2 {
