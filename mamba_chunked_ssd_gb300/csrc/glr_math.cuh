@@ -48,7 +48,8 @@ __device__ __forceinline__ float2 sigmoid2(float2 x) {
 // same for every token would be multiplied by the recurrence's memory 1 / (1 - a).  p / la to la^6
 // by a Remez exchange for the relative error on -1 .. 0 (2.7e-9).  WIDE, where A is below -1:
 // la = n ln 2 + y, |y| <= ln 2 / 2, and e^la - 1 = 2^n p + (2^n - 1) without cancellation, p / y
-// to y^5 (1.1e-8); below -87 a is 1.6e-38.
+// to y^5 (1.1e-8); below -87 (kLeastLog) a is 1.6e-38.
+constexpr float kLeastLog = -87.f;
 template <bool WIDE>
 __device__ __forceinline__ void decay2(float2 la, float2& a, float2& m) {
     float2 e;  // a - 1
@@ -62,7 +63,7 @@ __device__ __forceinline__ void decay2(float2 la, float2& a, float2& m) {
         e = mul2(e, la);
         a = add2(e, f2(1.f));
     } else {
-        la.x = max_nan(la.x, -87.f), la.y = max_nan(la.y, -87.f);
+        la.x = max_nan(la.x, kLeastLog), la.y = max_nan(la.y, kLeastLog);
         // 1.5 2^23 + 127: its sum with a small number is rounded to a whole one, and ends in the bits of 2^n
         constexpr float kBig = 12582912.f + 127.f;
         const float2 t = fma2(la, f2(kLog2e), f2(kBig));
@@ -79,6 +80,13 @@ __device__ __forceinline__ void decay2(float2 la, float2& a, float2& m) {
         e = fma2(s, p, add2(s, f2(-1.f)));
     }
     m = mul2(e, fma2(e, f2(-1.f), f2(-2.f)));  // -e (e + 2)
+}
+
+// la a of that a: 0 to fp32 where a is, however far below kLeastLog la lies.
+template <bool WIDE>
+__device__ __forceinline__ float2 decay_slope2(float2 la, float2 a) {
+    if constexpr (WIDE) la.x = max_nan(la.x, kLeastLog), la.y = max_nan(la.y, kLeastLog);
+    return mul2(la, a);
 }
 
 // sqrt(m)
