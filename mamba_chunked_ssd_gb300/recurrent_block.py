@@ -10,6 +10,10 @@ sequences, ``backward`` gives the gradients of all of its inputs and weights,
 ``step`` runs one token of each sequence; the convolution's last inputs and the
 fp32 state are carried from call to call.
 
+Past a row's length n may hold anything: no result has a part of it.  The residual
+goes on there as it came (the norms know no lengths), with its own gradient: it and
+the gradients that come in have to be finite there.
+
 Run ``python -m mamba_chunked_ssd_gb300.recurrent_block`` for a training step on a ragged batch and
 a few decoded tokens on random weights (``--help`` for the sizes).
 """
@@ -88,6 +92,9 @@ class RecurrentBlock:
         dw["gates"] = flat(u).T @ flat(dgates)
         _, dw["conv"], dw["conv_bias"], dconv = bd.mamba2_causal_conv_bwd(
             du + dgates @ w["gates"].T, x, w["conv"], bias=w["conv_bias"], initial_state=conv, lengths=lengths, dx=dx)
+        if lengths is not None:  # (dproj is 0 past a row's length, but 0 times what is not finite is not)
+            past = torch.arange(n.shape[1], device=n.device) >= lengths[:, None]
+            n = n.masked_fill(past[..., None], 0)
         dw["in"] = flat(n).T @ flat(dproj)
         return dproj @ w["in"].T, dresidual, BlockState(dconv, dstate), dw
 
