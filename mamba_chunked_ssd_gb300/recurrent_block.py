@@ -74,9 +74,9 @@ class RecurrentBlock:
         kept = (n, x, z, u, r, i, y, chunks, out, res, carried.conv if carried else None, lengths) if keep else None
         return nxt, res, BlockState(conv, state), kept
 
-    def backward(self, kept, dnext, dres):
-        """Gradients from those of the next n and the next residual: (of n, of the residual, of the
-        carried state, of the weights by name)."""
+    def backward(self, kept, dnext, dres, dafter: BlockState | None = None):
+        """Gradients from those of the next n, the next residual and the state after each row's tokens
+        (None: zeros): (of n, of the residual, of the carried state, of the weights by name)."""
         w, C = self.w, self.channels
         n, x, z, u, r, i, y, chunks, out, res, conv, lengths = kept
         flat = lambda t: t.flatten(0, -2)  # noqa: E731
@@ -88,10 +88,12 @@ class RecurrentBlock:
         dx, dz = dproj.split(C, -1)
         dr, di = dgates.split(C, -1)
         du, _, _, _, dw["A"], dstate = bd.mamba2_glr_bwd(dout @ w["out"].T, u, r, i, w["A"], chunks, z=z, lengths=lengths,
+                                                         dfinal_state=dafter.state if dafter else None,
                                                          dr=dr, di=di, dz=dz)
         dw["gates"] = flat(u).T @ flat(dgates)
         _, dw["conv"], dw["conv_bias"], dconv = bd.mamba2_causal_conv_bwd(
-            du + dgates @ w["gates"].T, x, w["conv"], bias=w["conv_bias"], initial_state=conv, lengths=lengths, dx=dx)
+            du + dgates @ w["gates"].T, x, w["conv"], bias=w["conv_bias"], initial_state=conv, lengths=lengths,
+            dfinal_state=dafter.conv if dafter else None, dx=dx)
         if lengths is not None:  # (dproj is 0 past a row's length, but 0 times what is not finite is not)
             past = torch.arange(n.shape[1], device=n.device) >= lengths[:, None]
             n = n.masked_fill(past[..., None], 0)
