@@ -244,6 +244,13 @@ __device__ __forceinline__ float2 load_pair(const float* p, int lane, int have) 
     return make_float2(2 * lane < have ? p[2 * lane] : 0.f, 2 * lane + 1 < have ? p[2 * lane + 1] : 0.f);
 }
 
+// Blocks of `bytes` of shared memory each that an SM holds at once (of its 228 KB a block takes 1 KB more than it
+// asks for), of those `warps` warps of an SM that the registers are for.
+constexpr int blocks_of(int warps, int threads, int bytes) {
+    const int by_warps = warps * 32 / threads, by_bytes = 228 * 1024 / (bytes + 1024);
+    return by_warps < by_bytes ? by_warps : by_bytes;
+}
+
 // Blocks of a cluster split a sequence: each takes every K-th tile, and they exchange their tiles' summaries.
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -355,14 +362,17 @@ cudaError_t launch_strips(void (*kernel)(Args, int), const Args& a, dim3 grid, i
 // more than the GPU's places for them, the few that are left over when every SM has as many would keep a few SMs for
 // as long as all others: they are split, while the last of the others end (4 x 4096 x 4096 in bf16, gated, backward
 // 298 -> 258 us, 8 x 2048 x 2560 155 -> 126, 10 x 1024 x 2048 85 -> 71; but where all have places, 4 x 4096 x 4096,
-// 218 -> 241, and where places are taken three times, 16 x 2048 x 4096 forward, 183 -> 196).
+// 218 -> 241, and where places are taken three times, 16 x 2048 x 4096 forward, 183 -> 196).  As many are split as clusters
+// of eight blocks take the places once, three to an SM at least: in fp32 with a gate, backward, where an SM has two places,
+// 1 x 4096 x 11200 326 -> 288, on single elements 500 -> 400; 512 strips, 56 left over, 398 -> 418 and 664 -> 600.
 template <typename Args>
 cudaError_t launch_all(void (*one)(Args, int), void (*some)(Args, int), Args a, int64_t per_row, int per_sm, int threads,
                        int bytes_one, int bytes_some, cudaStream_t st) {
     const int64_t tiles = (a.seqlen + kTile - 1) / kTile, sms = sm_count() > 0 ? sm_count() : 152, places = per_sm * sms;
     const int64_t strips = a.batch * per_row, left = strips % sms;
     const int K = glr_cluster(strips, tiles);
-    const bool split = strips > places && strips < 2 * places && left > 0 && 8 * left <= places && tiles >= 16;
+    const int64_t beside = places > 3 * sms ? places : 3 * sms;
+    const bool split = strips > places && strips < 2 * places && left > 0 && 8 * left <= beside && tiles >= 16;
     a.first = K > 1 ? 0 : split ? strips - left : strips;
     if (K == 1) {
         const cudaError_t e = launch_strips(one, a, dim3((unsigned)per_row, (unsigned)a.batch), 1, threads, bytes_one, false, st);

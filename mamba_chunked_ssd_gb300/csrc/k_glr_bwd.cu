@@ -24,8 +24,8 @@ using namespace glr;
 
 constexpr int kStages = 2;
 constexpr int kLanes = 16;
-// Warps of an SM: as many as shared memory allows (4 x 4096 x 4096 in bf16: with 16 220 us, with 12 of more
-// registers each 259; gated, where 16 do not fit, 298).
+// Warps of an SM that the registers are for: as many as shared memory allows, too, but in fp32 with a gate (4 x 4096 x 4096
+// in bf16: with 16 220 us, with 12 of more registers each 259; gated, where 16 do not fit, 298).
 template <typename T, bool GATED>
 constexpr int kWarpsOf = sizeof(T) == 2 && !GATED ? 16 : 12;
 
@@ -35,6 +35,9 @@ constexpr int smem_bytes(bool cluster) {
            (4 * kGroups + (cluster ? 2 * 8 : 0)) * LANES * (int)sizeof(float4) +
            (sizeof(T) == 2 ? (2 + GATED) * kGroups * LANES * kTok * (int)sizeof(float2) : 0);
 }
+// Blocks of an SM: four of bf16 without a gate, else three, two of fp32 with a gate.
+template <typename T, bool GATED, int LANES>
+constexpr int kBlocks = blocks_of(kWarpsOf<T, GATED>, kGroups* LANES, smem_bytes<T, GATED, LANES>(false));
 
 // Two fp32 values in the places of two raw pairs (one of them where a raw pair is fp32).
 __device__ __forceinline__ void stash(uint32_t* p, uint32_t* q, float2 v) {
@@ -47,7 +50,7 @@ __device__ __forceinline__ void stash(float2* p, float2*, float2 v) { *p = v; }
 __device__ __forceinline__ float2 unstash(const float2* p, const float2*) { return *p; }
 
 template <typename T, Rows ROWS, bool GATED, int LANES, bool CLUSTER>
-__global__ void __launch_bounds__(kGroups* LANES, kWarpsOf<T, GATED> * 32 / (kGroups * LANES)) k_glr_bwd(const GlrBwdArgs a, int K) {
+__global__ void __launch_bounds__(kGroups* LANES, kBlocks<T, GATED, LANES>) k_glr_bwd(const GlrBwdArgs a, int K) {
     using W = Walk<T, ROWS, LANES>;
     constexpr int NT = 4 + GATED, S = kStages, kSub = W::kSub, kPlace = W::kPlace, kStrip = W::kStrip;
     constexpr int kWarps = kGroups / kSub, kThreads = kGroups * LANES;
@@ -280,7 +283,7 @@ cudaError_t launch(const GlrBwdArgs& a, cudaStream_t st) {
     const int64_t per_row = (a.channels + 2 * kLanes - 1) / (2 * kLanes);
     const cudaError_t e =
         launch_all(k_glr_bwd<T, ROWS, GATED, kLanes, false>, k_glr_bwd<T, ROWS, GATED, kLanes, true>, a, per_row,
-                   kWarpsOf<T, GATED> * 32 / (kGroups * kLanes), kGroups * kLanes, smem_bytes<T, GATED, kLanes>(false),
+                   kBlocks<T, GATED, kLanes>, kGroups * kLanes, smem_bytes<T, GATED, kLanes>(false),
                    smem_bytes<T, GATED, kLanes>(true), st);
     if (e != cudaSuccess) return e;
     return launch_sum_rows(a.partials, a.batch, {a.dA, a.channels}, {}, {}, a.A, st);

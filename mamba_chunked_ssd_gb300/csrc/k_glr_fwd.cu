@@ -35,10 +35,13 @@ constexpr int smem_bytes(bool cluster) {
     return kStages<T> * kGroups * LANES * 2 * (3 + GATED) * kTok * (int)sizeof(T) +
            (2 * kGroups + (cluster ? 2 * 8 : 0)) * LANES * (int)sizeof(float4) + (cluster ? (int)sizeof(Mail) + 8 : 0);
 }
+// Four blocks of an SM, three of fp32 with a gate.
+template <typename T, bool GATED, int LANES>
+constexpr int kBlocks = blocks_of(kWarpsOf, kGroups* LANES, smem_bytes<T, GATED, LANES>(false));
 
 // CLUSTER: K blocks take a sequence's tiles in turn, else K is 1.
 template <typename T, Rows ROWS, bool GATED, int LANES, bool CLUSTER>
-__global__ void __launch_bounds__(kGroups* LANES, kWarpsOf * 32 / (kGroups * LANES)) k_glr_fwd(const GlrArgs a, int K) {
+__global__ void __launch_bounds__(kGroups* LANES, kBlocks<T, GATED, LANES>) k_glr_fwd(const GlrArgs a, int K) {
     using W = Walk<T, ROWS, LANES>;
     constexpr int NT = 3 + GATED, S = kStages<T>, kSub = W::kSub, kPlace = W::kPlace, kStrip = W::kStrip;
     constexpr int kWarps = kGroups / kSub;
@@ -196,7 +199,7 @@ cudaError_t launch(GlrArgs a, cudaStream_t st) {
     constexpr int LANES = kLanes;
     const int64_t per_row = (a.channels + 2 * LANES - 1) / (2 * LANES);
     return launch_all(k_glr_fwd<T, ROWS, GATED, LANES, false>, k_glr_fwd<T, ROWS, GATED, LANES, true>, a, per_row,
-                      kWarpsOf * 32 / (kGroups * LANES), kGroups * LANES, smem_bytes<T, GATED, LANES>(false),
+                      kBlocks<T, GATED, LANES>, kGroups * LANES, smem_bytes<T, GATED, LANES>(false),
                       smem_bytes<T, GATED, LANES>(true), st);
 }
 
