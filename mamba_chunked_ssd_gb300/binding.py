@@ -583,8 +583,8 @@ def _stride(t, name):
     return 0 if t is None or t.is_contiguous() else _rows(t, name, 1)
 
 
-def _glr_args(x, r, i, z, A, y, dims, gpu):
-    """The shape of a recurrence's call on this GPU; y: the output, or its gradient."""
+def _glr_args(x, r, i, z, A, y, dims, gpu, name="y"):
+    """The shape of a recurrence's call on this GPU; y: the output, or its gradient, by its name."""
     shape, dt = x.shape, x.dtype
     if len(shape) != dims:
         raise ValueError(f"x must have {dims} dimensions, not {tuple(shape)}")
@@ -592,11 +592,11 @@ def _glr_args(x, r, i, z, A, y, dims, gpu):
         raise ValueError("r and i must be given")
     if not (_same(r, shape, dt, gpu) and _same(i, shape, dt, gpu) and _same(z, shape, dt, gpu) and
             _same(y, shape, dt, gpu)):
-        _refuse(("r", "i", "z", "y"), (r, i, z, y), shape, dt, gpu)
+        _refuse(("r", "i", "z", name), (r, i, z, y), shape, dt, gpu)
     C = shape[-1]
     _want(A, "A", torch.float32, (C,), gpu)
     return _glr_shape(shape[0], shape[1] if dims == 3 else 1, C, _stride(x, "x"), _stride(r, "r"), _stride(i, "i"),
-                      _stride(z, "z"), _stride(y, "y"), _dtype_code(x), 0)
+                      _stride(z, "z"), _stride(y, name), _dtype_code(x), 0)
 
 
 def mamba2_glr_fwd(x, r, i, A, z=None, initial_state=None, lengths=None, y=None, final_state=None,
@@ -635,7 +635,7 @@ def mamba2_glr_bwd(dy, x, r, i, A, chunk_states, z=None, dfinal_state=None, leng
     [b, C] fp32 or None, with that call's chunk_states.  Returns (dx, dr, di,
     dz or None, dA [C] fp32, dinitial_state [b, C] fp32 or None)."""
     gpu = _gpu(x, "x")
-    shape = _glr_args(x, r, i, z, A, dy, 3, gpu)
+    shape = _glr_args(x, r, i, z, A, dy, 3, gpu, "dy")
     b, L, C = x.shape
     if dy is None:
         raise ValueError("dy must be given")
