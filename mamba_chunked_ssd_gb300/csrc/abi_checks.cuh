@@ -1,6 +1,6 @@
 // abi_checks.cuh — argument checks shared by the extern "C" entry points: tensor
 // pointers are present and aligned, and no output overlaps an input or another
-// output.
+// output, where both may be runs of elements side by side in rows of a wider tensor.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -51,6 +51,33 @@ inline mamba2_status check_ptrs(const Arg* in, int nin, const Arg* out, int nout
             if (out[j].p && overlap(ro, range_of(out[j].p, out[j].bytes))) return MAMBA2_ERR_INVALID_ARG;
     }
     return MAMBA2_OK;
+}
+
+// A tensor argument: `rows` runs of `width` bytes, `stride` bytes from start to start.
+struct Tensor {
+    const void* p;
+    int64_t rows, width, stride;
+    bool optional;
+    int align;
+};
+inline Tensor sequence(const void* p, int64_t rows, int64_t channels, int64_t stride, int e, bool optional = false) {
+    return {p, rows, channels * e, stride * e, optional, e};
+}
+inline Tensor packed(const void* p, int64_t bytes, bool optional = false, int align = 16) {
+    return {p, bytes > 0, bytes, bytes, optional, align};
+}
+
+inline bool overlap(const Tensor& a, const Tensor& b) {
+    if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
+    const Range ra = range_of(a.p, (a.rows - 1) * a.stride + a.width),
+                rb = range_of(b.p, (b.rows - 1) * b.stride + b.width);
+    if (!overlap(ra, rb)) return false;
+    if (a.stride != b.stride || a.rows < 2 || b.rows < 2) return true;
+    // one stride: b's runs lie at one place between a's, or over them
+    const int64_t s = a.stride;
+    const int64_t d = rb.lo >= ra.lo ? (int64_t)((rb.lo - ra.lo) % (uint64_t)s)
+                                     : (s - (int64_t)((ra.lo - rb.lo) % (uint64_t)s)) % s;
+    return d < a.width || d + b.width > s;
 }
 
 inline mamba2_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MAMBA2_OK : MAMBA2_ERR_CUDA; }

@@ -15,33 +15,6 @@ constexpr size_t kWorkspaceAlign = 256;
 bool is_dtype(int32_t d) { return d == MAMBA2_F32 || d == MAMBA2_BF16; }
 int elt_bytes(int32_t dtype) { return dtype == MAMBA2_BF16 ? 2 : 4; }
 
-// A tensor argument: `rows` runs of `width` bytes, `stride` bytes from start to start.
-struct Tensor {
-    const void* p;
-    int64_t rows, width, stride;
-    bool optional;
-    int align;
-};
-Tensor sequence(const void* p, int64_t rows, int64_t channels, int64_t stride, int e, bool optional = false) {
-    return {p, rows, channels * e, stride * e, optional, e};
-}
-Tensor packed(const void* p, int64_t bytes, bool optional = false, int align = 16) {
-    return {p, bytes > 0, bytes, bytes, optional, align};
-}
-
-bool overlap(const Tensor& a, const Tensor& b) {
-    if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
-    const Range ra = range_of(a.p, (a.rows - 1) * a.stride + a.width),
-                rb = range_of(b.p, (b.rows - 1) * b.stride + b.width);
-    if (!m2::overlap(ra, rb)) return false;
-    if (a.stride != b.stride || a.rows < 2 || b.rows < 2) return true;
-    // one stride: b's runs lie at one place between a's, or over them
-    const int64_t s = a.stride;
-    const int64_t d = rb.lo >= ra.lo ? (int64_t)((rb.lo - ra.lo) % (uint64_t)s)
-                                     : (s - (int64_t)((ra.lo - rb.lo) % (uint64_t)s)) % s;
-    return d < a.width || d + b.width > s;
-}
-
 // Every tensor is there and aligned; no output lies over an input or another output (but for those of `same`, which
 // may be one tensor: an output's index and an input's, both with one stride).
 template <int NI, int NO>
