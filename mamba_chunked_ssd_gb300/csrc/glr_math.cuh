@@ -45,10 +45,11 @@ __device__ __forceinline__ float2 sigmoid2(float2 x) {
 
 // a = e^la and m = 1 - a^2 of la <= 0.  A polynomial p of e^la - 1 keeps m's precision for a
 // next to 1, where m sets the state's scale, and gives an a that is e^la rounded: an error of a that is the
-// same for every token would be multiplied by the recurrence's memory 1 / (1 - a).  p / la to la^6
-// by a Remez exchange for the relative error on -1 .. 0 (2.7e-9).  WIDE, where A is below -1:
+// same for every token would be multiplied by the recurrence's memory 1 / (1 - a), and p's is a share of 1 - a.
+// p / la to la^6 by a Remez exchange for the relative error on -1 .. 0 (9.3e-9 with these fp32 coefficients).  WIDE, where A
+// is below -1:
 // la = n ln 2 + y, |y| <= ln 2 / 2, and e^la - 1 = 2^n p + (2^n - 1) without cancellation, p / y
-// to y^5 (1.1e-8); below -87 (kLeastLog) a is 1.6e-38.
+// to y^5 (3.1e-8); below -87 (kLeastLog) a is 1.6e-38.
 constexpr float kLeastLog = -87.f;
 template <bool WIDE>
 __device__ __forceinline__ void decay2(float2 la, float2& a, float2& m) {
