@@ -230,7 +230,8 @@ __global__ void __launch_bounds__(kGroups* LANES, kBlocks<T, GATED, LANES>) k_gl
                     dh = add2(dh, c);
                     const float2 sr = unstash(pr + k * 32, pi + k * 32);
                     const float2 slope = decay_slope2<decltype(wide)::value>(mul2(A, sr), f[k]);
-                    const float2 e = mul2(mul2(dh, slope), fma2(take(pi, 1, k), f2(-1.f), u[k]));
+                    float2 e = mul2(mul2(dh, slope), fma2(take(pi, 1, k), f2(-1.f), u[k]));
+                    if (!kAll && k >= live) e = f2(0.f);  // (0 A is not a number where A is -infinity)
                     e8 = add2(e8, e);
                     c = mul2(f[k], dh);
                     ox.template put<kAll>(mul2(dh, s[k]), lane, have, k < live);
