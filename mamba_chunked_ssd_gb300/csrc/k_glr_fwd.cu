@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kGroups* LANES, kBlocks<T, GATED, LANES>) k_gl
                     float2 o = h;
                     if (GATED) {
                         const float2 g = P::get(z[GATED ? k : 0]);
-                        o = mul2(mul2(h, g), sigmoid2(g));
+                        o = mul2(h, mul2(g, sigmoid2(g)));  // (h g could pass the largest number where the gate is shut)
                     }
                     out.template put<decltype(all)::value>(o, lane, have, t + k < n);
                 }

@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(kBlock) k_glr_step(const GlrArgs a) {
     store<float, true>(a.final_state + b * a.channels + c, h, 0, have);
     if (GATED) {
         const float2 z = pair(a.z, a.z_stride);
-        h = mul2(mul2(h, z), sigmoid2(z));
+        h = mul2(h, mul2(z, sigmoid2(z)));
     }
     store<T, ODD>(static_cast<T*>(a.y) + b * a.y_stride + c, h, 0, have);
 }

@@ -41,3 +41,27 @@ def test_glr_gradients_of_decays_beyond_all_exponents(gated, dtype):
     bd.mamba2_check_device_status()
     assert dr.abs().max() <= 1e-33 and dA.abs().max() <= 1e-33 and dh.abs().max() <= 1e-33
     assert torch.isfinite(dx).all() and torch.isfinite(di).all()
+
+
+@BOTH
+def test_gates_of_the_lowest_value_are_shut(dtype):
+    """z at its dtype's lowest value, as masks have it: SiLU(z) is 0, whatever it meets."""
+    b, L, C = 2, 70, 64
+    d, h0 = glr_inputs(b, L, C, dtype, seed=11, gated=True)
+    h0 *= 8
+    d["z"][:, 20:30] = d["z"][1, :, 5::7] = torch.finfo(dtype).min
+    shut = d["z"] == torch.finfo(dtype).min
+    y, fin, cs = bd.mamba2_glr_fwd(**d, initial_state=h0, want_chunk_states=True)
+    f = {k: ref.f64(t) for k, t in d.items()}
+    y_ref, fin_ref, _ = ref.glr(**f, init=ref.f64(h0))
+    assert bool((y[shut] == 0).all()) and (y.cpu().double() - y_ref).abs().max() <= TOL[dtype] * y_ref.abs().max()
+    assert (fin.cpu().double() - fin_ref).abs().max() <= 1e-5 * fin_ref.abs().max()
+    dy = gen(3)(b, L, C).to(dtype).cuda()
+    dx, dr, di, dz, dA, dh = bd.mamba2_glr_bwd(dy, **d, chunk_states=cs)
+    want, size = ref.glr_grads(ref.f64(dy), **f, init=ref.f64(h0))
+    for got, k in ((dx, "dx"), (dr, "dr"), (di, "di"), (dz, "dz")):
+        assert (got.cpu().double() - want[k]).abs().max() <= TOL[dtype] * want[k].abs().max(), k
+    assert bool((dz[shut] == 0).all()) and (dA.cpu().double() - want["dA"]).abs().max() <= 1e-5 * size.max()
+    one = {k: t[:, 25].contiguous() if t.dim() == 3 else t for k, t in d.items()}
+    y, _ = bd.mamba2_glr_step(**one, state_in=h0)
+    assert bool((y == 0).all())
