@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm(const BlockNormArgs a, 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float2 p = mul2(mul2(f[i], f2(k1)), w1[i]);
-            if (GATED) p = mul2(mul2(p, g[i]), sigmoid2(g[i]));
+            if (GATED) p = mul2(p, mul2(g[i], sigmoid2(g[i])));  // (p g could pass the largest number where the gate is shut)
             v[i] = add2(v[i], p);
             s = fma2(v[i], v[i], s);  // (0 where there is no channel)
         }

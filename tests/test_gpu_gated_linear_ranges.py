@@ -1,4 +1,4 @@
-"""GPU checks of the gated linear recurrence at the ends of its arguments' ranges.
+"""GPU checks of the recurrent block's operators at the ends of its arguments' ranges.
 
 Tolerances are those of the parity tests beside this file, on max|err| / max|ref|: a value that
 leaves as bf16 is rounded once, by 2^-8 of it at most; the fp32 work before it is within 1e-5.
@@ -8,7 +8,7 @@ import torch
 
 import gated_linear_ref as ref
 from mamba_chunked_ssd_gb300 import binding as bd
-from test_gpu_gated_linear import BOTH, INF, TOL, gen, glr_inputs
+from test_gpu_gated_linear import BOTH, INF, TOL, check_norm, gen, glr_inputs, norm_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +65,12 @@ def test_gates_of_the_lowest_value_are_shut(dtype):
     one = {k: t[:, 25].contiguous() if t.dim() == 3 else t for k, t in d.items()}
     y, _ = bd.mamba2_glr_step(**one, state_in=h0)
     assert bool((y == 0).all())
+
+
+@BOTH
+def test_block_norm_gates_of_the_lowest_value_are_shut(dtype):
+    d, res, dr, dy = norm_inputs(9, 300, dtype, dtype)
+    d["z"][3], d["z"][:, 11::5] = torch.finfo(dtype).min, torch.finfo(dtype).min
+    out, y, got = check_norm(d, res, dr, dy)
+    shut = d["z"] == torch.finfo(dtype).min
+    assert torch.equal(out[shut], res[shut]) and bool((got[1][shut] == 0).all())
