@@ -117,7 +117,9 @@ MAMBA2_API mamba2_status mamba2_causal_conv_bwd(const mamba2_conv_shape* shape, 
  *   residual_out [rows, channels] residual_dtype; may be the same pointer as residual
  *                (with the same stride): updated in place
  *   post_weight, scale, pre_weight [channels] fp32; NULL means 1
- * Sums in fp32; y comes from the sum before it is rounded to residual_dtype.  At
+ * Sums in fp32: a row whose sum of squares passes fp32's largest number has N = 0, and
+ * passes no gradient through it.  y comes from the sum before it is rounded to
+ * residual_dtype, which is no narrower than dtype (else MAMBA2_ERR_UNSUPPORTED).  At
  * most 32768 channels, fewer than 2^31 rows, rows x stride up to 2^40. */
 enum { MAMBA2_BLOCK_NORM_POST = 1, MAMBA2_BLOCK_NORM_PRE = 2 };
 

@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm_bwd(const BlockNormBwdA
             group_sums(sums, smem3, count3, by);
             if (post) k1 = rsqrtf(fmaf(sums[0], inv, a.eps));
             if (pre) k2 = rsqrtf(fmaf(sums[1], inv, a.eps));
-            m2 = -k2 * k2 * (sums[2] * inv);
+            m2 = -k2 * k2 * (k2 > 0.f ? sums[2] * inv : 0.f);  // (a sum that k2 = 0 comes from takes this one along)
         }
         float2 last = f2(0.f);
 #pragma unroll

@@ -8,7 +8,8 @@ import torch
 
 import gated_linear_ref as ref
 from mamba_chunked_ssd_gb300 import binding as bd
-from test_gpu_gated_linear import BOTH, INF, TOL, check_norm, gen, glr_inputs, norm_inputs
+from test_gpu_gated_linear import (BOTH, DTYPES, INF, TOL, check_norm, close, f64s, gen, glr_inputs,
+                                   norm_inputs)
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +75,22 @@ def test_block_norm_gates_of_the_lowest_value_are_shut(dtype):
     out, y, got = check_norm(d, res, dr, dy)
     shut = d["z"] == torch.finfo(dtype).min
     assert torch.equal(out[shut], res[shut]) and bool((got[1][shut] == 0).all())
+
+
+@DTYPES
+@pytest.mark.parametrize("C", [300, 4608])
+def test_block_norm_rows_whose_squares_pass_fp32(C, dtype, rdtype):
+    """A sum of squares beyond fp32's largest number is a norm without end: the row's N is 0 and passes no gradient on,
+    the residual's own goes through; other rows are as they were."""
+    d, res, dr, dy = norm_inputs(6, C, dtype, rdtype, gated=False)
+    res[2, 7], d["x"][4, 9] = torch.finfo(rdtype).min, torch.finfo(dtype).min
+    dy *= 4
+    out, y = bd.mamba2_block_norm_fwd(**d, residual=res)
+    dx, _, dres, *weights = bd.mamba2_block_norm_bwd(dr, dy, residual_out=out, **d)
+    assert bool((y[2] == 0).all()) and torch.equal(out[4], res[4]) and torch.equal(dres[2], dr[2])
+    assert bool((dx[4] == 0).all())
+    want, size = ref.block_norm_grads(ref.f64(dr), ref.f64(dy), **f64s(d), out=ref.f64(out))
+    rest = [0, 1, 3, 5]
+    close(dx[rest], want["dx"][rest], TOL[dtype], size["dx"][rest], name="dx")
+    close(dres[rest], want["dresidual"][rest], TOL[rdtype], size["dresidual"][rest], name="dresidual")
+    assert all(torch.isfinite(t).all() for t in (dx, dres, *weights))
