@@ -103,9 +103,8 @@ __global__ void __launch_bounds__(kThreads, per_sm(W)) k_causal_conv_bwd(const C
                     float2 p = bias[i];
 #pragma unroll
                     for (int w = 0; w < W; ++w) p = fma2(wt[w][i], xs[w][i], p);
-                    const float2 g = sigmoid2(p);
-                    const float2 h = mul2(ds[0][i], g);
-                    ds[0][i] = fma2(mul2(h, p), fma2(g, f2(-1.f), f2(1.f)), h);
+                    const float2 g = sigmoid2(p);  // (act' first: d p could pass the largest number where act' is 1)
+                    ds[0][i] = mul2(ds[0][i], mul2(g, fma2(p, fma2(g, f2(-1.f), f2(1.f)), f2(1.f))));
                     if (!live) ds[0][i] = f2(0.f);  // (p of what is not finite)
                 }
                 if (sum) {

@@ -8,7 +8,7 @@ import torch
 
 import gated_linear_ref as ref
 from mamba_chunked_ssd_gb300 import binding as bd
-from test_gpu_gated_linear import (BOTH, DTYPES, INF, TOL, check_norm, close, f64s, gen, glr_inputs,
+from test_gpu_gated_linear import (BOTH, DTYPES, INF, TOL, check_norm, close, conv_inputs, f64s, gen, glr_inputs,
                                    norm_inputs)
 
 pytestmark = pytest.mark.gpu
@@ -94,3 +94,19 @@ def test_block_norm_rows_whose_squares_pass_fp32(C, dtype, rdtype):
     close(dx[rest], want["dx"][rest], TOL[dtype], size["dx"][rest], name="dx")
     close(dres[rest], want["dresidual"][rest], TOL[rdtype], size["dresidual"][rest], name="dresidual")
     assert all(torch.isfinite(t).all() for t in (dx, dres, *weights))
+
+
+@BOTH
+def test_conv_bwd_activations_of_the_largest_values(dtype):
+    """An input at its dtype's lowest value, times weights of both signs: SiLU' is 0 or 1 there, whatever it meets.  (The
+    weights' own gradients are products with that input, beyond fp32.)"""
+    d, init, dy, dfin = conv_inputs(2, 60, 40, 4, dtype, seed=12)
+    d["weight"] = d["weight"] / d["weight"].abs().sum(1, keepdim=True) * 0.9
+    d["x"][0, 20], d["x"][1, 33:36, ::3] = torch.finfo(dtype).min, torch.finfo(dtype).min
+    dy *= 8
+    dx, dw, _, dinit = bd.mamba2_causal_conv_bwd(dy, **d, initial_state=init, dfinal_state=dfin)
+    f = f64s(d)
+    want, _ = ref.conv_grads(ref.f64(dy), f["x"], f["weight"], f["bias"], init=ref.f64(init), dfinal=ref.f64(dfin))
+    close(dx, want["dx"], TOL[dtype], name="dx"), close(dinit, want["dinit"], TOL[dtype], name="dinit")
+    clean = [c for c in range(40) if c % 3]
+    assert not torch.isnan(dw[clean]).any()
