@@ -181,6 +181,17 @@ __device__ __forceinline__ void copy_piece(uint32_t to, const void* from, int by
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
 
+// A gate z as it comes, but no lower than -1000: SiLU is 0 from there down, and the product of z with what it gates stays
+// a number at the dtype's lowest value, too.  NaN stays.  (As p (z sigmoid(z)) instead, which keeps z for longer,
+// 8192 x 8192 in bf16 with an fp32 residual takes 185 us for 139, in registers that are all taken.)
+__device__ __forceinline__ float gate(float z) { return glr::max_nan(z, -1000.f); }
+__device__ __forceinline__ float2 gate(float2 z) { return make_float2(gate(z.x), gate(z.y)); }
+__device__ __forceinline__ uint32_t gate(uint32_t z) {  // two of bf16
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(z), "r"(0xc47ac47au));
+    return r;
+}
+
 // A walker's rows of one input.
 template <typename E, int GRP>
 struct RowIn {
@@ -239,7 +250,8 @@ struct RowIn {
         }
         next += step;
     }
-    // `row`: the row's first channel in memory (but kOwn); zeros where there is no channel
+    // `row`: the row's first channel in memory (but kOwn); zeros where there is no channel.  GATE: values of a gate
+    template <bool GATE = false>
     static __device__ __forceinline__ void read(const uint8_t* place, const E* row, int n, float2 (&f)[4]) {
         if constexpr (kOwn) {
 #pragma unroll
@@ -247,14 +259,15 @@ struct RowIn {
                 const Unit v = *reinterpret_cast<const Unit*>(place + (i * blockDim.x + threadIdx.x) * kBytes);
                 const auto* p = reinterpret_cast<const typename glr::Pair<E>::raw*>(&v);
 #pragma unroll
-                for (int k = 0; k < GRP / 2; ++k) f[i * GRP / 2 + k] = glr::Pair<E>::get(p[k]);
+                for (int k = 0; k < GRP / 2; ++k) f[i * GRP / 2 + k] = glr::Pair<E>::get(GATE ? gate(p[k]) : p[k]);
             }
         } else {
             const E* from = reinterpret_cast<const E*>(place + (reinterpret_cast<uintptr_t>(row) & 15));
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
                 const int c = channel<GRP>(i);
-                const float v = c < n ? to_f32(from[c]) : 0.f;
+                float v = c < n ? to_f32(from[c]) : 0.f;
+                if (GATE) v = gate(v);
                 if (i % 2) f[i / 2].y = v;
                 else f[i / 2].x = v;
             }

@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm(const BlockNormArgs a, 
         auto first = [&](auto* base, int64_t stride) { return base + row * stride + c0; };
         float2 f[4], g[4], v[4];
         InT::read(at, first(static_cast<const T*>(a.x), a.x_stride), n, f);
-        if (GATED) InT::read(at + bx, first(static_cast<const T*>(a.z), a.z_stride), n, g);
+        if (GATED) InT::template read<true>(at + bx, first(static_cast<const T*>(a.z), a.z_stride), n, g);
         if (a.res) {
             InR::read(at + at_res, first(static_cast<const R*>(a.res), a.res_stride), n, v);
         } else {
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kMost, 1) k_block_norm(const BlockNormArgs a, 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float2 p = mul2(mul2(f[i], f2(k1)), w1[i]);
-            if (GATED) p = mul2(p, mul2(g[i], sigmoid2(g[i])));  // (p g could pass the largest number where the gate is shut)
+            if (GATED) p = mul2(mul2(p, g[i]), sigmoid2(g[i]));
             v[i] = add2(v[i], p);
             s = fma2(v[i], v[i], s);  // (0 where there is no channel)
         }
