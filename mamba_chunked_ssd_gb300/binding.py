@@ -541,7 +541,8 @@ def mamba2_group_norm(x, weight, ngroups, z=None, bias=None, eps=1e-5, subtract_
 
 
 # The recurrent block's entry points.  A gradient that is given goes where it lies (a slice of a
-# wider tensor is fine); one that is not given comes back as a new tensor.
+# wider tensor is fine); one that is not given comes back as a new tensor.  Autograd records none of
+# the calls: what they return is cut off from inputs that require gradients.
 _glr_shape = functools.lru_cache(maxsize=1024)(lambda *a: mamba2_glr_shape(*a))
 _glr_grad_strides = functools.lru_cache(maxsize=1024)(lambda *a: mamba2_glr_grad_strides(*a))
 _block_norm_shape = functools.lru_cache(maxsize=1024)(lambda *a: mamba2_block_norm_shape(*a))

@@ -50,6 +50,8 @@ __device__ __forceinline__ float2 sigmoid2(float2 x) {
 // is below -1:
 // la = n ln 2 + y, |y| <= ln 2 / 2, and e^la - 1 = 2^n p + (2^n - 1) without cancellation, p / y
 // to y^5 (3.1e-8); below -87 (kLeastLog) a is 1.6e-38.
+// A strip takes the wide form for any A below -1 (forward, 16 x 2048 x 4096 in bf16: 177 us with the narrow one, 193 with
+// the wide one; forward and backward, 4 x 4096 x 4096, gated: 137 and 252, 146 and 263).
 constexpr float kLeastLog = -87.f;
 template <bool WIDE>
 __device__ __forceinline__ void decay2(float2 la, float2& a, float2& m) {
@@ -322,7 +324,8 @@ inline Rows rows_of(const void* const* p, const int64_t* strides, int count, int
 // else one (an exchange between blocks costs more than it gives where strips alone fill half of the GPU).
 // 1 x 4096 tokens in bf16, us with 1, 4 and 8.  Forward: 32 strips 50, 28, 24; 64 strips 52, 34, 31 (gated 63, 38, 48);
 // 100 strips 52, 38, 44; 128 strips 52, 45, 50 (gated 63, 64, 69).  Backward: 32 strips 104, 46, 34; 64 strips
-// 108, 56, 67; 100 strips 112, 65, 71; 128 strips 114, 104, 95.
+// 108, 56, 67; 100 strips 112, 65, 71; 128 strips 114, 104, 95.  One rule for both directions and with or without a gate is
+// not the best of each: 64 strips forward without a gate lose 3 us by it, 128 strips 7, and 19 backward.
 inline int glr_cluster(int64_t strips, int64_t tiles) {
     const int64_t most = 3 * (int64_t)(sm_count() > 0 ? sm_count() : 152);
     if (tiles >= 8 && 8 * strips <= most) return 8;

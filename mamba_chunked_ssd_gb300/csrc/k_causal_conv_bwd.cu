@@ -10,8 +10,10 @@
 // run reads W - 1 tokens of the next one too.  Inputs come through shared memory, each thread's
 // to its own place, 16 tokens ahead.  Sums over a run stay in registers and go to a row of
 // partial sums, which a second kernel adds up.  About 22 instructions an element (19 of them packed multiplications
-// and additions of two) in 16 warps of an SM bound it next to memory: 4 x 8192 x 8192 in bf16 282 us, 5.7
-// TB/s; 4 x 4096 x 8192 in fp32 259 us, 6.2 TB/s.  (Vectors of four bytes, with 24 to 32 warps: 347 to 357 us.)
+// and additions of two) in 16 warps of an SM bound it next to memory: 4 x 8192 x 8192 in bf16 273 us, 5.9
+// TB/s; 4 x 4096 x 8192 in fp32 250 us, 6.4 TB/s.  (Vectors of four bytes, with 24 to 32 warps: 328 and 319 us.)
+// Wider than four taps registers leave eight warps: widths 2 to 8 of 4 x 8192 x 8192 in bf16 246, 253, 273, 316, 341, 369,
+// 416 us; of 4 x 4096 x 4096 in fp32 128, 131, 132, 133, 143, 146, 159.
 #include "glr_math.cuh"
 
 namespace m2 {
@@ -27,7 +29,8 @@ constexpr int kThreads = 128;
 // Blocks of an SM that registers have to allow.
 constexpr int per_sm(int W) { return W <= 4 ? 4 : 2; }
 constexpr int kAhead = 8;
-// Eights of tokens under way per thread (4 x 8192 x 8192 in bf16: one 339 us, two 295, three 306).
+// Eights of tokens under way per thread (4 x 8192 x 8192 in bf16: one 293 us, two 273, three 272; 16 x 1024 x 4096 93, 92
+// and 93).
 constexpr int kDepth = 2;
 
 template <typename T, int VEC>
@@ -225,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(W)) k_causal_conv_bwd(const C
 
 // Runs of each row, as blocks that fill the GPU's places whole times, with the least time: that of a run of tokens and
 // of about 11 more a tap (the next run's first ones, the weights and the sums), for each filling.  16 x 1024 x 4096 in
-// bf16: runs of 256 tokens, of which one filling lacks a sixth, 104 us; of 114, in two whole ones, 110.
+// bf16: runs of 256 tokens, of which one filling lacks a sixth, 92 us; of 114, in two whole ones, 95.
 int64_t runs_of(int64_t batch, int64_t seqlen, int64_t gx, int width) {
     const int sms = sm_count();
     const int64_t places = per_sm(width) * (int64_t)(sms > 0 ? sms : 152), blocks = gx * batch, most = (seqlen + 31) / 32;

@@ -11,8 +11,10 @@
 // pass kept, by the same exchange of maps as there; the maps of the gradients, c -> A c + R
 // from the other end, go through the same barrier.  What both halves need stays in
 // registers or in shared memory, in the places of inputs that have been used where they fit.
-// About 60 instructions an element in 16 (gated 12) warps of an SM bound it next to memory: 16 x 1024 x 4096 in bf16 196 us,
-// 4.8 TB/s, gated 243 us, 5.0 TB/s; 4 x 4096 x 4096 216 us, gated 258.
+// About 60 instructions an element, and 16 (gated 12) warps of an SM that wait for one another at each tile's exchange: neither
+// the issue slots (55 % of them, gated) nor DRAM (61 %) are full, three or four warps to a scheduler are what bounds
+// it.  16 x 1024 x 4096 in bf16 196 us, 4.8 TB/s, gated 243 us, 5.0 TB/s; 4 x 4096 x 4096 216 us, gated 258; in fp32 326 us,
+// gated, with 8 warps, 417.
 #include <type_traits>
 
 #include "glr_math.cuh"

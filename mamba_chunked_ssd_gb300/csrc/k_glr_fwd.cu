@@ -12,7 +12,8 @@
 // About 32 instructions an element (a third of them the gates', the rest the decay's, the exchange's and
 // the loads') leave 60 % of the issue slots used by 16 warps of 128 registers: that is what bounds it next to
 // memory.  16 x 2048 x 4096 in bf16: 183 us, 5.9 TB/s; 4 x 8192 x 4096, 512 strips of which some SMs have three
-// and some four: 214 us, 5.0 TB/s.
+// and some four: 214 us, 5.0 TB/s.  In fp32 4 x 4096 x 4096 173 us, 6.2 TB/s, gated 214.  Rows on pairs take copies of four
+// bytes and spill registers, one block a strip: 4 x 8192 x 4090 in bf16 756 us.
 #include <type_traits>
 
 #include "glr_math.cuh"
